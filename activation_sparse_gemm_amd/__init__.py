@@ -27,6 +27,9 @@ __all__ = [
     "RTL_VARIANT_STREAM_K",
     "rtl_status_string", "rtl_version",
     "rtl_quantize_weight_fp8", "rtl_linear_fused_fp8", "rtl_linear_fused_fp8_workspace_bytes",
+    "RTL_ROPE_ADJACENT", "RTL_ROPE_HALVES", "rtl_rope_axes", "rtl_qk_norm_rope", "rtl_qk_norm_rope_backward",
+    "rtl_qk_norm_rope_backward_workspace_bytes",
+    "RTL_ACT_SILU", "RTL_ACT_GELU", "rtl_glu_fused", "rtl_glu_backward", "rtl_glu_backward_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +42,8 @@ RTL_VARIANT_AUTO, RTL_VARIANT_PROLOGUE, RTL_VARIANT_PRECOMPRESSED, RTL_VARIANT_S
 EPS = 1e-8
 RTL_NOALLOC_SCRATCH_BYTES = 192 << 20  # include/rtl.h
 RTL_MLP_AUTO, RTL_MLP_PRODUCER, RTL_MLP_CONSUMER = 0, 1, 2
+RTL_ROPE_ADJACENT, RTL_ROPE_HALVES = 0, 1
+RTL_ACT_SILU, RTL_ACT_GELU = 0, 1
 STATUS = {0: "RTL_OK", 1: "RTL_ERR_NULL", 2: "RTL_ERR_SHAPE", 3: "RTL_ERR_ALIGN", 4: "RTL_ERR_UNSUPPORTED",
           5: "RTL_ERR_ARG", 6: "RTL_ERR_WORKSPACE", 7: "RTL_ERR_HIP"}
 
@@ -46,7 +51,9 @@ STATUS = {0: "RTL_OK", 1: "RTL_ERR_NULL", 2: "RTL_ERR_SHAPE", 3: "RTL_ERR_ALIGN"
 EXPORTS = ["rtl_sparsify", "rtl_linear_fused_workspace_bytes", "rtl_linear_fused", "rtl_linear_fused_ex",
            "rtl_linear_fused_prep", "rtl_linear_fused_main", "rtl_linear_fused_noalloc", "rtl_linear_dense_ref",
            "rtl_mlp_fused_workspace_bytes", "rtl_mlp_fused", "rtl_quantize_weight_fp8",
-           "rtl_linear_fused_fp8_workspace_bytes", "rtl_linear_fused_fp8", "rtl_status_string",
+           "rtl_linear_fused_fp8_workspace_bytes", "rtl_linear_fused_fp8", "rtl_rope_axes", "rtl_qk_norm_rope",
+           "rtl_qk_norm_rope_backward_workspace_bytes", "rtl_qk_norm_rope_backward", "rtl_glu_fused",
+           "rtl_glu_backward_workspace_bytes", "rtl_glu_backward", "rtl_status_string",
            "rtl_last_error", "rtl_version"]
 
 
@@ -88,6 +95,24 @@ def _load() -> ctypes.CDLL:
     L.rtl_linear_fused_fp8_workspace_bytes.restype = sz
     L.rtl_linear_fused_fp8.argtypes = [i64, i64, i64, i64, p, p, p, p, p, i32, f32, p, p, sz, p, p, p]
     L.rtl_linear_fused_fp8.restype = i32
+    f64, dims = ctypes.c_double, ctypes.POINTER(ctypes.c_int32)
+    heads = [p, i64, i64]  # pointer, row stride, head stride
+    rope = [p, i32, dims, f64, i32]  # pos, n_axes, axis_dims, theta, pairs
+    L.rtl_rope_axes.argtypes = [i32, i64, i64, i64, *heads, *rope, i32, *heads, p]
+    L.rtl_rope_axes.restype = i32
+    L.rtl_qk_norm_rope.argtypes = [i32, i64, i64, i64, i64, *heads, *heads, p, p, f32, *rope, *heads, *heads, p]
+    L.rtl_qk_norm_rope.restype = i32
+    L.rtl_qk_norm_rope_backward_workspace_bytes.argtypes = [i64]
+    L.rtl_qk_norm_rope_backward_workspace_bytes.restype = sz
+    L.rtl_qk_norm_rope_backward.argtypes = [i32, i64, i64, i64, i64, *heads, *heads, p, p, f32, *rope, *heads, *heads,
+                                            *heads, *heads, p, p, p, sz, p]
+    L.rtl_qk_norm_rope_backward.restype = i32
+    L.rtl_glu_fused.argtypes = [i32, i32, i64, i64, i64, p, p, p, p, p, p, p]
+    L.rtl_glu_fused.restype = i32
+    L.rtl_glu_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.rtl_glu_backward_workspace_bytes.restype = sz
+    L.rtl_glu_backward.argtypes = [i32, i32, i64, i64, i64, p, p, p, p, p, p, p, p, p, p, sz, p]
+    L.rtl_glu_backward.restype = i32
     L.rtl_status_string.argtypes = [i32]
     L.rtl_status_string.restype = ctypes.c_char_p
     L.rtl_last_error.argtypes = []
@@ -320,3 +345,164 @@ def rtl_linear_fused_fp8(X: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor, LA
     _check(lib.rtl_linear_fused_fp8(M, N, K, R, _ptr(X), _ptr(Wq), _ptr(sw), _ptr(LA), _ptr(LB), tie, eps, _ptr(Y),
                                     _ptr(workspace), ws_bytes, _ptr(dbg_xq), _ptr(dbg_sx), _stream(stream)))
     return Y
+
+
+def _one_device(*tensors):
+    """The device that every given tensor is on; the call is made with that device current, so
+    that a call without ``stream`` runs on that device's current stream."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError(f"tensors must be on one GPU, got {sorted(map(str, devices))}")
+    return torch.cuda.device(next(iter(devices)))
+
+
+def _expect(name, t, shape, dtype):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _heads(t):
+    """Pointer, row stride and head stride of a [M, H, D] tensor whose channels are contiguous."""
+    if t is None:
+        return None, 0, 0
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError("the channels of a head must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0), t.stride(1)
+
+
+def _rope_args(pos, axis_dims, theta, pairs, M):
+    dims = [int(d) for d in axis_dims]
+    if dims:
+        _expect("pos", pos, (M, len(dims)), torch.float32)
+    return _ptr(pos) if dims else None, len(dims), (ctypes.c_int32 * max(len(dims), 1))(*dims), float(theta), pairs
+
+
+def rtl_rope_axes(X: torch.Tensor, pos: torch.Tensor, axis_dims, theta: float = 10000.0,
+                  pairs: int = RTL_ROPE_ADJACENT, inverse: bool = False, Y=None, stream=None) -> torch.Tensor:
+    """X [M,H,D] (any row and head strides) turned by the positions ``pos`` [M, axes] float32.
+
+    ``axis_dims`` holds the channels that each axis turns (even; their sum a multiple of 8, at
+    most D).  ``pairs``: RTL_ROPE_ADJACENT pairs channels 2p and 2p + 1, RTL_ROPE_HALVES p and
+    p + sum / 2.  ``inverse`` turns back, which is also the gradient.  ``Y`` may be X."""
+    M, H, D = X.shape
+    with _one_device(X, pos, Y):
+        if Y is None:
+            Y = _empty((M, H, D), X.dtype, X.device, stream)
+        _expect("Y", Y, (M, H, D), X.dtype)
+        _check(lib.rtl_rope_axes(_dt(X), M, H, D, *_heads(X), *_rope_args(pos, axis_dims, theta, pairs, M),
+                                 int(inverse), *_heads(Y), _stream(stream)))
+    return Y
+
+
+def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 10000.0, eps: float = 1e-6,
+                     pairs: int = RTL_ROPE_ADJACENT, Qo=None, Ko=None, stream=None):
+    """RMS norm of every head of Q [M,Hq,D] and K [M,Hk,D] (weights ``qw`` and ``kw`` [D], None:
+    ones), then the rotation of rtl_rope_axes (``axis_dims`` empty: none), in one pass.  K None:
+    queries only.  Q and K may be views of a packed projection.  Returns (Qo, Ko); outputs given
+    by the caller are written in place and may be Q and K."""
+    M, Hq, D = Q.shape
+    Hk = 0 if K is None else K.shape[1]
+    with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, Qo, Ko):
+        if Qo is None:
+            Qo = _empty((M, Hq, D), Q.dtype, Q.device, stream)
+        if Ko is None and K is not None:
+            Ko = _empty((M, Hk, D), Q.dtype, Q.device, stream)
+        for name, t, shape in (("K", K, (M, Hk, D)), ("qw", qw, (D,)), ("kw", kw, (D,)), ("Qo", Qo, (M, Hq, D)),
+                               ("Ko", Ko, (M, Hk, D))):
+            _expect(name, t, shape, Q.dtype)
+        _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _ptr(qw), _ptr(kw), eps,
+                                    *_rope_args(pos, axis_dims, theta, pairs, M), *_heads(Qo), *_heads(Ko),
+                                    _stream(stream)))
+    return Qo, Ko
+
+
+def rtl_qk_norm_rope_backward_workspace_bytes(D: int) -> int:
+    return int(lib.rtl_qk_norm_rope_backward_workspace_bytes(D))
+
+
+def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: torch.Tensor, dKo,
+                              theta: float = 10000.0, eps: float = 1e-6, pairs: int = RTL_ROPE_ADJACENT, dQ=None,
+                              dK=None, dqw=None, dkw=None, workspace=None, stream=None):
+    """Gradient of rtl_qk_norm_rope: (dQ, dK, dqw, dkw) from its inputs and the gradients of its
+    outputs; dqw and dkw [D] are float32 sums over all tokens and heads.  Outputs given by the
+    caller are written in place; dQ and dK may be dQo and dKo, or Q and K."""
+    M, Hq, D = Q.shape
+    Hk = 0 if K is None else K.shape[1]
+    with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, dQo, dKo, dQ, dK, dqw, dkw, workspace):
+        if dQ is None:
+            dQ = _empty((M, Hq, D), Q.dtype, Q.device, stream)
+        if dqw is None:
+            dqw = _empty((D,), torch.float32, Q.device, stream)
+        if K is not None:
+            if dK is None:
+                dK = _empty((M, Hk, D), Q.dtype, Q.device, stream)
+            if dkw is None:
+                dkw = _empty((D,), torch.float32, Q.device, stream)
+        for name, t, shape in (("K", K, (M, Hk, D)), ("qw", qw, (D,)), ("kw", kw, (D,)), ("dQo", dQo, (M, Hq, D)),
+                               ("dKo", dKo, (M, Hk, D)), ("dQ", dQ, (M, Hq, D)), ("dK", dK, (M, Hk, D))):
+            _expect(name, t, shape, Q.dtype)
+        _expect("dqw", dqw, (D,), torch.float32)
+        _expect("dkw", dkw, (D,), torch.float32)
+        if workspace is None:
+            workspace = _empty((max(rtl_qk_norm_rope_backward_workspace_bytes(D), 1),), torch.uint8, Q.device, stream)
+        _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _ptr(qw), _ptr(kw), eps,
+                                             *_rope_args(pos, axis_dims, theta, pairs, M), *_heads(dQo), *_heads(dKo),
+                                             *_heads(dQ), *_heads(dK), _ptr(dqw), _ptr(dkw), _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dQ, dK, dqw, dkw
+
+
+def rtl_glu_fused(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: int = RTL_ACT_SILU, Y=None, G=None, U=None,
+                  stream=None) -> torch.Tensor:
+    """Y = act(X Wg^T) * (X Wu^T) in one kernel (bf16).  X [M,K], Wg and Wu [H,K], Y [M,H].
+    ``G`` and ``U`` [M,H], when given, receive the two products (rtl_glu_backward takes them)."""
+    M, K = X.shape
+    H = Wg.shape[0]
+    with _one_device(X, Wg, Wu, Y, G, U):
+        if Y is None:
+            Y = _empty((M, H), torch.bfloat16, X.device, stream)
+        for name, t, shape in (("X", X, (M, K)), ("Wg", Wg, (H, K)), ("Wu", Wu, (H, K)), ("Y", Y, (M, H)),
+                               ("G", G, (M, H)), ("U", U, (M, H))):
+            _expect(name, t, shape, torch.bfloat16)
+        _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Y), _ptr(G), _ptr(U),
+                                 _stream(stream)))
+    return Y
+
+
+def rtl_glu_backward_workspace_bytes(M: int, K: int, H: int) -> int:
+    return int(lib.rtl_glu_backward_workspace_bytes(M, K, H))
+
+
+def rtl_glu_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
+                     dY: torch.Tensor, act: int = RTL_ACT_SILU, dX=None, dWg=None, dWu=None, workspace=None,
+                     need_dx: bool = True, need_dw: bool = True, stream=None):
+    """Gradient of rtl_glu_fused: (dX, dWg, dWu) from its inputs, G and U as it left them, and dY
+    [M,H] (bf16).  ``need_dx`` or ``need_dw`` False leaves those out (None).  Outputs given by the
+    caller are written in place; pass ``workspace`` (uint8) to keep the call free of allocations."""
+    M, K = X.shape
+    H = Wg.shape[0]
+    with _one_device(X, Wg, Wu, G, U, dY, dX, dWg, dWu, workspace):
+        if need_dx and dX is None:
+            dX = _empty((M, K), torch.bfloat16, X.device, stream)
+        if need_dw and dWg is None:
+            dWg = _empty((H, K), torch.bfloat16, X.device, stream)
+        if need_dw and dWu is None:
+            dWu = _empty((H, K), torch.bfloat16, X.device, stream)
+        if not need_dx:
+            dX = None
+        if not need_dw:
+            dWg = dWu = None
+        for name, t, shape in (("X", X, (M, K)), ("Wg", Wg, (H, K)), ("Wu", Wu, (H, K)), ("G", G, (M, H)),
+                               ("U", U, (M, H)), ("dY", dY, (M, H)), ("dX", dX, (M, K)), ("dWg", dWg, (H, K)),
+                               ("dWu", dWu, (H, K))):
+            _expect(name, t, shape, torch.bfloat16)
+        if workspace is None:
+            workspace = _empty((max(rtl_glu_backward_workspace_bytes(M, K, H), 1),), torch.uint8, X.device, stream)
+        _check(lib.rtl_glu_backward(act, RTL_BF16, M, K, H, _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(G), _ptr(U), _ptr(dY),
+                                    _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dX, dWg, dWu

@@ -15,7 +15,10 @@
 //    vector ALUs have time to spare); the down GEMM.
 // The consumer variant is the faster on gfx950 at the text-to-image MLP shape and is the
 // default (AUTO).
+//
+// The gated block (act(X Wg^T) (X Wu^T), dense) and its gradient are compiled in this unit too.
 #include "bf16_common.h"
+#include "glu_bf16.h"
 
 namespace rtl {
 

@@ -395,3 +395,324 @@ rtl_status rtl_linear_fused_fp8(int64_t M, int64_t N, int64_t K, int64_t R, cons
 }
 
 }  // extern "C"
+
+namespace {
+
+// A [M, H, D] tensor with strides, in elements; the stride of an extent of 1 counts as 0.
+struct View {
+  const void* p;
+  int64_t M, H, D, row, head;
+  size_t es;
+  View(const void* p_, int64_t M_, int64_t H_, int64_t D_, int64_t row_, int64_t head_, size_t es_)
+      : p(p_), M(M_), H(H_), D(D_), row(M_ == 1 ? 0 : row_), head(H_ == 1 ? 0 : head_), es(es_) {}
+  int64_t span() const { return (M - 1) * row + (H - 1) * head + D; }  // elements
+  bool same(const View& o) const { return p == o.p && row == o.row && head == o.head; }
+};
+
+rtl_status check_view(const View& v, const char* name, bool output) {
+  if (!v.p) return fail(RTL_ERR_NULL, "%s is required", name);
+  if (v.row < 0 || v.head < 0 || (__int128)(v.M - 1) * v.row + (__int128)(v.H - 1) * v.head > ((int64_t)1 << 48))
+    return fail(RTL_ERR_SHAPE, "strides of %s out of range (row %lld, head %lld)", name, (long long)v.row,
+                (long long)v.head);
+  if (misaligned(v.p) || (v.row * v.es) % 16 != 0 || (v.head * v.es) % 16 != 0)
+    return fail(RTL_ERR_ALIGN, "%s and its strides must be 16-byte aligned", name);
+  if (output) {
+    const bool rows = (v.H == 1 || v.head >= v.D) && (v.M == 1 || v.row >= (v.H - 1) * v.head + v.D);
+    const bool heads = (v.M == 1 || v.row >= v.D) && (v.H == 1 || v.head >= (v.M - 1) * v.row + v.D);
+    if (!rows && !heads) return fail(RTL_ERR_ARG, "the elements of %s overlap", name);
+  }
+  return RTL_OK;
+}
+
+// Windows [0, na) and [d, d + nb) that both repeat every `period` elements share none.
+bool windows_apart(int64_t d, int64_t na, int64_t nb, int64_t period) {
+  const int64_t r = ((d % period) + period) % period;
+  return r >= na && r + nb <= period;
+}
+
+// Two views that share no element: apart as byte ranges, or interleaved in one buffer with
+// the same row stride (each row's heads in a window of its own), the same head stride (each
+// head's rows likewise), or the same head stride inside rows of whole heads.
+bool apart(const View& a, const View& b) {
+  if (!overlap(a.p, (size_t)a.span() * a.es, b.p, (size_t)b.span() * b.es)) return true;
+  const int64_t bytes = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+  if (bytes % (int64_t)a.es != 0) return false;
+  const int64_t d = bytes / (int64_t)a.es;
+  const int64_t ra = (a.H - 1) * a.head + a.D, rb = (b.H - 1) * b.head + b.D;  // a row's window
+  const int64_t ha = (a.M - 1) * a.row + a.D, hb = (b.M - 1) * b.row + b.D;    // a head's window
+  if (a.row == b.row && a.row > 0 && windows_apart(d, ra, rb, a.row)) return true;
+  if (a.head == b.head && a.head > 0 && windows_apart(d, ha, hb, a.head)) return true;
+  return a.head == b.head && a.head > 0 && a.row % a.head == 0 && b.row % b.head == 0 &&
+         windows_apart(d, a.D, b.D, a.head);
+}
+
+bool apart_flat(const View& a, const void* p, size_t bytes) { return !overlap(a.p, (size_t)a.span() * a.es, p, bytes); }
+
+// Checks shared by rtl_rope_axes, rtl_qk_norm_rope and its gradient (everything but the
+// tensors); need_axes: a call without axes is refused.
+rtl_status check_rope(rtl_dtype dt, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const float* pos, int32_t n_axes,
+                      const int32_t* axis_dims, double theta, rtl_rope_pairs pairs, bool need_axes) {
+  rtl_status st;
+  if ((st = check_dtype(dt)) != RTL_OK) return st;
+  if (M <= 0 || Hq <= 0 || Hk < 0 || D <= 0)
+    return fail(RTL_ERR_SHAPE, "need M, heads, D > 0 (M=%lld H=%lld,%lld D=%lld)", (long long)M, (long long)Hq,
+                (long long)Hk, (long long)D);
+  if (Hq > INT32_MAX || Hk > INT32_MAX || M > INT32_MAX || M * (Hq + Hk) > INT32_MAX)
+    return fail(RTL_ERR_SHAPE, "M x heads is too large (M=%lld H=%lld,%lld)", (long long)M, (long long)Hq,
+                (long long)Hk);
+  if (D % 8 != 0 || D > 256) return fail(RTL_ERR_UNSUPPORTED, "need D %% 8 == 0 and D <= 256 (D=%lld)", (long long)D);
+  if (pairs != RTL_ROPE_ADJACENT && pairs != RTL_ROPE_HALVES)
+    return fail(RTL_ERR_UNSUPPORTED, "unsupported pairing %d", (int)pairs);
+  if (n_axes < (need_axes ? 1 : 0) || n_axes > 4) return fail(RTL_ERR_UNSUPPORTED, "unsupported number of axes %d", n_axes);
+  if (n_axes == 0) return RTL_OK;
+  if (!pos || !axis_dims) return fail(RTL_ERR_NULL, "pos and axis_dims are required");
+  if (misaligned(pos)) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  int64_t sum = 0;
+  for (int a = 0; a < n_axes; a++) {
+    if (axis_dims[a] < 2 || axis_dims[a] % 2 != 0 || axis_dims[a] > D)
+      return fail(RTL_ERR_SHAPE, "axis %d turns %d channels: need an even number of 2 to D", a, axis_dims[a]);
+    sum += axis_dims[a];
+  }
+  if (sum > D) return fail(RTL_ERR_SHAPE, "the axes turn %lld of %lld channels", (long long)sum, (long long)D);
+  if (sum % 8 != 0) return fail(RTL_ERR_UNSUPPORTED, "the axes must turn a multiple of 8 channels (%lld)", (long long)sum);
+  if (!(theta > 0.0 && theta <= 1e300)) return fail(RTL_ERR_ARG, "theta must be finite and above 0 (got %g)", theta);
+  return RTL_OK;
+}
+
+rtl::RopeCall rope_call(rtl_dtype dt, bool norm, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const float* pos,
+                        int32_t n_axes, const int32_t* axis_dims, double theta, rtl_rope_pairs pairs, bool inverse) {
+  rtl::RopeCall c{};
+  c.dt = dt == RTL_BF16 ? rtl::kDtBF16 : rtl::kDtF32;
+  c.norm = norm;
+  c.halves = pairs == RTL_ROPE_HALVES;
+  c.inverse = inverse;
+  c.M = M;
+  c.H[0] = Hq;
+  c.H[1] = Hk;
+  c.D = D;
+  c.pos = pos;
+  c.axes = n_axes;
+  c.dims = axis_dims;
+  c.theta = theta;
+  return c;
+}
+
+rtl::StridedHeads heads(const View& v) { return rtl::StridedHeads{v.p, v.row, v.head}; }
+
+// eps of the head norms: above 0, so that a head of zeros has a finite r.
+rtl_status check_norm_eps(float eps) {
+  if (!(eps > 0.f && eps <= 1.f)) return fail(RTL_ERR_ARG, "eps must lie in (0, 1] (got %g)", (double)eps);
+  return RTL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rtl_status rtl_rope_axes(rtl_dtype dt, int64_t M, int64_t H, int64_t D, const void* X, int64_t x_row, int64_t x_head,
+                         const float* pos, int32_t n_axes, const int32_t* axis_dims, double theta,
+                         rtl_rope_pairs pairs, int32_t inverse, void* Y, int64_t y_row, int64_t y_head, void* stream) {
+  rtl_status st;
+  if ((st = check_rope(dt, M, H, 0, D, pos, n_axes, axis_dims, theta, pairs, true)) != RTL_OK) return st;
+  if (inverse != 0 && inverse != 1) return fail(RTL_ERR_ARG, "inverse must be 0 or 1 (got %d)", inverse);
+  const View x(X, M, H, D, x_row, x_head, elem_size(dt)), y(Y, M, H, D, y_row, y_head, elem_size(dt));
+  if ((st = check_view(x, "X", false)) != RTL_OK || (st = check_view(y, "Y", true)) != RTL_OK) return st;
+  if ((!x.same(y) && !apart(x, y)) || !apart_flat(y, pos, (size_t)M * n_axes * 4))
+    return fail(RTL_ERR_ARG, "Y overlaps an input");
+  rtl::RopeCall c = rope_call(dt, false, M, H, 0, D, pos, n_axes, axis_dims, theta, pairs, inverse != 0);
+  c.x[0] = heads(x);
+  c.y[0] = heads(y);
+  return hip_status(rtl::launch_rope(c, (hipStream_t)stream), "rtl_rope_axes launch");
+}
+
+rtl_status rtl_qk_norm_rope(rtl_dtype dt, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const void* Q, int64_t q_row,
+                            int64_t q_head, const void* K, int64_t k_row, int64_t k_head, const void* qw,
+                            const void* kw, float eps, const float* pos, int32_t n_axes, const int32_t* axis_dims,
+                            double theta, rtl_rope_pairs pairs, void* Qo, int64_t qo_row, int64_t qo_head, void* Ko,
+                            int64_t ko_row, int64_t ko_head, void* stream) {
+  rtl_status st;
+  if ((st = check_rope(dt, M, Hq, Hk, D, pos, n_axes, axis_dims, theta, pairs, false)) != RTL_OK) return st;
+  if ((st = check_norm_eps(eps)) != RTL_OK) return st;
+  const size_t es = elem_size(dt);
+  const int n = Hk > 0 ? 2 : 1;
+  const View in[2] = {View(Q, M, Hq, D, q_row, q_head, es), View(K, M, Hk, D, k_row, k_head, es)};
+  const View out[2] = {View(Qo, M, Hq, D, qo_row, qo_head, es), View(Ko, M, Hk, D, ko_row, ko_head, es)};
+  const void* w[2] = {qw, n == 2 ? kw : nullptr};
+  const char* names[2][2] = {{"Q", "K"}, {"Qo", "Ko"}};
+  for (int i = 0; i < n; i++) {
+    if ((st = check_view(in[i], names[0][i], false)) != RTL_OK || (st = check_view(out[i], names[1][i], true)) != RTL_OK)
+      return st;
+    if (misaligned(w[i])) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  }
+  for (int o = 0; o < n; o++) {
+    for (int i = 0; i < n; i++) {
+      if (!(i == o && in[i].same(out[o])) && !apart(in[i], out[o])) return fail(RTL_ERR_ARG, "an output overlaps an input");
+      if (!apart_flat(out[o], w[i], (size_t)D * es)) return fail(RTL_ERR_ARG, "an output overlaps an input");
+    }
+    if (n_axes > 0 && !apart_flat(out[o], pos, (size_t)M * n_axes * 4))
+      return fail(RTL_ERR_ARG, "an output overlaps an input");
+  }
+  if (n == 2 && !apart(out[0], out[1])) return fail(RTL_ERR_ARG, "outputs overlap each other");
+  rtl::RopeCall c = rope_call(dt, true, M, Hq, Hk, D, pos, n_axes, axis_dims, theta, pairs, false);
+  c.eps = eps;
+  for (int i = 0; i < n; i++) {
+    c.x[i] = heads(in[i]);
+    c.y[i] = heads(out[i]);
+    c.w[i] = w[i];
+  }
+  return hip_status(rtl::launch_rope(c, (hipStream_t)stream), "rtl_qk_norm_rope launch");
+}
+
+size_t rtl_qk_norm_rope_backward_workspace_bytes(int64_t D) {
+  return D <= 0 || D > 256 ? 0 : rtl::qk_back_workspace(D);
+}
+
+rtl_status rtl_qk_norm_rope_backward(rtl_dtype dt, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const void* Q,
+                                     int64_t q_row, int64_t q_head, const void* K, int64_t k_row, int64_t k_head,
+                                     const void* qw, const void* kw, float eps, const float* pos, int32_t n_axes,
+                                     const int32_t* axis_dims, double theta, rtl_rope_pairs pairs, const void* dQo,
+                                     int64_t dqo_row, int64_t dqo_head, const void* dKo, int64_t dko_row,
+                                     int64_t dko_head, void* dQ, int64_t dq_row, int64_t dq_head, void* dK,
+                                     int64_t dk_row, int64_t dk_head, float* dqw, float* dkw, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+  rtl_status st;
+  if ((st = check_rope(dt, M, Hq, Hk, D, pos, n_axes, axis_dims, theta, pairs, false)) != RTL_OK) return st;
+  if ((st = check_norm_eps(eps)) != RTL_OK) return st;
+  const size_t es = elem_size(dt);
+  const int n = Hk > 0 ? 2 : 1;
+  const View in[2] = {View(Q, M, Hq, D, q_row, q_head, es), View(K, M, Hk, D, k_row, k_head, es)};
+  const View dy[2] = {View(dQo, M, Hq, D, dqo_row, dqo_head, es), View(dKo, M, Hk, D, dko_row, dko_head, es)};
+  const View dx[2] = {View(dQ, M, Hq, D, dq_row, dq_head, es), View(dK, M, Hk, D, dk_row, dk_head, es)};
+  const void* w[2] = {qw, n == 2 ? kw : nullptr};
+  float* dw[2] = {dqw, n == 2 ? dkw : nullptr};
+  const char* names[3][2] = {{"Q", "K"}, {"dQo", "dKo"}, {"dQ", "dK"}};
+  const size_t need = rtl::qk_back_workspace(D), wb = (size_t)D * es, dwb = (size_t)D * 4, pb = (size_t)M * n_axes * 4;
+  for (int i = 0; i < n; i++) {
+    if ((st = check_view(in[i], names[0][i], false)) != RTL_OK || (st = check_view(dy[i], names[1][i], false)) != RTL_OK ||
+        (st = check_view(dx[i], names[2][i], true)) != RTL_OK)
+      return st;
+    if (misaligned(w[i]) || misaligned(dw[i])) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  }
+  if (misaligned(workspace)) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  // flat outputs against everything, then the strided ones against what is left
+  const void* flat[3] = {dw[0], dw[1], workspace};
+  const size_t flatb[3] = {dwb, dwb, need};
+  for (int f = 0; f < 3; f++) {
+    if (n_axes > 0 && overlap(flat[f], flatb[f], pos, pb)) return fail(RTL_ERR_ARG, "an output or the workspace overlaps an input");
+    for (int i = 0; i < n; i++) {
+      if (overlap(flat[f], flatb[f], w[i], wb) || !apart_flat(in[i], flat[f], flatb[f]) || !apart_flat(dy[i], flat[f], flatb[f]))
+        return fail(RTL_ERR_ARG, "an output or the workspace overlaps an input");
+      if (!apart_flat(dx[i], flat[f], flatb[f])) return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+    }
+    for (int g = f + 1; g < 3; g++)
+      if (overlap(flat[f], flatb[f], flat[g], flatb[g]))
+        return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+  }
+  for (int o = 0; o < n; o++) {
+    for (int i = 0; i < n; i++)
+      if ((!(i == o && in[i].same(dx[o])) && !apart(in[i], dx[o])) ||
+          (!(i == o && dy[i].same(dx[o])) && !apart(dy[i], dx[o])) || !apart_flat(dx[o], w[i], wb))
+        return fail(RTL_ERR_ARG, "an output overlaps an input");
+    if (n_axes > 0 && !apart_flat(dx[o], pos, pb)) return fail(RTL_ERR_ARG, "an output overlaps an input");
+  }
+  if (n == 2 && !apart(dx[0], dx[1])) return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+  if (!workspace || ws_bytes < need)
+    return fail(RTL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  rtl::RopeCall c = rope_call(dt, true, M, Hq, Hk, D, pos, n_axes, axis_dims, theta, pairs, true);
+  c.eps = eps;
+  for (int i = 0; i < n; i++) {
+    c.x[i] = heads(in[i]);
+    c.y[i] = heads(dy[i]);
+    c.dx[i] = heads(dx[i]);
+    c.w[i] = w[i];
+  }
+  return hip_status(rtl::launch_qk_back(c, dw[0], dw[1], workspace, (hipStream_t)stream),
+                    "rtl_qk_norm_rope_backward launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+rtl_status check_glu(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H) {
+  rtl_status st;
+  if ((st = check_dtype(dt)) != RTL_OK) return st;
+  if (dt != RTL_BF16) return fail(RTL_ERR_UNSUPPORTED, "the gated block is bf16 only");
+  if (act != RTL_ACT_SILU && act != RTL_ACT_GELU) return fail(RTL_ERR_UNSUPPORTED, "unsupported activation %d", (int)act);
+  if (M <= 0 || K <= 0 || H <= 0)
+    return fail(RTL_ERR_SHAPE, "need M, K, H > 0 (M=%lld K=%lld H=%lld)", (long long)M, (long long)K, (long long)H);
+  // a tile's rows are reached with 32-bit offsets: 256 rows of K bf16 values stay below 2^31 bytes
+  if (K >= kMaxK) return fail(RTL_ERR_SHAPE, "K must be below %lld (K=%lld)", (long long)kMaxK, (long long)K);
+  if (M > INT32_MAX || H > INT32_MAX || ((M + 127) / 128) * ((H + 63) / 64) > INT32_MAX)
+    return fail(RTL_ERR_SHAPE, "M x H is too large (M=%lld H=%lld)", (long long)M, (long long)H);
+  if (K % 64 != 0) return fail(RTL_ERR_UNSUPPORTED, "the gated block needs K %% 64 == 0 (K=%lld)", (long long)K);
+  return RTL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rtl_status rtl_glu_fused(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
+                         const void* Wu, void* Y, void* G, void* U, void* stream) {
+  rtl_status st;
+  if ((st = check_glu(act, dt, M, K, H)) != RTL_OK) return st;
+  if (!X || !Wg || !Wu || !Y) return fail(RTL_ERR_NULL, "X, Wg, Wu and Y are required");
+  const void* ins[3] = {X, Wg, Wu};
+  const size_t inb[3] = {(size_t)M * K * 2, (size_t)H * K * 2, (size_t)H * K * 2};
+  const void* outs[3] = {Y, G, U};
+  const size_t outb = (size_t)M * H * 2;
+  for (int i = 0; i < 3; i++)
+    if (misaligned(ins[i]) || misaligned(outs[i])) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  for (int o = 0; o < 3; o++) {
+    for (int i = 0; i < 3; i++)
+      if (overlap(outs[o], outb, ins[i], inb[i])) return fail(RTL_ERR_ARG, "an output overlaps an input");
+    for (int o2 = o + 1; o2 < 3; o2++)
+      if (overlap(outs[o], outb, outs[o2], outb)) return fail(RTL_ERR_ARG, "outputs overlap each other");
+  }
+  return hip_status(rtl::launch_glu_bf16(act == RTL_ACT_SILU ? rtl::kActSilu : rtl::kActGelu, M, K, H, X, Wg, Wu, Y, G, U,
+                                         (hipStream_t)stream),
+                    "rtl_glu_fused launch");
+}
+
+size_t rtl_glu_backward_workspace_bytes(int64_t M, int64_t K, int64_t H) {
+  if (M <= 0 || K <= 0 || H <= 0 || M > INT32_MAX || H > INT32_MAX || K > kMaxK) return 0;
+  return rtl::glu_back_workspace(M, K, H);
+}
+
+rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
+                            const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
+                            void* dWu, void* workspace, size_t ws_bytes, void* stream) {
+  rtl_status st;
+  if ((st = check_glu(act, dt, M, K, H)) != RTL_OK) return st;
+  // the products sum over 2 H padded (dX) and over M padded (dWg, dWu)
+  if (M > kMaxK - 64 || H > kMaxK / 2 - 64)
+    return fail(RTL_ERR_SHAPE, "the gradient needs M <= %lld and H <= %lld (M=%lld H=%lld)", (long long)kMaxK - 64,
+                (long long)kMaxK / 2 - 64, (long long)M, (long long)H);
+  if (!G || !U || !dY || (!dX && !dWg) || (dWg == nullptr) != (dWu == nullptr) || (dX && (!Wg || !Wu)) || (dWg && !X))
+    return fail(RTL_ERR_NULL, "G, U, dY, dX (with Wg, Wu) or dWg and dWu (with X) are required");
+  const void* ins[6] = {dWg ? X : nullptr, dX ? Wg : nullptr, dX ? Wu : nullptr, G, U, dY};
+  const size_t xb = (size_t)M * K * 2, wb = (size_t)H * K * 2, yb = (size_t)M * H * 2;
+  const size_t inb[6] = {xb, wb, wb, yb, yb, yb};
+  const size_t need = rtl::glu_back_workspace(M, K, H);
+  const void* outs[4] = {dX, dWg, dWu, workspace};
+  const size_t outb[4] = {xb, wb, wb, need};
+  for (const void* q : ins)
+    if (misaligned(q)) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  for (const void* q : outs)
+    if (misaligned(q)) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  for (int o = 0; o < 4; o++) {
+    for (int i = 0; i < 6; i++)
+      if (overlap(outs[o], outb[o], ins[i], inb[i])) return fail(RTL_ERR_ARG, "an output or the workspace overlaps an input");
+    for (int o2 = o + 1; o2 < 4; o2++)
+      if (overlap(outs[o], outb[o], outs[o2], outb[o2]))
+        return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+  }
+  if (!workspace || ws_bytes < need)
+    return fail(RTL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  return hip_status(rtl::launch_glu_back_bf16(act == RTL_ACT_SILU ? rtl::kActSilu : rtl::kActGelu, M, K, H, X, Wg, Wu, G,
+                                              U, dY, dX, dWg, dWu, workspace, (hipStream_t)stream),
+                    "rtl_glu_backward launch");
+}
+
+}  // extern "C"

@@ -74,6 +74,36 @@ hipError_t launch_prep_gelu_bf16(int64_t M, int64_t N, int64_t K, int64_t R, con
 hipError_t launch_split_reduce_bf16(int64_t M, int64_t R, int ks, const float* tpart, const double* npart, float eps,
                                     void* T, float* s, float* dbg_s, hipStream_t stream);
 
+// Rotary embedding over several axes and per-head norms of queries and keys (qk_rope.h).
+struct StridedHeads {
+  const void* p;      // [M, H, D], D contiguous
+  int64_t row, head;  // strides in elements
+};
+struct RopeCall {
+  int dt;
+  bool norm, halves, inverse;
+  int64_t M, H[2], D;      // heads of the two tensors (queries, keys); H[1] may be 0
+  StridedHeads x[2], y[2], dx[2];  // gradient: y holds dy, dx the outputs; else y the outputs
+  const void* w[2];        // norm weights [D] or null
+  float eps;
+  const float* pos;        // [M, axes]
+  int axes;
+  const int32_t* dims;     // host: even widths of the axes
+  double theta;
+};
+hipError_t launch_rope(const RopeCall& c, hipStream_t stream);
+size_t qk_back_workspace(int64_t D);
+hipError_t launch_qk_back(const RopeCall& c, float* dqw, float* dkw, void* ws, hipStream_t stream);
+
+// Gated feed-forward block (glu_bf16.h): Y = act(X Wg^T) (X Wu^T), and its gradient.
+constexpr int kActSilu = 0, kActGelu = 1;
+hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg, const void* Wu,
+                           void* Y, void* G, void* U, hipStream_t stream);
+size_t glu_back_workspace(int64_t M, int64_t K, int64_t H);
+hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
+                                const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
+                                void* dWu, void* ws, hipStream_t stream);
+
 // Allocation-free workspace: the per-device scratch array (noalloc.hip).  `mismatch` is set
 // when `stream` does not belong to the current device (no address is resolved then).
 size_t noalloc_scratch_bytes();

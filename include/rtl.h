@@ -277,6 +277,98 @@ rtl_status rtl_linear_fused_fp8(int64_t M, int64_t N, int64_t K, int64_t R, cons
                                 rtl_tie_rule tie, float eps, void* Y, void* workspace, size_t ws_bytes,
                                 uint8_t* dbg_xq, float* dbg_sx, void* stream);
 
+/*
+ * Rotary positions over several axes (a token of an image or a video has a time, a height and
+ * a width), and the RMS norm of each query and key head with the rotation in the same pass:
+ * what a block of a diffusion transformer runs on the output of its QKV projection.
+ *
+ * Tensors are [M, H, D] (token, head, channel) with D contiguous and a row and a head stride
+ * in elements, so the queries and keys can be views of the packed projection and the outputs
+ * can lie token-major or head-major.  Strides are at least 0 and keep 16-byte alignment (the
+ * stride of an extent of 1 is ignored); inputs may repeat (stride 0), the elements of an output
+ * are distinct.  An output may be its own input (same pointer and strides), else outputs
+ * overlap no input and no other output; views that interleave in one buffer are told apart
+ * where their row strides or their head strides agree.
+ *
+ *   pos [M, n_axes] fp32: each token's position on each axis (whole or not, either sign).
+ *   axis_dims [n_axes] (HOST pointer): the even number of channels that each axis turns;
+ *     their sum Dr is a multiple of 8 and at most D; the channels Dr..D-1 are not turned.
+ *   Pair i of axis a turns by pos[m, a] * theta^(-2 i / axis_dims[a]); pairs are counted over
+ *     the axes in order.  RTL_ROPE_ADJACENT: pair p is channels 2p and 2p + 1;
+ *     RTL_ROPE_HALVES: channels p and p + Dr / 2.  (x0, x1) -> (x0 cos - x1 sin,
+ *     x1 cos + x0 sin).
+ * Angles are formed in double precision, all else in fp32, rounded once at the end.
+ * dt is bf16 or fp32.  Limits: D % 8 == 0, D <= 256, n_axes <= 4, M * heads below 2^31; theta
+ * finite and above 0.
+ */
+typedef enum { RTL_ROPE_RANGE_MIN_ = -0x7FFFFFFF - 1, RTL_ROPE_ADJACENT = 0, RTL_ROPE_HALVES = 1, RTL_ROPE_RANGE_MAX_ = 0x7FFFFFFF } rtl_rope_pairs;
+
+/*
+ * Y = the rotation of X by the positions (n_axes >= 1); `inverse` (0 or 1) turns back, which
+ * is also the gradient: dX is the inverse rotation of dY.
+ */
+rtl_status rtl_rope_axes(rtl_dtype dt, int64_t M, int64_t H, int64_t D, const void* X, int64_t x_row, int64_t x_head,
+                         const float* pos, int32_t n_axes, const int32_t* axis_dims, double theta,
+                         rtl_rope_pairs pairs, int32_t inverse, void* Y, int64_t y_row, int64_t y_head, void* stream);
+
+/*
+ * For each head of Q [M, Hq, D] and K [M, Hk, D]:
+ *   Qo = rotation(x r qw), r = 1 / sqrt(mean(x^2) + eps), and Ko likewise with kw.
+ * qw and kw [D] (dtype dt) may be NULL (ones).  n_axes == 0 drops the rotation (pos and
+ * axis_dims may then be NULL); Hk == 0 drops K (its pointers are ignored).  eps must lie in
+ * (0, 1].  The squares are summed in fp32 and must lie in its range.
+ */
+rtl_status rtl_qk_norm_rope(rtl_dtype dt, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const void* Q, int64_t q_row,
+                            int64_t q_head, const void* K, int64_t k_row, int64_t k_head, const void* qw,
+                            const void* kw, float eps, const float* pos, int32_t n_axes, const int32_t* axis_dims,
+                            double theta, rtl_rope_pairs pairs, void* Qo, int64_t qo_row, int64_t qo_head, void* Ko,
+                            int64_t ko_row, int64_t ko_head, void* stream);
+
+/*
+ * Gradient of rtl_qk_norm_rope: from its inputs and the gradients dQo, dKo of its outputs, the
+ * gradients dQ and dK (which may be their own dQo, dKo or Q, K) and, summed over all tokens and
+ * heads, dqw and dkw [D] fp32 (NULL to skip).  Nothing is kept from the forward call.  The sums
+ * run in one order: the same result on every run.  Calls that share a workspace must be
+ * serialised.
+ */
+size_t rtl_qk_norm_rope_backward_workspace_bytes(int64_t D);
+rtl_status rtl_qk_norm_rope_backward(rtl_dtype dt, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const void* Q,
+                                     int64_t q_row, int64_t q_head, const void* K, int64_t k_row, int64_t k_head,
+                                     const void* qw, const void* kw, float eps, const float* pos, int32_t n_axes,
+                                     const int32_t* axis_dims, double theta, rtl_rope_pairs pairs, const void* dQo,
+                                     int64_t dqo_row, int64_t dqo_head, const void* dKo, int64_t dko_row,
+                                     int64_t dko_head, void* dQ, int64_t dq_row, int64_t dq_head, void* dK,
+                                     int64_t dk_row, int64_t dk_head, float* dqw, float* dkw, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * The gated feed-forward block's two projections, activation and product in one kernel (bf16),
+ * for blocks whose up projections stay dense (rtl_linear_fused or rtl_linear_dense_ref then
+ * takes Y through the down projection):
+ *   G = X Wg^T,  U = X Wu^T,  Y = act(G) * U
+ *   X [M,K], Wg [H,K], Wu [H,K], Y [M,H]; G and U [M,H] are optional outputs (NULL to skip),
+ *   the pre-activations that rtl_glu_backward takes.
+ * act: RTL_ACT_SILU g / (1 + exp(-g)) or RTL_ACT_GELU g Phi(g) (exact erf form), evaluated on
+ * the fp32 accumulators; every output is rounded once.  Limits: K % 64 == 0, K < 2^22; M and H
+ * are arbitrary.  Outputs must not overlap inputs or each other.
+ */
+typedef enum { RTL_ACT_RANGE_MIN_ = -0x7FFFFFFF - 1, RTL_ACT_SILU = 0, RTL_ACT_GELU = 1, RTL_ACT_RANGE_MAX_ = 0x7FFFFFFF } rtl_act;
+rtl_status rtl_glu_fused(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
+                         const void* Wu, void* Y, void* G, void* U, void* stream);
+
+/*
+ * Gradient of rtl_glu_fused from its inputs, the pre-activations G and U and the gradient dY:
+ *   dG = dY U act'(G),  dU = dY act(G)  (rounded to bf16, as operands of the products)
+ *   dX = dG Wg + dU Wu [M,K],  dWg = dG^T X [H,K],  dWu = dU^T X [H,K]
+ * accumulated in fp32, rounded once.  dX may be NULL (Wg and Wu are then not read), or dWg and
+ * dWu both (X is then not read).  The workspace size covers every choice of outputs.  Calls
+ * that share a workspace must be serialised.
+ */
+size_t rtl_glu_backward_workspace_bytes(int64_t M, int64_t K, int64_t H);
+rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
+                            const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
+                            void* dWu, void* workspace, size_t ws_bytes, void* stream);
+
 const char* rtl_status_string(rtl_status st);
 const char* rtl_last_error(void); /* message of this thread's last failed call, or "" */
 int rtl_version(void);            /* major * 10000 + minor * 100 + patch */
