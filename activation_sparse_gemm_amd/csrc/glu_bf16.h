@@ -4,14 +4,16 @@
 //   G = X Wg^T,  U = X Wu^T,  Y = act(G) U           act: SiLU g / (1 + exp(-g)), or exact GELU
 //   dG = dY U act'(G),  dU = dY act(G),  dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X
 //
-// Forward, many rows: one matrix product over both weights.  A workgroup's tile holds the gate
-// and the up columns of the same outputs, placed so that each lane's accumulators hold G and U
-// of the same four consecutive columns; the activation and the product are formed from the
-// fp32 accumulators and G and U reach memory only where the caller keeps them.
+// Forward, many rows: one matrix product over both weights (ring_gemm.h).  A workgroup's tile
+// holds the gate and the up columns of the same outputs, placed so that each lane's
+// accumulators hold G and U of the same consecutive columns; the activation and the product are
+// formed from the fp32 accumulators and G and U reach memory only where the caller keeps them.
 // Forward, few rows: both weights are streamed once, the K range split over a workgroup's
 // waves and added in LDS.
+// Gradient: one pass forms P = [dG | dU], then dX = P [Wg; Wu] and [dWg; dWu] = P^T X read P, X
+// and the weights as they lie (ring_gemm.h's transposing reads).
 #pragma once
-#include "gemm_common.h"
+#include "ring_gemm.h"
 
 namespace rtl {
 
@@ -40,122 +42,86 @@ __device__ __forceinline__ void glu_act_slope(float g, float& v, float& d) {
   }
 }
 
-// Four consecutive values of row `row` from column `col` on, rounded to bf16 (nearest even).
-__device__ __forceinline__ void store4(uint16_t* Y, int64_t M, int64_t N, int64_t row, int64_t col, const float (&v)[4]) {
+// N (2 or 4) consecutive values of row `row` from column `col` on, rounded to bf16 (nearest even).
+template <int N>
+__device__ __forceinline__ void store_cols(uint16_t* Y, int64_t M, int64_t H, int64_t row, int64_t col,
+                                           const float (&v)[N]) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-  const uint32_t w0 = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[0], (__bf16)v[1]});
-  const uint32_t w1 = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[2], (__bf16)v[3]});
-  if (row >= M) return;
-  uint16_t* y = Y + row * N + col;
-  if ((N & 3) == 0 && col + 4 <= N) {
-    __builtin_nontemporal_store(u32x2{w0, w1}, reinterpret_cast<u32x2*>(y));
-  } else {
-    const uint32_t w[2] = {w0, w1};
+  uint32_t w[N / 2];
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-      if (col + e < N) y[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+  for (int i = 0; i < N / 2; i++)
+    w[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+  if (row >= M) return;
+  uint16_t* y = Y + row * H + col;
+  if (H % N == 0 && col + N <= H) {
+    if constexpr (N == 4) __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(y));
+    else *reinterpret_cast<uint32_t*>(y) = w[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e++)
+      if (col + e < H) y[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
   }
 }
 
-// The tiled product: WM x WN waves, each on 16 RB rows and 64 gate + 64 up columns, K in steps
-// of 64.  X and weight tiles go straight to LDS (two buffers): step kt's loads are waited for
-// before its barrier, step kt + 1's are issued right after it, into the buffer that every wave
-// has finished with.
-//
-// LDS row n of a wave column's 128 weight rows: gate for n < 64, up for the rest; row 16 nb +
-// r16 of either half is output column 4 r16 + nb, so that lane r16 holds four consecutive
-// columns over the blocks nb = 0..3.
-template <int ACT, int WM, int WN, int RB>
-__global__ __launch_bounds__(64 * WM * WN) void glu_kernel(const GluArgs a) {
-  constexpr int NW = WM * WN, BM = 16 * RB * WM, BN = 128 * WN, NB = 8;
-  constexpr int ABLK = BM / 8, LD = (BM + BN) / 8 / NW;  // 8-row blocks of the X tile; loads per wave and step
-  constexpr int STAGE = (BM + BN) * 128;
-  static_assert(ABLK % NW == 0 && 8 % NW == 0 && LD * NW * 8 == BM + BN, "whole blocks per wave");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+// Buffer resource of `bytes` (as make_rsrc clamps them), or of none: loads then read zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void* p, int64_t bytes) {
+  return make_rsrc(p, live ? bytes : 0);
+}
 
+// The tiled product: 2 x 2 waves of RB x NB blocks, 32 RB rows and 32 NB weight rows (16 NB
+// outputs) a tile.  Of a wave column's 16 NB weight rows the first half are gate rows, the
+// second up; row 16 nb + r16 of either half is output column NB / 2 r16 + nb, so that lane r16
+// holds NB / 2 consecutive columns over its blocks.
+template <int ACT, int RB, int NB>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(RB == 8 ? 1 : 2, RB == 8 ? 1 : 2)))
+void glu_kernel(const GluArgs a) {
+  constexpr int BM = 32 * RB, BN = 32 * NB, NC = NB / 2;
+  typedef KRows<BM> OpA;
+  typedef KRows<BN> OpB;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * OpA::kBytes];
   int tm, tn;
   tile_coords(a.tiles_m, a.tiles_n, tm, tn);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave % WM, wn = wave / WM;
+  const int wm = wave & 1, wn = wave >> 1;
   const int q = lane >> 4, r16 = lane & 15;
   const int64_t M = a.M, K = a.K, H = a.H;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * (BN / 2);
-  const int KT = (int)(K / kBK);
-
+  const int steps = (int)(K / kRK);
   // Rows past M or H lie outside the buffers and read as zeros.
-  const __amdgpu_buffer_rsrc_t xres = make_rsrc(a.X + m0 * K, (M - m0) * K * 2);
-  const __amdgpu_buffer_rsrc_t gres = make_rsrc(a.Wg + n0 * K, (H - n0) * K * 2);
-  const __amdgpu_buffer_rsrc_t ures = make_rsrc(a.Wu + n0 * K, (H - n0) * K * 2);
-  // Lane l of a load writes 16-byte position l % 8 of row l / 8 of its 8-row block, where
-  // sw_off keeps chunk (l % 8) ^ (l / 8).
-  const int row8 = lane >> 3;
-  const uint32_t chunk = 16 * ((lane & 7) ^ row8);
-  const uint32_t a_voff = (uint32_t)(row8 * K * 2) + chunk, b_voff = (uint32_t)(4 * row8 * K * 2) + chunk;
-  auto load = [&](int kt, int buf) {
-#pragma unroll
-    for (int i = 0; i < LD; i++) {
-      auto* dst = (__attribute__((address_space(3))) void*)(lds + buf * STAGE + (i * NW + wave) * 1024);
-      if (i * NW < ABLK) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(xres, dst, 16, a_voff,
-                                                 (int)((int64_t)(i * NW + wave) * 8 * K * 2 + (int64_t)kt * 128), 0, 0);
-      } else {
-        const int n8 = i * NW + wave - ABLK, at = n8 & 7;  // 8-row block among the weight rows, within its half
-        const int64_t col = 64 * (n8 >> 4) + 32 * (at & 1) + (at >> 1);
-        const bool up = ((i * NW - ABLK) >> 3) & 1;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ures : gres, dst, 16, b_voff,
-                                                 (int)(col * K * 2 + (int64_t)kt * 128), 0, 0);
-      }
-    }
+  const uint16_t *X = a.X + m0 * K, *Wg = a.Wg + n0 * K, *Wu = a.Wu + n0 * K;
+  const int64_t xb = (M - m0) * K * 2, wb = (H - n0) * K * 2;
+  const OpA oa(K, 1, wave, lane);
+  const OpB ob(K, NC, wave, lane);
+  auto load_a = [&](int kt, uint8_t* dst, int i) {
+    oa.load(rsrc_if(kt >= 0, X, xb), dst, i, 8 * (i * kRingWaves + wave), kt < 0 ? 0 : kt);
   };
-
+  auto load_b = [&](int kt, uint8_t* dst, int i) {
+    const int blk = i * kRingWaves + wave, at = blk % (2 * NB);  // 8-row block, and within its wave column
+    const bool up = at >= NB;
+    const int of = up ? at - NB : at;  // half `of & 1` of block nb = of / 2
+    ob.load(rsrc_if(kt >= 0, up ? Wu : Wg, wb), dst, i, blk / (2 * NB) * (16 * NC) + (of & 1) * (8 * NC) + (of >> 1),
+            kt < 0 ? 0 : kt);
+  };
   f32x4 acc[RB][NB];
-#pragma unroll
-  for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-    for (int nb = 0; nb < NB; nb++) acc[rb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  ring_product(acc, lds, oa, ob, load_a, load_b, steps, (tm + tn) % 8 % steps, wm, wn);
 
-  load(0, 0);
-  for (int kt = 0; kt < KT; kt++) {
-    const int buf = kt & 1;
-    wait_vmcnt<0>();
-    barrier_nofence();
-    if (kt + 1 < KT) load(kt + 1, buf ^ 1);
-    const uint8_t* al = lds + buf * STAGE;
-    const uint8_t* bl = al + BM * 128;
-#pragma unroll
-    for (int kk = 0; kk < 2; kk++) {
-      u32x4 av[RB];
-#pragma unroll
-      for (int rb = 0; rb < RB; rb++)
-        av[rb] = *reinterpret_cast<const u32x4*>(al + sw_off(16 * RB * wm + 16 * rb + r16, 4 * kk + q));
-#pragma unroll
-      for (int nb = 0; nb < NB; nb++) {
-        const u32x4 bv = *reinterpret_cast<const u32x4*>(bl + sw_off(128 * wn + 16 * nb + r16, 4 * kk + q));
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++)
-          acc[rb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, av[rb]), __builtin_bit_cast(bf16x8, bv), acc[rb][nb], 0, 0, 0);
-      }
-    }
-  }
-
-  const int64_t col = n0 + 64 * wn + 4 * r16;
+  const int64_t col = n0 + 16 * NC * wn + NC * r16;
 #pragma unroll
   for (int rb = 0; rb < RB; rb++)
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const int64_t row = m0 + 16 * RB * wm + 16 * rb + 4 * q + j;
-      float g[4], u[4], y[4];
+      const int64_t row = m0 + 16 * (RB * wm + rb) + 4 * q + j;
+      float g[NC], u[NC], y[NC];
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
+      for (int e = 0; e < NC; e++) {
         g[e] = acc[rb][e][j];
-        u[e] = acc[rb][4 + e][j];
+        u[e] = acc[rb][NC + e][j];
         y[e] = glu_act<ACT>(g[e]) * u[e];
       }
-      store4(a.Y, M, H, row, col, y);
-      if (a.G != nullptr) store4(a.G, M, H, row, col, g);
-      if (a.U != nullptr) store4(a.U, M, H, row, col, u);
+      store_cols<NC>(a.Y, M, H, row, col, y);
+      if (a.G != nullptr) store_cols<NC>(a.G, M, H, row, col, g);
+      if (a.U != nullptr) store_cols<NC>(a.U, M, H, row, col, u);
     }
 }
 
@@ -236,13 +202,12 @@ __global__ __launch_bounds__(64 * NW) void glu_rows_kernel(const GluArgs a) {
 
 namespace {
 
-template <int ACT, int WM, int WN, int RB>
+// Tiles of 32 R rows by 16 R outputs.
+template <int ACT, int R>
 void glu_tiles(GluArgs a, hipStream_t stream) {
-  constexpr int BM = 16 * RB * WM, BH = 64 * WN;
-  a.tiles_m = (int)((a.M + BM - 1) / BM);
-  a.tiles_n = (int)((a.H + BH - 1) / BH);
-  hipLaunchKernelGGL((glu_kernel<ACT, WM, WN, RB>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(64 * WM * WN), 0,
-                     stream, a);
+  a.tiles_m = (int)((a.M + 32 * R - 1) / (32 * R));
+  a.tiles_n = (int)((a.H + 16 * R - 1) / (16 * R));
+  hipLaunchKernelGGL((glu_kernel<ACT, R, R>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
 }
 
 template <int ACT>
@@ -250,9 +215,8 @@ void glu_launch(const GluArgs& a, hipStream_t stream) {
   const dim3 cols((unsigned)((a.H + 15) / 16)), block(512);
   if (a.M <= 16) hipLaunchKernelGGL((glu_rows_kernel<ACT, 1, 8>), cols, block, 0, stream, a);
   else if (a.M <= 32) hipLaunchKernelGGL((glu_rows_kernel<ACT, 2, 8>), cols, block, 0, stream, a);
-  else if (((a.M + 255) / 256) * ((a.H + 127) / 128) >= 256) glu_tiles<ACT, 4, 2, 4>(a, stream);
-  else if (((a.M + 127) / 128) * ((a.H + 127) / 128) >= 256) glu_tiles<ACT, 2, 2, 4>(a, stream);
-  else glu_tiles<ACT, 2, 1, 4>(a, stream);
+  else if (((a.M + 255) / 256) * ((a.H + 127) / 128) >= 192) glu_tiles<ACT, 8>(a, stream);
+  else glu_tiles<ACT, 4>(a, stream);
 }
 
 }  // namespace
@@ -270,71 +234,217 @@ hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void*
 
 // ------------------------------------------------------------------ gradient
 
-// Transpose of a 64 x 64 tile: src [rows, cols] -> dst [cols, ld] at column at0 on; rows of
-// src past `rows` (up to the tile's end) are written as zeros.
-__global__ __launch_bounds__(256) void glu_transpose_kernel(const uint16_t* src, int64_t rows, int64_t cols,
-                                                            uint16_t* dst, int64_t ld, int64_t at0) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += 4)
-    tile[i][x] = r0 + i < rows && c0 + x < cols ? src[(r0 + i) * cols + c0 + x] : (uint16_t)0;
-  __syncthreads();
-  for (int i = y; i < 64; i += 4)
-    if (c0 + i < cols) dst[(c0 + i) * ld + at0 + r0 + x] = tile[x][i];
+// P [M, 2 Hp] = [dG | dU], each padded to Hp columns with zeros, rounded to bf16: the matrix
+// cores' operand.  (Formed inside the products instead, it would be formed again for every
+// tile that reads it, 2 H / 256 + K / 256 times.)  One 16-byte chunk of each half per thread.
+template <int ACT>
+__global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int64_t Hp, const uint16_t* G,
+                                                       const uint16_t* U, const uint16_t* dY, uint16_t* P) {
+  const int64_t c8 = Hp / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= M * c8) return;
+  const int64_t m = id / c8, h = (id - m * c8) * 8, at = m * H + h;
+  u32x4 g{}, u{}, d{};
+  if (H % 8 == 0 && h + 8 <= H) {
+    g = *reinterpret_cast<const u32x4*>(G + at);
+    u = *reinterpret_cast<const u32x4*>(U + at);
+    d = *reinterpret_cast<const u32x4*>(dY + at);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (h + e < H) {
+        g[e >> 1] |= (uint32_t)G[at + e] << (16 * (e & 1));
+        u[e >> 1] |= (uint32_t)U[at + e] << (16 * (e & 1));
+        d[e >> 1] |= (uint32_t)dY[at + e] << (16 * (e & 1));
+      }
+  }
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  u32x4 dg, du;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    float v0, s0, v1, s1;
+    glu_act_slope<ACT>(bf16lo(g[i]), v0, s0);
+    glu_act_slope<ACT>(bf16hi(g[i]), v1, s1);
+    const float d0 = bf16lo(d[i]), d1 = bf16hi(d[i]);
+    dg[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * bf16lo(u[i]) * s0), (__bf16)(d1 * bf16hi(u[i]) * s1)});
+    du[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * v0), (__bf16)(d1 * v1)});
+  }
+  *reinterpret_cast<u32x4*>(P + m * 2 * Hp + h) = dg;
+  *reinterpret_cast<u32x4*>(P + m * 2 * Hp + Hp + h) = du;
 }
 
-// dG and dU of a 64 x 64 tile, rounded to bf16 (they are the matrix cores' operands), as rows
-// P [M, 2 Hp] (dU from column Hp on) and transposed, [H, Mp] each; zeros in the padding.
-template <int ACT>
-__global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, const uint16_t* G, const uint16_t* U,
-                                                       const uint16_t* dY, uint16_t* P, int64_t Hp, uint16_t* dGt,
-                                                       uint16_t* dUt, int64_t Mp) {
-  __shared__ uint16_t tg[64][66], tu[64][66];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += 4) {
-    uint16_t dg = 0, du = 0;
-    if (r0 + i < M && c0 + x < H) {
-      const int64_t at = (r0 + i) * H + c0 + x;
-      const float g = __uint_as_float((uint32_t)G[at] << 16), u = __uint_as_float((uint32_t)U[at] << 16);
-      const float d = __uint_as_float((uint32_t)dY[at] << 16);
-      float v, s;
-      glu_act_slope<ACT>(g, v, s);
-      dg = (uint16_t)f32_to_bf16_bits(d * u * s);
-      du = (uint16_t)f32_to_bf16_bits(d * v);
-    }
-    tg[i][x] = dg;
-    tu[i][x] = du;
-    if (P != nullptr && r0 + i < M) {
-      P[(r0 + i) * 2 * Hp + c0 + x] = dg;
-      P[(r0 + i) * 2 * Hp + Hp + c0 + x] = du;
+// A wave's RB x NB blocks to bf16 rows through its LDS block of 16 * (32 NB + 16) bytes, as
+// 16-byte chunks; row(i) gives the address of the wave's row i at its first column or null,
+// `cols` (a multiple of 8) the columns from there on.
+template <int RB, int NB, typename Row>
+__device__ __forceinline__ void store_rows(const f32x4 (&acc)[RB][NB], uint8_t* blk, int lane, int64_t cols, Row row) {
+  constexpr int CW = NB * 16, PITCH = 2 * CW + 16, CPR = CW / 8;
+  const int q = lane >> 4, r16 = lane & 15;
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int rb = 0; rb < RB; rb++) {
+#pragma unroll
+    for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const uint32_t w = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)acc[rb][nb][j], (__bf16)acc[rb][nb][j + 1]});
+        uint8_t* at = blk + (4 * q + j) * PITCH + (nb * 16 + r16) * 2;
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+        *reinterpret_cast<uint16_t*>(at + PITCH) = (uint16_t)(w >> 16);
+      }
+#pragma unroll
+    for (int c = 0; c < 16 * CPR / 64; c++) {
+      const int id = lane + 64 * c, rr = id / CPR, cc = id % CPR;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(blk + rr * PITCH + cc * 16);
+      uint16_t* y = row(16 * rb + rr);
+      if (y != nullptr && 8 * cc < cols) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + 8 * cc));
     }
   }
-  if (dGt == nullptr) return;
-  __syncthreads();
-  for (int i = y; i < 64; i += 4)
-    if (c0 + i < H) {
-      dGt[(c0 + i) * Mp + r0 + x] = tg[x][i];
-      dUt[(c0 + i) * Mp + r0 + x] = tu[x][i];
-    }
+}
+
+struct GluBackArgs {
+  int64_t M, K, H, Hp;
+  const uint16_t *P, *X, *Wg, *Wu;
+  uint16_t *dX, *dWg, *dWu;
+  float* part;       // split sum of dX: [splits][M][K]
+  int per;           // K steps per split
+  int tiles_m, tiles_n;
+};
+
+// dX = P [Wg; Wu]: k runs over P's 2 Hp columns, along P's rows and down the weights' columns.
+// With SPLIT, blockIdx.y takes `per` of the steps and leaves its fp32 sums in its part.
+template <int R, bool SPLIT>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(R == 8 ? 1 : 2, R == 8 ? 1 : 2)))
+void glu_dx_kernel(const GluBackArgs a) {
+  constexpr int T = 32 * R;
+  typedef KRows<T> OpA;
+  typedef KCols<T> OpB;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * OpA::kBytes];
+  int tm, tn;
+  tile_coords(a.tiles_m, a.tiles_n, tm, tn);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int64_t M = a.M, K = a.K, H = a.H, ld = 2 * a.Hp;
+  const int64_t m0 = (int64_t)tm * T, c0 = (int64_t)tn * T;
+  const int half = (int)(a.Hp / kRK), all = 2 * half;
+  const int first = SPLIT ? blockIdx.y * a.per : 0, steps = SPLIT ? min(a.per, all - first) : all;
+  const uint16_t* P = a.P + m0 * ld;
+  const OpA oa(ld, 1, wave, lane);
+  const OpB ob(K, wave, lane);
+  auto load_a = [&](int kt, uint8_t* dst, int i) {
+    oa.load(rsrc_if(kt >= 0, P, (M - m0) * ld * 2), dst, i, 8 * (i * kRingWaves + wave), kt < 0 ? 0 : first + kt);
+  };
+  auto load_b = [&](int kt, uint8_t* dst, int i) {
+    // rows of Wg, then of Wu; past H (P's padding) they read as zeros
+    const int s = first + (kt < 0 ? 0 : kt);
+    const int64_t h = (int64_t)(s < half ? s : s - half) * kRK;
+    ob.load(rsrc_if(kt >= 0, (s < half ? a.Wg : a.Wu) + h * K + c0, ((H - h) * K - c0) * 2), dst, i);
+  };
+  f32x4 acc[R][R];
+  ring_product(acc, lds, oa, ob, load_a, load_b, steps, (tm + tn) % 8 % steps, wm, wn);
+
+  const int64_t row0 = m0 + 16 * R * wm, col0 = c0 + 16 * R * wn;
+  if constexpr (SPLIT) {
+    float* out = a.part + (int64_t)blockIdx.y * M * K;
+    const int q = lane >> 4, r16 = lane & 15;
+#pragma unroll
+    for (int rb = 0; rb < R; rb++)
+#pragma unroll
+      for (int nb = 0; nb < R; nb++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const int64_t row = row0 + 16 * rb + 4 * q + j, col = col0 + 16 * nb + r16;
+          if (row < M && col < K) out[row * K + col] = acc[rb][nb][j];
+        }
+  } else {
+    __syncthreads();  // the ring is free
+    store_rows<R, R>(acc, lds + wave * 16 * (32 * R + 16), lane, K - col0, [&](int i) {
+      return row0 + i < M ? a.dX + (row0 + i) * K + col0 : (uint16_t*)nullptr;
+    });
+  }
+}
+
+// dX = the splits' sum in order, four values per thread (K % 64 == 0).
+__global__ __launch_bounds__(256) void glu_sum_kernel(const float* part, int splits, int64_t n, uint16_t* dX) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= n) return;
+  f32x4 s = *reinterpret_cast<const f32x4*>(part + at);
+  for (int k = 1; k < splits; k++) s += *reinterpret_cast<const f32x4*>(part + (int64_t)k * n + at);
+  *reinterpret_cast<u32x2*>(dX + at) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+}
+
+// [dWg; dWu] = P^T X: k runs over the tokens, down the columns of both.
+template <int R>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(R == 8 ? 1 : 2, R == 8 ? 1 : 2)))
+void glu_dw_kernel(const GluBackArgs a) {
+  constexpr int T = 32 * R;
+  typedef KCols<T> Op;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * Op::kBytes];
+  int tm, tn;
+  tile_coords(a.tiles_m, a.tiles_n, tm, tn);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int64_t M = a.M, K = a.K, H = a.H, Hp = a.Hp, ld = 2 * Hp;
+  const int64_t r0 = (int64_t)tm * T, c0 = (int64_t)tn * T;
+  const int steps = (int)((M + kRK - 1) / kRK);
+  const Op oa(ld, wave, lane), ob(K, wave, lane);
+  // tokens past M lie outside the buffers and read as zeros
+  auto load_a = [&](int kt, uint8_t* dst, int i) {
+    const int64_t m = (int64_t)(kt < 0 ? 0 : kt) * kRK;
+    oa.load(rsrc_if(kt >= 0, a.P + m * ld + r0, ((M - m) * ld - r0) * 2), dst, i);
+  };
+  auto load_b = [&](int kt, uint8_t* dst, int i) {
+    const int64_t m = (int64_t)(kt < 0 ? 0 : kt) * kRK;
+    ob.load(rsrc_if(kt >= 0, a.X + m * K + c0, ((M - m) * K - c0) * 2), dst, i);
+  };
+  f32x4 acc[R][R];
+  ring_product(acc, lds, oa, ob, load_a, load_b, steps, (tm + tn) % 8 % steps, wm, wn);
+
+  __syncthreads();  // the ring is free
+  const int64_t row0 = r0 + 16 * R * wm, col0 = c0 + 16 * R * wn;
+  store_rows<R, R>(acc, lds + wave * 16 * (32 * R + 16), lane, K - col0, [&](int i) {
+    const int64_t r = row0 + i;  // 0 .. H - 1: a row of dWg; Hp .. Hp + H - 1: of dWu
+    return r < H ? a.dWg + r * K + col0 : r >= Hp && r < Hp + H ? a.dWu + (r - Hp) * K + col0 : (uint16_t*)nullptr;
+  });
 }
 
 namespace {
 inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// dX: 256 x 256 tiles where they occupy three quarters of the CUs; else 128 x 128 tiles, and
+// where those do not give every CU its two workgroups, the sum over the 2 Hp columns is split,
+// in parts of at least 16 steps.
+struct GluDxPlan {
+  int splits, per;
+  bool big;
+};
+GluDxPlan glu_dx_plan(int64_t M, int64_t K, int64_t H) {
+  const int64_t steps = 2 * pad64(H) / kRK;
+  if (((M + 255) / 256) * ((K + 255) / 256) >= 192) return {1, (int)steps, true};
+  const int64_t tiles = ((M + 127) / 128) * ((K + 127) / 128);
+  const int64_t splits = std::max<int64_t>(1, std::min(512 / tiles, steps / 16));
+  const int64_t per = (steps + splits - 1) / splits;
+  return {(int)((steps + per - 1) / per), (int)per, false};
+}
+
 struct GluBackLayout {
-  size_t p, wt, dgt, dut, xt, total;
+  size_t p, part, total;
 };
 GluBackLayout glu_back_layout(int64_t M, int64_t K, int64_t H) {
   GluBackLayout L;
-  const int64_t Hp = pad64(H), Mp = pad64(M);
+  const GluDxPlan d = glu_dx_plan(M, K, H);
   L.p = 0;
-  L.wt = L.p + align256((size_t)(M * 2 * Hp * 2));
-  L.dgt = L.wt + align256((size_t)(K * 2 * Hp * 2));
-  L.dut = L.dgt + align256((size_t)(H * Mp * 2));
-  L.xt = L.dut + align256((size_t)(H * Mp * 2));
-  L.total = L.xt + align256((size_t)(K * Mp * 2));
+  L.part = align256((size_t)(M * 2 * pad64(H) * 2));
+  L.total = L.part + (d.splits > 1 ? align256((size_t)d.splits * M * K * 4) : 0);
   return L;
+}
+
+template <int R>
+void glu_dw_launch(GluBackArgs a, hipStream_t stream) {
+  a.tiles_m = (int)((2 * a.Hp + 32 * R - 1) / (32 * R));
+  a.tiles_n = (int)((a.K + 32 * R - 1) / (32 * R));
+  hipLaunchKernelGGL((glu_dw_kernel<R>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
 }
 }  // namespace
 
@@ -343,38 +453,40 @@ size_t glu_back_workspace(int64_t M, int64_t K, int64_t H) { return glu_back_lay
 hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
                                 const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
                                 void* dWu, void* ws, hipStream_t stream) {
-  const bool want_dx = dX != nullptr, want_dw = dWg != nullptr;
   const GluBackLayout L = glu_back_layout(M, K, H);
-  const int64_t Hp = pad64(H), Mp = pad64(M);
-  uint8_t* b = (uint8_t*)ws;
-  uint16_t *P = want_dx ? (uint16_t*)(b + L.p) : nullptr, *wt = (uint16_t*)(b + L.wt);
-  uint16_t *dgt = want_dw ? (uint16_t*)(b + L.dgt) : nullptr, *dut = (uint16_t*)(b + L.dut);
-  uint16_t* xt = (uint16_t*)(b + L.xt);
-  const dim3 block(256), tiles((unsigned)(Mp / 64), (unsigned)(Hp / 64));
+  GluBackArgs a{};
+  a.M = M; a.K = K; a.H = H; a.Hp = pad64(H);
+  uint16_t* P = (uint16_t*)((uint8_t*)ws + L.p);
+  a.P = P; a.X = (const uint16_t*)X; a.Wg = (const uint16_t*)Wg; a.Wu = (const uint16_t*)Wu;
+  a.dX = (uint16_t*)dX; a.dWg = (uint16_t*)dWg; a.dWu = (uint16_t*)dWu;
+  a.part = (float*)((uint8_t*)ws + L.part);
+  const dim3 block(256), chunks((unsigned)((M * (a.Hp / 8) + 255) / 256));
   if (act == kActSilu)
-    hipLaunchKernelGGL((glu_back_kernel<kActSilu>), tiles, block, 0, stream, M, H, (const uint16_t*)G,
-                       (const uint16_t*)U, (const uint16_t*)dY, P, Hp, dgt, dut, Mp);
+    hipLaunchKernelGGL((glu_back_kernel<kActSilu>), chunks, block, 0, stream, M, H, a.Hp, (const uint16_t*)G,
+                       (const uint16_t*)U, (const uint16_t*)dY, P);
   else
-    hipLaunchKernelGGL((glu_back_kernel<kActGelu>), tiles, block, 0, stream, M, H, (const uint16_t*)G,
-                       (const uint16_t*)U, (const uint16_t*)dY, P, Hp, dgt, dut, Mp);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (want_dx) {
-    const dim3 wtiles((unsigned)(Hp / 64), (unsigned)(K / 64));
-    hipLaunchKernelGGL(glu_transpose_kernel, wtiles, block, 0, stream, (const uint16_t*)Wg, H, K, wt, 2 * Hp,
-                       (int64_t)0);
-    hipLaunchKernelGGL(glu_transpose_kernel, wtiles, block, 0, stream, (const uint16_t*)Wu, H, K, wt, 2 * Hp, Hp);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_dense_bf16(M, K, 2 * Hp, P, wt, dX, stream)) != hipSuccess) return e;
+    hipLaunchKernelGGL((glu_back_kernel<kActGelu>), chunks, block, 0, stream, M, H, a.Hp, (const uint16_t*)G,
+                       (const uint16_t*)U, (const uint16_t*)dY, P);
+  if (dX != nullptr) {
+    const GluDxPlan d = glu_dx_plan(M, K, H);
+    const int64_t T = d.big ? 256 : 128;
+    a.per = d.per;
+    a.tiles_m = (int)((M + T - 1) / T);
+    a.tiles_n = (int)((K + T - 1) / T);
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n), (unsigned)d.splits);
+    if (d.big) hipLaunchKernelGGL((glu_dx_kernel<8, false>), grid, block, 0, stream, a);
+    else if (d.splits == 1) hipLaunchKernelGGL((glu_dx_kernel<4, false>), grid, block, 0, stream, a);
+    else {
+      hipLaunchKernelGGL((glu_dx_kernel<4, true>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL(glu_sum_kernel, dim3((unsigned)((M * K / 4 + 255) / 256)), block, 0, stream, a.part, d.splits,
+                         M * K, a.dX);
+    }
   }
-  if (want_dw) {
-    hipLaunchKernelGGL(glu_transpose_kernel, dim3((unsigned)(Mp / 64), (unsigned)(K / 64)), block, 0, stream,
-                       (const uint16_t*)X, M, K, xt, Mp, (int64_t)0);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_dense_bf16(H, K, Mp, dgt, xt, dWg, stream)) != hipSuccess) return e;
-    if ((e = launch_dense_bf16(H, K, Mp, dut, xt, dWu, stream)) != hipSuccess) return e;
+  if (dWg != nullptr) {
+    if (((2 * a.Hp + 255) / 256) * ((K + 255) / 256) >= 192) glu_dw_launch<8>(a, stream);
+    else glu_dw_launch<4>(a, stream);
   }
-  return hipSuccess;
+  return hipGetLastError();
 }
 
 }  // namespace rtl
