@@ -24,22 +24,27 @@ struct GluArgs {
   int tiles_m, tiles_n;
 };
 
+// act(g) and act'(g).  SiLU: g p, p (1 + g (1 - p)) with p = 1 / (1 + exp(-g)).  GELU: g Phi(g),
+// Phi(g) + g phi(g), with Phi from Abramowitz and Stegun 7.1.26 (erf within 1.5e-7): for x = |g| /
+// sqrt 2, t = 1 / (1 + 0.3275911 x), Phi(-|g|) = (a1 t + .. + a5 t^5) exp(-x^2) / 2, whose exp(-x^2)
+// is also that of phi(g).  A fifth of the instructions of the library's erf, which took a sixth
+// of a tile's time at K = 2560.
+struct ActValue {
+  float v, slope;
+};
 template <int ACT>
-__device__ __forceinline__ float glu_act(float g) {
-  return ACT == kActSilu ? g / (1.f + __expf(-g)) : gelu_erf(g);
-}
-// act(g) and act'(g).
-template <int ACT>
-__device__ __forceinline__ void glu_act_slope(float g, float& v, float& d) {
+__device__ __forceinline__ ActValue glu_act(float g) {
   if (ACT == kActSilu) {
-    const float p = 1.f / (1.f + __expf(-g));
-    v = g * p;
-    d = p * (1.f + g * (1.f - p));
-  } else {
-    const float p = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-    v = g * p;
-    d = p + g * (0.39894228040143268f * __expf(-0.5f * g * g));
+    const float p = __builtin_amdgcn_rcpf(1.f + __expf(-g));
+    return {g * p, p * (1.f + g * (1.f - p))};
   }
+  const float x = fabsf(g) * 0.70710678118654752f, e = __expf(-x * x);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                              0.254829592f);
+  const float tail = 0.5f * poly * e;  // Phi(-|g|)
+  const float p = g < 0.f ? tail : 1.f - tail;
+  return {g * p, fmaf(g, 0.39894228040143268f * e, p)};
 }
 
 // N (2 or 4) consecutive values of row `row` from column `col` on, rounded to bf16 (nearest even).
@@ -93,22 +98,27 @@ void glu_kernel(const GluArgs a) {
   const int64_t xb = (M - m0) * K * 2, wb = (H - n0) * K * 2;
   const OpA oa(K, 1, wave, lane);
   const OpB ob(K, NC, wave, lane);
-  auto load_a = [&](int kt, uint8_t* dst, int i) {
-    oa.load(rsrc_if(kt >= 0, X, xb), dst, i, 8 * (i * kRingWaves + wave), kt < 0 ? 0 : kt);
+  auto at_a = [&](int kt) { return typename OpA::Tile{oa, rsrc_if(kt >= 0, X, xb), max(kt, 0) * (kRK * 2)}; };
+  struct Weights {
+    const OpB& op;
+    __amdgpu_buffer_rsrc_t gate, up;
+    int koff;
+    __device__ __forceinline__ void load(uint8_t* dst, int i) const {
+      const int blk = i * kRingWaves + op.wave, at = blk % (2 * NB);  // 8-row block, and within its wave column
+      const int of = at % NB;  // half `of & 1` of block nb = of / 2
+      op.load(at >= NB ? up : gate, dst, i, blk / (2 * NB) * (16 * NC) + (of & 1) * (8 * NC) + (of >> 1), koff);
+    }
   };
-  auto load_b = [&](int kt, uint8_t* dst, int i) {
-    const int blk = i * kRingWaves + wave, at = blk % (2 * NB);  // 8-row block, and within its wave column
-    const bool up = at >= NB;
-    const int of = up ? at - NB : at;  // half `of & 1` of block nb = of / 2
-    ob.load(rsrc_if(kt >= 0, up ? Wu : Wg, wb), dst, i, blk / (2 * NB) * (16 * NC) + (of & 1) * (8 * NC) + (of >> 1),
-            kt < 0 ? 0 : kt);
+  auto at_b = [&](int kt) {
+    return Weights{ob, rsrc_if(kt >= 0, Wg, wb), rsrc_if(kt >= 0, Wu, wb), max(kt, 0) * (kRK * 2)};
   };
   f32x4 acc[RB][NB];
-  ring_product(acc, lds, oa, ob, load_a, load_b, steps, (tm + tn) % 8 % steps, wm, wn);
+  ring_product(acc, lds, oa, ob, at_a, at_b, steps, (tm + tn) % 8 % steps, wm, wn);
 
   const int64_t col = n0 + 16 * NC * wn + NC * r16;
 #pragma unroll
-  for (int rb = 0; rb < RB; rb++)
+  for (int rb = 0; rb < RB; rb++) {
+    settle(acc[rb]);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       const int64_t row = m0 + 16 * (RB * wm + rb) + 4 * q + j;
@@ -117,12 +127,13 @@ void glu_kernel(const GluArgs a) {
       for (int e = 0; e < NC; e++) {
         g[e] = acc[rb][e][j];
         u[e] = acc[rb][NC + e][j];
-        y[e] = glu_act<ACT>(g[e]) * u[e];
+        y[e] = glu_act<ACT>(g[e]).v * u[e];
       }
       store_cols<NC>(a.Y, M, H, row, col, y);
       if (a.G != nullptr) store_cols<NC>(a.G, M, H, row, col, g);
       if (a.U != nullptr) store_cols<NC>(a.U, M, H, row, col, u);
     }
+  }
 }
 
 // Few rows (M <= 16 MB): a workgroup of NW waves forms 16 output columns; wave w takes the K
@@ -193,7 +204,7 @@ __global__ __launch_bounds__(64 * NW) void glu_rows_kernel(const GluArgs a) {
     for (int j = 0; j < 4; j++) {
       const int64_t row = 16 * mb + 4 * q + j;
       if (row >= M || col >= H) continue;
-      a.Y[row * H + col] = (uint16_t)f32_to_bf16_bits(glu_act<ACT>(g[j]) * u[j]);
+      a.Y[row * H + col] = (uint16_t)f32_to_bf16_bits(glu_act<ACT>(g[j]).v * u[j]);
       if (a.G != nullptr) a.G[row * H + col] = (uint16_t)f32_to_bf16_bits(g[j]);
       if (a.U != nullptr) a.U[row * H + col] = (uint16_t)f32_to_bf16_bits(u[j]);
     }
@@ -261,116 +272,153 @@ __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int
   u32x4 dg, du;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    float v0, s0, v1, s1;
-    glu_act_slope<ACT>(bf16lo(g[i]), v0, s0);
-    glu_act_slope<ACT>(bf16hi(g[i]), v1, s1);
+    const ActValue a0 = glu_act<ACT>(bf16lo(g[i])), a1 = glu_act<ACT>(bf16hi(g[i]));
     const float d0 = bf16lo(d[i]), d1 = bf16hi(d[i]);
-    dg[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * bf16lo(u[i]) * s0), (__bf16)(d1 * bf16hi(u[i]) * s1)});
-    du[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * v0), (__bf16)(d1 * v1)});
+    dg[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * bf16lo(u[i]) * a0.slope), (__bf16)(d1 * bf16hi(u[i]) * a1.slope)});
+    du[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * a0.v), (__bf16)(d1 * a1.v)});
   }
   *reinterpret_cast<u32x4*>(P + m * 2 * Hp + h) = dg;
   *reinterpret_cast<u32x4*>(P + m * 2 * Hp + Hp + h) = du;
 }
 
-// A wave's RB x NB blocks to bf16 rows through its LDS block of 16 * (32 NB + 16) bytes, as
-// 16-byte chunks; row(i) gives the address of the wave's row i at its first column or null,
-// `cols` (a multiple of 8) the columns from there on.
-template <int RB, int NB, typename Row>
-__device__ __forceinline__ void store_rows(const f32x4 (&acc)[RB][NB], uint8_t* blk, int lane, int64_t cols, Row row) {
+// A wave's row of NB blocks to 16 bf16 rows through its LDS block of 16 * (32 NB + 16) bytes, as
+// 16-byte chunks; row(i) gives the address of row i at its first column or null, `cols` (a
+// multiple of 8) the columns from there on.
+template <int NB, typename Row>
+__device__ __forceinline__ void store_rows(const f32x4 (&acc)[NB], uint8_t* blk, int lane, int64_t cols, Row row) {
   constexpr int CW = NB * 16, PITCH = 2 * CW + 16, CPR = CW / 8;
   const int q = lane >> 4, r16 = lane & 15;
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int rb = 0; rb < RB; rb++) {
+  for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-    for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        const uint32_t w = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)acc[rb][nb][j], (__bf16)acc[rb][nb][j + 1]});
-        uint8_t* at = blk + (4 * q + j) * PITCH + (nb * 16 + r16) * 2;
-        *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
-        *reinterpret_cast<uint16_t*>(at + PITCH) = (uint16_t)(w >> 16);
-      }
-#pragma unroll
-    for (int c = 0; c < 16 * CPR / 64; c++) {
-      const int id = lane + 64 * c, rr = id / CPR, cc = id % CPR;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(blk + rr * PITCH + cc * 16);
-      uint16_t* y = row(16 * rb + rr);
-      if (y != nullptr && 8 * cc < cols) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + 8 * cc));
+    for (int j = 0; j < 4; j += 2) {
+      const uint32_t w = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)acc[nb][j], (__bf16)acc[nb][j + 1]});
+      uint8_t* at = blk + (4 * q + j) * PITCH + (nb * 16 + r16) * 2;
+      *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+      *reinterpret_cast<uint16_t*>(at + PITCH) = (uint16_t)(w >> 16);
     }
+#pragma unroll
+  for (int c = 0; c < 16 * CPR / 64; c++) {
+    const int id = lane + 64 * c, rr = id / CPR, cc = id % CPR;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(blk + rr * PITCH + cc * 16);
+    uint16_t* y = row(rr);
+    if (y != nullptr && 8 * cc < cols) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + 8 * cc));
   }
 }
 
+// The two products of the gradient.  Their tiles are dealt out in whole rounds (256 x 256 tiles,
+// one to a CU, or 128 x 128, two); the tiles of a last round that would leave CUs idle are split
+// along k, `splits` workgroups to a tile, whose fp32 sums go to `part` in accumulator order and are
+// added in split order by glu_join_kernel.
 struct GluBackArgs {
   int64_t M, K, H, Hp;
   const uint16_t *P, *X, *Wg, *Wu;
   uint16_t *dX, *dWg, *dWu;
-  float* part;       // split sum of dX: [splits][M][K]
-  int per;           // K steps per split
+  float* part;             // [splits][tail][T * T]
   int tiles_m, tiles_n;
+  int full, tail, splits;  // whole tiles, then split ones
+  int per;                 // K steps per split
 };
 
+// What workgroup `w` does: a tile, its K steps, and its part (-1: the whole tile).
+struct GluJob {
+  int tm, tn, first, steps, part;
+};
+__device__ __forceinline__ GluJob glu_job(const GluBackArgs& a, int w, int all) {
+  // Workgroups go round the XCDs (`full` is a multiple of 8 where there is a tail): each XCD gets
+  // a contiguous run of the tiles, and of the parts, split by split.
+  const bool whole = w < a.full;
+  const int i = whole ? w : w - a.full, n = whole ? a.full : a.tail * a.splits;
+  const int at = (i & 7) * (n >> 3) + min(i & 7, n & 7) + (i >> 3);
+  GluJob j;
+  j.part = whole ? -1 : at;
+  j.first = whole ? 0 : at / a.tail * a.per;
+  j.steps = whole ? all : min(a.per, all - j.first);
+  tile_from_index(whole ? at : a.full + at % a.tail, a.tiles_m, a.tiles_n, j.tm, j.tn);
+  return j;
+}
+
+// Output row r: of dX, or of [dWg; padding; dWu; padding] (Hp rows each).
+template <bool DW>
+__device__ __forceinline__ uint16_t* glu_row(const GluBackArgs& a, int64_t r) {
+  if (!DW) return r < a.M ? a.dX + r * a.K : nullptr;
+  return r < a.H ? a.dWg + r * a.K : r >= a.Hp && r < a.Hp + a.H ? a.dWu + (r - a.Hp) * a.K : nullptr;
+}
+
+// Stores a wave's blocks to the output's rows or to its part (decided row of blocks by row of
+// blocks: as two loops the accumulators move about on the way to them).
+template <int R, bool DW>
+__device__ __forceinline__ void glu_finish(const GluBackArgs& a, const GluJob& j, f32x4 (&acc)[R][R], uint8_t* lds,
+                                           int wave, int lane) {
+  __syncthreads();  // the ring is free
+  f32x4* part = reinterpret_cast<f32x4*>(a.part) + ((int64_t)j.part * kRingWaves + wave) * (R * R * 64) + lane;
+  const int64_t row0 = (int64_t)j.tm * (32 * R) + 16 * R * (wave & 1), col0 = (int64_t)j.tn * (32 * R) + 16 * R * (wave >> 1);
+#pragma unroll
+  for (int rb = 0; rb < R; rb++) {
+    settle(acc[rb]);
+    if (j.part >= 0) {
+#pragma unroll
+      for (int nb = 0; nb < R; nb++) part[(rb * R + nb) * 64] = acc[rb][nb];
+    } else {
+      store_rows<R>(acc[rb], lds + wave * 16 * (32 * R + 16), lane, a.K - col0, [&](int i) {
+        uint16_t* y = glu_row<DW>(a, row0 + 16 * rb + i);
+        return y == nullptr ? y : y + col0;
+      });
+    }
+  }
+}
+
+// One wave per 16-row strip of a split tile's wave: the parts' sum in split order, stored.
+template <int R, bool DW>
+__global__ __launch_bounds__(64) void glu_join_kernel(const GluBackArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[16 * (32 * R + 16)];
+  const int lane = threadIdx.x, rb = blockIdx.x % R, wave = blockIdx.x / R % kRingWaves, i = blockIdx.x / R / kRingWaves;
+  int tm, tn;
+  tile_from_index(a.full + i, a.tiles_m, a.tiles_n, tm, tn);
+  f32x4 acc[R];
+  for (int s = 0; s < a.splits; s++) {
+    const f32x4* in = reinterpret_cast<const f32x4*>(a.part) +
+                      (((int64_t)s * a.tail + i) * kRingWaves + wave) * (R * R * 64) + rb * R * 64 + lane;
+#pragma unroll
+    for (int nb = 0; nb < R; nb++) acc[nb] = s == 0 ? in[nb * 64] : acc[nb] + in[nb * 64];
+  }
+  const int64_t row0 = (int64_t)tm * (32 * R) + 16 * (R * (wave & 1) + rb), col0 = (int64_t)tn * (32 * R) + 16 * R * (wave >> 1);
+  store_rows<R>(acc, lds, lane, a.K - col0, [&](int r) {
+    uint16_t* y = glu_row<DW>(a, row0 + r);
+    return y == nullptr ? y : y + col0;
+  });
+}
+
 // dX = P [Wg; Wu]: k runs over P's 2 Hp columns, along P's rows and down the weights' columns.
-// With SPLIT, blockIdx.y takes `per` of the steps and leaves its fp32 sums in its part.
-template <int R, bool SPLIT>
+template <int R>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(R == 8 ? 1 : 2, R == 8 ? 1 : 2)))
 void glu_dx_kernel(const GluBackArgs a) {
   constexpr int T = 32 * R;
   typedef KRows<T> OpA;
   typedef KCols<T> OpB;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * OpA::kBytes];
-  int tm, tn;
-  tile_coords(a.tiles_m, a.tiles_n, tm, tn);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
   const int64_t M = a.M, K = a.K, H = a.H, ld = 2 * a.Hp;
-  const int64_t m0 = (int64_t)tm * T, c0 = (int64_t)tn * T;
-  const int half = (int)(a.Hp / kRK), all = 2 * half;
-  const int first = SPLIT ? blockIdx.y * a.per : 0, steps = SPLIT ? min(a.per, all - first) : all;
+  const int half = (int)(a.Hp / kRK);
+  const GluJob j = glu_job(a, blockIdx.x, 2 * half);
+  const int64_t m0 = (int64_t)j.tm * T, c0 = (int64_t)j.tn * T;
   const uint16_t* P = a.P + m0 * ld;
   const OpA oa(ld, 1, wave, lane);
   const OpB ob(K, wave, lane);
-  auto load_a = [&](int kt, uint8_t* dst, int i) {
-    oa.load(rsrc_if(kt >= 0, P, (M - m0) * ld * 2), dst, i, 8 * (i * kRingWaves + wave), kt < 0 ? 0 : first + kt);
+  auto at_a = [&](int kt) {
+    return typename OpA::Tile{oa, rsrc_if(kt >= 0, P, (M - m0) * ld * 2), (j.first + max(kt, 0)) * (kRK * 2)};
   };
-  auto load_b = [&](int kt, uint8_t* dst, int i) {
+  auto at_b = [&](int kt) {
     // rows of Wg, then of Wu; past H (P's padding) they read as zeros
-    const int s = first + (kt < 0 ? 0 : kt);
+    const int s = j.first + max(kt, 0);
     const int64_t h = (int64_t)(s < half ? s : s - half) * kRK;
-    ob.load(rsrc_if(kt >= 0, (s < half ? a.Wg : a.Wu) + h * K + c0, ((H - h) * K - c0) * 2), dst, i);
+    return typename OpB::Tile{ob, rsrc_if(kt >= 0, (s < half ? a.Wg : a.Wu) + h * K + c0, ((H - h) * K - c0) * 2)};
   };
   f32x4 acc[R][R];
-  ring_product(acc, lds, oa, ob, load_a, load_b, steps, (tm + tn) % 8 % steps, wm, wn);
-
-  const int64_t row0 = m0 + 16 * R * wm, col0 = c0 + 16 * R * wn;
-  if constexpr (SPLIT) {
-    float* out = a.part + (int64_t)blockIdx.y * M * K;
-    const int q = lane >> 4, r16 = lane & 15;
-#pragma unroll
-    for (int rb = 0; rb < R; rb++)
-#pragma unroll
-      for (int nb = 0; nb < R; nb++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const int64_t row = row0 + 16 * rb + 4 * q + j, col = col0 + 16 * nb + r16;
-          if (row < M && col < K) out[row * K + col] = acc[rb][nb][j];
-        }
-  } else {
-    __syncthreads();  // the ring is free
-    store_rows<R, R>(acc, lds + wave * 16 * (32 * R + 16), lane, K - col0, [&](int i) {
-      return row0 + i < M ? a.dX + (row0 + i) * K + col0 : (uint16_t*)nullptr;
-    });
-  }
-}
-
-// dX = the splits' sum in order, four values per thread (K % 64 == 0).
-__global__ __launch_bounds__(256) void glu_sum_kernel(const float* part, int splits, int64_t n, uint16_t* dX) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (at >= n) return;
-  f32x4 s = *reinterpret_cast<const f32x4*>(part + at);
-  for (int k = 1; k < splits; k++) s += *reinterpret_cast<const f32x4*>(part + (int64_t)k * n + at);
-  *reinterpret_cast<u32x2*>(dX + at) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, (j.tm + j.tn) % 8 % j.steps, wave & 1, wave >> 1);
+  glu_finish<R, false>(a, j, acc, lds, wave, lane);
 }
 
 // [dWg; dWu] = P^T X: k runs over the tokens, down the columns of both.
@@ -380,71 +428,90 @@ void glu_dw_kernel(const GluBackArgs a) {
   constexpr int T = 32 * R;
   typedef KCols<T> Op;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * Op::kBytes];
-  int tm, tn;
-  tile_coords(a.tiles_m, a.tiles_n, tm, tn);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
-  const int64_t M = a.M, K = a.K, H = a.H, Hp = a.Hp, ld = 2 * Hp;
-  const int64_t r0 = (int64_t)tm * T, c0 = (int64_t)tn * T;
-  const int steps = (int)((M + kRK - 1) / kRK);
+  const int64_t M = a.M, K = a.K, ld = 2 * a.Hp;
+  const GluJob j = glu_job(a, blockIdx.x, (int)((M + kRK - 1) / kRK));
+  const int64_t r0 = (int64_t)j.tm * T, c0 = (int64_t)j.tn * T;
   const Op oa(ld, wave, lane), ob(K, wave, lane);
   // tokens past M lie outside the buffers and read as zeros
-  auto load_a = [&](int kt, uint8_t* dst, int i) {
-    const int64_t m = (int64_t)(kt < 0 ? 0 : kt) * kRK;
-    oa.load(rsrc_if(kt >= 0, a.P + m * ld + r0, ((M - m) * ld - r0) * 2), dst, i);
+  auto at_a = [&](int kt) {
+    const int64_t m = (int64_t)(j.first + max(kt, 0)) * kRK;
+    return typename Op::Tile{oa, rsrc_if(kt >= 0, a.P + m * ld + r0, ((M - m) * ld - r0) * 2)};
   };
-  auto load_b = [&](int kt, uint8_t* dst, int i) {
-    const int64_t m = (int64_t)(kt < 0 ? 0 : kt) * kRK;
-    ob.load(rsrc_if(kt >= 0, a.X + m * K + c0, ((M - m) * K - c0) * 2), dst, i);
+  auto at_b = [&](int kt) {
+    const int64_t m = (int64_t)(j.first + max(kt, 0)) * kRK;
+    return typename Op::Tile{ob, rsrc_if(kt >= 0, a.X + m * K + c0, ((M - m) * K - c0) * 2)};
   };
   f32x4 acc[R][R];
-  ring_product(acc, lds, oa, ob, load_a, load_b, steps, (tm + tn) % 8 % steps, wm, wn);
-
-  __syncthreads();  // the ring is free
-  const int64_t row0 = r0 + 16 * R * wm, col0 = c0 + 16 * R * wn;
-  store_rows<R, R>(acc, lds + wave * 16 * (32 * R + 16), lane, K - col0, [&](int i) {
-    const int64_t r = row0 + i;  // 0 .. H - 1: a row of dWg; Hp .. Hp + H - 1: of dWu
-    return r < H ? a.dWg + r * K + col0 : r >= Hp && r < Hp + H ? a.dWu + (r - Hp) * K + col0 : (uint16_t*)nullptr;
-  });
+  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, (j.tm + j.tn) % 8 % j.steps, wave & 1, wave >> 1);
+  glu_finish<R, true>(a, j, acc, lds, wave, lane);
 }
 
 namespace {
 inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// dX: 256 x 256 tiles where they occupy three quarters of the CUs; else 128 x 128 tiles, and
-// where those do not give every CU its two workgroups, the sum over the 2 Hp columns is split,
-// in parts of at least 16 steps.
-struct GluDxPlan {
-  int splits, per;
-  bool big;
+// How a product of `rows` x `cols` outputs over `steps` K steps is dealt out.
+struct GluPlan {
+  int R, tiles_m, tiles_n, full, tail, splits, per;
+  double cost;
+  size_t part_bytes() const { return (size_t)splits * tail * (32 * R) * (32 * R) * 4; }
 };
-GluDxPlan glu_dx_plan(int64_t M, int64_t K, int64_t H) {
-  const int64_t steps = 2 * pad64(H) / kRK;
-  if (((M + 255) / 256) * ((K + 255) / 256) >= 192) return {1, (int)steps, true};
-  const int64_t tiles = ((M + 127) / 128) * ((K + 127) / 128);
-  const int64_t splits = std::max<int64_t>(1, std::min(512 / tiles, steps / 16));
-  const int64_t per = (steps + splits - 1) / splits;
-  return {(int)((steps + per - 1) / per), (int)per, false};
+// With tiles of 32 R: rounds of 256 (R = 8) or 512 workgroups, a last round of at most half of
+// them split as many ways as fill it, where that saves more than the parts' way through memory.
+// Costs in microseconds: a K step takes a round 1.45 (R = 8) or 1.29, a tile's first loads and
+// stores 8 or 5, a part's way out and back 0.1 or 0.026.
+GluPlan glu_plan_for(int R, int64_t rows, int64_t cols, int64_t steps) {
+  const int64_t T = 32 * R, P = R == 8 ? 256 : 512;
+  const double step = R == 8 ? 1.45 : 1.29, tile = R == 8 ? 8 : 5, way = R == 8 ? 0.1 : 0.026;
+  const int64_t tm = (rows + T - 1) / T, tn = (cols + T - 1) / T, tiles = tm * tn, rest = tiles % P;
+  GluPlan p{R, (int)tm, (int)tn, (int)tiles, 0, 1, (int)steps, (double)((tiles + P - 1) / P) * (steps * step + tile)};
+  if (rest == 0) return p;
+  for (int64_t s = std::min(P / rest, steps / 4); s >= 2; s /= 2) {
+    const int64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
+    const double cost = (double)(tiles / P) * (steps * step + tile) + per * step + tile + way * splits * rest;
+    if (cost < p.cost)
+      p = GluPlan{R, (int)tm, (int)tn, (int)(tiles - rest), (int)rest, (int)splits, (int)per, cost};
+  }
+  return p;
 }
+GluPlan glu_plan(int64_t rows, int64_t cols, int64_t steps) {
+  const GluPlan a = glu_plan_for(8, rows, cols, steps), b = glu_plan_for(4, rows, cols, steps);
+  return a.cost <= b.cost ? a : b;
+}
+GluPlan glu_dx_plan(int64_t M, int64_t K, int64_t H) { return glu_plan(M, K, 2 * pad64(H) / kRK); }
+GluPlan glu_dw_plan(int64_t M, int64_t K, int64_t H) { return glu_plan(2 * pad64(H), K, (M + kRK - 1) / kRK); }
 
+// Workspace: P [M, 2 Hp] bf16 | parts of the product that runs (dX's, then dW's).
 struct GluBackLayout {
   size_t p, part, total;
 };
 GluBackLayout glu_back_layout(int64_t M, int64_t K, int64_t H) {
   GluBackLayout L;
-  const GluDxPlan d = glu_dx_plan(M, K, H);
   L.p = 0;
   L.part = align256((size_t)(M * 2 * pad64(H) * 2));
-  L.total = L.part + (d.splits > 1 ? align256((size_t)d.splits * M * K * 4) : 0);
+  L.total = L.part + align256(std::max(glu_dx_plan(M, K, H).part_bytes(), glu_dw_plan(M, K, H).part_bytes()));
   return L;
 }
 
-template <int R>
-void glu_dw_launch(GluBackArgs a, hipStream_t stream) {
-  a.tiles_m = (int)((2 * a.Hp + 32 * R - 1) / (32 * R));
-  a.tiles_n = (int)((a.K + 32 * R - 1) / (32 * R));
-  hipLaunchKernelGGL((glu_dw_kernel<R>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
+template <int R, bool DW>
+void glu_product(const GluBackArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.full + a.tail * a.splits));
+  if (DW) hipLaunchKernelGGL((glu_dw_kernel<R>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((glu_dx_kernel<R>), grid, dim3(256), 0, stream, a);
+  if (a.tail > 0)
+    hipLaunchKernelGGL((glu_join_kernel<R, DW>), dim3((unsigned)(a.tail * kRingWaves * R)), dim3(64), 0, stream, a);
+}
+template <bool DW>
+void glu_product(GluBackArgs a, const GluPlan& p, hipStream_t stream) {
+  a.tiles_m = p.tiles_m;
+  a.tiles_n = p.tiles_n;
+  a.full = p.full;
+  a.tail = p.tail;
+  a.splits = p.splits;
+  a.per = p.per;
+  if (p.R == 8) glu_product<8, DW>(a, stream);
+  else glu_product<4, DW>(a, stream);
 }
 }  // namespace
 
@@ -467,25 +534,8 @@ hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const 
   else
     hipLaunchKernelGGL((glu_back_kernel<kActGelu>), chunks, block, 0, stream, M, H, a.Hp, (const uint16_t*)G,
                        (const uint16_t*)U, (const uint16_t*)dY, P);
-  if (dX != nullptr) {
-    const GluDxPlan d = glu_dx_plan(M, K, H);
-    const int64_t T = d.big ? 256 : 128;
-    a.per = d.per;
-    a.tiles_m = (int)((M + T - 1) / T);
-    a.tiles_n = (int)((K + T - 1) / T);
-    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n), (unsigned)d.splits);
-    if (d.big) hipLaunchKernelGGL((glu_dx_kernel<8, false>), grid, block, 0, stream, a);
-    else if (d.splits == 1) hipLaunchKernelGGL((glu_dx_kernel<4, false>), grid, block, 0, stream, a);
-    else {
-      hipLaunchKernelGGL((glu_dx_kernel<4, true>), grid, block, 0, stream, a);
-      hipLaunchKernelGGL(glu_sum_kernel, dim3((unsigned)((M * K / 4 + 255) / 256)), block, 0, stream, a.part, d.splits,
-                         M * K, a.dX);
-    }
-  }
-  if (dWg != nullptr) {
-    if (((2 * a.Hp + 255) / 256) * ((K + 255) / 256) >= 192) glu_dw_launch<8>(a, stream);
-    else glu_dw_launch<4>(a, stream);
-  }
+  if (dX != nullptr) glu_product<false>(a, glu_dx_plan(M, K, H), stream);
+  if (dWg != nullptr) glu_product<true>(a, glu_dw_plan(M, K, H), stream);
   return hipGetLastError();
 }
 

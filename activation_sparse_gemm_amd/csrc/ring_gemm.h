@@ -38,12 +38,21 @@ struct KRows {
     rd[0] = sw_off(r16, q);
     rd[1] = sw_off(r16, 4 + q);
   }
-  // Load i of a step, whose first row is `row`, into the tile at `dst`.
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t res, uint8_t* dst, int i, int64_t row, int kt) const {
+  // Load i of a step from `res`, whose first row is `row` and first k `koff` / 2, into the tile at `dst`.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t res, uint8_t* dst, int i, int64_t row, int koff) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         res, (__attribute__((address_space(3))) void*)(dst + (i * kRingWaves + wave) * 1024), 16, voff,
-        (int)(row * ld * 2 + (int64_t)kt * (kRK * 2)), 0, 0);
+        (int)(row * ld * 2) + koff, 0, 0);
   }
+  // A step's tile of consecutive rows.
+  struct Tile {
+    const KRows& op;
+    __amdgpu_buffer_rsrc_t res;
+    int koff;
+    __device__ __forceinline__ void load(uint8_t* dst, int i) const {
+      op.load(res, dst, i, 8 * (i * kRingWaves + op.wave), koff);
+    }
+  };
   // Fragment of 16-row block `blk`, K half kk: lane (r16, q) holds row r16, k = 32 kk + 8q .. + 7.
   __device__ __forceinline__ u32x4 read(const uint8_t* tile, int blk, int kk) const {
     return *reinterpret_cast<const u32x4*>(tile + blk * 2048 + rd[kk]);
@@ -79,6 +88,11 @@ struct KCols {
         res, (__attribute__((address_space(3))) void*)(dst + (i * kRingWaves + wave) * 1024), 16, voff[i & 1],
         (int)((i >> 1) * (COLS == 256 ? 16 : 32) * ld * 2), 0, 0);
   }
+  struct Tile {
+    const KCols& op;
+    __amdgpu_buffer_rsrc_t res;
+    __device__ __forceinline__ void load(uint8_t* dst, int i) const { op.load(res, dst, i); }
+  };
   __device__ __forceinline__ u32x4 read(const uint8_t* tile, int blk, int kk) const {
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     // blocks 0..7 of a row by the swizzle, 8..15 256 bytes on; the second four k (c = 1) one row on
@@ -98,16 +112,20 @@ struct KCols {
 __device__ __forceinline__ void mfma_acc(f32x4& acc, u32x4 a, u32x4 b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
-// Waits until the products of mfma_acc are written (the compiler does not see them): every
-// accumulator passes through a statement that idles longer than the instruction takes.
-template <int RB, int NB>
-__device__ __forceinline__ void settle(f32x4 (&acc)[RB][NB]) {
+// acc = 0, as a product of zeros: of plain zeros the compiler makes one register and copies it.
+__device__ __forceinline__ void mfma_zero(f32x4& acc) {
+  const u32x4 z{};
+  asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %1, 0" : "=a"(acc) : "v"(z));
+}
+// Waits until the products of mfma_acc on a row of blocks are written (the compiler does not see
+// them): the accumulators pass through a statement that idles longer than the instruction takes.
+// Called where the row is used: as one statement for all rows it has the compiler copy all of
+// them to general registers at once.
+template <int NB>
+__device__ __forceinline__ void settle(f32x4 (&acc)[NB]) {
 #pragma unroll
-  for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-    for (int nb = 0; nb < NB; nb += 4)
-      asm volatile("s_nop 15\n\ts_nop 15"
-                   : "+a"(acc[rb][nb]), "+a"(acc[rb][nb + 1]), "+a"(acc[rb][nb + 2]), "+a"(acc[rb][nb + 3]));
+  for (int nb = 0; nb < NB; nb += 4)
+    asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc[nb]), "+a"(acc[nb + 1]), "+a"(acc[nb + 2]), "+a"(acc[nb + 3]));
 }
 
 template <int RB>
@@ -116,14 +134,13 @@ struct ARegs {
 };
 
 // One ring step of a wave's RB x NB blocks of 16 x 16.  tb, ta1, tb1: the tiles of B_s, A_{s+1},
-// B_{s+1}; da, db: where load(dst, i, true) puts load i of A_{s+2} and load(dst, i, false) of
-// B_{s+2}.  The five slots are distinct (__restrict__ says so: without it the compiler has every
+// B_{s+1}; da, db: where sa.load(da, i) puts load i of A_{s+2} and sb.load(db, i) of B_{s+2}.  The five slots are distinct (__restrict__ says so: without it the compiler has every
 // transposing read wait for every load in flight).
-template <int RB, int NB, typename OpA, typename OpB, typename Load>
+template <int RB, int NB, typename OpA, typename OpB, typename SrcA, typename SrcB>
 __device__ __forceinline__ void ring_step(f32x4 (&acc)[RB][NB], const uint8_t* __restrict__ tb,
                                           const uint8_t* __restrict__ ta1, const uint8_t* __restrict__ tb1,
                                           uint8_t* __restrict__ da, uint8_t* __restrict__ db, const OpA& oa,
-                                          const OpB& ob, Load load, const ARegs<RB>& cur, ARegs<RB>& next,
+                                          const OpB& ob, const SrcA& sa, const SrcB& sb, const ARegs<RB>& cur, ARegs<RB>& next,
                                           u32x4 (&bv)[4][2], int wm, int wn) {
   constexpr int LA = OpA::kLoads, LD = LA + OpB::kLoads;
   static_assert(NB % 4 == 0 && 3 * (NB - 1) >= LD && 3 * (NB - 1) >= 2 * RB, "three reads and loads a block suffice");
@@ -145,8 +162,8 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[RB][NB], const uint8_t* _
         const int i = 3 * nb + t;
         if (nb < NB - 1 && p == 2 + t * (RB / 2) && i < 2 * RB) next.v[i / RB][i % RB] = oa.read(ta1, RB * wm + i % RB, i / RB);
         if (nb < NB - 1 && p == 2 + RB / 4 + t * (RB / 2) && i < LD) {
-          if (i < LA) load(da, i, true);
-          else load(db, i - LA, false);
+          if (i < LA) sa.load(da, i);
+          else sb.load(db, i - LA);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -154,30 +171,31 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[RB][NB], const uint8_t* _
   }
 }
 
-// The product over `steps` K steps.  load_a(kt, dst, i) and load_b issue load i of physical step
-// kt; steps run from `k0` on and round; past the end (kt = -1) the loads read zeros.
-template <int RB, int NB, typename OpA, typename OpB, typename LoadA, typename LoadB>
+// The product over `steps` K steps.  at_a(kt) and at_b(kt) give the source of physical step kt's
+// tile, whose load(dst, i) issues its load i; steps run from `k0` on and round; past the end (kt =
+// -1) the loads read zeros.  The caller settles each row of blocks before it reads it.
+template <int RB, int NB, typename OpA, typename OpB, typename AtA, typename AtB>
 __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds, const OpA& oa, const OpB& ob,
-                                             LoadA load_a, LoadB load_b, int steps, int k0, int wm, int wn) {
+                                             AtA at_a, AtB at_b, int steps, int k0, int wm, int wn) {
   static_assert(OpA::kBytes == OpB::kBytes, "either operand's tile fits every slot");
   constexpr int SLOT = OpA::kBytes, LA = OpA::kLoads, LB = OpB::kLoads;
-  auto load = [&](int s, uint8_t* dst, int i, bool a) {
-    int kt = s + k0;
-    kt = s >= steps ? -1 : kt >= steps ? kt - steps : kt;
-    if (a) load_a(kt, dst, i);
-    else load_b(kt, dst, i);
+  auto physical = [&](int s) {
+    const int kt = s + k0;
+    return s >= steps ? -1 : kt >= steps ? kt - steps : kt;
   };
 #pragma unroll
   for (int rb = 0; rb < RB; rb++)
 #pragma unroll
-    for (int nb = 0; nb < NB; nb++) acc[rb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int nb = 0; nb < NB; nb++) mfma_zero(acc[rb][nb]);
   // A_0, B_0, A_1, B_1 into slots 0..3
 #pragma unroll
   for (int s = 0; s < 2; s++) {
+    const auto sa = at_a(physical(s));
+    const auto sb = at_b(physical(s));
 #pragma unroll
-    for (int i = 0; i < LA; i++) load(s, lds + 2 * s * SLOT, i, true);
+    for (int i = 0; i < LA; i++) sa.load(lds + 2 * s * SLOT, i);
 #pragma unroll
-    for (int i = 0; i < LB; i++) load(s, lds + (2 * s + 1) * SLOT, i, false);
+    for (int i = 0; i < LB; i++) sb.load(lds + (2 * s + 1) * SLOT, i);
   }
   wait_vmcnt<LB>();
   barrier_nofence();
@@ -195,8 +213,9 @@ __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds,
   // Slots of B_{s+2} (A_s's), B_s, A_{s+1}, B_{s+1}, A_{s+2} (B_{s-1}'s); two on with every step.
   int o0 = 0, o1 = SLOT, o2 = 2 * SLOT, o3 = 3 * SLOT, o4 = 4 * SLOT;
   auto step = [&](int s, const ARegs<RB>& cur, ARegs<RB>& next) {
-    ring_step<RB, NB>(acc, lds + o1, lds + o2, lds + o3, lds + o4, lds + o0, oa, ob,
-                      [&](uint8_t* dst, int i, bool a) { load(s + 2, dst, i, a); }, cur, next, bv, wm, wn);
+    const int kt = physical(s + 2);
+    ring_step<RB, NB>(acc, lds + o1, lds + o2, lds + o3, lds + o4, lds + o0, oa, ob, at_a(kt), at_b(kt), cur, next, bv,
+                      wm, wn);
     const int t0 = o0, t1 = o1;
     o0 = o2; o1 = o3; o2 = o4; o3 = t0; o4 = t1;
   };
@@ -207,7 +226,6 @@ __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds,
   }
   if (s < steps) step(s, av[0], av[1]);
   wait_vmcnt<0>();  // no load into the ring is left in flight
-  settle<RB, NB>(acc);
 }
 
 }  // namespace rtl

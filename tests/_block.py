@@ -90,8 +90,9 @@ def act(g, kind):
 
 def act_bound(g):
     """Error of the kernels' act(g) and act'(g): exp of an argument rounded to fp32 is within
-    (2 |g| + 4) u, the rest a few roundings; GELU's 1 + erf is within 4 u of 1 in absolute
-    terms, times |g|; the slope's g exp(-g^2 / 2) is below 1."""
+    (2 |g| + 4) u, the rest a few roundings; GELU's Phi is within 5 u in absolute terms
+    (Abramowitz and Stegun 7.1.26 halved, 1.3 u, and its roundings), times |g|; the slope's
+    g exp(-g^2 / 2) is below 1."""
     return (8 + 4 * np.abs(g)) * U * (1 + np.abs(g))
 
 
