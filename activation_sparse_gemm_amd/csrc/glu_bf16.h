@@ -113,7 +113,7 @@ void glu_kernel(const GluArgs a) {
     return Weights{ob, rsrc_if(kt >= 0, Wg, wb), rsrc_if(kt >= 0, Wu, wb), max(kt, 0) * (kRK * 2)};
   };
   f32x4 acc[RB][NB];
-  ring_product(acc, lds, oa, ob, at_a, at_b, steps, (tm + tn) % 8 % steps, wm, wn);
+  ring_product(acc, lds, oa, ob, at_a, at_b, steps, wm, wn);
 
   const int64_t col = n0 + 16 * NC * wn + NC * r16;
 #pragma unroll
@@ -136,68 +136,88 @@ void glu_kernel(const GluArgs a) {
   }
 }
 
-// Few rows (M <= 16 MB): a workgroup of NW waves forms 16 output columns; wave w takes the K
-// steps w, w + NW, ..., each lane loading 16-byte chunks of its weight row straight into the
-// MFMA's operand order, and the waves' partial sums are added in LDS in wave order.  Bound by
-// the weights' bytes.
-template <int ACT, int MB, int NW>
-__global__ __launch_bounds__(64 * NW) void glu_rows_kernel(const GluArgs a) {
-  __shared__ f32x4 red[NW][2 * MB][64];
+// Few rows (M <= 16 MB): a workgroup forms 16 output columns; wave w takes the K steps w, w + 4, ...
+// of 64, each with a ring of D LDS slots of its own (16 gate rows, 16 up rows and the rows of X,
+// in whole 128-byte lines that go straight to LDS) and no barrier, and the waves' sums are added
+// in wave order.  Bound by the weights' bytes: 1 x 5120 x 13824 reads 283 MB.  (Loading fragments
+// straight into registers, 64 pieces of 16 bytes an instruction, is held by the address path
+// instead: 16 rows of X then cost 25% of the time.)
+template <int ACT, int MB>
+__global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs a) {
+  constexpr int D = 2;  // 48 KB a workgroup at MB = 1, three to a CU; D = 4 measured 5-15% slower
+  constexpr int LOADS = 4 + 2 * MB, SLOT = LOADS * 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRingWaves * D * SLOT];
+  static_assert(kRingWaves * D * SLOT >= kRingWaves * 2 * MB * 1024, "the sums fit the rings");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r16 = lane & 15;
   const int64_t M = a.M, K = a.K, H = a.H, n0 = (int64_t)blockIdx.x * 16;
   const int KT = (int)(K / kBK);
-  const __amdgpu_buffer_rsrc_t xres = make_rsrc(a.X, M * K * 2);
-  const __amdgpu_buffer_rsrc_t gres = make_rsrc(a.Wg + n0 * K, (H - n0) * K * 2);
-  const __amdgpu_buffer_rsrc_t ures = make_rsrc(a.Wu + n0 * K, (H - n0) * K * 2);
-  const uint32_t voff = (uint32_t)(r16 * K * 2 + 16 * q);
+  uint8_t* const ring = lds + wave * (D * SLOT);
+  const KRows<256> op(K, 1, 0, lane);  // eight rows a load, block by block
+  auto load = [&](int s, uint8_t* slot) {
+    const bool live = s < KT;  // past the end: zeros
+    const int koff = live ? s * (kBK * 2) : 0;
+    const __amdgpu_buffer_rsrc_t gr = rsrc_if(live, a.Wg + n0 * K, (H - n0) * K * 2),
+                                 ur = rsrc_if(live, a.Wu + n0 * K, (H - n0) * K * 2), xr = rsrc_if(live, a.X, M * K * 2);
+    auto one = [&](__amdgpu_buffer_rsrc_t res, int at, int row) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (__attribute__((address_space(3))) void*)(slot + at * 1024), 16, op.voff,
+                                               (int)(row * K * 2) + koff, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      one(gr, i, 8 * i);
+      one(ur, 2 + i, 8 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * MB; i++) one(xr, 4 + i, 8 * i);
+  };
   f32x4 acc[2][MB];
 #pragma unroll
   for (int p = 0; p < 2; p++)
 #pragma unroll
     for (int mb = 0; mb < MB; mb++) acc[p][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // UN K steps at a time: every load of the batch is issued before the first product.
-  auto batch = [&](int s0, auto un) {
-    constexpr int UN = decltype(un)::value;
-    u32x4 w[UN][2][2], x[UN][MB][2];
 #pragma unroll
-    for (int i = 0; i < UN; i++)
+  for (int i = 0; i < D; i++) load(wave + i * kRingWaves, ring + i * SLOT);
+  for (int s = wave; s < KT; s += D * kRingWaves)
+#pragma unroll
+    for (int i = 0; i < D; i++) {
+      uint8_t* slot = ring + i * SLOT;
+      wait_vmcnt<(D - 1) * LOADS>();  // this slot's loads have arrived
+      asm volatile("" ::: "memory");
+      u32x4 w[2][2], x[MB][2];
 #pragma unroll
       for (int kk = 0; kk < 2; kk++) {
-        const int at = (s0 + i * NW) * 128 + 64 * kk;
-        w[i][0][kk] = __builtin_amdgcn_raw_buffer_load_b128(gres, voff, at, 0);
-        w[i][1][kk] = __builtin_amdgcn_raw_buffer_load_b128(ures, voff, at, 0);
 #pragma unroll
-        for (int mb = 0; mb < MB; mb++)
-          x[i][mb][kk] = __builtin_amdgcn_raw_buffer_load_b128(xres, voff, (int)(16 * mb * K * 2) + at, 0);
+        for (int p = 0; p < 2; p++) w[p][kk] = op.read(slot, p, kk);
+#pragma unroll
+        for (int mb = 0; mb < MB; mb++) x[mb][kk] = op.read(slot, 2 + mb, kk);
       }
-#pragma unroll
-    for (int i = 0; i < UN; i++)
+      __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt(0): the slot is free
+      asm volatile("" ::: "memory");
+      load(s + (D + i) * kRingWaves, slot);
 #pragma unroll
       for (int kk = 0; kk < 2; kk++)
 #pragma unroll
         for (int p = 0; p < 2; p++)
 #pragma unroll
           for (int mb = 0; mb < MB; mb++)
-            acc[p][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[i][mb][kk]),
-                                                                 __builtin_bit_cast(bf16x8, w[i][p][kk]), acc[p][mb],
-                                                                 0, 0, 0);
-  };
-  constexpr int UN = MB == 1 ? 4 : 2;
-  int s = wave;
-  for (; s + (UN - 1) * NW < KT; s += UN * NW) batch(s, std::integral_constant<int, UN>());
-  for (; s < KT; s += NW) batch(s, std::integral_constant<int, 1>());
+            acc[p][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[mb][kk]),
+                                                                 __builtin_bit_cast(bf16x8, w[p][kk]), acc[p][mb], 0, 0, 0);
+    }
+  wait_vmcnt<0>();
+  __syncthreads();  // every wave's ring is free
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
   for (int p = 0; p < 2; p++)
 #pragma unroll
-    for (int mb = 0; mb < MB; mb++) red[wave][p * MB + mb][lane] = acc[p][mb];
+    for (int mb = 0; mb < MB; mb++) red[(wave * 2 * MB + p * MB + mb) * 64 + lane] = acc[p][mb];
   __syncthreads();
-  for (int mb = wave; mb < MB; mb += NW) {
-    f32x4 g = red[0][mb][lane], u = red[0][MB + mb][lane];
-    for (int w = 1; w < NW; w++) {
-      g += red[w][mb][lane];
-      u += red[w][MB + mb][lane];
+  for (int mb = wave; mb < MB; mb += kRingWaves) {
+    f32x4 g = red[mb * 64 + lane], u = red[(MB + mb) * 64 + lane];
+    for (int w = 1; w < kRingWaves; w++) {
+      g += red[(w * 2 * MB + mb) * 64 + lane];
+      u += red[(w * 2 * MB + MB + mb) * 64 + lane];
     }
     const int64_t col = n0 + r16;
 #pragma unroll
@@ -221,12 +241,22 @@ void glu_tiles(GluArgs a, hipStream_t stream) {
   hipLaunchKernelGGL((glu_kernel<ACT, R, R>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
 }
 
+template <int ACT, int MB>
+void glu_rows(const GluArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((glu_rows_kernel<ACT, MB>), dim3((unsigned)((a.H + 15) / 16)), dim3(64 * kRingWaves), 0, stream,
+                     a);
+}
+
+// Up to 32 rows, and up to 64 where 128 x 64 tiles would leave a third of the CUs without one,
+// stream the weights (64 x 2560 x 6912, 108 tiles: 21 us against 29; 64 x 5120 x 13824, 216 tiles:
+// 75 against 60).  Else 256 x 128 tiles where they occupy three quarters of the CUs, or 128 x 64.
 template <int ACT>
 void glu_launch(const GluArgs& a, hipStream_t stream) {
-  const dim3 cols((unsigned)((a.H + 15) / 16)), block(512);
-  if (a.M <= 16) hipLaunchKernelGGL((glu_rows_kernel<ACT, 1, 8>), cols, block, 0, stream, a);
-  else if (a.M <= 32) hipLaunchKernelGGL((glu_rows_kernel<ACT, 2, 8>), cols, block, 0, stream, a);
-  else if (((a.M + 255) / 256) * ((a.H + 127) / 128) >= 192) glu_tiles<ACT, 8>(a, stream);
+  const int64_t small = ((a.M + 127) / 128) * ((a.H + 63) / 64), big = ((a.M + 255) / 256) * ((a.H + 127) / 128);
+  if (a.M <= 16) glu_rows<ACT, 1>(a, stream);
+  else if (a.M <= 32) glu_rows<ACT, 2>(a, stream);
+  else if (a.M <= 64 && small < 171) glu_rows<ACT, 4>(a, stream);
+  else if (big >= 192) glu_tiles<ACT, 8>(a, stream);
   else glu_tiles<ACT, 4>(a, stream);
 }
 
@@ -417,7 +447,7 @@ void glu_dx_kernel(const GluBackArgs a) {
     return typename OpB::Tile{ob, rsrc_if(kt >= 0, (s < half ? a.Wg : a.Wu) + h * K + c0, ((H - h) * K - c0) * 2)};
   };
   f32x4 acc[R][R];
-  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, (j.tm + j.tn) % 8 % j.steps, wave & 1, wave >> 1);
+  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, wave & 1, wave >> 1);
   glu_finish<R, false>(a, j, acc, lds, wave, lane);
 }
 
@@ -444,7 +474,7 @@ void glu_dw_kernel(const GluBackArgs a) {
     return typename Op::Tile{ob, rsrc_if(kt >= 0, a.X + m * K + c0, ((M - m) * K - c0) * 2)};
   };
   f32x4 acc[R][R];
-  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, (j.tm + j.tn) % 8 % j.steps, wave & 1, wave >> 1);
+  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, wave & 1, wave >> 1);
   glu_finish<R, true>(a, j, acc, lds, wave, lane);
 }
 
@@ -459,17 +489,19 @@ struct GluPlan {
 };
 // With tiles of 32 R: rounds of 256 (R = 8) or 512 workgroups, a last round of at most half of
 // them split as many ways as fill it, where that saves more than the parts' way through memory.
-// Costs in microseconds: a K step takes a round 1.45 (R = 8) or 1.29, a tile's first loads and
-// stores 8 or 5, a part's way out and back 0.1 or 0.026.
+// Costs in microseconds, as measured: a K step takes a round 1.45 (R = 8) or 1.29, a tile's first
+// loads and stores 10.5 or 4.5, a part's way out and back 0.1 or 0.026; a last round of small tiles
+// that leaves each CU one takes 0.6 of a round.
 GluPlan glu_plan_for(int R, int64_t rows, int64_t cols, int64_t steps) {
-  const int64_t T = 32 * R, P = R == 8 ? 256 : 512;
-  const double step = R == 8 ? 1.45 : 1.29, tile = R == 8 ? 8 : 5, way = R == 8 ? 0.1 : 0.026;
+  const bool big = R == 8;
+  const int64_t T = 32 * R, P = big ? 256 : 512;
+  const double step = big ? 1.45 : 1.29, tile = big ? 10.5 : 4.5, way = big ? 0.1 : 0.026;
   const int64_t tm = (rows + T - 1) / T, tn = (cols + T - 1) / T, tiles = tm * tn, rest = tiles % P;
-  GluPlan p{R, (int)tm, (int)tn, (int)tiles, 0, 1, (int)steps, (double)((tiles + P - 1) / P) * (steps * step + tile)};
-  if (rest == 0) return p;
-  for (int64_t s = std::min(P / rest, steps / 4); s >= 2; s /= 2) {
+  const double whole = steps * step + tile, last = rest == 0 ? 0. : !big && rest <= 256 ? 0.6 : 1.;
+  GluPlan p{R, (int)tm, (int)tn, (int)tiles, 0, 1, (int)steps, (double)(tiles / P) * whole + last * whole};
+  for (int64_t s = rest == 0 ? 0 : std::min(P / rest, steps / 4); s >= 2; s /= 2) {
     const int64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
-    const double cost = (double)(tiles / P) * (steps * step + tile) + per * step + tile + way * splits * rest;
+    const double cost = (double)(tiles / P) * whole + per * step + tile + way * splits * rest;
     if (cost < p.cost)
       p = GluPlan{R, (int)tm, (int)tn, (int)(tiles - rest), (int)rest, (int)splits, (int)per, cost};
   }

@@ -171,18 +171,16 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[RB][NB], const uint8_t* _
   }
 }
 
-// The product over `steps` K steps.  at_a(kt) and at_b(kt) give the source of physical step kt's
-// tile, whose load(dst, i) issues its load i; steps run from `k0` on and round; past the end (kt =
-// -1) the loads read zeros.  The caller settles each row of blocks before it reads it.
+// The product over `steps` K steps.  at_a(kt) and at_b(kt) give the source of step kt's tile, whose
+// load(dst, i) issues its load i; past the end (kt = -1) the loads read zeros.  The caller settles
+// each row of blocks before it reads it.  (Tiles that start at different steps and go round, so
+// that one of those that share an operand takes each L2 miss, measured 2% slower.)
 template <int RB, int NB, typename OpA, typename OpB, typename AtA, typename AtB>
 __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds, const OpA& oa, const OpB& ob,
-                                             AtA at_a, AtB at_b, int steps, int k0, int wm, int wn) {
+                                             AtA at_a, AtB at_b, int steps, int wm, int wn) {
   static_assert(OpA::kBytes == OpB::kBytes, "either operand's tile fits every slot");
   constexpr int SLOT = OpA::kBytes, LA = OpA::kLoads, LB = OpB::kLoads;
-  auto physical = [&](int s) {
-    const int kt = s + k0;
-    return s >= steps ? -1 : kt >= steps ? kt - steps : kt;
-  };
+  auto step_or_none = [&](int s) { return s < steps ? s : -1; };
 #pragma unroll
   for (int rb = 0; rb < RB; rb++)
 #pragma unroll
@@ -190,8 +188,8 @@ __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds,
   // A_0, B_0, A_1, B_1 into slots 0..3
 #pragma unroll
   for (int s = 0; s < 2; s++) {
-    const auto sa = at_a(physical(s));
-    const auto sb = at_b(physical(s));
+    const auto sa = at_a(step_or_none(s));
+    const auto sb = at_b(step_or_none(s));
 #pragma unroll
     for (int i = 0; i < LA; i++) sa.load(lds + 2 * s * SLOT, i);
 #pragma unroll
@@ -213,7 +211,7 @@ __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds,
   // Slots of B_{s+2} (A_s's), B_s, A_{s+1}, B_{s+1}, A_{s+2} (B_{s-1}'s); two on with every step.
   int o0 = 0, o1 = SLOT, o2 = 2 * SLOT, o3 = 3 * SLOT, o4 = 4 * SLOT;
   auto step = [&](int s, const ARegs<RB>& cur, ARegs<RB>& next) {
-    const int kt = physical(s + 2);
+    const int kt = step_or_none(s + 2);
     ring_step<RB, NB>(acc, lds + o1, lds + o2, lds + o3, lds + o4, lds + o0, oa, ob, at_a(kt), at_b(kt), cur, next, bv,
                       wm, wn);
     const int t0 = o0, t1 = o1;
