@@ -14,6 +14,7 @@ Method: "RT-Lynx: Putting the GEMM Sparsity In a Right Way for Diffusion Models"
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -347,38 +348,84 @@ def rtl_linear_fused_fp8(X: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor, LA
     return Y
 
 
+class _Here:
+    """The context of a call whose tensors are on the current device."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
 def _one_device(*tensors):
-    """The device that every given tensor is on; the call is made with that device current, so
-    that a call without ``stream`` runs on that device's current stream."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError(f"tensors must be on one GPU, got {sorted(map(str, devices))}")
-    return torch.cuda.device(next(iter(devices)))
+    """The context in which the GPU that every given tensor is on is the current device, so that
+    a call without ``stream`` runs on that GPU's current stream."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or (dev is not None and d != dev):
+                raise ValueError("tensors must be on one GPU, got "
+                                 f"{sorted({str(u.device) for u in tensors if u is not None})}")
+            dev = d
+    return _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _expect(name, t, shape, dtype):
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t is not None and (t.dtype is not dtype or t.shape != shape):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _flat(t):
+    """Address of a contiguous tensor on the GPU (None: null)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
 def _heads(t):
-    """Pointer, row stride and head stride of a [M, H, D] tensor whose channels are contiguous."""
+    """Address, row stride and head stride of a [M, H, D] tensor whose channels are contiguous."""
     if t is None:
         return None, 0, 0
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    row, head, channel = t.stride()
+    if channel != 1 and t.shape[2] > 1:
         raise ValueError("the channels of a head must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0), t.stride(1)
+    return t.data_ptr(), row, head
+
+
+def _new(stream, like, shape, dtype):
+    """A tensor on `like`'s device, as _empty allocates it."""
+    return like.new_empty(shape, dtype=dtype) if stream is None else _empty(shape, dtype, like.device, stream)
+
+
+def _queue(stream, like):
+    """The hipStream_t of `stream`, or of the current stream of `like`'s device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return _stream(stream)
+
+
+@functools.lru_cache(maxsize=64)
+def _dims(axis_dims):
+    if any(not 0 <= d < 2 ** 31 for d in axis_dims):
+        raise ValueError(f"axis_dims must be whole numbers of channels, got {axis_dims}")
+    return (ctypes.c_int32 * max(len(axis_dims), 1))(*axis_dims)
 
 
 def _rope_args(pos, axis_dims, theta, pairs, M):
-    dims = [int(d) for d in axis_dims]
-    if dims:
-        _expect("pos", pos, (M, len(dims)), torch.float32)
-    return _ptr(pos) if dims else None, len(dims), (ctypes.c_int32 * max(len(dims), 1))(*dims), float(theta), pairs
+    dims = tuple(axis_dims)
+    if not dims:
+        return None, 0, _dims(dims), theta, pairs
+    _expect("pos", pos, (M, len(dims)), torch.float32)
+    return _flat(pos), len(dims), _dims(dims), theta, pairs
 
 
 def rtl_rope_axes(X: torch.Tensor, pos: torch.Tensor, axis_dims, theta: float = 10000.0,
@@ -391,10 +438,11 @@ def rtl_rope_axes(X: torch.Tensor, pos: torch.Tensor, axis_dims, theta: float = 
     M, H, D = X.shape
     with _one_device(X, pos, Y):
         if Y is None:
-            Y = _empty((M, H, D), X.dtype, X.device, stream)
-        _expect("Y", Y, (M, H, D), X.dtype)
+            Y = _new(stream, X, (M, H, D), X.dtype)
+        else:
+            _expect("Y", Y, (M, H, D), X.dtype)
         _check(lib.rtl_rope_axes(_dt(X), M, H, D, *_heads(X), *_rope_args(pos, axis_dims, theta, pairs, M),
-                                 int(inverse), *_heads(Y), _stream(stream)))
+                                 bool(inverse), *_heads(Y), _queue(stream, X)))
     return Y
 
 
@@ -405,18 +453,24 @@ def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 
     queries only.  Q and K may be views of a packed projection.  Returns (Qo, Ko); outputs given
     by the caller are written in place and may be Q and K."""
     M, Hq, D = Q.shape
+    dt = Q.dtype
     Hk = 0 if K is None else K.shape[1]
     with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, Qo, Ko):
         if Qo is None:
-            Qo = _empty((M, Hq, D), Q.dtype, Q.device, stream)
-        if Ko is None and K is not None:
-            Ko = _empty((M, Hk, D), Q.dtype, Q.device, stream)
-        for name, t, shape in (("K", K, (M, Hk, D)), ("qw", qw, (D,)), ("kw", kw, (D,)), ("Qo", Qo, (M, Hq, D)),
-                               ("Ko", Ko, (M, Hk, D))):
-            _expect(name, t, shape, Q.dtype)
-        _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _ptr(qw), _ptr(kw), eps,
+            Qo = _new(stream, Q, (M, Hq, D), dt)
+        else:
+            _expect("Qo", Qo, (M, Hq, D), dt)
+        if K is not None:
+            _expect("K", K, (M, Hk, D), dt)
+            if Ko is None:
+                Ko = _new(stream, Q, (M, Hk, D), dt)
+            else:
+                _expect("Ko", Ko, (M, Hk, D), dt)
+        _expect("qw", qw, (D,), dt)
+        _expect("kw", kw, (D,), dt)
+        _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _flat(qw), _flat(kw), eps,
                                     *_rope_args(pos, axis_dims, theta, pairs, M), *_heads(Qo), *_heads(Ko),
-                                    _stream(stream)))
+                                    _queue(stream, Q)))
     return Qo, Ko
 
 
@@ -431,28 +485,29 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
     outputs; dqw and dkw [D] are float32 sums over all tokens and heads.  Outputs given by the
     caller are written in place; dQ and dK may be dQo and dKo, or Q and K."""
     M, Hq, D = Q.shape
+    dt = Q.dtype
     Hk = 0 if K is None else K.shape[1]
     with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, dQo, dKo, dQ, dK, dqw, dkw, workspace):
         if dQ is None:
-            dQ = _empty((M, Hq, D), Q.dtype, Q.device, stream)
+            dQ = _new(stream, Q, (M, Hq, D), dt)
         if dqw is None:
-            dqw = _empty((D,), torch.float32, Q.device, stream)
+            dqw = _new(stream, Q, (D,), torch.float32)
         if K is not None:
             if dK is None:
-                dK = _empty((M, Hk, D), Q.dtype, Q.device, stream)
+                dK = _new(stream, Q, (M, Hk, D), dt)
             if dkw is None:
-                dkw = _empty((D,), torch.float32, Q.device, stream)
+                dkw = _new(stream, Q, (D,), torch.float32)
         for name, t, shape in (("K", K, (M, Hk, D)), ("qw", qw, (D,)), ("kw", kw, (D,)), ("dQo", dQo, (M, Hq, D)),
                                ("dKo", dKo, (M, Hk, D)), ("dQ", dQ, (M, Hq, D)), ("dK", dK, (M, Hk, D))):
-            _expect(name, t, shape, Q.dtype)
+            _expect(name, t, shape, dt)
         _expect("dqw", dqw, (D,), torch.float32)
         _expect("dkw", dkw, (D,), torch.float32)
         if workspace is None:
-            workspace = _empty((max(rtl_qk_norm_rope_backward_workspace_bytes(D), 1),), torch.uint8, Q.device, stream)
-        _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _ptr(qw), _ptr(kw), eps,
+            workspace = _new(stream, Q, (max(rtl_qk_norm_rope_backward_workspace_bytes(D), 1),), torch.uint8)
+        _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _flat(qw), _flat(kw), eps,
                                              *_rope_args(pos, axis_dims, theta, pairs, M), *_heads(dQo), *_heads(dKo),
-                                             *_heads(dQ), *_heads(dK), _ptr(dqw), _ptr(dkw), _ptr(workspace),
-                                             workspace.numel() * workspace.element_size(), _stream(stream)))
+                                             *_heads(dQ), *_heads(dK), _flat(dqw), _flat(dkw), _flat(workspace),
+                                             workspace.numel() * workspace.element_size(), _queue(stream, Q)))
     return dQ, dK, dqw, dkw
 
 
@@ -462,14 +517,17 @@ def rtl_glu_fused(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: int 
     ``G`` and ``U`` [M,H], when given, receive the two products (rtl_glu_backward takes them)."""
     M, K = X.shape
     H = Wg.shape[0]
+    bf16 = torch.bfloat16
     with _one_device(X, Wg, Wu, Y, G, U):
         if Y is None:
-            Y = _empty((M, H), torch.bfloat16, X.device, stream)
-        for name, t, shape in (("X", X, (M, K)), ("Wg", Wg, (H, K)), ("Wu", Wu, (H, K)), ("Y", Y, (M, H)),
-                               ("G", G, (M, H)), ("U", U, (M, H))):
-            _expect(name, t, shape, torch.bfloat16)
-        _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(Y), _ptr(G), _ptr(U),
-                                 _stream(stream)))
+            Y = _new(stream, X, (M, H), bf16)
+        _expect("X", X, (M, K), bf16)
+        _expect("Wg", Wg, (H, K), bf16)
+        _expect("Wu", Wu, (H, K), bf16)
+        for name, t in (("Y", Y), ("G", G), ("U", U)):
+            _expect(name, t, (M, H), bf16)
+        _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _flat(X), _flat(Wg), _flat(Wu), _flat(Y), _flat(G), _flat(U),
+                                 _queue(stream, X)))
     return Y
 
 
@@ -485,24 +543,24 @@ def rtl_glu_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: tor
     caller are written in place; pass ``workspace`` (uint8) to keep the call free of allocations."""
     M, K = X.shape
     H = Wg.shape[0]
+    bf16 = torch.bfloat16
     with _one_device(X, Wg, Wu, G, U, dY, dX, dWg, dWu, workspace):
-        if need_dx and dX is None:
-            dX = _empty((M, K), torch.bfloat16, X.device, stream)
-        if need_dw and dWg is None:
-            dWg = _empty((H, K), torch.bfloat16, X.device, stream)
-        if need_dw and dWu is None:
-            dWu = _empty((H, K), torch.bfloat16, X.device, stream)
         if not need_dx:
             dX = None
+        elif dX is None:
+            dX = _new(stream, X, (M, K), bf16)
         if not need_dw:
             dWg = dWu = None
+        else:
+            dWg = _new(stream, X, (H, K), bf16) if dWg is None else dWg
+            dWu = _new(stream, X, (H, K), bf16) if dWu is None else dWu
         for name, t, shape in (("X", X, (M, K)), ("Wg", Wg, (H, K)), ("Wu", Wu, (H, K)), ("G", G, (M, H)),
                                ("U", U, (M, H)), ("dY", dY, (M, H)), ("dX", dX, (M, K)), ("dWg", dWg, (H, K)),
                                ("dWu", dWu, (H, K))):
-            _expect(name, t, shape, torch.bfloat16)
+            _expect(name, t, shape, bf16)
         if workspace is None:
-            workspace = _empty((max(rtl_glu_backward_workspace_bytes(M, K, H), 1),), torch.uint8, X.device, stream)
-        _check(lib.rtl_glu_backward(act, RTL_BF16, M, K, H, _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(G), _ptr(U), _ptr(dY),
-                                    _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+            workspace = _new(stream, X, (max(rtl_glu_backward_workspace_bytes(M, K, H), 1),), torch.uint8)
+        _check(lib.rtl_glu_backward(act, RTL_BF16, M, K, H, _flat(X), _flat(Wg), _flat(Wu), _flat(G), _flat(U),
+                                    _flat(dY), _flat(dX), _flat(dWg), _flat(dWu), _flat(workspace),
+                                    workspace.numel() * workspace.element_size(), _queue(stream, X)))
     return dX, dWg, dWu

@@ -41,16 +41,16 @@ struct RopeTensor {
 };
 
 struct RopeArgs {
-  int64_t M, items;        // items: (token, chunk of HC heads) pairs
   int H[2];                // heads of the two tensors (queries, keys); the second may be 0
-  int nq, nc;              // chunks of the first tensor, of both
+  uint32_t items, nq, nc;  // items: (token, chunk of HC heads) pairs; chunks of the first tensor, of both
+  uint32_t blocks[2];      // backward: workgroups on the first tensor, on the second
   int D, pairs, axes;
   float eps, sign;
   const float* pos;
   RopeTensor x[2], y[2];   // backward: y is dy, dx the output
   RopeTensor dx[2];
   const void* w[2];
-  float* part;             // backward: [workgroups][2][D]
+  float* part;             // backward: [workgroups][D]
 };
 
 // Eight values of a head as fp32: values 2i and 2i + 1 are pair 4 u + i of unit u.  Units at
@@ -108,15 +108,15 @@ struct RopeUnit {
         w[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
       uint16_t* p = (uint16_t*)base + at;
       if (HALVES) {
-        *reinterpret_cast<u32x2*>(p + lo) = u32x2{w[0], w[1]};
-        *reinterpret_cast<u32x2*>(p + hi) = u32x2{w[2], w[3]};
+        __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p + lo));
+        __builtin_nontemporal_store(u32x2{w[2], w[3]}, reinterpret_cast<u32x2*>(p + hi));
       } else {
-        *reinterpret_cast<u32x4*>(p + lo) = u32x4{w[0], w[1], w[2], w[3]};
+        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(p + lo));
       }
     } else {
       float* p = (float*)base + at;
-      *reinterpret_cast<f32x4*>(p + lo) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(p + hi) = f32x4{v[4], v[5], v[6], v[7]};
+      __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p + lo));
+      __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + hi));
     }
   }
   // Rotates the unit's four pairs: (2i, 2i + 1) in place, or (i, 4 + i).
@@ -131,7 +131,9 @@ struct RopeUnit {
   }
 };
 
-// cos and sin (times `sign`) of the unit's four angles; 1 and 0 past the rotated channels.
+// cos and sin (times `sign`) of the unit's four angles; 1 and 0 past the rotated channels.  By the
+// hardware's instructions, which take revolutions: within 2.2 * 2^-24 of the exact values at every
+// multiple of 2^-24 in [-1/2, 1/2] (measured), as near as the library's functions.
 __device__ __forceinline__ void rope_angles(const RopeArgs& a, const RopeTable& t, int64_t m, int u, float (&c)[4],
                                             float (&s)[4]) {
 #pragma unroll
@@ -145,16 +147,25 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& a, const RopeTable& 
     const int p = 4 * u + i;
     const double rev = (double)a.pos[m * a.axes + t.axis[p]] * t.f[p];
     const float r = (float)(rev - rint(rev));
-    sincospif(2.f * r, &s[i], &c[i]);
-    s[i] *= a.sign;
+    s[i] = a.sign * __builtin_amdgcn_sinf(r);
+    c[i] = __builtin_amdgcn_cosf(r);
   }
 }
 
-// Sum over the GL lanes of a group, the same in each of them.
+// v + v of the lane that the row pattern CTRL names (no LDS: the exchange is an operand of the sum).
+template <int CTRL>
+__device__ __forceinline__ float add_row(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+// Sum over the GL lanes of a group, the same in each of them: over lanes 1, 2, 4 and 8 apart (by
+// swaps in a quad, then mirrors, whose halves are uniform by then), 16 apart through a shuffle.
 template <int GL>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = GL / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  v = add_row<0xB1>(v);   // quad_perm 1,0,3,2
+  v = add_row<0x4E>(v);   // quad_perm 2,3,0,1
+  if (GL >= 8) v = add_row<0x141>(v);   // row_half_mirror
+  if (GL >= 16) v = add_row<0x140>(v);  // row_mirror
+  if (GL >= 32) v += __shfl_xor(v, 16, 64);
   return v;
 }
 
@@ -172,13 +183,13 @@ __device__ __forceinline__ void rope_weights(const RopeUnit<BF16, HALVES>& un, c
 template <bool BF16, bool HALVES, bool NORM, int GL, int HC>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, const RopeTable t) {
   const int u = threadIdx.x % GL;
-  const int64_t item = (int64_t)blockIdx.x * (kRopeThreads / GL) + threadIdx.x / GL;
+  const uint32_t item = blockIdx.x * (kRopeThreads / GL) + threadIdx.x / GL;
   const bool live = item < a.items && 8 * u < a.D;
   if (!NORM && !live) return;
-  const int64_t m = live ? item / a.nc : 0;
-  const int chunk = live ? (int)(item % a.nc) : 0;
+  const uint32_t token = live ? item / a.nc : 0, chunk = live ? item - token * a.nc : 0;
+  const int64_t m = token;
   const int which = chunk >= a.nq;
-  const int h0 = (which ? chunk - a.nq : chunk) * HC;
+  const int h0 = (int)(which ? chunk - a.nq : chunk) * HC;
   const int nh = live ? min(HC, a.H[which] - h0) : 0;
   const RopeUnit<BF16, HALVES> un(u, a.pairs);
   const RopeTensor x = a.x[which], y = a.y[which];
@@ -216,50 +227,56 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
   }
 }
 
-// Gradient of norm and rotation.  A fixed number of workgroups walks over the items; each
-// lane sums its channels' dw in fp32 over the items it meets, the workgroup adds its groups in
-// LDS, and qk_dw_kernel adds the workgroups: one order, the same result on every run.
+// Gradient of norm and rotation.  A fixed number of workgroups walks over the items, each on one
+// of the two tensors (shared out by their heads), the next item's loads in flight while one is
+// formed; each lane sums its channels' dw in fp32 over the items it meets, the workgroup adds its
+// groups in LDS, and qk_dw_kernel adds the workgroups: one order, the same result on every run.
 template <bool BF16, bool HALVES, int GL, int HC>
 __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a, const RopeTable t) {
   constexpr int NG = kRopeThreads / GL;
-  __shared__ float red[2][NG * GL * 8];
+  typedef RopeUnit<BF16, HALVES> Unit;
+  __shared__ float red[NG * GL * 8];
   const int u = threadIdx.x % GL, g = threadIdx.x / GL;
-  const RopeUnit<BF16, HALVES> un(u, a.pairs);
+  const Unit un(u, a.pairs);
   const bool lane = 8 * u < a.D;
-  float dw[2][8];
+  const int which = blockIdx.x >= a.blocks[0];
+  const uint32_t block = which ? blockIdx.x - a.blocks[0] : blockIdx.x;
+  const int H = a.H[which];
+  const uint32_t nc = (uint32_t)(H + HC - 1) / HC, items = a.items * nc, stride = a.blocks[which] * NG;  // a.items: tokens
+  const RopeTensor x = a.x[which], y = a.y[which], dx = a.dx[which];
+  float w[8], dw[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) dw[0][i] = dw[1][i] = 0.f;
-  for (int64_t first = (int64_t)blockIdx.x * NG; first < a.items; first += (int64_t)gridDim.x * NG) {
-    const int64_t item = first + g;
-    const bool live = item < a.items && lane;
-    const int64_t m = live ? item / a.nc : 0;
-    const int chunk = live ? (int)(item % a.nc) : 0;
-    const int which = chunk >= a.nq;
-    const int h0 = (which ? chunk - a.nq : chunk) * HC;
-    const int nh = live ? min(HC, a.H[which] - h0) : 0;
-    const RopeTensor x = a.x[which], y = a.y[which], dx = a.dx[which];
-    typename RopeUnit<BF16, HALVES>::Raw rx[HC], ry[HC];
+  for (int i = 0; i < 8; i++) w[i] = dw[i] = 0.f;
+  if (lane) rope_weights<BF16, HALVES>(un, a.w[which], w);
+
+  struct Item {
+    typename Unit::Raw x[HC], y[HC];
+    uint32_t m;
+    int h0, nh;
+  };
+  auto fetch = [&](uint32_t item, Item& it) {
+    const bool live = item < items && lane;
+    it.m = live ? item / nc : 0;
+    it.h0 = live ? (int)(item - it.m * nc) * HC : 0;
+    it.nh = live ? min(HC, H - it.h0) : 0;
 #pragma unroll
     for (int j = 0; j < HC; j++)
-      if (j < nh) {
-        rx[j] = un.load(x.p, m * x.row + (int64_t)(h0 + j) * x.head);
-        ry[j] = un.load(y.p, m * y.row + (int64_t)(h0 + j) * y.head);
+      if (j < it.nh) {
+        it.x[j] = un.load(x.p, (int64_t)it.m * x.row + (int64_t)(it.h0 + j) * x.head);
+        it.y[j] = un.load(y.p, (int64_t)it.m * y.row + (int64_t)(it.h0 + j) * y.head);
       }
-    float c[4], s[4], w[8], acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) w[i] = acc[i] = 0.f;
-    if (nh > 0) {
-      rope_angles(a, t, m, u, c, s);
-      rope_weights<BF16, HALVES>(un, a.w[which], w);
-    }
+  };
+  auto form = [&](const Item& it) {
+    float c[4], s[4];
+    if (it.nh > 0) rope_angles(a, t, it.m, u, c, s);
 #pragma unroll
     for (int j = 0; j < HC; j++) {
       float v[8], d[8];
 #pragma unroll
       for (int i = 0; i < 8; i++) v[i] = d[i] = 0.f;
-      if (j < nh) {
-        RopeUnit<BF16, HALVES>::unpack(rx[j], v);
-        RopeUnit<BF16, HALVES>::unpack(ry[j], d);
+      if (j < it.nh) {
+        Unit::unpack(it.x[j], v);
+        Unit::unpack(it.y[j], d);
         un.rotate(d, c, s);
       }
       float q = 0.f, p = 0.f;
@@ -274,42 +291,62 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const float n = v[i] * r;
-        acc[i] += d[i] * n;
+        dw[i] += d[i] * n;
         v[i] = r * (d[i] * w[i]) - n * k;
       }
-      if (j < nh) un.store(dx.p, m * dx.row + (int64_t)(h0 + j) * dx.head, v);
+      if (j < it.nh) un.store(dx.p, (int64_t)it.m * dx.row + (int64_t)(it.h0 + j) * dx.head, v);
     }
-#pragma unroll
-    for (int i = 0; i < 8; i++) dw[which][i] += acc[i];
+  };
+  Item one, two;
+  uint32_t item = block * NG + g;
+  const uint32_t rounds = (items + stride - 1) / stride;  // the same for every lane: the sums are exchanged
+  fetch(item, one);
+  for (uint32_t r = 0; r < rounds; r += 2) {
+    fetch(item + stride, two);
+    form(one);
+    if (r + 1 == rounds) break;
+    fetch(item + 2 * stride, one);
+    form(two);
+    item += 2 * stride;
   }
 #pragma unroll
-  for (int k = 0; k < 2; k++)
-#pragma unroll
-    for (int i = 0; i < 8; i++) red[k][(g * GL + u) * 8 + i] = dw[k][i];
+  for (int i = 0; i < 8; i++) red[(g * GL + u) * 8 + i] = dw[i];
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * GL * 8; e += kRopeThreads) {
-    const int k = e / (GL * 8), at = e % (GL * 8);
+  for (int at = threadIdx.x; at < a.D; at += kRopeThreads) {
     float sum = 0.f;
-    for (int j = 0; j < NG; j++) sum += red[k][j * GL * 8 + at];
-    const RopeUnit<BF16, HALVES> ue(at / 8, a.pairs);
-    const int i = at % 8, ch = i < 4 ? ue.lo + i : ue.hi + i - 4;
-    if (at < a.D) a.part[((int64_t)blockIdx.x * 2 + k) * a.D + ch] = sum;
+    for (int j = 0; j < NG; j++) sum += red[j * GL * 8 + at];
+    const Unit ue(at / 8, a.pairs);
+    a.part[(int64_t)blockIdx.x * a.D + (at % 8 < 4 ? ue.lo + at % 8 : ue.hi + at % 8 - 4)] = sum;
   }
 }
 
-// dw[k][ch] = sum over workgroups of part[.][k][ch], in double precision.
-__global__ __launch_bounds__(256) void qk_dw_kernel(const float* part, int blocks, int D, float* dqw, float* dkw) {
-  __shared__ double red[256];
-  const int col = blockIdx.x * 16 + threadIdx.x % 16, lane = threadIdx.x / 16;
-  double sum = 0.0;
-  if (col < 2 * D)
-    for (int b = lane; b < blocks; b += 16) sum += (double)part[(int64_t)b * 2 * D + col];
-  red[threadIdx.x] = sum;
+// dw[k][ch] = sum over tensor k's workgroups of part[.][ch], in double precision: 16 columns a
+// workgroup, 64 bytes of a row to four lanes, 64 rows at a time.
+__global__ __launch_bounds__(256) void qk_dw_kernel(const float* part, int blocks_q, int blocks_k, int D, float* dqw,
+                                                    float* dkw) {
+  __shared__ double red[64][16];
+  const int c4 = (threadIdx.x & 3) * 4, lane = threadIdx.x >> 2, col0 = blockIdx.x * 16, k = blockIdx.y;
+  const float* rows = part + (k ? (int64_t)blocks_q * D : 0);
+  const int blocks = k ? blocks_k : blocks_q;
+  float* out = k ? dkw : dqw;
+  if (out == nullptr) return;
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+  if (col0 + c4 < D) {
+#pragma unroll 4
+    for (int b = lane; b < blocks; b += 64) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(rows + (int64_t)b * D + col0 + c4);
+#pragma unroll
+      for (int i = 0; i < 4; i++) sum[i] += (double)v[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) red[lane][c4 + i] = sum[i];
   __syncthreads();
-  if (lane == 0 && col < 2 * D) {
-    for (int j = 1; j < 16; j++) sum += red[j * 16 + threadIdx.x];
-    float* out = col < D ? dqw : dkw;
-    if (out != nullptr) out[col < D ? col : col - D] = (float)sum;
+  const int col = col0 + threadIdx.x;
+  if (threadIdx.x < 16 && col < D) {
+    double all = 0.0;
+    for (int j = 0; j < 64; j++) all += red[j][threadIdx.x];
+    out[col] = (float)all;
   }
 }
 
@@ -318,6 +355,9 @@ namespace {
 // Workgroups of the gradient kernel: enough to fill the chip, few enough that the sum over
 // them stays small against the pass itself.
 constexpr int64_t kQkBackBlocks = 1024;
+// Heads per group there (with the next item's in flight; measured at 32760 x 80 x 128: one 519 us,
+// two 458, four 573, whose registers leave two waves a SIMD).
+constexpr int kQkBackHeads = 2;
 
 int rope_heads(int64_t M, int64_t H, int gl) {
   // Heads per group: eight where the lanes still fill the chip (256 CUs of 2048), else fewer, so
@@ -329,12 +369,11 @@ int rope_heads(int64_t M, int64_t H, int gl) {
 
 void rope_fill(const RopeCall& c, int hc, RopeArgs& a, RopeTable& t) {
   a = RopeArgs{};
-  a.M = c.M;
   a.H[0] = (int)c.H[0];
   a.H[1] = (int)c.H[1];
-  a.nq = (a.H[0] + hc - 1) / hc;
-  a.nc = a.nq + (a.H[1] + hc - 1) / hc;
-  a.items = c.M * a.nc;
+  a.nq = (uint32_t)((c.H[0] + hc - 1) / hc);
+  a.nc = a.nq + (uint32_t)((c.H[1] + hc - 1) / hc);
+  a.items = (uint32_t)c.M * a.nc;
   a.D = (int)c.D;
   a.axes = c.axes;
   a.eps = c.eps;
@@ -373,14 +412,21 @@ void rope_launch(const RopeCall& c, hipStream_t stream) {
 }
 
 template <bool BF16, bool HALVES, int GL>
-void qk_back_launch(const RopeCall& c, float* part, int64_t blocks, hipStream_t stream) {
-  RopeArgs a;
+void qk_back_launch(const RopeCall& c, float* part, RopeArgs& a, hipStream_t stream) {
   RopeTable t;
-  const int hc = rope_heads(c.M, c.H[0] + c.H[1], GL) >= 4 ? 4 : 1;
+  const int hc = rope_heads(c.M, c.H[0] + c.H[1], GL) >= kQkBackHeads ? kQkBackHeads : 1;
   rope_fill(c, hc, a, t);
+  a.items = (uint32_t)c.M;  // tokens; the kernel counts its own tensor's chunks
   a.part = part;
-  const dim3 grid((unsigned)blocks), block(kRopeThreads);
-  if (hc == 4) hipLaunchKernelGGL((qk_back_kernel<BF16, HALVES, GL, 4>), grid, block, 0, stream, a, t);
+  // Workgroups: up to kQkBackBlocks, shared out by heads, no more than a tensor has items for.
+  const int64_t ng = kRopeThreads / GL;
+  for (int k = 0; k < 2; k++) {
+    const int64_t want = (c.M * ((c.H[k] + hc - 1) / hc) + ng - 1) / ng;
+    const int64_t share = std::max<int64_t>(1, kQkBackBlocks * c.H[k] / (c.H[0] + c.H[1]) - 1);
+    a.blocks[k] = (uint32_t)std::min(want, share);
+  }
+  const dim3 grid(a.blocks[0] + a.blocks[1]), block(kRopeThreads);
+  if (hc == kQkBackHeads) hipLaunchKernelGGL((qk_back_kernel<BF16, HALVES, GL, kQkBackHeads>), grid, block, 0, stream, a, t);
   else hipLaunchKernelGGL((qk_back_kernel<BF16, HALVES, GL, 1>), grid, block, 0, stream, a, t);
 }
 
@@ -394,16 +440,9 @@ void rope_lanes(int64_t D, F f) {
   else f(std::integral_constant<int, 32>());
 }
 
-int64_t qk_back_blocks(const RopeCall& c) {
-  int64_t gl = 4;
-  while (8 * gl < c.D) gl *= 2;
-  const int64_t groups = c.M * (c.H[0] + c.H[1]), per = kRopeThreads / gl;
-  return std::min(kQkBackBlocks, (groups + per - 1) / per);
-}
-
 }  // namespace
 
-size_t qk_back_workspace(int64_t D) { return (size_t)kQkBackBlocks * 2 * D * 4; }
+size_t qk_back_workspace(int64_t D) { return (size_t)kQkBackBlocks * D * 4; }
 
 hipError_t launch_rope(const RopeCall& c, hipStream_t stream) {
   const bool norm = c.norm, halves = c.halves, bf16 = c.dt == kDtBF16;
@@ -423,20 +462,20 @@ hipError_t launch_rope(const RopeCall& c, hipStream_t stream) {
 }
 
 hipError_t launch_qk_back(const RopeCall& c, float* dqw, float* dkw, void* ws, hipStream_t stream) {
-  const int64_t blocks = qk_back_blocks(c);
+  RopeArgs a{};
   float* part = (float*)ws;
   const bool halves = c.halves, bf16 = c.dt == kDtBF16;
   rope_lanes(c.D, [&](auto gl) {
     constexpr int GL = decltype(gl)::value;
-    if (bf16 && halves) qk_back_launch<true, true, GL>(c, part, blocks, stream);
-    else if (bf16) qk_back_launch<true, false, GL>(c, part, blocks, stream);
-    else if (halves) qk_back_launch<false, true, GL>(c, part, blocks, stream);
-    else qk_back_launch<false, false, GL>(c, part, blocks, stream);
+    if (bf16 && halves) qk_back_launch<true, true, GL>(c, part, a, stream);
+    else if (bf16) qk_back_launch<true, false, GL>(c, part, a, stream);
+    else if (halves) qk_back_launch<false, true, GL>(c, part, a, stream);
+    else qk_back_launch<false, false, GL>(c, part, a, stream);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (dqw == nullptr && dkw == nullptr)) return e;
-  hipLaunchKernelGGL(qk_dw_kernel, dim3((unsigned)((2 * c.D + 15) / 16)), dim3(256), 0, stream, part, (int)blocks,
-                     (int)c.D, dqw, dkw);
+  hipLaunchKernelGGL(qk_dw_kernel, dim3((unsigned)((c.D + 15) / 16), 2), dim3(256), 0, stream, part, (int)a.blocks[0],
+                     (int)a.blocks[1], (int)c.D, dqw, dkw);
   return hipGetLastError();
 }
 
