@@ -337,35 +337,39 @@ __device__ __forceinline__ void store_rows(const f32x4 (&acc)[NB], uint8_t* blk,
   }
 }
 
-// The two products of the gradient.  Their tiles are dealt out in whole rounds (256 x 256 tiles,
-// one to a CU, or 128 x 128, two); the tiles of a last round that would leave CUs idle are split
-// along k, `splits` workgroups to a tile, whose fp32 sums go to `part` in accumulator order and are
-// added in split order by glu_join_kernel.
+// The gradient's two products, dX = P [Wg; Wu] (0) and [dWg; dWu] = P^T X (1), run as one launch,
+// the one with the longer jobs first, so that the other's tiles fill the CUs that its last round
+// would leave idle.  A job is a tile over all of k, or, where a product has few tiles, a part of a
+// tile's k: the parts' fp32 sums go to `part` in accumulator order and are added in split order by
+// glu_join_kernel.
+struct GluJobs {
+  int tiles_m, tiles_n, splits;
+  int steps, per;  // K steps of a tile, of a part
+  int count;       // workgroups, tiles * splits; 0 if the product is not wanted
+  float* part;     // [splits][tiles][T * T]
+};
 struct GluBackArgs {
   int64_t M, K, H, Hp;
   const uint16_t *P, *X, *Wg, *Wu;
   uint16_t *dX, *dWg, *dWu;
-  float* part;             // [splits][tail][T * T]
-  int tiles_m, tiles_n;
-  int full, tail, splits;  // whole tiles, then split ones
-  int per;                 // K steps per split
+  GluJobs jobs[2];
+  int join[2];           // tiles of each that are split
+  int first, second_at;  // the product that goes first; workgroup from which the second runs (a multiple of 8)
 };
 
-// What workgroup `w` does: a tile, its K steps, and its part (-1: the whole tile).
+// What workgroup i of a product does: a tile, its K steps, and its part (-1: the whole tile).
 struct GluJob {
   int tm, tn, first, steps, part;
 };
-__device__ __forceinline__ GluJob glu_job(const GluBackArgs& a, int w, int all) {
-  // Workgroups go round the XCDs (`full` is a multiple of 8 where there is a tail): each XCD gets
-  // a contiguous run of the tiles, and of the parts, split by split.
-  const bool whole = w < a.full;
-  const int i = whole ? w : w - a.full, n = whole ? a.full : a.tail * a.splits;
-  const int at = (i & 7) * (n >> 3) + min(i & 7, n & 7) + (i >> 3);
+__device__ __forceinline__ GluJob glu_job(const GluJobs& g, int w) {
+  // Workgroups go round the XCDs: each gets a contiguous run of the jobs, split by split.
+  const int n = g.count, tiles = g.tiles_m * g.tiles_n;
+  const int at = (w & 7) * (n >> 3) + min(w & 7, n & 7) + (w >> 3);
   GluJob j;
-  j.part = whole ? -1 : at;
-  j.first = whole ? 0 : at / a.tail * a.per;
-  j.steps = whole ? all : min(a.per, all - j.first);
-  tile_from_index(whole ? at : a.full + at % a.tail, a.tiles_m, a.tiles_n, j.tm, j.tn);
+  j.part = g.splits > 1 ? at : -1;
+  j.first = at / tiles * g.per;
+  j.steps = min(g.per, g.steps - j.first);
+  tile_from_index(at % tiles, g.tiles_m, g.tiles_n, j.tm, j.tn);
   return j;
 }
 
@@ -382,7 +386,7 @@ template <int R, bool DW>
 __device__ __forceinline__ void glu_finish(const GluBackArgs& a, const GluJob& j, f32x4 (&acc)[R][R], uint8_t* lds,
                                            int wave, int lane) {
   __syncthreads();  // the ring is free
-  f32x4* part = reinterpret_cast<f32x4*>(a.part) + ((int64_t)j.part * kRingWaves + wave) * (R * R * 64) + lane;
+  f32x4* part = reinterpret_cast<f32x4*>(a.jobs[DW].part) + ((int64_t)j.part * kRingWaves + wave) * (R * R * 64) + lane;
   const int64_t row0 = (int64_t)j.tm * (32 * R) + 16 * R * (wave & 1), col0 = (int64_t)j.tn * (32 * R) + 16 * R * (wave >> 1);
 #pragma unroll
   for (int rb = 0; rb < R; rb++) {
@@ -399,40 +403,15 @@ __device__ __forceinline__ void glu_finish(const GluBackArgs& a, const GluJob& j
   }
 }
 
-// One wave per 16-row strip of a split tile's wave: the parts' sum in split order, stored.
-template <int R, bool DW>
-__global__ __launch_bounds__(64) void glu_join_kernel(const GluBackArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[16 * (32 * R + 16)];
-  const int lane = threadIdx.x, rb = blockIdx.x % R, wave = blockIdx.x / R % kRingWaves, i = blockIdx.x / R / kRingWaves;
-  int tm, tn;
-  tile_from_index(a.full + i, a.tiles_m, a.tiles_n, tm, tn);
-  f32x4 acc[R];
-  for (int s = 0; s < a.splits; s++) {
-    const f32x4* in = reinterpret_cast<const f32x4*>(a.part) +
-                      (((int64_t)s * a.tail + i) * kRingWaves + wave) * (R * R * 64) + rb * R * 64 + lane;
-#pragma unroll
-    for (int nb = 0; nb < R; nb++) acc[nb] = s == 0 ? in[nb * 64] : acc[nb] + in[nb * 64];
-  }
-  const int64_t row0 = (int64_t)tm * (32 * R) + 16 * (R * (wave & 1) + rb), col0 = (int64_t)tn * (32 * R) + 16 * R * (wave >> 1);
-  store_rows<R>(acc, lds, lane, a.K - col0, [&](int r) {
-    uint16_t* y = glu_row<DW>(a, row0 + r);
-    return y == nullptr ? y : y + col0;
-  });
-}
-
 // dX = P [Wg; Wu]: k runs over P's 2 Hp columns, along P's rows and down the weights' columns.
 template <int R>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(R == 8 ? 1 : 2, R == 8 ? 1 : 2)))
-void glu_dx_kernel(const GluBackArgs a) {
+__device__ __forceinline__ void glu_dx_tile(const GluBackArgs& a, int w, uint8_t* lds, int wave, int lane) {
   constexpr int T = 32 * R;
   typedef KRows<T> OpA;
   typedef KCols<T> OpB;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * OpA::kBytes];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const GluJob j = glu_job(a.jobs[0], w);
   const int64_t M = a.M, K = a.K, H = a.H, ld = 2 * a.Hp;
   const int half = (int)(a.Hp / kRK);
-  const GluJob j = glu_job(a, blockIdx.x, 2 * half);
   const int64_t m0 = (int64_t)j.tm * T, c0 = (int64_t)j.tn * T;
   const uint16_t* P = a.P + m0 * ld;
   const OpA oa(ld, 1, wave, lane);
@@ -453,15 +432,11 @@ void glu_dx_kernel(const GluBackArgs a) {
 
 // [dWg; dWu] = P^T X: k runs over the tokens, down the columns of both.
 template <int R>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(R == 8 ? 1 : 2, R == 8 ? 1 : 2)))
-void glu_dw_kernel(const GluBackArgs a) {
+__device__ __forceinline__ void glu_dw_tile(const GluBackArgs& a, int w, uint8_t* lds, int wave, int lane) {
   constexpr int T = 32 * R;
   typedef KCols<T> Op;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * Op::kBytes];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const GluJob j = glu_job(a.jobs[1], w);
   const int64_t M = a.M, K = a.K, ld = 2 * a.Hp;
-  const GluJob j = glu_job(a, blockIdx.x, (int)((M + kRK - 1) / kRK));
   const int64_t r0 = (int64_t)j.tm * T, c0 = (int64_t)j.tn * T;
   const Op oa(ld, wave, lane), ob(K, wave, lane);
   // tokens past M lie outside the buffers and read as zeros
@@ -478,87 +453,153 @@ void glu_dw_kernel(const GluBackArgs a) {
   glu_finish<R, true>(a, j, acc, lds, wave, lane);
 }
 
+template <int R>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(R == 8 ? 1 : 2, R == 8 ? 1 : 2)))
+void glu_grad_kernel(const GluBackArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * KCols<32 * R>::kBytes];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool second = (int)blockIdx.x >= a.second_at;
+  const int which = second ? 1 - a.first : a.first, w = second ? blockIdx.x - a.second_at : blockIdx.x;
+  if (w >= a.jobs[which].count) return;  // between the products, up to the multiple of 8
+  if (which == 0) glu_dx_tile<R>(a, w, lds, wave, lane);
+  else glu_dw_tile<R>(a, w, lds, wave, lane);
+}
+
+// One wave per 16-row strip of a split tile's wave: the parts' sum in split order, stored.
+template <int R, bool DW>
+__device__ __forceinline__ void glu_join(const GluBackArgs& a, int at, uint8_t* lds, int lane) {
+  const GluJobs& g = a.jobs[DW];
+  const int rb = at % R, wave = at / R % kRingWaves, i = at / R / kRingWaves;
+  const int tiles = g.tiles_m * g.tiles_n;
+  int tm, tn;
+  tile_from_index(i, g.tiles_m, g.tiles_n, tm, tn);
+  f32x4 acc[R];
+  for (int s = 0; s < g.splits; s++) {
+    const f32x4* in = reinterpret_cast<const f32x4*>(g.part) +
+                      (((int64_t)s * tiles + i) * kRingWaves + wave) * (R * R * 64) + rb * R * 64 + lane;
+#pragma unroll
+    for (int nb = 0; nb < R; nb++) acc[nb] = s == 0 ? in[nb * 64] : acc[nb] + in[nb * 64];
+  }
+  const int64_t row0 = (int64_t)tm * (32 * R) + 16 * (R * (wave & 1) + rb), col0 = (int64_t)tn * (32 * R) + 16 * R * (wave >> 1);
+  store_rows<R>(acc, lds, lane, a.K - col0, [&](int r) {
+    uint16_t* y = glu_row<DW>(a, row0 + r);
+    return y == nullptr ? y : y + col0;
+  });
+}
+template <int R>
+__global__ __launch_bounds__(64) void glu_join_kernel(const GluBackArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[16 * (32 * R + 16)];
+  const int dx = a.join[0] * kRingWaves * R;
+  if ((int)blockIdx.x < dx) glu_join<R, false>(a, blockIdx.x, lds, threadIdx.x);
+  else glu_join<R, true>(a, blockIdx.x - dx, lds, threadIdx.x);
+}
+
 namespace {
 inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// How a product of `rows` x `cols` outputs over `steps` K steps is dealt out.
+// Costs in microseconds, fitted to measured calls: P workgroups run at once; each takes `step` per
+// K step and `tile` for its first loads and its stores, a part `way` through memory and back.
+struct GluCost {
+  int64_t P;
+  double step, tile, way;
+};
+constexpr GluCost kGluCost[2] = {{512, 1.02, 3.5, 0.026}, {256, 1.55, 12., 0.1}};  // R = 4, R = 8
+
 struct GluPlan {
-  int R, tiles_m, tiles_n, full, tail, splits, per;
+  int R;
+  GluJobs jobs[2];
   double cost;
-  size_t part_bytes() const { return (size_t)splits * tail * (32 * R) * (32 * R) * 4; }
+  size_t part_bytes(int k) const { return jobs[k].splits > 1 ? (size_t)jobs[k].count * (32 * R) * (32 * R) * 4 : 0; }
 };
-// With tiles of 32 R: rounds of 256 (R = 8) or 512 workgroups, a last round of at most half of
-// them split as many ways as fill it, where that saves more than the parts' way through memory.
-// Costs in microseconds, as measured: a K step takes a round 1.45 (R = 8) or 1.29, a tile's first
-// loads and stores 10.5 or 4.5, a part's way out and back 0.1 or 0.026; a last round of small tiles
-// that leaves each CU one takes 0.6 of a round.
-GluPlan glu_plan_for(int R, int64_t rows, int64_t cols, int64_t steps) {
-  const bool big = R == 8;
-  const int64_t T = 32 * R, P = big ? 256 : 512;
-  const double step = big ? 1.45 : 1.29, tile = big ? 10.5 : 4.5, way = big ? 0.1 : 0.026;
-  const int64_t tm = (rows + T - 1) / T, tn = (cols + T - 1) / T, tiles = tm * tn, rest = tiles % P;
-  const double whole = steps * step + tile, last = rest == 0 ? 0. : !big && rest <= 256 ? 0.6 : 1.;
-  GluPlan p{R, (int)tm, (int)tn, (int)tiles, 0, 1, (int)steps, (double)(tiles / P) * whole + last * whole};
-  for (int64_t s = rest == 0 ? 0 : std::min(P / rest, steps / 4); s >= 2; s /= 2) {
-    const int64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
-    const double cost = (double)(tiles / P) * whole + per * step + tile + way * splits * rest;
-    if (cost < p.cost)
-      p = GluPlan{R, (int)tm, (int)tn, (int)(tiles - rest), (int)rest, (int)splits, (int)per, cost};
+
+// The jobs of one product of `rows` x `cols` outputs: its tiles, each in `splits` parts.
+GluJobs glu_jobs(int R, int64_t rows, int64_t cols, int64_t steps, int64_t splits) {
+  const int64_t T = 32 * R, tm = (rows + T - 1) / T, tn = (cols + T - 1) / T;
+  const int64_t per = (steps + splits - 1) / splits;
+  GluJobs g{};
+  g.tiles_m = (int)tm;
+  g.tiles_n = (int)tn;
+  g.splits = (int)((steps + per - 1) / per);
+  g.steps = (int)steps;
+  g.per = (int)per;
+  g.count = (int)(tm * tn) * g.splits;
+  return g;
+}
+
+// When n1 jobs of length l1, then n2 of length l2 <= l1 are done on P workgroups: the first leave r1
+// of them one l1 behind the others, which meanwhile take late = ceil(l1 / l2) of the second each.
+double glu_makespan(int64_t P, int64_t n1, double l1, int64_t n2, double l2) {
+  const int64_t q1 = n1 / P, r1 = n1 % P, late = r1 > 0 ? (int64_t)std::ceil(l1 / l2) : 0;
+  int64_t i = (n2 + r1 * late + P - 1) / P;
+  if (i < late) i = (n2 + P - r1 - 1) / (P - r1);
+  return std::max(q1 * l1 + i * l2, (r1 > 0 ? q1 + 1 : q1) * l1);
+}
+
+// Tile size and splits with the least makespan.  (The plan does not depend on whether both products
+// are wanted: each has the same bits with the other and without.)
+GluPlan glu_plan(int64_t M, int64_t K, int64_t H) {
+  const int64_t rows[2] = {M, 2 * pad64(H)}, steps[2] = {2 * pad64(H) / kRK, (M + kRK - 1) / kRK};
+  GluPlan best{};
+  for (int R : {8, 4}) {
+    const GluCost& c = kGluCost[R == 8];
+    GluJobs options[2][6];
+    int n[2] = {0, 0};
+    for (int k = 0; k < 2; k++)
+      for (int64_t s : {1, 2, 3, 5, 8, 16}) {
+        const GluJobs g = glu_jobs(R, rows[k], K, steps[k], s);
+        if (s > 1 && (s > steps[k] / 4 || g.count > 2 * c.P)) break;
+        options[k][n[k]++] = g;
+      }
+    for (int x = 0; x < n[0]; x++)
+      for (int w = 0; w < n[1]; w++) {
+        const GluJobs &dx = options[0][x], &dw = options[1][w];
+        const bool dx_first = dx.per >= dw.per;
+        const GluJobs &one = dx_first ? dx : dw, &two = dx_first ? dw : dx;
+        const double cost = glu_makespan(c.P, one.count, one.per * c.step + c.tile, two.count, two.per * c.step + c.tile) +
+                            c.way * ((dx.splits > 1 ? dx.count : 0) + (dw.splits > 1 ? dw.count : 0));
+        if (best.R == 0 || cost < best.cost) best = GluPlan{R, {dx, dw}, cost};
+      }
   }
-  return p;
-}
-GluPlan glu_plan(int64_t rows, int64_t cols, int64_t steps) {
-  const GluPlan a = glu_plan_for(8, rows, cols, steps), b = glu_plan_for(4, rows, cols, steps);
-  return a.cost <= b.cost ? a : b;
-}
-GluPlan glu_dx_plan(int64_t M, int64_t K, int64_t H) { return glu_plan(M, K, 2 * pad64(H) / kRK); }
-GluPlan glu_dw_plan(int64_t M, int64_t K, int64_t H) { return glu_plan(2 * pad64(H), K, (M + kRK - 1) / kRK); }
-
-// Workspace: P [M, 2 Hp] bf16 | parts of the product that runs (dX's, then dW's).
-struct GluBackLayout {
-  size_t p, part, total;
-};
-GluBackLayout glu_back_layout(int64_t M, int64_t K, int64_t H) {
-  GluBackLayout L;
-  L.p = 0;
-  L.part = align256((size_t)(M * 2 * pad64(H) * 2));
-  L.total = L.part + align256(std::max(glu_dx_plan(M, K, H).part_bytes(), glu_dw_plan(M, K, H).part_bytes()));
-  return L;
+  return best;
 }
 
-template <int R, bool DW>
-void glu_product(const GluBackArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.full + a.tail * a.splits));
-  if (DW) hipLaunchKernelGGL((glu_dw_kernel<R>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((glu_dx_kernel<R>), grid, dim3(256), 0, stream, a);
-  if (a.tail > 0)
-    hipLaunchKernelGGL((glu_join_kernel<R, DW>), dim3((unsigned)(a.tail * kRingWaves * R)), dim3(64), 0, stream, a);
-}
-template <bool DW>
-void glu_product(GluBackArgs a, const GluPlan& p, hipStream_t stream) {
-  a.tiles_m = p.tiles_m;
-  a.tiles_n = p.tiles_n;
-  a.full = p.full;
-  a.tail = p.tail;
-  a.splits = p.splits;
-  a.per = p.per;
-  if (p.R == 8) glu_product<8, DW>(a, stream);
-  else glu_product<4, DW>(a, stream);
+template <int R>
+void glu_products(const GluBackArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.second_at + a.jobs[1 - a.first].count));
+  hipLaunchKernelGGL((glu_grad_kernel<R>), grid, dim3(256), 0, stream, a);
+  const int split = a.join[0] + a.join[1];
+  if (split > 0)
+    hipLaunchKernelGGL((glu_join_kernel<R>), dim3((unsigned)(split * kRingWaves * R)), dim3(64), 0, stream, a);
 }
 }  // namespace
 
-size_t glu_back_workspace(int64_t M, int64_t K, int64_t H) { return glu_back_layout(M, K, H).total; }
+// Workspace: P [M, 2 Hp] bf16 | parts of dX | parts of [dWg; dWu].
+size_t glu_back_workspace(int64_t M, int64_t K, int64_t H) {
+  const GluPlan p = glu_plan(M, K, H);
+  return align256((size_t)(M * 2 * pad64(H) * 2)) + align256(p.part_bytes(0)) + align256(p.part_bytes(1));
+}
 
 hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
                                 const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
                                 void* dWu, void* ws, hipStream_t stream) {
-  const GluBackLayout L = glu_back_layout(M, K, H);
+  const GluPlan p = glu_plan(M, K, H);
   GluBackArgs a{};
   a.M = M; a.K = K; a.H = H; a.Hp = pad64(H);
-  uint16_t* P = (uint16_t*)((uint8_t*)ws + L.p);
+  uint16_t* P = (uint16_t*)ws;
   a.P = P; a.X = (const uint16_t*)X; a.Wg = (const uint16_t*)Wg; a.Wu = (const uint16_t*)Wu;
   a.dX = (uint16_t*)dX; a.dWg = (uint16_t*)dWg; a.dWu = (uint16_t*)dWu;
-  a.part = (float*)((uint8_t*)ws + L.part);
+  uint8_t* parts = (uint8_t*)ws + align256((size_t)(M * 2 * a.Hp * 2));
+  const bool want[2] = {dX != nullptr, dWg != nullptr};
+  for (int k = 0; k < 2; k++) {
+    a.jobs[k] = p.jobs[k];
+    if (!want[k]) a.jobs[k].count = 0;
+    a.join[k] = want[k] && p.jobs[k].splits > 1 ? p.jobs[k].tiles_m * p.jobs[k].tiles_n : 0;
+  }
+  a.jobs[0].part = (float*)parts;
+  a.jobs[1].part = (float*)(parts + align256(p.part_bytes(0)));
+  a.first = p.jobs[1].per > p.jobs[0].per ? 1 : 0;
+  a.second_at = (a.jobs[a.first].count + 7) / 8 * 8;
   const dim3 block(256), chunks((unsigned)((M * (a.Hp / 8) + 255) / 256));
   if (act == kActSilu)
     hipLaunchKernelGGL((glu_back_kernel<kActSilu>), chunks, block, 0, stream, M, H, a.Hp, (const uint16_t*)G,
@@ -566,8 +607,8 @@ hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const 
   else
     hipLaunchKernelGGL((glu_back_kernel<kActGelu>), chunks, block, 0, stream, M, H, a.Hp, (const uint16_t*)G,
                        (const uint16_t*)U, (const uint16_t*)dY, P);
-  if (dX != nullptr) glu_product<false>(a, glu_dx_plan(M, K, H), stream);
-  if (dWg != nullptr) glu_product<true>(a, glu_dw_plan(M, K, H), stream);
+  if (p.R == 8) glu_products<8>(a, stream);
+  else glu_products<4>(a, stream);
   return hipGetLastError();
 }
 
