@@ -224,9 +224,9 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
     for (int j = 0; j < 4; j++) {
       const int64_t row = 16 * mb + 4 * q + j;
       if (row >= M || col >= H) continue;
-      a.Y[row * H + col] = (uint16_t)f32_to_bf16_bits(glu_act<ACT>(g[j]).v * u[j]);
-      if (a.G != nullptr) a.G[row * H + col] = (uint16_t)f32_to_bf16_bits(g[j]);
-      if (a.U != nullptr) a.U[row * H + col] = (uint16_t)f32_to_bf16_bits(u[j]);
+      a.Y[row * H + col] = __builtin_bit_cast(uint16_t, (__bf16)(glu_act<ACT>(g[j]).v * u[j]));
+      if (a.G != nullptr) a.G[row * H + col] = __builtin_bit_cast(uint16_t, (__bf16)g[j]);
+      if (a.U != nullptr) a.U[row * H + col] = __builtin_bit_cast(uint16_t, (__bf16)u[j]);
     }
   }
 }

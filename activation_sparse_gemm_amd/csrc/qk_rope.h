@@ -183,7 +183,7 @@ __device__ __forceinline__ void rope_weights(const RopeUnit<BF16, HALVES>& un, c
 template <bool BF16, bool HALVES, bool NORM, int GL, int HC>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, const RopeTable t) {
   const int u = threadIdx.x % GL;
-  const uint32_t item = blockIdx.x * (kRopeThreads / GL) + threadIdx.x / GL;
+  const uint32_t item = (blockIdx.y * gridDim.x + blockIdx.x) * (kRopeThreads / GL) + threadIdx.x / GL;
   const bool live = item < a.items && 8 * u < a.D;
   if (!NORM && !live) return;
   const uint32_t token = live ? item / a.nc : 0, chunk = live ? item - token * a.nc : 0;
@@ -404,7 +404,9 @@ void rope_launch(const RopeCall& c, hipStream_t stream) {
   RopeTable t;
   const int hc = rope_heads(c.M, c.H[0] + c.H[1], GL);
   rope_fill(c, hc, a, t);
-  const dim3 grid((unsigned)((a.items + kRopeThreads / GL - 1) / (kRopeThreads / GL))), block(kRopeThreads);
+  // rows of 2^20 workgroups: a launch takes fewer than 2^32 threads in one dimension
+  const uint32_t blocks = (a.items + kRopeThreads / GL - 1) / (kRopeThreads / GL), row = std::min(blocks, 1u << 20);
+  const dim3 grid(row, (blocks + row - 1) / row), block(kRopeThreads);
   if (hc == 8) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, GL, 8>), grid, block, 0, stream, a, t);
   else if (hc == 4) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, GL, 4>), grid, block, 0, stream, a, t);
   else if (hc == 2) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, GL, 2>), grid, block, 0, stream, a, t);

@@ -475,7 +475,7 @@ rtl_status check_rope(rtl_dtype dt, int64_t M, int64_t Hq, int64_t Hk, int64_t D
   }
   if (sum > D) return fail(RTL_ERR_SHAPE, "the axes turn %lld of %lld channels", (long long)sum, (long long)D);
   if (sum % 8 != 0) return fail(RTL_ERR_UNSUPPORTED, "the axes must turn a multiple of 8 channels (%lld)", (long long)sum);
-  if (!(theta > 0.0 && theta <= 1e300)) return fail(RTL_ERR_ARG, "theta must be finite and above 0 (got %g)", theta);
+  if (!(theta >= 1.0 && theta <= 1e30)) return fail(RTL_ERR_ARG, "theta must lie in [1, 1e30] (got %g)", theta);
   return RTL_OK;
 }
 

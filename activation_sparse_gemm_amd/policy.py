@@ -8,6 +8,9 @@ layers is too large for the rank-64 branch, so FLUX keeps the attention output p
 and MLP-down of its single-stream blocks dense and Z-Image keeps the attention output
 projection and MLP-up dense; every other layer uses the sparse layer.
 
+Beside the projections, what such a block runs on their outputs: the queries' and keys' head norms
+and rotary positions (AttentionInput) and the gated feed-forward block (GatedMLP).
+
 Reading taken where the page is silent: Qwen-Image's attention output projection, which the
 page does not list, stays dense; FLUX's double-stream blocks sparsify all four projections.
 """
@@ -15,9 +18,10 @@ from __future__ import annotations
 
 import torch
 
-from . import EPS, rtl_linear_dense_ref, rtl_linear_fused, rtl_linear_fused_workspace_bytes, _dt
+from . import (EPS, RTL_ACT_SILU, RTL_ROPE_ADJACENT, rtl_glu_fused, rtl_linear_dense_ref, rtl_linear_fused,
+               rtl_linear_fused_workspace_bytes, rtl_qk_norm_rope, _dt)
 
-__all__ = ["LAYER_KINDS", "MODELS", "dense_layers", "is_sparse", "Linear", "build_block"]
+__all__ = ["LAYER_KINDS", "MODELS", "dense_layers", "is_sparse", "Linear", "build_block", "AttentionInput", "GatedMLP"]
 
 LAYER_KINDS = ("attn.qkv", "attn.o_proj", "mlp.up", "mlp.down")
 
@@ -88,3 +92,42 @@ def build_block(model: str, stream: str, weights: dict) -> dict:
         sp = is_sparse(model, stream, kind)
         out[kind] = Linear(W, LA if sp else None, LB if sp else None, sparse=sp)
     return out
+
+
+class AttentionInput:
+    """Queries, keys and values of an attention layer from its tokens: the `qkv` projection (a
+    Linear with (heads + 2 kv_heads) * D outputs: queries, then keys, then values), then the RMS
+    norm of every query and key head (weights [D], None: ones) and the rotation by each token's
+    positions (rtl_rope_axes; no `axis_dims`: none), in one pass over the projection's output,
+    in place."""
+
+    def __init__(self, qkv: Linear, heads: int, kv_heads: int, q_weight=None, k_weight=None, axis_dims=(),
+                 theta: float = 10000.0, eps: float = 1e-6, pairs: int = RTL_ROPE_ADJACENT):
+        outputs = qkv.W.shape[0]
+        if heads < 1 or kv_heads < 1 or outputs % (heads + 2 * kv_heads) != 0:
+            raise ValueError(f"{outputs} outputs are not {heads} query heads and twice {kv_heads} key heads")
+        self.qkv, self.heads, self.kv_heads = qkv, heads, kv_heads
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.axis_dims, self.theta, self.eps, self.pairs = tuple(axis_dims), theta, eps, pairs
+
+    def __call__(self, X: torch.Tensor, pos=None, stream=None):
+        """(q [M, heads, D], k and v [M, kv_heads, D]), views of one buffer; `pos` [M, axes] float32."""
+        n = self.heads + 2 * self.kv_heads
+        rows = self.qkv(X, stream=stream).view(X.shape[0], n, -1)
+        q, k, v = rows.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
+        rtl_qk_norm_rope(q, k, self.q_weight, self.k_weight, pos, self.axis_dims, theta=self.theta, eps=self.eps,
+                         pairs=self.pairs, Qo=q, Ko=k, stream=stream)
+        return q, k, v
+
+
+class GatedMLP:
+    """A gated feed-forward block whose up projections are dense (Z-Image's policy for mlp.up):
+    rtl_glu_fused with weights Wg and Wu [H,K], then `down`, a Linear, sparse or dense."""
+
+    def __init__(self, Wg: torch.Tensor, Wu: torch.Tensor, down: Linear, act: int = RTL_ACT_SILU):
+        if Wg.shape != Wu.shape or down.W.shape[1] != Wg.shape[0]:
+            raise ValueError("Wg and Wu are [H,K] and the down projection's weights [N,H]")
+        self.Wg, self.Wu, self.down, self.act = Wg, Wu, down, act
+
+    def __call__(self, X: torch.Tensor, Y=None, stream=None) -> torch.Tensor:
+        return self.down(rtl_glu_fused(X, self.Wg, self.Wu, act=self.act, stream=stream), Y=Y, stream=stream)

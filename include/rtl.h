@@ -299,7 +299,7 @@ rtl_status rtl_linear_fused_fp8(int64_t M, int64_t N, int64_t K, int64_t R, cons
  *     x1 cos + x0 sin).
  * Angles are formed in double precision, all else in fp32, rounded once at the end.
  * dt is bf16 or fp32.  Limits: D % 8 == 0, D <= 256, n_axes <= 4, M * heads below 2^31; theta
- * finite and above 0.
+ * in [1, 1e30].
  */
 typedef enum { RTL_ROPE_RANGE_MIN_ = -0x7FFFFFFF - 1, RTL_ROPE_ADJACENT = 0, RTL_ROPE_HALVES = 1, RTL_ROPE_RANGE_MAX_ = 0x7FFFFFFF } rtl_rope_pairs;
 

@@ -189,3 +189,17 @@ def test_python_refuses_host_tensors_and_wrong_shapes():
                           torch.zeros(8, 64, dtype=torch.bfloat16))
     assert rtl.rtl_qk_norm_rope_backward_workspace_bytes(0) == 0
     assert rtl.rtl_glu_backward_workspace_bytes(0, 64, 64) == 0
+
+
+def test_policy_objects_check_their_weights():
+    from activation_sparse_gemm_amd import policy
+
+    W = torch.zeros(8 * 64, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        policy.AttentionInput(policy.Linear(W, sparse=False), heads=3, kv_heads=1)
+    with pytest.raises(ValueError):
+        policy.AttentionInput(policy.Linear(W, sparse=False), heads=0, kv_heads=4)
+    with pytest.raises(ValueError):
+        policy.GatedMLP(W, W, policy.Linear(W, sparse=False))
+    with pytest.raises(ValueError):
+        policy.GatedMLP(W, W[:64], policy.Linear(torch.zeros(64, 8 * 64, dtype=torch.bfloat16), sparse=False))
