@@ -73,22 +73,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
   return make_rsrc(p, live ? bytes : 0);
 }
 
-// The tiled product: 2 x 2 waves of RB x NB blocks, 32 RB rows and 32 NB weight rows (16 NB
-// outputs) a tile.  Of a wave column's 16 NB weight rows the first half are gate rows, the
+// The tiled product: WM x WN waves of RB x NB blocks, 16 RB WM rows and 16 NB WN weight rows (8 NB
+// WN outputs) a tile.  Of a wave column's 16 NB weight rows the first half are gate rows, the
 // second up; row 16 nb + r16 of either half is output column NB / 2 r16 + nb, so that lane r16
 // holds NB / 2 consecutive columns over its blocks.
-template <int ACT, int RB, int NB>
+template <int ACT, int RB, int NB, int WM, int WN, int DEPTH>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(RB == 8 ? 1 : 2, RB == 8 ? 1 : 2)))
 void glu_kernel(const GluArgs a) {
-  constexpr int BM = 32 * RB, BN = 32 * NB, NC = NB / 2;
+  static_assert(WM * WN == kRingWaves, "four waves");
+  constexpr int BM = 16 * RB * WM, BN = 16 * NB * WN, NC = NB / 2;
   typedef KRows<BM> OpA;
   typedef KRows<BN> OpB;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * OpA::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ring_slots(DEPTH) * OpA::kBytes];
   int tm, tn;
   tile_coords(a.tiles_m, a.tiles_n, tm, tn);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % WM, wn = wave / WM;
   const int q = lane >> 4, r16 = lane & 15;
   const int64_t M = a.M, K = a.K, H = a.H;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * (BN / 2);
@@ -113,7 +114,7 @@ void glu_kernel(const GluArgs a) {
     return Weights{ob, rsrc_if(kt >= 0, Wg, wb), rsrc_if(kt >= 0, Wu, wb), max(kt, 0) * (kRK * 2)};
   };
   f32x4 acc[RB][NB];
-  ring_product(acc, lds, oa, ob, at_a, at_b, steps, wm, wn);
+  ring_product<DEPTH>(acc, lds, oa, ob, at_a, at_b, steps, wm, wn);
 
   const int64_t col = n0 + 16 * NC * wn + NC * r16;
 #pragma unroll
@@ -193,7 +194,7 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
 #pragma unroll
         for (int mb = 0; mb < MB; mb++) x[mb][kk] = op.read(slot, 2 + mb, kk);
       }
-      __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt(0): the slot is free
+      wait_ring<63>();  // the reads: the slot is free
       asm volatile("" ::: "memory");
       load(s + (D + i) * kRingWaves, slot);
 #pragma unroll
@@ -233,12 +234,12 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
 
 namespace {
 
-// Tiles of 32 R rows by 16 R outputs.
-template <int ACT, int R>
+template <int ACT, int RB, int NB, int WM, int WN, int DEPTH>
 void glu_tiles(GluArgs a, hipStream_t stream) {
-  a.tiles_m = (int)((a.M + 32 * R - 1) / (32 * R));
-  a.tiles_n = (int)((a.H + 16 * R - 1) / (16 * R));
-  hipLaunchKernelGGL((glu_kernel<ACT, R, R>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
+  constexpr int BM = 16 * RB * WM, BH = 8 * NB * WN;
+  a.tiles_m = (int)((a.M + BM - 1) / BM);
+  a.tiles_n = (int)((a.H + BH - 1) / BH);
+  hipLaunchKernelGGL((glu_kernel<ACT, RB, NB, WM, WN, DEPTH>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
 }
 
 template <int ACT, int MB>
@@ -247,17 +248,23 @@ void glu_rows(const GluArgs& a, hipStream_t stream) {
                      a);
 }
 
-// Up to 32 rows, and up to 64 where 128 x 64 tiles would leave a third of the CUs without one,
-// stream the weights (64 x 2560 x 6912, 108 tiles: 21 us against 29; 64 x 5120 x 13824, 216 tiles:
-// 75 against 60).  Else 256 x 128 tiles where they occupy three quarters of the CUs, or 128 x 64.
+// By rows, then by the number of 128 x 64 tiles (microseconds at K = 2560 where none is given):
+//  - up to 32 rows, and up to 64 where such tiles would leave a third of the CUs without one: the
+//    weights streamed (64 x 6912, 108 tiles: 21 against 25; 64 x 13824, K = 5120, 216: 75 against 53);
+//  - at most half as many tiles as CUs: half as wide ones (100 x 6912: 20 against 25);
+//  - at most one to a CU: four steps ahead, since nothing else hides a load (200 x 6912: 27
+//    against 33; 100 x 10000, K = 5120: 41 against 53);
+//  - at most two to a CU, then 256 x 128 tiles (900 x 5000, 640 tiles: 60 against 65).
 template <int ACT>
 void glu_launch(const GluArgs& a, hipStream_t stream) {
-  const int64_t small = ((a.M + 127) / 128) * ((a.H + 63) / 64), big = ((a.M + 255) / 256) * ((a.H + 127) / 128);
+  const int64_t tiles = ((a.M + 127) / 128) * ((a.H + 63) / 64);
   if (a.M <= 16) glu_rows<ACT, 1>(a, stream);
   else if (a.M <= 32) glu_rows<ACT, 2>(a, stream);
-  else if (a.M <= 64 && small < 171) glu_rows<ACT, 4>(a, stream);
-  else if (big >= 192) glu_tiles<ACT, 8>(a, stream);
-  else glu_tiles<ACT, 4>(a, stream);
+  else if (a.M <= 64 && tiles < 171) glu_rows<ACT, 4>(a, stream);
+  else if (tiles <= 128) glu_tiles<ACT, 2, 4, 4, 1, 4>(a, stream);
+  else if (tiles <= 256) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
+  else if (tiles <= 512) glu_tiles<ACT, 4, 4, 2, 2, 2>(a, stream);
+  else glu_tiles<ACT, 8, 8, 2, 2, 2>(a, stream);
 }
 
 }  // namespace
@@ -278,9 +285,18 @@ hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void*
 // P [M, 2 Hp] = [dG | dU], each padded to Hp columns with zeros, rounded to bf16: the matrix
 // cores' operand.  (Formed inside the products instead, it would be formed again for every
 // tile that reads it, 2 H / 256 + K / 256 times.)  One 16-byte chunk of each half per thread.
+//
+// The rounding, 2^-8 of an element at most, adds to a gradient what the gradient's own rounding
+// to bf16 does, as long as many elements share the sum of squares; in a product of few of them
+// one large element's error shows in full.  Up to kGluFewElements of them (where the products
+// are held by the weights' bytes) what the rounding took is kept as well, rounded to bf16 in a
+// second P, and the products run over both: dG and dU then hold to 2^-16.
+// (Twice the products' steps: 1 x 5120 x 13824 takes 220 us instead of 170.)
+constexpr int64_t kGluFewElements = 1 << 14;
+inline int glu_passes(int64_t M, int64_t H) { return M * H <= kGluFewElements ? 2 : 1; }
 template <int ACT>
 __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int64_t Hp, const uint16_t* G,
-                                                       const uint16_t* U, const uint16_t* dY, uint16_t* P) {
+                                                       const uint16_t* U, const uint16_t* dY, uint16_t* P, int passes) {
   const int64_t c8 = Hp / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= M * c8) return;
   const int64_t m = id / c8, h = (id - m * c8) * 8, at = m * H + h;
@@ -299,16 +315,24 @@ __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int
       }
   }
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-  u32x4 dg, du;
+  u32x4 p[2][2];  // pass; dG, dU
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const ActValue a0 = glu_act<ACT>(bf16lo(g[i])), a1 = glu_act<ACT>(bf16hi(g[i]));
     const float d0 = bf16lo(d[i]), d1 = bf16hi(d[i]);
-    dg[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * bf16lo(u[i]) * a0.slope), (__bf16)(d1 * bf16hi(u[i]) * a1.slope)});
-    du[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(d0 * a0.v), (__bf16)(d1 * a1.v)});
+    const float v[2][2] = {{d0 * bf16lo(u[i]) * a0.slope, d1 * bf16hi(u[i]) * a1.slope}, {d0 * a0.v, d1 * a1.v}};
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const bf16x2_t hi = {(__bf16)v[k][0], (__bf16)v[k][1]};
+      p[0][k][i] = __builtin_bit_cast(uint32_t, hi);
+      p[1][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(v[k][0] - (float)hi[0]), (__bf16)(v[k][1] - (float)hi[1])});
+    }
   }
-  *reinterpret_cast<u32x4*>(P + m * 2 * Hp + h) = dg;
-  *reinterpret_cast<u32x4*>(P + m * 2 * Hp + Hp + h) = du;
+  for (int pass = 0; pass < passes; pass++) {
+    uint16_t* row = P + ((int64_t)pass * M + m) * 2 * Hp + h;
+    *reinterpret_cast<u32x4*>(row) = pass ? p[1][0] : p[0][0];
+    *reinterpret_cast<u32x4*>(row + Hp) = pass ? p[1][1] : p[0][1];
+  }
 }
 
 // A wave's row of NB blocks to 16 bf16 rows through its LDS block of 16 * (32 NB + 16) bytes, as
@@ -353,6 +377,7 @@ struct GluBackArgs {
   const uint16_t *P, *X, *Wg, *Wu;
   uint16_t *dX, *dWg, *dWu;
   GluJobs jobs[2];
+  int passes;            // step s is K step s / passes of P's s % passes
   int join[2];           // tiles of each that are split
   int first, second_at;  // the product that goes first; workgroup from which the second runs (a multiple of 8)
 };
@@ -414,19 +439,21 @@ __device__ __forceinline__ void glu_dx_tile(const GluBackArgs& a, int w, uint8_t
   const int half = (int)(a.Hp / kRK);
   const int64_t m0 = (int64_t)j.tm * T, c0 = (int64_t)j.tn * T;
   const uint16_t* P = a.P + m0 * ld;
+  const int two = a.passes - 1;
   const OpA oa(ld, 1, wave, lane);
   const OpB ob(K, wave, lane);
   auto at_a = [&](int kt) {
-    return typename OpA::Tile{oa, rsrc_if(kt >= 0, P, (M - m0) * ld * 2), (j.first + max(kt, 0)) * (kRK * 2)};
+    const int s = j.first + max(kt, 0);
+    return typename OpA::Tile{oa, rsrc_if(kt >= 0, P + (s & two) * M * ld, (M - m0) * ld * 2), (s >> two) * (kRK * 2)};
   };
   auto at_b = [&](int kt) {
     // rows of Wg, then of Wu; past H (P's padding) they read as zeros
-    const int s = j.first + max(kt, 0);
+    const int s = (j.first + max(kt, 0)) >> two;
     const int64_t h = (int64_t)(s < half ? s : s - half) * kRK;
     return typename OpB::Tile{ob, rsrc_if(kt >= 0, (s < half ? a.Wg : a.Wu) + h * K + c0, ((H - h) * K - c0) * 2)};
   };
   f32x4 acc[R][R];
-  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, wave & 1, wave >> 1);
+  ring_product<2>(acc, lds, oa, ob, at_a, at_b, j.steps, wave & 1, wave >> 1);
   glu_finish<R, false>(a, j, acc, lds, wave, lane);
 }
 
@@ -439,24 +466,26 @@ __device__ __forceinline__ void glu_dw_tile(const GluBackArgs& a, int w, uint8_t
   const int64_t M = a.M, K = a.K, ld = 2 * a.Hp;
   const int64_t r0 = (int64_t)j.tm * T, c0 = (int64_t)j.tn * T;
   const Op oa(ld, wave, lane), ob(K, wave, lane);
+  const int two = a.passes - 1;
   // tokens past M lie outside the buffers and read as zeros
   auto at_a = [&](int kt) {
-    const int64_t m = (int64_t)(j.first + max(kt, 0)) * kRK;
-    return typename Op::Tile{oa, rsrc_if(kt >= 0, a.P + m * ld + r0, ((M - m) * ld - r0) * 2)};
+    const int s = j.first + max(kt, 0);
+    const int64_t m = (int64_t)(s >> two) * kRK;
+    return typename Op::Tile{oa, rsrc_if(kt >= 0, a.P + ((s & two) * M + m) * ld + r0, ((M - m) * ld - r0) * 2)};
   };
   auto at_b = [&](int kt) {
-    const int64_t m = (int64_t)(j.first + max(kt, 0)) * kRK;
+    const int64_t m = (int64_t)((j.first + max(kt, 0)) >> two) * kRK;
     return typename Op::Tile{ob, rsrc_if(kt >= 0, a.X + m * K + c0, ((M - m) * K - c0) * 2)};
   };
   f32x4 acc[R][R];
-  ring_product(acc, lds, oa, ob, at_a, at_b, j.steps, wave & 1, wave >> 1);
+  ring_product<2>(acc, lds, oa, ob, at_a, at_b, j.steps, wave & 1, wave >> 1);
   glu_finish<R, true>(a, j, acc, lds, wave, lane);
 }
 
 template <int R>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(R == 8 ? 1 : 2, R == 8 ? 1 : 2)))
 void glu_grad_kernel(const GluBackArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * KCols<32 * R>::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ring_slots(2) * KCols<32 * R>::kBytes];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool second = (int)blockIdx.x >= a.second_at;
@@ -498,13 +527,16 @@ __global__ __launch_bounds__(64) void glu_join_kernel(const GluBackArgs a) {
 namespace {
 inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// Costs in microseconds, fitted to measured calls: P workgroups run at once; each takes `step` per
-// K step and `tile` for its first loads and its stores, a part `way` through memory and back.
-struct GluCost {
+// Ways to run the jobs, with costs in microseconds fitted to measured calls: tiles of 32 R, P
+// workgroups at once, each `step` per K step and `tile` for its first loads and its stores, a part
+// `way` through memory and back.  (Small tiles four steps ahead, one to a CU, as in the forward
+// product: 25% faster where one such round holds all jobs, up to 20% slower elsewhere; not kept.)
+struct GluWay {
+  int R;
   int64_t P;
   double step, tile, way;
 };
-constexpr GluCost kGluCost[2] = {{512, 1.02, 3.5, 0.026}, {256, 1.55, 12., 0.1}};  // R = 4, R = 8
+constexpr GluWay kGluWays[2] = {{8, 256, 1.55, 12., 0.1}, {4, 512, 1.02, 3.5, 0.026}};
 
 struct GluPlan {
   int R;
@@ -539,15 +571,15 @@ double glu_makespan(int64_t P, int64_t n1, double l1, int64_t n2, double l2) {
 // Tile size and splits with the least makespan.  (The plan does not depend on whether both products
 // are wanted: each has the same bits with the other and without.)
 GluPlan glu_plan(int64_t M, int64_t K, int64_t H) {
-  const int64_t rows[2] = {M, 2 * pad64(H)}, steps[2] = {2 * pad64(H) / kRK, (M + kRK - 1) / kRK};
+  const int64_t rows[2] = {M, 2 * pad64(H)}, passes = glu_passes(M, H);
+  const int64_t steps[2] = {passes * 2 * pad64(H) / kRK, passes * ((M + kRK - 1) / kRK)};
   GluPlan best{};
-  for (int R : {8, 4}) {
-    const GluCost& c = kGluCost[R == 8];
+  for (const GluWay& c : kGluWays) {
     GluJobs options[2][6];
     int n[2] = {0, 0};
     for (int k = 0; k < 2; k++)
       for (int64_t s : {1, 2, 3, 5, 8, 16}) {
-        const GluJobs g = glu_jobs(R, rows[k], K, steps[k], s);
+        const GluJobs g = glu_jobs(c.R, rows[k], K, steps[k], s);
         if (s > 1 && (s > steps[k] / 4 || g.count > 2 * c.P)) break;
         options[k][n[k]++] = g;
       }
@@ -558,7 +590,7 @@ GluPlan glu_plan(int64_t M, int64_t K, int64_t H) {
         const GluJobs &one = dx_first ? dx : dw, &two = dx_first ? dw : dx;
         const double cost = glu_makespan(c.P, one.count, one.per * c.step + c.tile, two.count, two.per * c.step + c.tile) +
                             c.way * ((dx.splits > 1 ? dx.count : 0) + (dw.splits > 1 ? dw.count : 0));
-        if (best.R == 0 || cost < best.cost) best = GluPlan{R, {dx, dw}, cost};
+        if (best.R == 0 || cost < best.cost) best = GluPlan{c.R, {dx, dw}, cost};
       }
   }
   return best;
@@ -574,10 +606,10 @@ void glu_products(const GluBackArgs& a, hipStream_t stream) {
 }
 }  // namespace
 
-// Workspace: P [M, 2 Hp] bf16 | parts of dX | parts of [dWg; dWu].
+// Workspace: P [passes, M, 2 Hp] bf16 | parts of dX | parts of [dWg; dWu].
 size_t glu_back_workspace(int64_t M, int64_t K, int64_t H) {
   const GluPlan p = glu_plan(M, K, H);
-  return align256((size_t)(M * 2 * pad64(H) * 2)) + align256(p.part_bytes(0)) + align256(p.part_bytes(1));
+  return align256((size_t)(glu_passes(M, H) * M * 2 * pad64(H) * 2)) + align256(p.part_bytes(0)) + align256(p.part_bytes(1));
 }
 
 hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
@@ -589,7 +621,8 @@ hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const 
   uint16_t* P = (uint16_t*)ws;
   a.P = P; a.X = (const uint16_t*)X; a.Wg = (const uint16_t*)Wg; a.Wu = (const uint16_t*)Wu;
   a.dX = (uint16_t*)dX; a.dWg = (uint16_t*)dWg; a.dWu = (uint16_t*)dWu;
-  uint8_t* parts = (uint8_t*)ws + align256((size_t)(M * 2 * a.Hp * 2));
+  a.passes = glu_passes(M, H);
+  uint8_t* parts = (uint8_t*)ws + align256((size_t)(a.passes * M * 2 * a.Hp * 2));
   const bool want[2] = {dX != nullptr, dWg != nullptr};
   for (int k = 0; k < 2; k++) {
     a.jobs[k] = p.jobs[k];
@@ -603,10 +636,10 @@ hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const 
   const dim3 block(256), chunks((unsigned)((M * (a.Hp / 8) + 255) / 256));
   if (act == kActSilu)
     hipLaunchKernelGGL((glu_back_kernel<kActSilu>), chunks, block, 0, stream, M, H, a.Hp, (const uint16_t*)G,
-                       (const uint16_t*)U, (const uint16_t*)dY, P);
+                       (const uint16_t*)U, (const uint16_t*)dY, P, a.passes);
   else
     hipLaunchKernelGGL((glu_back_kernel<kActGelu>), chunks, block, 0, stream, M, H, a.Hp, (const uint16_t*)G,
-                       (const uint16_t*)U, (const uint16_t*)dY, P);
+                       (const uint16_t*)U, (const uint16_t*)dY, P, a.passes);
   if (p.R == 8) glu_products<8>(a, stream);
   else glu_products<4>(a, stream);
   return hipGetLastError();

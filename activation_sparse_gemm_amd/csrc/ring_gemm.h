@@ -2,13 +2,14 @@
 // with either operand stored with k along its rows or along its columns (so that the
 // gradients' products need no transposed copies), on output tiles of four waves.
 //
-// K runs in steps of 64.  A step's A tile and its B tile are items of a ring of five LDS slots,
-// filled with 16-byte loads that go straight to LDS.  All through step s a wave reads the
-// fragments it needs next, B_s two blocks ahead and all of A_{s+1} into the other set of
-// registers, and issues the loads of A_{s+2} (into B_{s-1}'s slot) and B_{s+2} (into A_s's, read
-// in step s - 1).  Behind the next to last column block, when its last read of the step has
-// returned, it waits for its loads of A_{s+2} and B_{s+1} and meets the others at the step's one
-// barrier; the last block's products then cover the first reads of B_{s+1}.
+// K runs in steps of 64.  A step's A tile and its B tile are items of a ring of 2 d + 1 LDS slots
+// (d = 2, or 4 where a CU has one small tile only), filled with 16-byte loads that go straight to
+// LDS.  All through step s a wave reads the fragments it needs next, B_s two blocks ahead and all
+// of A_{s+1} into the other set of registers, and issues the loads of A_{s+d} (into B_{s-1}'s slot)
+// and B_{s+d} (into A_s's, read in step s - 1).  Behind the next to last column block, when its
+// last read of the step has returned, it waits for its loads of A_{s+2} and B_{s+1} and meets the
+// others at the step's one barrier; the last block's products then cover the first reads of
+// B_{s+1}.
 //
 // Bound: the vector-memory path.  Rows are loaded in whole 128-byte lines: half lines double
 // the requests to L2, which then take longer than the products (7.4 against 5.4 ms without
@@ -20,7 +21,9 @@
 namespace rtl {
 
 constexpr int kRK = 64;      // K per ring step
-constexpr int kSlots = 5;    // LDS slots: 256 x 256 tiles take all 160 KB, two 128 x 128 ones likewise
+// LDS slots at d steps ahead.  Five slots of 256 x 256 tiles take all 160 KB, two 128 x 128 tiles'
+// likewise; nine of a 128 x 128 tile 144 KB.
+constexpr int ring_slots(int d) { return 2 * d + 1; }
 constexpr int kRingWaves = 4;
 
 // Operand with k along its rows: element (r, k) at p[r * ld + k].  A tile holds ROWS rows of 128
@@ -128,15 +131,22 @@ __device__ __forceinline__ void settle(f32x4 (&acc)[NB]) {
     asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc[nb]), "+a"(acc[nb + 1]), "+a"(acc[nb + 2]), "+a"(acc[nb + 3]));
 }
 
+// Waits until at most N of the wave's loads are in flight and all its LDS reads have returned.
+template <int N>
+__device__ __forceinline__ void wait_ring() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | ((N >> 4) << 14));
+}
+
 template <int RB>
 struct ARegs {
   u32x4 v[2][RB];
 };
 
 // One ring step of a wave's RB x NB blocks of 16 x 16.  tb, ta1, tb1: the tiles of B_s, A_{s+1},
-// B_{s+1}; da, db: where sa.load(da, i) puts load i of A_{s+2} and sb.load(db, i) of B_{s+2}.  The five slots are distinct (__restrict__ says so: without it the compiler has every
+// B_{s+1}; da, db: where sa.load(da, i) puts load i of A_{s+d} and sb.load(db, i) of B_{s+d}.  The five slots are distinct (__restrict__ says so: without it the compiler has every
 // transposing read wait for every load in flight).
-template <int RB, int NB, typename OpA, typename OpB, typename SrcA, typename SrcB>
+template <int DEPTH, int RB, int NB, typename OpA, typename OpB, typename SrcA, typename SrcB>
 __device__ __forceinline__ void ring_step(f32x4 (&acc)[RB][NB], const uint8_t* __restrict__ tb,
                                           const uint8_t* __restrict__ ta1, const uint8_t* __restrict__ tb1,
                                           uint8_t* __restrict__ da, uint8_t* __restrict__ db, const OpA& oa,
@@ -147,21 +157,22 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[RB][NB], const uint8_t* _
 #pragma unroll
   for (int nb = 0; nb < NB; nb++) {
     if (nb == NB - 1) {
-      __builtin_amdgcn_s_waitcnt((OpB::kLoads & 15) | (7 << 4) | (0 << 8));  // vmcnt(B_{s+2}'s loads), lgkmcnt(0)
+      wait_ring<OpB::kLoads + (DEPTH - 2) * LD>();  // in flight: B_{s+2}, and A and B of s + 3 .. s + d
       barrier_nofence();
     }
 #pragma unroll
     for (int p = 0; p < 2 * RB; p++) {
       mfma_acc(acc[p % RB][nb], cur.v[p / RB][p % RB], bv[nb % 4][p / RB]);
       // what else the block does, a little behind each product: a lone wave's pipe runs empty
-      // where several other instructions follow one another
+      // where several other instructions follow one another (the last product takes what is left)
+      constexpr int A0 = 2, L0 = 2 + RB / 4, D = RB >= 4 ? RB / 2 : 1;
       if (nb + 2 < NB && p < 2) bv[(nb + 2) % 4][p] = ob.read(tb, NB * wn + nb + 2, p);
       if (nb == NB - 1 && p < 4) bv[p / 2][p % 2] = ob.read(tb1, NB * wn + p / 2, p % 2);
 #pragma unroll
       for (int t = 0; t < 3; t++) {
         const int i = 3 * nb + t;
-        if (nb < NB - 1 && p == 2 + t * (RB / 2) && i < 2 * RB) next.v[i / RB][i % RB] = oa.read(ta1, RB * wm + i % RB, i / RB);
-        if (nb < NB - 1 && p == 2 + RB / 4 + t * (RB / 2) && i < LD) {
+        if (nb < NB - 1 && p == min(A0 + t * D, 2 * RB - 1) && i < 2 * RB) next.v[i / RB][i % RB] = oa.read(ta1, RB * wm + i % RB, i / RB);
+        if (nb < NB - 1 && p == min(L0 + t * D, 2 * RB - 1) && i < LD) {
           if (i < LA) sa.load(da, i);
           else sb.load(db, i - LA);
         }
@@ -175,19 +186,19 @@ __device__ __forceinline__ void ring_step(f32x4 (&acc)[RB][NB], const uint8_t* _
 // load(dst, i) issues its load i; past the end (kt = -1) the loads read zeros.  The caller settles
 // each row of blocks before it reads it.  (Tiles that start at different steps and go round, so
 // that one of those that share an operand takes each L2 miss, measured 2% slower.)
-template <int RB, int NB, typename OpA, typename OpB, typename AtA, typename AtB>
+template <int DEPTH, int RB, int NB, typename OpA, typename OpB, typename AtA, typename AtB>
 __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds, const OpA& oa, const OpB& ob,
                                              AtA at_a, AtB at_b, int steps, int wm, int wn) {
-  static_assert(OpA::kBytes == OpB::kBytes, "either operand's tile fits every slot");
-  constexpr int SLOT = OpA::kBytes, LA = OpA::kLoads, LB = OpB::kLoads;
+  static_assert(OpB::kBytes <= OpA::kBytes, "either operand's tile fits every slot");
+  constexpr int SLOT = OpA::kBytes, LA = OpA::kLoads, LB = OpB::kLoads, RING = ring_slots(DEPTH) * SLOT;
   auto step_or_none = [&](int s) { return s < steps ? s : -1; };
 #pragma unroll
   for (int rb = 0; rb < RB; rb++)
 #pragma unroll
     for (int nb = 0; nb < NB; nb++) mfma_zero(acc[rb][nb]);
-  // A_0, B_0, A_1, B_1 into slots 0..3
+  // A_0, B_0, A_1, B_1, .. into slots 0, 1, 2, 3, ..
 #pragma unroll
-  for (int s = 0; s < 2; s++) {
+  for (int s = 0; s < DEPTH; s++) {
     const auto sa = at_a(step_or_none(s));
     const auto sb = at_b(step_or_none(s));
 #pragma unroll
@@ -195,7 +206,7 @@ __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds,
 #pragma unroll
     for (int i = 0; i < LB; i++) sb.load(lds + (2 * s + 1) * SLOT, i);
   }
-  wait_vmcnt<LB>();
+  wait_vmcnt<LB + (DEPTH - 2) * (LA + LB)>();  // A_0, B_0, A_1 have arrived
   barrier_nofence();
   ARegs<RB> av[2];
   u32x4 bv[4][2];
@@ -206,16 +217,21 @@ __device__ __forceinline__ void ring_product(f32x4 (&acc)[RB][NB], uint8_t* lds,
 #pragma unroll
     for (int nb = 0; nb < 2; nb++) bv[nb][kk] = ob.read(lds + SLOT, NB * wn + nb, kk);
   }
-  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt(0): A_0's slot is free
+  wait_ring<63>();  // the reads: A_0's slot is free
   barrier_nofence();
-  // Slots of B_{s+2} (A_s's), B_s, A_{s+1}, B_{s+1}, A_{s+2} (B_{s-1}'s); two on with every step.
-  int o0 = 0, o1 = SLOT, o2 = 2 * SLOT, o3 = 3 * SLOT, o4 = 4 * SLOT;
+  // Slots of B_{s+d} (A_s's), B_s, A_{s+1}, B_{s+1}, A_{s+d} (B_{s-1}'s); two on with every step.
+  int o0 = 0, o1 = SLOT, o2 = 2 * SLOT, o3 = 3 * SLOT, o4 = 2 * DEPTH * SLOT;
+  auto on = [&](int o) { return o + 2 * SLOT >= RING ? o + 2 * SLOT - RING : o + 2 * SLOT; };
   auto step = [&](int s, const ARegs<RB>& cur, ARegs<RB>& next) {
-    const int kt = step_or_none(s + 2);
-    ring_step<RB, NB>(acc, lds + o1, lds + o2, lds + o3, lds + o4, lds + o0, oa, ob, at_a(kt), at_b(kt), cur, next, bv,
-                      wm, wn);
-    const int t0 = o0, t1 = o1;
-    o0 = o2; o1 = o3; o2 = o4; o3 = t0; o4 = t1;
+    const int kt = step_or_none(s + DEPTH);
+    ring_step<DEPTH, RB, NB>(acc, lds + o1, lds + o2, lds + o3, lds + o4, lds + o0, oa, ob, at_a(kt), at_b(kt), cur, next,
+                             bv, wm, wn);
+    if (DEPTH == 2) {  // the five are the whole ring
+      const int t0 = o0, t1 = o1;
+      o0 = o2; o1 = o3; o2 = o4; o3 = t0; o4 = t1;
+    } else {
+      o0 = o2; o1 = o3; o2 = on(o2); o3 = on(o3); o4 = on(o4);
+    }
   };
   int s = 0;
   for (; s + 2 <= steps; s += 2) {  // the two sets of A fragments

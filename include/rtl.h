@@ -358,7 +358,8 @@ rtl_status rtl_glu_fused(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_
 
 /*
  * Gradient of rtl_glu_fused from its inputs, the pre-activations G and U and the gradient dY:
- *   dG = dY U act'(G),  dU = dY act(G)  (rounded to bf16, as operands of the products)
+ *   dG = dY U act'(G),  dU = dY act(G)  (rounded to bf16, as operands of the products; for
+ *   M * H up to 2^14, where that rounding would not average out, to twice the digits)
  *   dX = dG Wg + dU Wu [M,K],  dWg = dG^T X [H,K],  dWu = dU^T X [H,K]
  * accumulated in fp32, rounded once.  dX may be NULL (Wg and Wu are then not read), or dWg and
  * dWu both (X is then not read).  The workspace size covers every choice of outputs.  Calls

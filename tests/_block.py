@@ -107,15 +107,18 @@ def glu_forward(x, wg, wu, kind, dtype=torch.bfloat16):
 
 
 def glu_backward(x, wg, wu, g, u, dy, kind):
-    """dx, dwg, dwu and their bounds: dG and dU round once to bf16 (2^-8 of each) after an
-    activation within act_bound; the products add as in glu_forward."""
+    """dx, dwg, dwu and their bounds: dG and dU round once to bf16 (2^-8 of each; up to 2^14
+    elements twice, 2^-16) after an activation within act_bound; the products add as in
+    glu_forward, twice as many where they run over both roundings."""
     v, s = act(g, kind)
     dg, du = dy * u * s, dy * v
     b = act_bound(g)
-    eg = np.abs(dg) * (2.0 ** -8 + 4 * U) + 1.01 * np.abs(dy * u) * b
-    eu = np.abs(du) * (2.0 ** -8 + 4 * U) + 1.01 * np.abs(dy) * b
+    few = g.size <= 2 ** 14
+    step = 2.0 ** -16 if few else 2.0 ** -8
+    eg = np.abs(dg) * (step + 4 * U) + 1.01 * np.abs(dy * u) * b
+    eu = np.abs(du) * (step + 4 * U) + 1.01 * np.abs(dy) * b
     dx, dwg, dwu = dg @ wg + du @ wu, dg.T @ x, du.T @ x
-    H, M = g.shape[1] + 64, g.shape[0] + 64  # the kernels pad both sums with zeros
+    H, M = (2 if few else 1) * (g.shape[1] + 64), (2 if few else 1) * (g.shape[0] + 64)  # padded with zeros
     ag, au = np.abs(dg) + eg, np.abs(du) + eu
     bx = eg @ np.abs(wg) + eu @ np.abs(wu) + 4 * H * U * (ag @ np.abs(wg) + au @ np.abs(wu))
     bwg = eg.T @ np.abs(x) + 2 * M * U * (ag.T @ np.abs(x))

@@ -33,7 +33,7 @@ SHAPES = [
     (1, 64, 16), (1, 1344, 333), (2, 320, 7), (15, 640, 130), (16, 64, 1), (17, 128, 50), (32, 704, 96), (33, 192, 64),
     (48, 512, 31), (64, 256, 200), (65, 64, 65), (130, 448, 1), (200, 1088, 77), (257, 320, 516), (300, 256, 260),
     (700, 128, 1000), (1029, 192, 4100), (3000, 64, 2049),
-    (64, 64, 11000), (3100, 4096, 70), (90, 3200, 2049),  # the gradients' larger tiles
+    (64, 64, 11000), (100, 1344, 1500), (140, 832, 5000), (400, 320, 6000), (3100, 4096, 70), (90, 3200, 2049),  # the gradients' larger tiles
 ]
 
 
