@@ -13,9 +13,9 @@
 // the group's lanes.  A group takes HC heads of its token, so that a lane's four angles are
 // formed once for HC heads and HC loads are in flight before the first is used.
 //
-// Angles are formed in double precision and in revolutions (pos f / 2 pi, reduced by its
-// nearest whole number), so a far position loses nothing; the reduced angle is rounded to
-// fp32 (2^-25 revolutions = 1.9e-7 radians at most).
+// Angles are formed in revolutions (pos f / 2 pi), from frequencies in two fp32 words and reduced
+// by their nearest whole number before the product is rounded, so a position as far as 2^24 loses
+// nothing: the reduced angle is within 2^-25 revolutions.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -29,9 +29,10 @@ namespace rtl {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxPairs = 128;
 
-// Frequencies in revolutions per unit of position, and the position axis, of each pair.
+// Frequencies in revolutions per unit of position (the sum of two fp32 words), and the position
+// axis, of each pair.
 struct RopeTable {
-  double f[kRopeMaxPairs];
+  float hi[kRopeMaxPairs], lo[kRopeMaxPairs];
   uint8_t axis[kRopeMaxPairs];
 };
 
@@ -45,7 +46,7 @@ struct RopeArgs {
   uint32_t items, nq, nc;  // items: (token, chunk of HC heads) pairs; chunks of the first tensor, of both
   uint32_t blocks[2];      // backward: workgroups on the first tensor, on the second
   int D, pairs, axes;
-  float eps, sign;
+  float eps, sign, inv_d;
   const float* pos;
   RopeTensor x[2], y[2];   // backward: y is dy, dx the output
   RopeTensor dx[2];
@@ -131,22 +132,36 @@ struct RopeUnit {
   }
 };
 
-// cos and sin (times `sign`) of the unit's four angles; 1 and 0 past the rotated channels.  By the
-// hardware's instructions, which take revolutions: within 2.2 * 2^-24 of the exact values at every
-// multiple of 2^-24 in [-1/2, 1/2] (measured), as near as the library's functions.
-__device__ __forceinline__ void rope_angles(const RopeArgs& a, const RopeTable& t, int64_t m, int u, float (&c)[4],
+// A unit's four frequencies and axes.
+struct RopeFreq {
+  f32x4 hi, lo;
+  int axis[4];
+  bool turned;  // false past the rotated channels
+  __device__ __forceinline__ RopeFreq(const RopeArgs& a, const RopeTable& t, int u) : turned(4 * u < a.pairs) {
+    if (!turned) return;
+    hi = *reinterpret_cast<const f32x4*>(t.hi + 4 * u);
+    lo = *reinterpret_cast<const f32x4*>(t.lo + 4 * u);
+    const uint32_t four = *reinterpret_cast<const uint32_t*>(t.axis + 4 * u);
+#pragma unroll
+    for (int i = 0; i < 4; i++) axis[i] = (four >> (8 * i)) & 255;
+  }
+};
+// cos and sin (times `sign`) of the unit's four angles for token m; 1 and 0 past the rotated
+// channels.  By the hardware's instructions, which take revolutions: within 2.2 * 2^-24 of the exact
+// values at every multiple of 2^-24 in [-1/2, 1/2] (measured), as near as the library's functions.
+__device__ __forceinline__ void rope_angles(const RopeArgs& a, const RopeFreq& f, int64_t m, float (&c)[4],
                                             float (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     c[i] = 1.f;
     s[i] = 0.f;
   }
-  if (4 * u >= a.pairs) return;
+  if (!f.turned) return;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int p = 4 * u + i;
-    const double rev = (double)a.pos[m * a.axes + t.axis[p]] * t.f[p];
-    const float r = (float)(rev - rint(rev));
+    const float p = a.pos[m * a.axes + f.axis[i]];
+    // p hi - (its nearest whole number) in one rounding, then p lo
+    const float r = fmaf(p, f.lo[i], fmaf(p, f.hi[i], -rintf(p * f.hi[i])));
     s[i] = a.sign * __builtin_amdgcn_sinf(r);
     c[i] = __builtin_amdgcn_cosf(r);
   }
@@ -200,7 +215,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
     if (j < nh) raw[j] = un.load(x.p, m * x.row + (int64_t)(h0 + j) * x.head);
   float c[4], s[4], w[8];
   if (nh > 0) {
-    rope_angles(a, t, m, u, c, s);
+    rope_angles(a, RopeFreq(a, t, u), m, c, s);
     if (NORM) rope_weights<BF16, HALVES>(un, a.w[which], w);
   }
 #pragma unroll
@@ -216,7 +231,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
       float q = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; i++) q += v[i] * v[i];
-      const float r = 1.f / sqrtf(group_sum<GL>(q) / (float)a.D + a.eps);
+      const float r = __builtin_amdgcn_rsqf(fmaf(group_sum<GL>(q), a.inv_d, a.eps));
 #pragma unroll
       for (int i = 0; i < 8; i++) v[i] = v[i] * r * w[i];
     }
@@ -249,52 +264,55 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
   for (int i = 0; i < 8; i++) w[i] = dw[i] = 0.f;
   if (lane) rope_weights<BF16, HALVES>(un, a.w[which], w);
 
+  const RopeFreq freq(a, t, u);
   struct Item {
     typename Unit::Raw x[HC], y[HC];
     uint32_t m;
-    int h0, nh;
+    int h0, nh;  // the same for all lanes of a group; lanes past D hold zeros
   };
   auto fetch = [&](uint32_t item, Item& it) {
-    const bool live = item < items && lane;
+    const bool live = item < items;
     it.m = live ? item / nc : 0;
-    it.h0 = live ? (int)(item - it.m * nc) * HC : 0;
+    it.h0 = (int)((live ? item : 0) - it.m * nc) * HC;
     it.nh = live ? min(HC, H - it.h0) : 0;
-#pragma unroll
-    for (int j = 0; j < HC; j++)
-      if (j < it.nh) {
-        it.x[j] = un.load(x.p, (int64_t)it.m * x.row + (int64_t)(it.h0 + j) * x.head);
-        it.y[j] = un.load(y.p, (int64_t)it.m * y.row + (int64_t)(it.h0 + j) * y.head);
-      }
-  };
-  auto form = [&](const Item& it) {
-    float c[4], s[4];
-    if (it.nh > 0) rope_angles(a, t, it.m, u, c, s);
+    const int64_t xat = (int64_t)it.m * x.row + (int64_t)it.h0 * x.head, yat = (int64_t)it.m * y.row + (int64_t)it.h0 * y.head;
 #pragma unroll
     for (int j = 0; j < HC; j++) {
+      it.x[j] = it.y[j] = typename Unit::Raw{};
+      if (j < it.nh && lane) {
+        it.x[j] = un.load(x.p, xat + j * x.head);
+        it.y[j] = un.load(y.p, yat + j * y.head);
+      }
+    }
+  };
+  auto form = [&](const Item& it) {
+    if (it.nh == 0) return;
+    float c[4], s[4];
+    rope_angles(a, freq, it.m, c, s);
+    const int64_t at = (int64_t)it.m * dx.row + (int64_t)it.h0 * dx.head;
+#pragma unroll
+    for (int j = 0; j < HC; j++) {
+      if (j >= it.nh) break;
       float v[8], d[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = d[i] = 0.f;
-      if (j < it.nh) {
-        Unit::unpack(it.x[j], v);
-        Unit::unpack(it.y[j], d);
-        un.rotate(d, c, s);
-      }
-      float q = 0.f, p = 0.f;
+      Unit::unpack(it.x[j], v);
+      Unit::unpack(it.y[j], d);
+      un.rotate(d, c, s);
+      float q = 0.f, p = 0.f, wd[8];
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        q += v[i] * v[i];
-        p += d[i] * w[i] * v[i];
+        wd[i] = d[i] * w[i];
+        q = fmaf(v[i], v[i], q);
+        p = fmaf(wd[i], v[i], p);
       }
-      const float r = 1.f / sqrtf(group_sum<GL>(q) / (float)a.D + a.eps);
-      // x r^3 / D sum(w t x) as (x r) (r (sum(w t x) r / D))
-      const float k = r * (group_sum<GL>(p) * r / (float)a.D);
+      const float r = __builtin_amdgcn_rsqf(fmaf(group_sum<GL>(q), a.inv_d, a.eps));
+      // dx = r w t - x r^3 / D sum(w t x)
+      const float k = r * r * r * a.inv_d * group_sum<GL>(p);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const float n = v[i] * r;
-        dw[i] += d[i] * n;
-        v[i] = r * (d[i] * w[i]) - n * k;
+        dw[i] = fmaf(d[i], v[i] * r, dw[i]);
+        v[i] = fmaf(wd[i], r, -(v[i] * k));
       }
-      if (j < it.nh) un.store(dx.p, (int64_t)it.m * dx.row + (int64_t)(it.h0 + j) * dx.head, v);
+      if (lane) un.store(dx.p, at + j * dx.head, v);
     }
   };
   Item one, two;
@@ -377,6 +395,7 @@ void rope_fill(const RopeCall& c, int hc, RopeArgs& a, RopeTable& t) {
   a.D = (int)c.D;
   a.axes = c.axes;
   a.eps = c.eps;
+  a.inv_d = 1.f / (float)c.D;
   a.pos = c.pos;
   for (int k = 0; k < 2; k++) {
     a.x[k] = RopeTensor{const_cast<void*>(c.x[k].p), c.x[k].row, c.x[k].head};
@@ -390,7 +409,8 @@ void rope_fill(const RopeCall& c, int hc, RopeArgs& a, RopeTable& t) {
     const double ratio = pow(c.theta, -2.0 / (double)c.dims[ax]);
     double f = 0.15915494309189533577;
     for (int i = 0; i < c.dims[ax] / 2; i++, p++, f *= ratio) {
-      t.f[p] = f;
+      t.hi[p] = (float)f;
+      t.lo[p] = (float)(f - (double)t.hi[p]);
       t.axis[p] = (uint8_t)ax;
     }
   }

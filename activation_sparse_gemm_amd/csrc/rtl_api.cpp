@@ -499,9 +499,9 @@ rtl::RopeCall rope_call(rtl_dtype dt, bool norm, int64_t M, int64_t Hq, int64_t 
 
 rtl::StridedHeads heads(const View& v) { return rtl::StridedHeads{v.p, v.row, v.head}; }
 
-// eps of the head norms: above 0, so that a head of zeros has a finite r.
+// eps of the head norms: a normal number, so that a head of zeros has a finite r.
 rtl_status check_norm_eps(float eps) {
-  if (!(eps > 0.f && eps <= 1.f)) return fail(RTL_ERR_ARG, "eps must lie in (0, 1] (got %g)", (double)eps);
+  if (!(eps >= 0x1p-126f && eps <= 1.f)) return fail(RTL_ERR_ARG, "eps must lie in [2^-126, 1] (got %g)", (double)eps);
   return RTL_OK;
 }
 

@@ -297,7 +297,8 @@ rtl_status rtl_linear_fused_fp8(int64_t M, int64_t N, int64_t K, int64_t R, cons
  *     the axes in order.  RTL_ROPE_ADJACENT: pair p is channels 2p and 2p + 1;
  *     RTL_ROPE_HALVES: channels p and p + Dr / 2.  (x0, x1) -> (x0 cos - x1 sin,
  *     x1 cos + x0 sin).
- * Angles are formed in double precision, all else in fp32, rounded once at the end.
+ * Angles are reduced by whole turns before they are rounded (within 2^-25 of a turn for positions
+ * up to 2^24 in magnitude); all else is fp32, rounded once at the end.
  * dt is bf16 or fp32.  Limits: D % 8 == 0, D <= 256, n_axes <= 4, M * heads below 2^31; theta
  * in [1, 1e30].
  */
@@ -316,7 +317,7 @@ rtl_status rtl_rope_axes(rtl_dtype dt, int64_t M, int64_t H, int64_t D, const vo
  *   Qo = rotation(x r qw), r = 1 / sqrt(mean(x^2) + eps), and Ko likewise with kw.
  * qw and kw [D] (dtype dt) may be NULL (ones).  n_axes == 0 drops the rotation (pos and
  * axis_dims may then be NULL); Hk == 0 drops K (its pointers are ignored).  eps must lie in
- * (0, 1].  The squares are summed in fp32 and must lie in its range.
+ * [2^-126, 1].  The squares are summed in fp32 and must lie in its range.
  */
 rtl_status rtl_qk_norm_rope(rtl_dtype dt, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const void* Q, int64_t q_row,
                             int64_t q_head, const void* K, int64_t k_row, int64_t k_head, const void* qw,

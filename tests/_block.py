@@ -44,8 +44,9 @@ def pair_sum(x, n, pairs):
     return y
 
 
-# A turned value x0 c - x1 s: the reduced angle is within 2^-26 revolutions (1.6 u radians),
-# cos and sin within 2.2 u of it, each product and the difference rounds once: 8 u of |x0| + |x1|.
+# A turned value x0 c - x1 s: the reduced angle is within 2^-25 revolutions (two roundings of at
+# most 2^-26: 3.2 u radians), cos and sin within 2.2 u of it, each product and the difference
+# rounds once: 8 u of |x0| + |x1|.
 TURN = 8 * U
 
 # A normed value x r w: 8 squares per lane and up to 5 exchanges sum within 14 u, the mean, eps,
