@@ -76,7 +76,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // The tiled product: WM x WN waves of RB x NB blocks, 16 RB WM rows and 16 NB WN weight rows (8 NB
 // WN outputs) a tile.  Of a wave column's 16 NB weight rows the first half are gate rows, the
 // second up; row 16 nb + r16 of either half is output column NB / 2 r16 + nb, so that lane r16
-// holds NB / 2 consecutive columns over its blocks.
+// holds NB / 2 consecutive columns over its blocks.  Measured: 32760 x 5120 x 13824 6.0-6.3 ms
+// (1.48-1.54 PFLOP/s; the matrix cores 78% busy at the 1.8 GHz that the power limit leaves), 4173 x
+// 2560 x 6916 with GELU, G and U kept 268 us (1.10): 935 tiles take four rounds of 256, and of a
+// tile's 67 us the first loads and the stores of three outputs 17.
 template <int ACT, int RB, int NB, int WM, int WN, int DEPTH>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(RB == 8 ? 1 : 2, RB == 8 ? 1 : 2)))
 void glu_kernel(const GluArgs a) {
@@ -140,7 +143,8 @@ void glu_kernel(const GluArgs a) {
 // Few rows (M <= 16 MB): a workgroup forms 16 output columns; wave w takes the K steps w, w + 4, ...
 // of 64, each with a ring of D LDS slots of its own (16 gate rows, 16 up rows and the rows of X,
 // in whole 128-byte lines that go straight to LDS) and no barrier, and the waves' sums are added
-// in wave order.  Bound by the weights' bytes: 1 x 5120 x 13824 reads 283 MB.  (Loading fragments
+// in wave order.  Bound by the weights' bytes: 1 x 5120 x 13824 reads 283 MB in 44-47 us (6.0-6.4
+// TB/s), 32 x 5120 x 13824 in 56.  (Loading fragments
 // straight into registers, 64 pieces of 16 bytes an instruction, is held by the address path
 // instead: 16 rows of X then cost 25% of the time.)
 template <int ACT, int MB>
@@ -285,6 +289,7 @@ hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void*
 // P [M, 2 Hp] = [dG | dU], each padded to Hp columns with zeros, rounded to bf16: the matrix
 // cores' operand.  (Formed inside the products instead, it would be formed again for every
 // tile that reads it, 2 H / 256 + K / 256 times.)  One 16-byte chunk of each half per thread.
+// Bound by memory: 8190 x 13824 reads three and writes two times 226 MB in 181 us (6.2 TB/s).
 //
 // The rounding, 2^-8 of an element at most, adds to a gradient what the gradient's own rounding
 // to bf16 does, as long as many elements share the sum of squares; in a product of few of them
@@ -365,7 +370,9 @@ __device__ __forceinline__ void store_rows(const f32x4 (&acc)[NB], uint8_t* blk,
 // the one with the longer jobs first, so that the other's tiles fill the CUs that its last round
 // would leave idle.  A job is a tile over all of k, or, where a product has few tiles, a part of a
 // tile's k: the parts' fp32 sums go to `part` in accumulator order and are added in split order by
-// glu_join_kernel.
+// glu_join_kernel.  Bound by the matrix cores and the power they draw (71% busy at 1.75 GHz) where
+// both sides are large: 8190 x 5120 x 13824 3.5-3.65 ms (1.27-1.33 PFLOP/s); by the tiles' first
+// loads and stores where few tokens meet whole weights: 333 x 2560 x 6912 80 us.
 struct GluJobs {
   int tiles_m, tiles_n, splits;
   int steps, per;  // K steps of a tile, of a part

@@ -195,6 +195,11 @@ __device__ __forceinline__ void rope_weights(const RopeUnit<BF16, HALVES>& un, c
   }
 }
 
+// The rotation, after the norm (NORM) or alone.  Measured in bf16: alone 32760 x 40 x 128 in 112-120
+// us (5.6-6.0 TB/s, where a copy of its size runs at 5.5); with the norm 32760 x 80 x 128 in 222-237
+// us (5.7-6.0) and 4608 x 48 x 128 in 20 us (5.8).  Stores that bypass the caches (the outputs are
+// read next by another kernel, from memory at these sizes) gained 8%; loads that do lost up to 20%
+// where the input still lay in the last-level cache.
 template <bool BF16, bool HALVES, bool NORM, int GL, int HC>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, const RopeTable t) {
   const int u = threadIdx.x % GL;
@@ -246,6 +251,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
 // of the two tensors (shared out by their heads), the next item's loads in flight while one is
 // formed; each lane sums its channels' dw in fp32 over the items it meets, the workgroup adds its
 // groups in LDS, and qk_dw_kernel adds the workgroups: one order, the same result on every run.
+// Bound by memory and, nearly as much, by its vector instructions (the norm, two sums and the
+// rotation for every element of two inputs).  Measured: 4608 x 32 x 128 in bf16 22 us (5.2 TB/s).
 template <bool BF16, bool HALVES, int GL, int HC>
 __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a, const RopeTable t) {
   constexpr int NG = kRopeThreads / GL;
@@ -339,7 +346,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
 }
 
 // dw[k][ch] = sum over tensor k's workgroups of part[.][ch], in double precision: 16 columns a
-// workgroup, 64 bytes of a row to four lanes, 64 rows at a time.
+// workgroup, 64 bytes of a row to four lanes, 64 rows at a time (D = 128: 4 us, a launch's latency).
 __global__ __launch_bounds__(256) void qk_dw_kernel(const float* part, int blocks_q, int blocks_k, int D, float* dqw,
                                                     float* dkw) {
   __shared__ double red[64][16];
