@@ -361,18 +361,16 @@ class _Here:
 _HERE = _Here()
 
 
-def _one_device(*tensors):
+def _one_device(first, *rest):
     """The context in which the GPU that every given tensor is on is the current device, so that
     a call without ``stream`` runs on that GPU's current stream."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0 or (dev is not None and d != dev):
-                raise ValueError("tensors must be on one GPU, got "
-                                 f"{sorted({str(u.device) for u in tensors if u is not None})}")
-            dev = d
-    return _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on one GPU, got {first.device} and {t.device}")
+    if dev < 0:
+        raise ValueError(f"tensors must be on one GPU, got {first.device}")
+    return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _expect(name, t, shape, dtype):
@@ -403,7 +401,9 @@ def _heads(t):
 
 def _new(stream, like, shape, dtype):
     """A tensor on `like`'s device, as _empty allocates it."""
-    return like.new_empty(shape, dtype=dtype) if stream is None else _empty(shape, dtype, like.device, stream)
+    if stream is not None:
+        return _empty(shape, dtype, like.device, stream)
+    return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
 
 
 def _queue(stream, like):
@@ -466,8 +466,10 @@ def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 
                 Ko = _new(stream, Q, (M, Hk, D), dt)
             else:
                 _expect("Ko", Ko, (M, Hk, D), dt)
+            _expect("kw", kw, (D,), dt)
+        elif Ko is not None:
+            raise ValueError("Ko without K")
         _expect("qw", qw, (D,), dt)
-        _expect("kw", kw, (D,), dt)
         _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _flat(qw), _flat(kw), eps,
                                     *_rope_args(pos, axis_dims, theta, pairs, M), *_heads(Qo), *_heads(Ko),
                                     _queue(stream, Q)))
@@ -488,20 +490,30 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
     dt = Q.dtype
     Hk = 0 if K is None else K.shape[1]
     with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, dQo, dKo, dQ, dK, dqw, dkw, workspace):
+        _expect("dQo", dQo, (M, Hq, D), dt)
+        _expect("qw", qw, (D,), dt)
         if dQ is None:
             dQ = _new(stream, Q, (M, Hq, D), dt)
+        else:
+            _expect("dQ", dQ, (M, Hq, D), dt)
         if dqw is None:
             dqw = _new(stream, Q, (D,), torch.float32)
+        else:
+            _expect("dqw", dqw, (D,), torch.float32)
         if K is not None:
+            _expect("K", K, (M, Hk, D), dt)
+            _expect("dKo", dKo, (M, Hk, D), dt)
+            _expect("kw", kw, (D,), dt)
             if dK is None:
                 dK = _new(stream, Q, (M, Hk, D), dt)
+            else:
+                _expect("dK", dK, (M, Hk, D), dt)
             if dkw is None:
                 dkw = _new(stream, Q, (D,), torch.float32)
-        for name, t, shape in (("K", K, (M, Hk, D)), ("qw", qw, (D,)), ("kw", kw, (D,)), ("dQo", dQo, (M, Hq, D)),
-                               ("dKo", dKo, (M, Hk, D)), ("dQ", dQ, (M, Hq, D)), ("dK", dK, (M, Hk, D))):
-            _expect(name, t, shape, dt)
-        _expect("dqw", dqw, (D,), torch.float32)
-        _expect("dkw", dkw, (D,), torch.float32)
+            else:
+                _expect("dkw", dkw, (D,), torch.float32)
+        elif dKo is not None or dK is not None or dkw is not None:
+            raise ValueError("dKo, dK or dkw without K")
         if workspace is None:
             workspace = _new(stream, Q, (max(rtl_qk_norm_rope_backward_workspace_bytes(D), 1),), torch.uint8)
         _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _flat(qw), _flat(kw), eps,
@@ -519,13 +531,17 @@ def rtl_glu_fused(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: int 
     H = Wg.shape[0]
     bf16 = torch.bfloat16
     with _one_device(X, Wg, Wu, Y, G, U):
-        if Y is None:
-            Y = _new(stream, X, (M, H), bf16)
         _expect("X", X, (M, K), bf16)
         _expect("Wg", Wg, (H, K), bf16)
         _expect("Wu", Wu, (H, K), bf16)
-        for name, t in (("Y", Y), ("G", G), ("U", U)):
-            _expect(name, t, (M, H), bf16)
+        if Y is None:
+            Y = _new(stream, X, (M, H), bf16)
+        else:
+            _expect("Y", Y, (M, H), bf16)
+        if G is not None:
+            _expect("G", G, (M, H), bf16)
+        if U is not None:
+            _expect("U", U, (M, H), bf16)
         _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _flat(X), _flat(Wg), _flat(Wu), _flat(Y), _flat(G), _flat(U),
                                  _queue(stream, X)))
     return Y

@@ -82,7 +82,8 @@ def erf(x):
 def act(g, kind):
     """value and slope; kind 0 SiLU, 1 GELU."""
     if kind == 0:
-        p = 1 / (1 + np.exp(-g))
+        with np.errstate(over="ignore"):  # exp(-g) = inf leaves p = 0
+            p = 1 / (1 + np.exp(-g))
         return g * p, p * (1 + g * (1 - p))
     p = 0.5 * (1 + erf(g / np.sqrt(2)))
     return g * p, p + g * np.exp(-g * g / 2) / np.sqrt(2 * np.pi)

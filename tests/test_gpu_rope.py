@@ -193,7 +193,11 @@ def test_qk_options():
     dY = rnd(53, M, H, D, dtype=BF)
     dQ, dK, dqw, dkw = rtl.rtl_qk_norm_rope_backward(Q, None, w, None, None, (), dY, None)
     assert dK is None and dkw is None and bool(torch.isfinite(dQ).all())
-    x, r = B.f64(Q), None
+    with pytest.raises(ValueError):
+        rtl.rtl_qk_norm_rope(Q, None, w, None, pos, dims, Ko=Q)
+    with pytest.raises(ValueError):
+        rtl.rtl_qk_norm_rope_backward(Q, None, w, None, None, (), dY, None, dkw=torch.zeros(D, device="cuda"))
+    x = B.f64(Q)
     rx, rw, bx, bw = B.qk_backward(x, B.f64(w), np.zeros((M, 0)), 0, 1e-6, B.f64(dY))
     B.check(dQ, rx, bx, BF, "dQ")
     B.check(dqw, rw, bw, F32, "dqw")
@@ -238,3 +242,20 @@ def test_streams_and_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+def test_python_refusals():
+    """Tensors that do not go together are refused before the call."""
+    Q, w, pos = rnd(1, 6, 2, 64, dtype=BF), rnd(2, 64, dtype=BF), positions(3, 6, 2)
+    ok = dict(Q=Q, K=Q.clone(), qw=w, kw=w, pos=pos, axis_dims=(32, 32))
+    for bad, err in ((dict(K=Q.float()), TypeError), (dict(K=Q[:5]), ValueError), (dict(qw=w.float()), TypeError),
+                     (dict(kw=w[:32]), ValueError), (dict(pos=pos[:, :1]), ValueError), (dict(pos=pos.double()), TypeError),
+                     (dict(pos=positions(3, 6, 4)[:, ::2]), ValueError), (dict(qw=w.cpu()), ValueError),
+                     (dict(Q=Q[..., ::2]), ValueError), (dict(axis_dims=(32, -32)), ValueError),
+                     (dict(Qo=Q[:, :1]), ValueError), (dict(Q=Q.half()), TypeError)):
+        with pytest.raises(err):
+            rtl.rtl_qk_norm_rope(**{**ok, **bad})
+    with pytest.raises(rtl.RtlError):  # no tokens
+        rtl.rtl_rope_axes(Q[:0], pos[:0], (32, 32))
+    with pytest.raises(rtl.RtlError):  # one buffer for both outputs
+        rtl.rtl_qk_norm_rope(**ok, Qo=ok["Q"], Ko=ok["Q"])
