@@ -562,7 +562,7 @@ GluJobs glu_jobs(int R, int64_t rows, int64_t cols, int64_t steps, int64_t split
   g.splits = (int)((steps + per - 1) / per);
   g.steps = (int)steps;
   g.per = (int)per;
-  g.count = (int)(tm * tn) * g.splits;
+  g.count = (int)std::min<int64_t>(tm * tn * g.splits, INT32_MAX);
   return g;
 }
 
@@ -587,7 +587,7 @@ GluPlan glu_plan(int64_t M, int64_t K, int64_t H) {
     for (int k = 0; k < 2; k++)
       for (int64_t s : {1, 2, 3, 5, 8, 16}) {
         const GluJobs g = glu_jobs(c.R, rows[k], K, steps[k], s);
-        if (s > 1 && (s > steps[k] / 4 || g.count > 2 * c.P)) break;
+        if (s > 1 && (s > steps[k] / 4 || (int64_t)g.tiles_m * g.tiles_n * g.splits > 2 * c.P)) break;
         options[k][n[k]++] = g;
       }
     for (int x = 0; x < n[0]; x++)

@@ -643,10 +643,17 @@ rtl_status check_glu(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H)
     return fail(RTL_ERR_SHAPE, "need M, K, H > 0 (M=%lld K=%lld H=%lld)", (long long)M, (long long)K, (long long)H);
   // a tile's rows are reached with 32-bit offsets: 256 rows of K bf16 values stay below 2^31 bytes
   if (K >= kMaxK) return fail(RTL_ERR_SHAPE, "K must be below %lld (K=%lld)", (long long)kMaxK, (long long)K);
-  if (M > INT32_MAX || H > INT32_MAX || ((M + 127) / 128) * ((H + 63) / 64) > INT32_MAX)
+  // a launch takes fewer than 2^32 threads: 256 to a 256 x 128 tile, or to 16 outputs of few rows
+  if (M > INT32_MAX || H >= (1 << 28) || ((M + 255) / 256) * ((H + 127) / 128) >= 1 << 24)
     return fail(RTL_ERR_SHAPE, "M x H is too large (M=%lld H=%lld)", (long long)M, (long long)H);
   if (K % 64 != 0) return fail(RTL_ERR_UNSUPPORTED, "the gated block needs K %% 64 == 0 (K=%lld)", (long long)K);
   return RTL_OK;
+}
+
+// The gradient's limits: its products sum over 2 H padded (dX) and over M padded (dWg, dWu), with the
+// same 32-bit offsets, and its first pass has a thread for every eight elements, fewer than 2^32.
+bool glu_back_fits(int64_t M, int64_t K, int64_t H) {
+  return M <= kMaxK - 64 && H <= kMaxK / 2 - 64 && K < kMaxK && M * ((H + 63) / 64 * 64) < (int64_t)1 << 35;
 }
 
 }  // namespace
@@ -676,8 +683,7 @@ rtl_status rtl_glu_fused(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_
 }
 
 size_t rtl_glu_backward_workspace_bytes(int64_t M, int64_t K, int64_t H) {
-  if (M <= 0 || K <= 0 || H <= 0 || M > INT32_MAX || H > INT32_MAX || K > kMaxK) return 0;
-  return rtl::glu_back_workspace(M, K, H);
+  return M <= 0 || K <= 0 || H <= 0 || !glu_back_fits(M, K, H) ? 0 : rtl::glu_back_workspace(M, K, H);
 }
 
 rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
@@ -685,10 +691,9 @@ rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int
                             void* dWu, void* workspace, size_t ws_bytes, void* stream) {
   rtl_status st;
   if ((st = check_glu(act, dt, M, K, H)) != RTL_OK) return st;
-  // the products sum over 2 H padded (dX) and over M padded (dWg, dWu)
-  if (M > kMaxK - 64 || H > kMaxK / 2 - 64)
-    return fail(RTL_ERR_SHAPE, "the gradient needs M <= %lld and H <= %lld (M=%lld H=%lld)", (long long)kMaxK - 64,
-                (long long)kMaxK / 2 - 64, (long long)M, (long long)H);
+  if (!glu_back_fits(M, K, H))
+    return fail(RTL_ERR_SHAPE, "the gradient needs M <= %lld, H <= %lld and M x H below 2^35 (M=%lld H=%lld)",
+                (long long)kMaxK - 64, (long long)kMaxK / 2 - 64, (long long)M, (long long)H);
   if (!G || !U || !dY || (!dX && !dWg) || (dWg == nullptr) != (dWu == nullptr) || (dX && (!Wg || !Wu)) || (dWg && !X))
     return fail(RTL_ERR_NULL, "G, U, dY, dX (with Wg, Wu) or dWg and dWu (with X) are required");
   const void* ins[6] = {dWg ? X : nullptr, dX ? Wg : nullptr, dX ? Wu : nullptr, G, U, dY};

@@ -349,9 +349,10 @@ rtl_status rtl_qk_norm_rope_backward(rtl_dtype dt, int64_t M, int64_t Hq, int64_
  *   G = X Wg^T,  U = X Wu^T,  Y = act(G) * U
  *   X [M,K], Wg [H,K], Wu [H,K], Y [M,H]; G and U [M,H] are optional outputs (NULL to skip),
  *   the pre-activations that rtl_glu_backward takes.
- * act: RTL_ACT_SILU g / (1 + exp(-g)) or RTL_ACT_GELU g Phi(g) (exact erf form), evaluated on
- * the fp32 accumulators; every output is rounded once.  Limits: K % 64 == 0, K < 2^22; M and H
- * are arbitrary.  Outputs must not overlap inputs or each other.
+ * act: RTL_ACT_SILU g / (1 + exp(-g)) or RTL_ACT_GELU g Phi(g) (the erf form, Phi within
+ * 4e-7), evaluated on the fp32 accumulators; every output is rounded once.  Limits: K % 64 == 0,
+ * K < 2^22, H < 2^28 and M * H below 2^38; M and H are arbitrary else.  Outputs must not overlap
+ * inputs or each other.
  */
 typedef enum { RTL_ACT_RANGE_MIN_ = -0x7FFFFFFF - 1, RTL_ACT_SILU = 0, RTL_ACT_GELU = 1, RTL_ACT_RANGE_MAX_ = 0x7FFFFFFF } rtl_act;
 rtl_status rtl_glu_fused(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,
@@ -364,7 +365,8 @@ rtl_status rtl_glu_fused(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_
  *   dX = dG Wg + dU Wu [M,K],  dWg = dG^T X [H,K],  dWu = dU^T X [H,K]
  * accumulated in fp32, rounded once.  dX may be NULL (Wg and Wu are then not read), or dWg and
  * dWu both (X is then not read).  The workspace size covers every choice of outputs.  Calls
- * that share a workspace must be serialised.
+ * that share a workspace must be serialised.  Limits besides rtl_glu_fused's: M <= 2^22 - 64,
+ * H <= 2^21 - 64, M * H (H padded to 64) below 2^35; the workspace size is 0 past them.
  */
 size_t rtl_glu_backward_workspace_bytes(int64_t M, int64_t K, int64_t H);
 rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H, const void* X, const void* Wg,

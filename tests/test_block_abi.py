@@ -24,6 +24,12 @@ class Buffers:
         return all((a == 0xAB).all() for a in self.all)
 
 
+def label(v):
+    """A case's name, the same in every process: what the call is given instead, or its status."""
+    return v if isinstance(v, str) else ",".join(f"{k}={'other' if callable(x) else str(x)[:16] if not hasattr(x, '_length_') else list(x)}"
+                                                 for k, x in v.items())
+
+
 def at(p, nbytes):
     return ctypes.c_void_p(p.value + nbytes)
 
@@ -69,7 +75,7 @@ ROPE = [
 ]
 
 
-@pytest.mark.parametrize("over,want", ROPE, ids=lambda v: str(v)[:40])
+@pytest.mark.parametrize("over,want", ROPE, ids=label)
 def test_rope_refusals(over, want):
     st, b = rope(**over)
     refused(st, want, b, over)
@@ -114,13 +120,13 @@ QK_BACKWARD = [
 ]
 
 
-@pytest.mark.parametrize("over,want", QK + QK_FORWARD, ids=lambda v: str(v)[:40])
+@pytest.mark.parametrize("over,want", QK + QK_FORWARD, ids=label)
 def test_qk_refusals(over, want):
     st, b = qk(**over)
     refused(st, want, b, over)
 
 
-@pytest.mark.parametrize("over,want", QK + QK_BACKWARD, ids=lambda v: str(v)[:40])
+@pytest.mark.parametrize("over,want", QK + QK_BACKWARD, ids=label)
 def test_qk_backward_refusals(over, want):
     st, b = qk(back=True, **over)
     refused(st, want, b, over)
@@ -154,7 +160,8 @@ GLU = [
     (dict(dt=9), "RTL_ERR_UNSUPPORTED"), (dict(M=0), "RTL_ERR_SHAPE"), (dict(K=0), "RTL_ERR_SHAPE"), (dict(H=-1), "RTL_ERR_SHAPE"),
     (dict(K=96), "RTL_ERR_UNSUPPORTED"), (dict(K=2 ** 22), "RTL_ERR_SHAPE"), (dict(M=2 ** 31), "RTL_ERR_SHAPE"),
     (dict(M=2 ** 62), "RTL_ERR_SHAPE"), (dict(M=2 ** 30, H=2 ** 30), "RTL_ERR_SHAPE"), (dict(X=None), "RTL_ERR_NULL"),
-    (dict(Wg=None), "RTL_ERR_NULL"), (dict(X=lambda a: at(a["X"], 2)), "RTL_ERR_ALIGN"),
+    (dict(Wg=None), "RTL_ERR_NULL"), (dict(M=1, H=2 ** 28), "RTL_ERR_SHAPE"), (dict(M=2 ** 31 - 1, H=129), "RTL_ERR_SHAPE"),
+    (dict(X=lambda a: at(a["X"], 2)), "RTL_ERR_ALIGN"),
     (dict(U=lambda a: at(a["U"], 4)), "RTL_ERR_ALIGN"),
 ]
 
@@ -162,7 +169,7 @@ GLU = [
 @pytest.mark.parametrize("over,want", GLU + [
     (dict(Y=None), "RTL_ERR_NULL"), (dict(Y=lambda a: a["X"]), "RTL_ERR_ARG"), (dict(G=lambda a: a["Wu"]), "RTL_ERR_ARG"),
     (dict(U=lambda a: a["Y"]), "RTL_ERR_ARG"), (dict(G=lambda a: a["U"]), "RTL_ERR_ARG"),
-], ids=lambda v: str(v)[:40])
+], ids=label)
 def test_glu_refusals(over, want):
     st, b = glu(**over)
     refused(st, want, b, over)
@@ -174,7 +181,8 @@ def test_glu_refusals(over, want):
     (dict(dX=lambda a: a["dY"]), "RTL_ERR_ARG"), (dict(ws=lambda a: a["G"]), "RTL_ERR_ARG"),
     (dict(ws=lambda a: at(a["ws"], 8)), "RTL_ERR_ALIGN"), (dict(ws=None), "RTL_ERR_WORKSPACE"),
     (dict(wsb=64), "RTL_ERR_WORKSPACE"), (dict(H=2 ** 21), "RTL_ERR_SHAPE"), (dict(M=2 ** 22), "RTL_ERR_SHAPE"),
-], ids=lambda v: str(v)[:40])
+    (dict(M=2 ** 20, H=2 ** 15), "RTL_ERR_SHAPE"),
+], ids=label)
 def test_glu_backward_refusals(over, want):
     st, b = glu_back(**over)
     refused(st, want, b, over)
@@ -189,6 +197,10 @@ def test_python_refuses_host_tensors_and_wrong_shapes():
                           torch.zeros(8, 64, dtype=torch.bfloat16))
     assert rtl.rtl_qk_norm_rope_backward_workspace_bytes(0) == 0
     assert rtl.rtl_glu_backward_workspace_bytes(0, 64, 64) == 0
+    for M, K, H in ((2 ** 22, 64, 64), (64, 64, 2 ** 21), (64, 2 ** 22, 64), (2 ** 20, 64, 2 ** 15), (2 ** 62, 64, 2 ** 62)):
+        assert rtl.rtl_glu_backward_workspace_bytes(M, K, H) == 0
+    # more output tiles than 32 bits hold of parts: no part of a tile, P alone
+    assert rtl.rtl_glu_backward_workspace_bytes(2 ** 22 - 64, 2 ** 22 - 64, 64) == (2 ** 22 - 64) * 2 * 64 * 2
 
 
 def test_policy_objects_check_their_weights():
