@@ -108,14 +108,15 @@ def glu_forward(x, wg, wu, kind, dtype=torch.bfloat16):
     return v * u, g, u, by, bg, bu
 
 
-def glu_backward(x, wg, wu, g, u, dy, kind):
-    """dx, dwg, dwu and their bounds: dG and dU round once to bf16 (2^-8 of each; up to 2^14
+def glu_backward(x, wg, wu, g, u, dy, kind, elements=None):
+    """dx, dwg, dwu and their bounds (`elements`: of G in the call, where g holds some of its
+    rows): dG and dU round once to bf16 (2^-8 of each; up to 2^14
     elements twice, 2^-16) after an activation within act_bound; the products add as in
     glu_forward, twice as many where they run over both roundings."""
     v, s = act(g, kind)
     dg, du = dy * u * s, dy * v
     b = act_bound(g)
-    few = g.size <= 2 ** 14
+    few = (elements or g.size) <= 2 ** 14
     step = 2.0 ** -16 if few else 2.0 ** -8
     eg = np.abs(dg) * (step + 4 * U) + 1.01 * np.abs(dy * u) * b
     eu = np.abs(du) * (step + 4 * U) + 1.01 * np.abs(dy) * b
