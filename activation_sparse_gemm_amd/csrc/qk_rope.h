@@ -9,9 +9,9 @@
 //
 // Bound: memory (each element read once and written once; the gradient reads two and writes
 // one).  A group of GL lanes owns one head of one token, a lane eight channels (four pairs):
-// one 16-byte access (two of 8 where a pair's channels lie D/2 apart), the norm's sum inside
-// the group's lanes.  A group takes HC heads of its token, so that a lane's four angles are
-// formed once for HC heads and HC loads are in flight before the first is used.
+// one 16-byte access (bf16, pairs side by side) or two, the norm's sum inside the group's lanes.
+// A group takes HC heads of its token, so that a lane's four angles are formed once for HC
+// heads and HC loads are in flight before the first is used.
 //
 // Angles are formed in revolutions (pos f / 2 pi), from frequencies in two fp32 words and reduced
 // by their nearest whole number before the product is rounded, so a position as far as 2^24 loses
@@ -54,13 +54,15 @@ struct RopeArgs {
   float* part;             // backward: [workgroups][D]
 };
 
-// Eight values of a head as fp32: values 2i and 2i + 1 are pair 4 u + i of unit u.  Units at
-// or past the rotated channels hold eight consecutive channels.
+// Eight values of a head as fp32, channels lo .. lo + 3 and hi .. hi + 3: one piece of 16 bytes in bf16,
+// or two pieces where a pair's channels lie half the rotated width apart, and in fp32, whose pieces
+// then follow on from lane to lane (side by side they are 32 bytes apart: 16000 x 32 x 64 in 53
+// us against 41).  Units at or past the rotated channels hold eight consecutive channels.
 template <bool BF16, bool HALVES>
 struct RopeUnit {
   int lo, hi;  // channel of the first four values and of the last four
   __device__ __forceinline__ RopeUnit(int u, int pairs) {
-    const bool split = HALVES && 4 * u < pairs;
+    const bool split = (HALVES || !BF16) && 4 * u < pairs;
     lo = split ? 4 * u : 8 * u;
     hi = split ? 4 * u + pairs : 8 * u + 4;
   }
@@ -100,6 +102,13 @@ struct RopeUnit {
       }
     }
   }
+  template <bool PAST, typename V>
+  __device__ __forceinline__ static void put(V v, void* p) {
+    if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+    else *reinterpret_cast<V*>(p) = v;
+  }
+  // PAST: by stores that bypass the caches.
+  template <bool PAST>
   __device__ __forceinline__ void store(void* base, int64_t at, const float (&v)[8]) const {
     if (BF16) {
       typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -109,15 +118,15 @@ struct RopeUnit {
         w[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
       uint16_t* p = (uint16_t*)base + at;
       if (HALVES) {
-        __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p + lo));
-        __builtin_nontemporal_store(u32x2{w[2], w[3]}, reinterpret_cast<u32x2*>(p + hi));
+        put<PAST>(u32x2{w[0], w[1]}, p + lo);
+        put<PAST>(u32x2{w[2], w[3]}, p + hi);
       } else {
-        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(p + lo));
+        put<PAST>(u32x4{w[0], w[1], w[2], w[3]}, p + lo);
       }
     } else {
       float* p = (float*)base + at;
-      __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p + lo));
-      __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + hi));
+      put<PAST>(f32x4{v[0], v[1], v[2], v[3]}, p + lo);
+      put<PAST>(f32x4{v[4], v[5], v[6], v[7]}, p + hi);
     }
   }
   // Rotates the unit's four pairs: (2i, 2i + 1) in place, or (i, 4 + i).
@@ -133,15 +142,20 @@ struct RopeUnit {
 };
 
 // A unit's four frequencies and axes.
+template <bool BF16, bool HALVES>
 struct RopeFreq {
   f32x4 hi, lo;
   int axis[4];
   bool turned;  // false past the rotated channels
   __device__ __forceinline__ RopeFreq(const RopeArgs& a, const RopeTable& t, int u) : turned(4 * u < a.pairs) {
     if (!turned) return;
-    hi = *reinterpret_cast<const f32x4*>(t.hi + 4 * u);
-    lo = *reinterpret_cast<const f32x4*>(t.lo + 4 * u);
-    const uint32_t four = *reinterpret_cast<const uint32_t*>(t.axis + 4 * u);
+    // the pairs of the unit's first four values and of its last (the same four in RTL_ROPE_HALVES)
+    const int p0 = BF16 || HALVES ? 4 * u : 2 * u, p1 = BF16 || HALVES ? 4 * u + 2 : 2 * u + a.pairs / 2;
+    const float2 h0 = *reinterpret_cast<const float2*>(t.hi + p0), h1 = *reinterpret_cast<const float2*>(t.hi + p1);
+    const float2 l0 = *reinterpret_cast<const float2*>(t.lo + p0), l1 = *reinterpret_cast<const float2*>(t.lo + p1);
+    hi = f32x4{h0.x, h0.y, h1.x, h1.y};
+    lo = f32x4{l0.x, l0.y, l1.x, l1.y};
+    const uint32_t four = *reinterpret_cast<const uint16_t*>(t.axis + p0) | (uint32_t)*reinterpret_cast<const uint16_t*>(t.axis + p1) << 16;
 #pragma unroll
     for (int i = 0; i < 4; i++) axis[i] = (four >> (8 * i)) & 255;
   }
@@ -149,7 +163,8 @@ struct RopeFreq {
 // cos and sin (times `sign`) of the unit's four angles for token m; 1 and 0 past the rotated
 // channels.  By the hardware's instructions, which take revolutions: within 2.2 * 2^-24 of the exact
 // values at every multiple of 2^-24 in [-1/2, 1/2] (measured), as near as the library's functions.
-__device__ __forceinline__ void rope_angles(const RopeArgs& a, const RopeFreq& f, int64_t m, float (&c)[4],
+template <typename Freq>
+__device__ __forceinline__ void rope_angles(const RopeArgs& a, const Freq& f, int64_t m, float (&c)[4],
                                             float (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -197,10 +212,9 @@ __device__ __forceinline__ void rope_weights(const RopeUnit<BF16, HALVES>& un, c
 
 // The rotation, after the norm (NORM) or alone.  Measured in bf16: alone 32760 x 40 x 128 in 112-120
 // us (5.6-6.0 TB/s, where a copy of its size runs at 5.5); with the norm 32760 x 80 x 128 in 222-237
-// us (5.7-6.0) and 4608 x 48 x 128 in 20 us (5.8).  Stores that bypass the caches (the outputs are
-// read next by another kernel, from memory at these sizes) gained 8%; loads that do lost up to 20%
-// where the input still lay in the last-level cache.
-template <bool BF16, bool HALVES, bool NORM, int GL, int HC>
+// us (5.7-6.0) and 4608 x 48 x 128 in 20 us (5.8).  PAST: stores that bypass the caches (rope_past).
+// Loads that do lost up to 20% where the input still lay in the last-level cache.
+template <bool BF16, bool HALVES, bool NORM, bool PAST, int GL, int HC>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, const RopeTable t) {
   const int u = threadIdx.x % GL;
   const uint32_t item = (blockIdx.y * gridDim.x + blockIdx.x) * (kRopeThreads / GL) + threadIdx.x / GL;
@@ -220,7 +234,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
     if (j < nh) raw[j] = un.load(x.p, m * x.row + (int64_t)(h0 + j) * x.head);
   float c[4], s[4], w[8];
   if (nh > 0) {
-    rope_angles(a, RopeFreq(a, t, u), m, c, s);
+    rope_angles(a, RopeFreq<BF16, HALVES>(a, t, u), m, c, s);
     if (NORM) rope_weights<BF16, HALVES>(un, a.w[which], w);
   }
 #pragma unroll
@@ -242,7 +256,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
     }
     if (j < nh) {
       un.rotate(v, c, s);
-      un.store(y.p, m * y.row + (int64_t)(h0 + j) * y.head, v);
+      un.template store<PAST>(y.p, m * y.row + (int64_t)(h0 + j) * y.head, v);
     }
   }
 }
@@ -271,7 +285,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
   for (int i = 0; i < 8; i++) w[i] = dw[i] = 0.f;
   if (lane) rope_weights<BF16, HALVES>(un, a.w[which], w);
 
-  const RopeFreq freq(a, t, u);
+  const RopeFreq<BF16, HALVES> freq(a, t, u);
   struct Item {
     typename Unit::Raw x[HC], y[HC];
     uint32_t m;
@@ -319,7 +333,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
         dw[i] = fmaf(d[i], v[i] * r, dw[i]);
         v[i] = fmaf(wd[i], r, -(v[i] * k));
       }
-      if (lane) un.store(dx.p, at + j * dx.head, v);
+      if (lane) un.template store<true>(dx.p, at + j * dx.head, v);
     }
   };
   Item one, two;
@@ -425,6 +439,20 @@ void rope_fill(const RopeCall& c, int hc, RopeArgs& a, RopeTable& t) {
   a.sign = c.inverse ? -1.f : 1.f;
 }
 
+// Whether the outputs are stored past the caches.  That pays where a head fills whole 128-byte lines
+// (rotation of 16000 x 32 heads: 128 wide in bf16 41 us against 48, 64 in fp32 41 against 45), or
+// whole halves of them and two lines at least (112 in fp32 79 against 98; 90000 tokens 508 against
+// 488); a line that is stored in parts goes out in parts (80 in bf16 41 against 28, 120 at 90000
+// tokens 411 against 275, 48 in fp32 39 against 33).  The gradient, whose passes are slower, gains or
+// is even at every width tried (64 to 128, 16000 x 32: 0-17%) and always stores so.
+bool rope_past(const RopeCall& c) {
+  const int64_t es = c.dt == kDtBF16 ? 2 : 4, width = c.D * es;
+  uint64_t bits = (uint64_t)width;
+  for (int k = 0; k < (c.H[1] > 0 ? 2 : 1); k++)
+    bits |= (uint64_t)(uintptr_t)c.y[k].p | (uint64_t)(c.y[k].row * es) | (uint64_t)(c.y[k].head * es);
+  return bits % 128 == 0 || (bits % 64 == 0 && width >= 256);
+}
+
 template <bool BF16, bool HALVES, bool NORM, int GL>
 void rope_launch(const RopeCall& c, hipStream_t stream) {
   RopeArgs a;
@@ -434,10 +462,15 @@ void rope_launch(const RopeCall& c, hipStream_t stream) {
   // rows of 2^20 workgroups: a launch takes fewer than 2^32 threads in one dimension
   const uint32_t blocks = (a.items + kRopeThreads / GL - 1) / (kRopeThreads / GL), row = std::min(blocks, 1u << 20);
   const dim3 grid(row, (blocks + row - 1) / row), block(kRopeThreads);
-  if (hc == 8) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, GL, 8>), grid, block, 0, stream, a, t);
-  else if (hc == 4) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, GL, 4>), grid, block, 0, stream, a, t);
-  else if (hc == 2) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, GL, 2>), grid, block, 0, stream, a, t);
-  else hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, GL, 1>), grid, block, 0, stream, a, t);
+  auto go = [&](auto p) {
+    constexpr bool P = decltype(p)::value;
+    if (hc == 8) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, P, GL, 8>), grid, block, 0, stream, a, t);
+    else if (hc == 4) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, P, GL, 4>), grid, block, 0, stream, a, t);
+    else if (hc == 2) hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, P, GL, 2>), grid, block, 0, stream, a, t);
+    else hipLaunchKernelGGL((rope_kernel<BF16, HALVES, NORM, P, GL, 1>), grid, block, 0, stream, a, t);
+  };
+  if (rope_past(c)) go(std::true_type());
+  else go(std::false_type());
 }
 
 template <bool BF16, bool HALVES, int GL>
