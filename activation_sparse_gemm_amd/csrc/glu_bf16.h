@@ -47,8 +47,9 @@ __device__ __forceinline__ ActValue glu_act(float g) {
   return {g * p, fmaf(g, 0.39894228040143268f * e, p)};
 }
 
-// N (2 or 4) consecutive values of row `row` from column `col` on, rounded to bf16 (nearest even).
-template <int N>
+// N (2 or 4) consecutive values of row `row` from column `col` on, rounded to bf16 (nearest even);
+// PAST: fours by stores that bypass the caches.
+template <int N, bool PAST>
 __device__ __forceinline__ void store_cols(uint16_t* Y, int64_t M, int64_t H, int64_t row, int64_t col,
                                            const float (&v)[N]) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -59,7 +60,8 @@ __device__ __forceinline__ void store_cols(uint16_t* Y, int64_t M, int64_t H, in
   if (row >= M) return;
   uint16_t* y = Y + row * H + col;
   if (H % N == 0 && col + N <= H) {
-    if constexpr (N == 4) __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(y));
+    if constexpr (N == 4 && PAST) __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(y));
+    else if constexpr (N == 4) *reinterpret_cast<u32x2*>(y) = u32x2{w[0], w[1]};
     else *reinterpret_cast<uint32_t*>(y) = w[0];
   } else {
 #pragma unroll
@@ -79,8 +81,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // holds NB / 2 consecutive columns over its blocks.  Measured: 32760 x 5120 x 13824 6.0-6.3 ms
 // (1.48-1.54 PFLOP/s; the matrix cores 78% busy at the 1.8 GHz that the power limit leaves), 4173 x
 // 2560 x 6916 with GELU, G and U kept 268 us (1.10): 935 tiles take four rounds of 256, and of a
-// tile's 67 us the first loads and the stores of three outputs 17.
-template <int ACT, int RB, int NB, int WM, int WN, int DEPTH>
+// tile's 67 us the first loads and the stores of three outputs 17.  PAST: G and U bypass the caches as
+// Y does, which pays (257 us against 265 at 4173 x 2560 x 6912) unless rows end inside a
+// 64-byte piece, whose parts then go out one by one (280 against 270 at 6916, 4096 x 640 x 8196 164
+// against 153); Y alone is even or 3% better so at every width.
+template <int ACT, int RB, int NB, int WM, int WN, int DEPTH, bool PAST>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(RB == 8 ? 1 : 2, RB == 8 ? 1 : 2)))
 void glu_kernel(const GluArgs a) {
   static_assert(WM * WN == kRingWaves, "four waves");
@@ -133,9 +138,9 @@ void glu_kernel(const GluArgs a) {
         u[e] = acc[rb][NC + e][j];
         y[e] = glu_act<ACT>(g[e]).v * u[e];
       }
-      store_cols<NC>(a.Y, M, H, row, col, y);
-      if (a.G != nullptr) store_cols<NC>(a.G, M, H, row, col, g);
-      if (a.U != nullptr) store_cols<NC>(a.U, M, H, row, col, u);
+      store_cols<NC, true>(a.Y, M, H, row, col, y);
+      if (a.G != nullptr) store_cols<NC, PAST>(a.G, M, H, row, col, g);
+      if (a.U != nullptr) store_cols<NC, PAST>(a.U, M, H, row, col, u);
     }
   }
 }
@@ -238,12 +243,12 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
 
 namespace {
 
-template <int ACT, int RB, int NB, int WM, int WN, int DEPTH>
+template <int ACT, int RB, int NB, int WM, int WN, int DEPTH, bool PAST = true>
 void glu_tiles(GluArgs a, hipStream_t stream) {
   constexpr int BM = 16 * RB * WM, BH = 8 * NB * WN;
   a.tiles_m = (int)((a.M + BM - 1) / BM);
   a.tiles_n = (int)((a.H + BH - 1) / BH);
-  hipLaunchKernelGGL((glu_kernel<ACT, RB, NB, WM, WN, DEPTH>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((glu_kernel<ACT, RB, NB, WM, WN, DEPTH, PAST>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
 }
 
 template <int ACT, int MB>
@@ -268,7 +273,8 @@ void glu_launch(const GluArgs& a, hipStream_t stream) {
   else if (tiles <= 128) glu_tiles<ACT, 2, 4, 4, 1, 4>(a, stream);
   else if (tiles <= 256) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
   else if (tiles <= 512) glu_tiles<ACT, 4, 4, 2, 2, 2>(a, stream);
-  else glu_tiles<ACT, 8, 8, 2, 2, 2>(a, stream);
+  else if (a.H % 32 == 0 || (a.G == nullptr && a.U == nullptr)) glu_tiles<ACT, 8, 8, 2, 2, 2>(a, stream);
+  else glu_tiles<ACT, 8, 8, 2, 2, 2, false>(a, stream);
 }
 
 }  // namespace
