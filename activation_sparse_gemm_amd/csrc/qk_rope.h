@@ -443,8 +443,10 @@ void rope_fill(const RopeCall& c, int hc, RopeArgs& a, RopeTable& t) {
 // (rotation of 16000 x 32 heads: 128 wide in bf16 41 us against 48, 64 in fp32 41 against 45), or
 // whole halves of them and two lines at least (112 in fp32 79 against 98; 90000 tokens 508 against
 // 488); a line that is stored in parts goes out in parts (80 in bf16 41 against 28, 120 at 90000
-// tokens 411 against 275, 48 in fp32 39 against 33).  The gradient, whose passes are slower, gains or
-// is even at every width tried (64 to 128, 16000 x 32: 0-17%) and always stores so.
+// tokens 411 against 275, 48 in fp32 39 against 33).  The gradient always stores so: it gains up to 17%
+// where a head fills lines (16000 x 32 x 128 in bf16 73 us against 85) and elsewhere loses at
+// most as much at many tokens (60000 x 32 x 56: 158 against 131) and gains it at fewer (16000 x
+// 32 x 56 in fp32 67 against 77, 4000 tokens 3-8%).
 bool rope_past(const RopeCall& c) {
   const int64_t es = c.dt == kDtBF16 ? 2 : 4, width = c.D * es;
   uint64_t bits = (uint64_t)width;
