@@ -269,7 +269,22 @@ void glu_rows(const GluArgs& a, hipStream_t stream) {
 //  - at most half as many tiles as CUs: half as wide ones (100 x 6912: 20 against 25);
 //  - at most one to a CU: four steps ahead, since nothing else hides a load (200 x 6912: 27
 //    against 33; 100 x 10000, K = 5120: 41 against 53);
-//  - at most two to a CU, then 256 x 128 tiles (900 x 5000, 640 tiles: 60 against 65).
+//  - at most two to a CU, or more where glu_small says so; else 256 x 128 tiles (900 x 5000, 640
+//    tiles: 52 against 65).
+
+// Whether more than two 128 x 64 tiles a CU take less time than 256 x 128 tiles: costs in
+// microseconds fitted to measured calls.  A large tile costs 1.15 a K step and 9 for its first
+// loads and its stores, which nothing covers, and a round of 256 lasts as long as its tiles; two
+// small ones a CU cost 0.8 a step and 4.2, a last round of one to a CU about two thirds.  (Small
+// against large: 3324 x 64 x 10672 72 and 94, 2048 x 2560 x 5120 98 and 110, 564 x 128 x 12712 24
+// and 39; 4173 x 2560 x 6916 266 and 227, 1024 x 5120 x 13824 277 and 221.)
+inline bool glu_small(int64_t M, int64_t K, int64_t H) {
+  const int64_t large = ((M + 255) / 256) * ((H + 127) / 128), small = ((M + 127) / 128) * ((H + 63) / 64);
+  const double steps = (double)(K / kRK), rest = (double)(small % 512);
+  const double rounds = (double)(small / 512) + (rest > 256 ? 1. : rest > 0 ? 0.65 : 0.);
+  return rounds * (0.8 * steps + 4.2) < (double)((large + 255) / 256) * (1.15 * steps + 9.);
+}
+
 template <int ACT>
 void glu_launch(const GluArgs& a, hipStream_t stream) {
   const int64_t tiles = ((a.M + 127) / 128) * ((a.H + 63) / 64);
@@ -278,7 +293,7 @@ void glu_launch(const GluArgs& a, hipStream_t stream) {
   else if (a.M <= 64 && tiles < 171) glu_rows<ACT, 4>(a, stream);
   else if (tiles <= 128) glu_tiles<ACT, 2, 4, 4, 1, 4>(a, stream);
   else if (tiles <= 256) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
-  else if (tiles <= 512) glu_tiles<ACT, 4, 4, 2, 2, 2>(a, stream);
+  else if (tiles <= 512 || glu_small(a.M, a.K, a.H)) glu_tiles<ACT, 4, 4, 2, 2, 2>(a, stream);
   else if (a.H % 32 == 0 || (a.G == nullptr && a.U == nullptr)) glu_tiles<ACT, 8, 8, 2, 2, 2>(a, stream);
   else glu_tiles<ACT, 8, 8, 2, 2, 2, false>(a, stream);
 }

@@ -37,11 +37,15 @@ SHAPES = [
 ]
 
 
+# the forward product's larger tiles: rows that end on a 128-byte line, inside one, and at an odd address
+LARGE = [(1700, 768, 4096), (1700, 768, 4100), (1601, 832, 3841), (1030, 1024, 5003)]
+
+
 def label(c):
     return "x".join(map(str, c))
 
 
-@pytest.mark.parametrize("c", SHAPES, ids=label)
+@pytest.mark.parametrize("c", SHAPES + LARGE, ids=label)
 @pytest.mark.parametrize("kind", (0, 1), ids=("silu", "gelu"))
 def test_glu_fused(c, kind):
     M, K, H = c
