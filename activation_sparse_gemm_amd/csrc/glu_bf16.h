@@ -87,10 +87,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // holds NB / 2 consecutive columns over its blocks.  Measured: 32760 x 5120 x 13824 6.0-6.3 ms
 // (1.48-1.54 PFLOP/s; the matrix cores 78% busy at the 1.8 GHz that the power limit leaves), 4173 x
 // 2560 x 6916 with GELU, G and U kept 268 us (1.10): 935 tiles take four rounds of 256, and of a
-// tile's 67 us the first loads and the stores of three outputs 17.  PAST: G and U bypass the caches as
-// Y does, which pays (257 us against 265 at 4173 x 2560 x 6912) unless rows end inside a
-// 64-byte piece, whose parts then go out one by one (280 us against 270 at 6916, 4096 x 640 x 8196 164
-// against 153); Y alone is even or 3% better so at every width.
+// tile's 67 us the first loads and the stores of three outputs 17.  PAST: outputs bypass the caches,
+// which pays (4173 x 2560 x 6912 with G and U 257 us against 265, 24830 x 192 x 4672 223 against
+// 235) unless rows end inside a 64-byte piece, whose parts then go out one by one (24830 x 192 x
+// 4666 179 against 152, 4096 x 640 x 8196 with G and U 164 against 153).
 template <int ACT, int RB, int NB, int WM, int WN, int DEPTH, bool PAST>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(RB == 8 ? 1 : 2, RB == 8 ? 1 : 2)))
 void glu_kernel(const GluArgs a) {
@@ -144,7 +144,7 @@ void glu_kernel(const GluArgs a) {
         u[e] = acc[rb][NC + e][j];
         y[e] = glu_act<ACT>(g[e]).v * u[e];
       }
-      store_cols<NC, true>(a.Y, M, H, row, col, y);
+      store_cols<NC, PAST>(a.Y, M, H, row, col, y);
       if (a.G != nullptr) store_cols<NC, PAST>(a.G, M, H, row, col, g);
       if (a.U != nullptr) store_cols<NC, PAST>(a.U, M, H, row, col, u);
     }
@@ -249,12 +249,14 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
 
 namespace {
 
-template <int ACT, int RB, int NB, int WM, int WN, int DEPTH, bool PAST = true>
+template <int ACT, int RB, int NB, int WM, int WN, int DEPTH>
 void glu_tiles(GluArgs a, hipStream_t stream) {
   constexpr int BM = 16 * RB * WM, BH = 8 * NB * WN;
   a.tiles_m = (int)((a.M + BM - 1) / BM);
   a.tiles_n = (int)((a.H + BH - 1) / BH);
-  hipLaunchKernelGGL((glu_kernel<ACT, RB, NB, WM, WN, DEPTH, PAST>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream, a);
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(256);
+  if (NB == 4 || a.H % 32 == 0) hipLaunchKernelGGL((glu_kernel<ACT, RB, NB, WM, WN, DEPTH, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((glu_kernel<ACT, RB, NB, WM, WN, DEPTH, NB == 4>), grid, block, 0, stream, a);
 }
 
 template <int ACT, int MB>
@@ -262,15 +264,6 @@ void glu_rows(const GluArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((glu_rows_kernel<ACT, MB>), dim3((unsigned)((a.H + 15) / 16)), dim3(64 * kRingWaves), 0, stream,
                      a);
 }
-
-// By rows, then by the number of 128 x 64 tiles (microseconds at K = 2560 where none is given):
-//  - up to 32 rows, and up to 64 where such tiles would leave a third of the CUs without one: the
-//    weights streamed (64 x 6912, 108 tiles: 21 against 25; 64 x 13824, K = 5120, 216: 75 against 53);
-//  - at most half as many tiles as CUs: half as wide ones (100 x 6912: 20 against 25);
-//  - at most one to a CU: four steps ahead, since nothing else hides a load (200 x 6912: 27
-//    against 33; 100 x 10000, K = 5120: 41 against 53);
-//  - at most two to a CU, or more where glu_small says so; else 256 x 128 tiles (900 x 5000, 640
-//    tiles: 52 against 65).
 
 // Whether more than two 128 x 64 tiles a CU take less time than 256 x 128 tiles: costs in
 // microseconds fitted to measured calls.  A large tile costs 1.15 a K step and 9 for its first
@@ -285,6 +278,18 @@ inline bool glu_small(int64_t M, int64_t K, int64_t H) {
   return rounds * (0.8 * steps + 4.2) < (double)((large + 255) / 256) * (1.15 * steps + 9.);
 }
 
+// By rows, then by the number of 128 x 64 tiles (microseconds at K = 2560 where none is given):
+//  - up to 32 rows, and up to 64 where such tiles would leave a third of the CUs without one: the
+//    weights streamed (64 x 6912, 108 tiles: 21 against 25; 64 x 13824, K = 5120, 216: 75 against 53);
+//  - at most half as many tiles as CUs: half as wide ones (100 x 6912: 20 against 25);
+//  - at most one to a CU: four steps ahead, since nothing else hides a load (200 x 6912: 27
+//    against 33; 100 x 10000, K = 5120: 41 against 53);
+//  - at most two to a CU, or more where glu_small says so; else 256 x 128 tiles (900 x 5000, 640
+//    tiles: 52 against 65).
+// Waves of 32 x 128 store whole 128-byte lines, waves of 64 x 64 read a fifth less from LDS: the
+// former but for one tile to a CU and K above 1280 (128 x 13824 at K = 640 with G and U 15 against
+// 17, 564 x 12712 at K = 128 22 against 26, 500 x 6912 43 against 42.5; four ahead 200 x 6912 26.5
+// against 25, 100 x 10000 at K = 5120 43 against 40).
 template <int ACT>
 void glu_launch(const GluArgs& a, hipStream_t stream) {
   const int64_t tiles = ((a.M + 127) / 128) * ((a.H + 63) / 64);
@@ -292,10 +297,10 @@ void glu_launch(const GluArgs& a, hipStream_t stream) {
   else if (a.M <= 32) glu_rows<ACT, 2>(a, stream);
   else if (a.M <= 64 && tiles < 171) glu_rows<ACT, 4>(a, stream);
   else if (tiles <= 128) glu_tiles<ACT, 2, 4, 4, 1, 4>(a, stream);
-  else if (tiles <= 256) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
-  else if (tiles <= 512 || glu_small(a.M, a.K, a.H)) glu_tiles<ACT, 4, 4, 2, 2, 2>(a, stream);
-  else if (a.H % 32 == 0 || (a.G == nullptr && a.U == nullptr)) glu_tiles<ACT, 8, 8, 2, 2, 2>(a, stream);
-  else glu_tiles<ACT, 8, 8, 2, 2, 2, false>(a, stream);
+  else if (tiles <= 256 && a.K > 1280) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
+  else if (tiles <= 256) glu_tiles<ACT, 2, 8, 4, 1, 4>(a, stream);
+  else if (tiles <= 512 || glu_small(a.M, a.K, a.H)) glu_tiles<ACT, 2, 8, 4, 1, 2>(a, stream);
+  else glu_tiles<ACT, 8, 8, 2, 2, 2>(a, stream);
 }
 
 }  // namespace

@@ -37,8 +37,10 @@ SHAPES = [
 ]
 
 
-# the forward product's larger tiles: rows that end on a 128-byte line, inside one, and at an odd address
-LARGE = [(1700, 768, 4096), (1700, 768, 4100), (1601, 832, 3841), (1030, 1024, 5003)]
+# the forward product's larger tiles and its small ones one and two to a CU: rows that end on a
+# 128-byte line, inside one, and at an odd address
+LARGE = [(300, 640, 4000), (300, 640, 4003), (200, 1408, 5001), (520, 192, 4096), (520, 192, 4099),
+         (1700, 768, 4096), (1700, 768, 4100), (1601, 832, 3841), (1030, 1024, 5003)]
 
 
 def label(c):
