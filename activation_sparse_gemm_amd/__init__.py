@@ -19,6 +19,12 @@ import os
 
 import torch
 
+try:  # the allocation alone, without the parsing of torch.empty_strided's arguments (half the time)
+    from torch._C._dynamo.guards import _empty_strided_cuda as _empty_cuda
+except ImportError:
+    def _empty_cuda(shape, stride, dtype):
+        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+
 __all__ = [
     "RTL_F32", "RTL_BF16", "RTL_TIE_LOWER_INDEX", "EPS", "RtlError", "lib", "library_path",
     "rtl_sparsify", "rtl_linear_fused", "rtl_linear_fused_workspace_bytes", "rtl_linear_fused_ex",
@@ -373,37 +379,52 @@ def _one_device(first, *rest):
     return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
-def _expect(name, t, shape, dtype):
-    if t is not None and (t.dtype is not dtype or t.shape != shape):
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _mismatch(name, t, shape, dtype):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _flat(t):
-    """Address of a contiguous tensor on the GPU (None: null)."""
+def _flat(name, t, shape, dtype):
+    """Address of a contiguous tensor of `shape` and `dtype` (None: null)."""
     if t is None:
         return None
+    if t.shape != shape or t.dtype is not dtype:
+        _mismatch(name, t, shape, dtype)
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
 
 
-def _heads(t):
-    """Address, row stride and head stride of a [M, H, D] tensor whose channels are contiguous."""
+_NO_HEADS = None, 0, 0
+
+
+def _heads(name, t, shape, dtype):
+    """Address, row stride and head stride of a tensor of `shape` [M, H, D] and `dtype` whose
+    channels are contiguous (None: null)."""
     if t is None:
-        return None, 0, 0
+        return _NO_HEADS
+    if t.shape != shape or t.dtype is not dtype:
+        _mismatch(name, t, shape, dtype)
     row, head, channel = t.stride()
-    if channel != 1 and t.shape[2] > 1:
+    if channel != 1 and shape[2] > 1:
         raise ValueError("the channels of a head must be contiguous")
     return t.data_ptr(), row, head
 
 
+def _space(t):
+    """Address and bytes of a workspace."""
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _new(stream, like, shape, dtype):
-    """A tensor on `like`'s device, as _empty allocates it."""
+    """A tensor on `like`'s device (the current one), as _empty allocates it."""
     if stream is not None:
         return _empty(shape, dtype, like.device, stream)
-    return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
+    n = len(shape)
+    return _empty_cuda(shape, (shape[1] * shape[2], shape[2], 1) if n == 3 else (shape[1], 1) if n == 2 else (1,), dtype)
 
 
 def _queue(stream, like):
@@ -424,8 +445,7 @@ def _rope_args(pos, axis_dims, theta, pairs, M):
     dims = tuple(axis_dims)
     if not dims:
         return None, 0, _dims(dims), theta, pairs
-    _expect("pos", pos, (M, len(dims)), torch.float32)
-    return _flat(pos), len(dims), _dims(dims), theta, pairs
+    return _flat("pos", pos, (M, len(dims)), torch.float32), len(dims), _dims(dims), theta, pairs
 
 
 def rtl_rope_axes(X: torch.Tensor, pos: torch.Tensor, axis_dims, theta: float = 10000.0,
@@ -436,13 +456,13 @@ def rtl_rope_axes(X: torch.Tensor, pos: torch.Tensor, axis_dims, theta: float = 
     most D).  ``pairs``: RTL_ROPE_ADJACENT pairs channels 2p and 2p + 1, RTL_ROPE_HALVES p and
     p + sum / 2.  ``inverse`` turns back, which is also the gradient.  ``Y`` may be X."""
     M, H, D = X.shape
+    shape, dt = (M, H, D), X.dtype
     with _one_device(X, pos, Y):
         if Y is None:
-            Y = _new(stream, X, (M, H, D), X.dtype)
-        else:
-            _expect("Y", Y, (M, H, D), X.dtype)
-        _check(lib.rtl_rope_axes(_dt(X), M, H, D, *_heads(X), *_rope_args(pos, axis_dims, theta, pairs, M),
-                                 bool(inverse), *_heads(Y), _queue(stream, X)))
+            Y = _new(stream, X, shape, dt)
+        _check(lib.rtl_rope_axes(_dt(X), M, H, D, *_heads("X", X, shape, dt),
+                                 *_rope_args(pos, axis_dims, theta, pairs, M), bool(inverse),
+                                 *_heads("Y", Y, shape, dt), _queue(stream, X)))
     return Y
 
 
@@ -454,24 +474,20 @@ def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 
     by the caller are written in place and may be Q and K."""
     M, Hq, D = Q.shape
     dt = Q.dtype
-    Hk = 0 if K is None else K.shape[1]
+    qs, ks, ws = (M, Hq, D), (M, 0 if K is None else K.shape[1], D), (D,)
     with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, Qo, Ko):
         if Qo is None:
-            Qo = _new(stream, Q, (M, Hq, D), dt)
-        else:
-            _expect("Qo", Qo, (M, Hq, D), dt)
+            Qo = _new(stream, Q, qs, dt)
+        keys, keys_out, kw_at = _NO_HEADS, _NO_HEADS, None
         if K is not None:
-            _expect("K", K, (M, Hk, D), dt)
             if Ko is None:
-                Ko = _new(stream, Q, (M, Hk, D), dt)
-            else:
-                _expect("Ko", Ko, (M, Hk, D), dt)
-            _expect("kw", kw, (D,), dt)
+                Ko = _new(stream, Q, ks, dt)
+            keys, keys_out, kw_at = _heads("K", K, ks, dt), _heads("Ko", Ko, ks, dt), _flat("kw", kw, ws, dt)
         elif Ko is not None:
             raise ValueError("Ko without K")
-        _expect("qw", qw, (D,), dt)
-        _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _flat(qw), _flat(kw), eps,
-                                    *_rope_args(pos, axis_dims, theta, pairs, M), *_heads(Qo), *_heads(Ko),
+        _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, ks[1], D, *_heads("Q", Q, qs, dt), *keys,
+                                    _flat("qw", qw, ws, dt), kw_at, eps,
+                                    *_rope_args(pos, axis_dims, theta, pairs, M), *_heads("Qo", Qo, qs, dt), *keys_out,
                                     _queue(stream, Q)))
     return Qo, Ko
 
@@ -488,38 +504,30 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
     caller are written in place; dQ and dK may be dQo and dKo, or Q and K."""
     M, Hq, D = Q.shape
     dt = Q.dtype
-    Hk = 0 if K is None else K.shape[1]
+    qs, ks, ws = (M, Hq, D), (M, 0 if K is None else K.shape[1], D), (D,)
     with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, dQo, dKo, dQ, dK, dqw, dkw, workspace):
-        _expect("dQo", dQo, (M, Hq, D), dt)
-        _expect("qw", qw, (D,), dt)
         if dQ is None:
-            dQ = _new(stream, Q, (M, Hq, D), dt)
-        else:
-            _expect("dQ", dQ, (M, Hq, D), dt)
+            dQ = _new(stream, Q, qs, dt)
         if dqw is None:
             dqw = _new(stream, Q, (D,), torch.float32)
-        else:
-            _expect("dqw", dqw, (D,), torch.float32)
+        keys, grads, grads_out, kw_at, dkw_at = _NO_HEADS, _NO_HEADS, _NO_HEADS, None, None
         if K is not None:
-            _expect("K", K, (M, Hk, D), dt)
-            _expect("dKo", dKo, (M, Hk, D), dt)
-            _expect("kw", kw, (D,), dt)
             if dK is None:
-                dK = _new(stream, Q, (M, Hk, D), dt)
-            else:
-                _expect("dK", dK, (M, Hk, D), dt)
+                dK = _new(stream, Q, ks, dt)
             if dkw is None:
                 dkw = _new(stream, Q, (D,), torch.float32)
-            else:
-                _expect("dkw", dkw, (D,), torch.float32)
+            keys, grads, grads_out = _heads("K", K, ks, dt), _heads("dKo", dKo, ks, dt), _heads("dK", dK, ks, dt)
+            kw_at, dkw_at = _flat("kw", kw, ws, dt), _flat("dkw", dkw, ws, torch.float32)
         elif dKo is not None or dK is not None or dkw is not None:
             raise ValueError("dKo, dK or dkw without K")
         if workspace is None:
             workspace = _new(stream, Q, (max(rtl_qk_norm_rope_backward_workspace_bytes(D), 1),), torch.uint8)
-        _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, Hk, D, *_heads(Q), *_heads(K), _flat(qw), _flat(kw), eps,
-                                             *_rope_args(pos, axis_dims, theta, pairs, M), *_heads(dQo), *_heads(dKo),
-                                             *_heads(dQ), *_heads(dK), _flat(dqw), _flat(dkw), _flat(workspace),
-                                             workspace.numel() * workspace.element_size(), _queue(stream, Q)))
+        _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, ks[1], D, *_heads("Q", Q, qs, dt), *keys,
+                                             _flat("qw", qw, ws, dt), kw_at, eps,
+                                             *_rope_args(pos, axis_dims, theta, pairs, M),
+                                             *_heads("dQo", dQo, qs, dt), *grads, *_heads("dQ", dQ, qs, dt), *grads_out,
+                                             _flat("dqw", dqw, ws, torch.float32), dkw_at, *_space(workspace),
+                                             _queue(stream, Q)))
     return dQ, dK, dqw, dkw
 
 
@@ -529,21 +537,13 @@ def rtl_glu_fused(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: int 
     ``G`` and ``U`` [M,H], when given, receive the two products (rtl_glu_backward takes them)."""
     M, K = X.shape
     H = Wg.shape[0]
-    bf16 = torch.bfloat16
+    xs, ws, ys, bf16 = (M, K), (H, K), (M, H), torch.bfloat16
     with _one_device(X, Wg, Wu, Y, G, U):
-        _expect("X", X, (M, K), bf16)
-        _expect("Wg", Wg, (H, K), bf16)
-        _expect("Wu", Wu, (H, K), bf16)
         if Y is None:
-            Y = _new(stream, X, (M, H), bf16)
-        else:
-            _expect("Y", Y, (M, H), bf16)
-        if G is not None:
-            _expect("G", G, (M, H), bf16)
-        if U is not None:
-            _expect("U", U, (M, H), bf16)
-        _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _flat(X), _flat(Wg), _flat(Wu), _flat(Y), _flat(G), _flat(U),
-                                 _queue(stream, X)))
+            Y = _new(stream, X, ys, bf16)
+        _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _flat("X", X, xs, bf16), _flat("Wg", Wg, ws, bf16),
+                                 _flat("Wu", Wu, ws, bf16), _flat("Y", Y, ys, bf16), _flat("G", G, ys, bf16),
+                                 _flat("U", U, ys, bf16), _queue(stream, X)))
     return Y
 
 
@@ -559,24 +559,21 @@ def rtl_glu_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: tor
     caller are written in place; pass ``workspace`` (uint8) to keep the call free of allocations."""
     M, K = X.shape
     H = Wg.shape[0]
-    bf16 = torch.bfloat16
+    xs, ws, ys, bf16 = (M, K), (H, K), (M, H), torch.bfloat16
     with _one_device(X, Wg, Wu, G, U, dY, dX, dWg, dWu, workspace):
         if not need_dx:
             dX = None
         elif dX is None:
-            dX = _new(stream, X, (M, K), bf16)
+            dX = _new(stream, X, xs, bf16)
         if not need_dw:
             dWg = dWu = None
         else:
-            dWg = _new(stream, X, (H, K), bf16) if dWg is None else dWg
-            dWu = _new(stream, X, (H, K), bf16) if dWu is None else dWu
-        for name, t, shape in (("X", X, (M, K)), ("Wg", Wg, (H, K)), ("Wu", Wu, (H, K)), ("G", G, (M, H)),
-                               ("U", U, (M, H)), ("dY", dY, (M, H)), ("dX", dX, (M, K)), ("dWg", dWg, (H, K)),
-                               ("dWu", dWu, (H, K))):
-            _expect(name, t, shape, bf16)
+            dWg = _new(stream, X, ws, bf16) if dWg is None else dWg
+            dWu = _new(stream, X, ws, bf16) if dWu is None else dWu
         if workspace is None:
             workspace = _new(stream, X, (max(rtl_glu_backward_workspace_bytes(M, K, H), 1),), torch.uint8)
-        _check(lib.rtl_glu_backward(act, RTL_BF16, M, K, H, _flat(X), _flat(Wg), _flat(Wu), _flat(G), _flat(U),
-                                    _flat(dY), _flat(dX), _flat(dWg), _flat(dWu), _flat(workspace),
-                                    workspace.numel() * workspace.element_size(), _queue(stream, X)))
+        _check(lib.rtl_glu_backward(act, RTL_BF16, M, K, H, _flat("X", X, xs, bf16), _flat("Wg", Wg, ws, bf16),
+                                    _flat("Wu", Wu, ws, bf16), _flat("G", G, ys, bf16), _flat("U", U, ys, bf16),
+                                    _flat("dY", dY, ys, bf16), _flat("dX", dX, xs, bf16), _flat("dWg", dWg, ws, bf16),
+                                    _flat("dWu", dWu, ws, bf16), *_space(workspace), _queue(stream, X)))
     return dX, dWg, dWu
