@@ -151,7 +151,7 @@ void glu_kernel(const GluArgs a) {
   }
 }
 
-// Few rows (M <= 16 MB): a workgroup forms 16 output columns; wave w takes the K steps w, w + 4, ...
+// Few rows, or few outputs: a workgroup forms 16 MB rows of 16 output columns; wave w takes the K steps w, w + 4, ...
 // of 64, each with a ring of D LDS slots of its own (16 gate rows, 16 up rows and the rows of X,
 // in whole 128-byte lines that go straight to LDS) and no barrier, and the waves' sums are added
 // in wave order.  Bound by the weights' bytes: 1 x 5120 x 13824 reads 283 MB in 44-47 us (6.0-6.4
@@ -167,7 +167,9 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r16 = lane & 15;
-  const int64_t M = a.M, K = a.K, H = a.H, n0 = (int64_t)blockIdx.x * 16;
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MB), M = min(a.M - m0, (int64_t)(16 * MB));
+  const int64_t K = a.K, H = a.H, n0 = (int64_t)blockIdx.x * 16;
+  const uint16_t* X = a.X + m0 * K;
   const int KT = (int)(K / kBK);
   uint8_t* const ring = lds + wave * (D * SLOT);
   const KRows<256> op(K, 1, 0, lane);  // eight rows a load, block by block
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
     const bool live = s < KT;  // past the end: zeros
     const int koff = live ? s * (kBK * 2) : 0;
     const __amdgpu_buffer_rsrc_t gr = rsrc_if(live, a.Wg + n0 * K, (H - n0) * K * 2),
-                                 ur = rsrc_if(live, a.Wu + n0 * K, (H - n0) * K * 2), xr = rsrc_if(live, a.X, M * K * 2);
+                                 ur = rsrc_if(live, a.Wu + n0 * K, (H - n0) * K * 2), xr = rsrc_if(live, X, M * K * 2);
     auto one = [&](__amdgpu_buffer_rsrc_t res, int at, int row) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (__attribute__((address_space(3))) void*)(slot + at * 1024), 16, op.voff,
                                                (int)(row * K * 2) + koff, 0, 0);
@@ -240,9 +242,10 @@ __global__ __launch_bounds__(64 * kRingWaves) void glu_rows_kernel(const GluArgs
     for (int j = 0; j < 4; j++) {
       const int64_t row = 16 * mb + 4 * q + j;
       if (row >= M || col >= H) continue;
-      a.Y[row * H + col] = __builtin_bit_cast(uint16_t, (__bf16)(glu_act<ACT>(g[j]).v * u[j]));
-      if (a.G != nullptr) a.G[row * H + col] = __builtin_bit_cast(uint16_t, (__bf16)g[j]);
-      if (a.U != nullptr) a.U[row * H + col] = __builtin_bit_cast(uint16_t, (__bf16)u[j]);
+      const int64_t at = (m0 + row) * H + col;
+      a.Y[at] = __builtin_bit_cast(uint16_t, (__bf16)(glu_act<ACT>(g[j]).v * u[j]));
+      if (a.G != nullptr) a.G[at] = __builtin_bit_cast(uint16_t, (__bf16)g[j]);
+      if (a.U != nullptr) a.U[at] = __builtin_bit_cast(uint16_t, (__bf16)u[j]);
     }
   }
 }
@@ -261,8 +264,8 @@ void glu_tiles(GluArgs a, hipStream_t stream) {
 
 template <int ACT, int MB>
 void glu_rows(const GluArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((glu_rows_kernel<ACT, MB>), dim3((unsigned)((a.H + 15) / 16)), dim3(64 * kRingWaves), 0, stream,
-                     a);
+  const dim3 grid((unsigned)((a.H + 15) / 16), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
+  hipLaunchKernelGGL((glu_rows_kernel<ACT, MB>), grid, dim3(64 * kRingWaves), 0, stream, a);
 }
 
 // Whether more than two 128 x 64 tiles a CU take less time than 256 x 128 tiles: costs in
@@ -281,6 +284,9 @@ inline bool glu_small(int64_t M, int64_t K, int64_t H) {
 // By rows, then by the number of 128 x 64 tiles (microseconds at K = 2560 where none is given):
 //  - up to 32 rows, and up to 64 where such tiles would leave a third of the CUs without one: the
 //    weights streamed (64 x 6912, 108 tiles: 21 against 25; 64 x 13824, K = 5120, 216: 75 against 53);
+//  - few outputs: the same kernel, whose waves share K, in workgroups of 16 rows up to one to two
+//    CUs, of 32 or 64 up to one to a CU (80 x 121, K = 5120: 9.5 against 25; 437 x 400: 13 against
+//    16.4, with 441 workgroups of 64 rows, 437 x 1000, 21.8 against 17.6);
 //  - at most half as many tiles as CUs: half as wide ones (100 x 6912: 20 against 25);
 //  - at most one to a CU: four steps ahead, since nothing else hides a load (200 x 6912: 27
 //    against 33; 100 x 10000, K = 5120: 41 against 53);
@@ -293,9 +299,10 @@ inline bool glu_small(int64_t M, int64_t K, int64_t H) {
 template <int ACT>
 void glu_launch(const GluArgs& a, hipStream_t stream) {
   const int64_t tiles = ((a.M + 127) / 128) * ((a.H + 63) / 64);
-  if (a.M <= 16) glu_rows<ACT, 1>(a, stream);
-  else if (a.M <= 32) glu_rows<ACT, 2>(a, stream);
-  else if (a.M <= 64 && tiles < 171) glu_rows<ACT, 4>(a, stream);
+  auto groups = [&](int64_t rows) { return (a.M + rows - 1) / rows * ((a.H + 15) / 16); };
+  if (a.M <= 16 || groups(16) <= 128) glu_rows<ACT, 1>(a, stream);
+  else if (a.M <= 32 || groups(32) <= 256) glu_rows<ACT, 2>(a, stream);
+  else if ((a.M <= 64 && tiles < 171) || groups(64) <= 256) glu_rows<ACT, 4>(a, stream);
   else if (tiles <= 128) glu_tiles<ACT, 2, 4, 4, 1, 4>(a, stream);
   else if (tiles <= 256 && a.K > 1280) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
   else if (tiles <= 256) glu_tiles<ACT, 2, 8, 4, 1, 4>(a, stream);
