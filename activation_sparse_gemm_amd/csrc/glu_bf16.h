@@ -8,8 +8,7 @@
 // holds the gate and the up columns of the same outputs, placed so that each lane's
 // accumulators hold G and U of the same consecutive columns; the activation and the product are
 // formed from the fp32 accumulators and G and U reach memory only where the caller keeps them.
-// Forward, few rows: both weights are streamed once, the K range split over a workgroup's
-// waves and added in LDS.
+// Forward, few rows or few outputs: the K range split over a workgroup's waves and added in LDS.
 // Gradient: one pass forms P = [dG | dU], then dX = P [Wg; Wu] and [dWg; dWu] = P^T X read P, X
 // and the weights as they lie (ring_gemm.h's transposing reads).
 #pragma once
@@ -151,8 +150,8 @@ void glu_kernel(const GluArgs a) {
   }
 }
 
-// Few rows, or few outputs: a workgroup forms 16 MB rows of 16 output columns; wave w takes the K steps w, w + 4, ...
-// of 64, each with a ring of D LDS slots of its own (16 gate rows, 16 up rows and the rows of X,
+// Few rows, or few outputs: a workgroup forms 16 MB rows of 16 output columns; wave w takes the K
+// steps w, w + 4, ... of 64, each with a ring of D LDS slots of its own (16 gate rows, 16 up rows and the rows of X,
 // in whole 128-byte lines that go straight to LDS) and no barrier, and the waves' sums are added
 // in wave order.  Bound by the weights' bytes: 1 x 5120 x 13824 reads 283 MB in 44-47 us (6.0-6.4
 // TB/s), 32 x 5120 x 13824 in 56.  (Loading fragments
@@ -284,9 +283,9 @@ inline bool glu_small(int64_t M, int64_t K, int64_t H) {
 // By rows, then by the number of 128 x 64 tiles (microseconds at K = 2560 where none is given):
 //  - up to 32 rows, and up to 64 where such tiles would leave a third of the CUs without one: the
 //    weights streamed (64 x 6912, 108 tiles: 21 against 25; 64 x 13824, K = 5120, 216: 75 against 53);
-//  - few outputs: the same kernel, whose waves share K, in workgroups of 16 rows up to one to two
-//    CUs, of 32 or 64 up to one to a CU (80 x 121, K = 5120: 9.5 against 25; 437 x 400: 13 against
-//    16.4, with 441 workgroups of 64 rows, 437 x 1000, 21.8 against 17.6);
+//  - few outputs: the same kernel, whose waves share K, by 16 rows where that makes at most one
+//    workgroup to two CUs, else by 32 or 64 where one to a CU (80 x 121, K = 5120: 9.5 against 25; 437 x
+//    400: 13 against 16.4; with 441 workgroups of 64 rows, 437 x 1000, 21.8 against 17.6);
 //  - at most half as many tiles as CUs: half as wide ones (100 x 6912: 20 against 25);
 //  - at most one to a CU: four steps ahead, since nothing else hides a load (200 x 6912: 27
 //    against 33; 100 x 10000, K = 5120: 41 against 53);
