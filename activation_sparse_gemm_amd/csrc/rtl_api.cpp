@@ -643,8 +643,8 @@ rtl_status check_glu(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int64_t H)
     return fail(RTL_ERR_SHAPE, "need M, K, H > 0 (M=%lld K=%lld H=%lld)", (long long)M, (long long)K, (long long)H);
   // a tile's rows are reached with 32-bit offsets: 256 rows of K bf16 values stay below 2^31 bytes
   if (K >= kMaxK) return fail(RTL_ERR_SHAPE, "K must be below %lld (K=%lld)", (long long)kMaxK, (long long)K);
-  // a launch takes fewer than 2^32 threads: 256 to a 256 x 128 tile, or to 16 outputs of few rows
-  if (M > INT32_MAX || H >= (1 << 28) || ((M + 255) / 256) * ((H + 127) / 128) >= 1 << 24)
+  // a launch takes fewer than 2^32 threads: 256 to a 128 x 64 tile, or to 16 outputs of few rows
+  if (M > INT32_MAX || H > (1 << 28) - 16 || ((M + 127) / 128) * ((H + 63) / 64) >= 1 << 24)
     return fail(RTL_ERR_SHAPE, "M x H is too large (M=%lld H=%lld)", (long long)M, (long long)H);
   if (K % 64 != 0) return fail(RTL_ERR_UNSUPPORTED, "the gated block needs K %% 64 == 0 (K=%lld)", (long long)K);
   return RTL_OK;

@@ -351,7 +351,7 @@ rtl_status rtl_qk_norm_rope_backward(rtl_dtype dt, int64_t M, int64_t Hq, int64_
  *   the pre-activations that rtl_glu_backward takes.
  * act: RTL_ACT_SILU g / (1 + exp(-g)) or RTL_ACT_GELU g Phi(g) (the erf form, Phi within
  * 4e-7), evaluated on the fp32 accumulators; every output is rounded once.  Limits: K % 64 == 0,
- * K < 2^22, H < 2^28 and M * H below 2^38; M and H are arbitrary else.  Outputs must not overlap
+ * K < 2^22, H <= 2^28 - 16, fewer than 2^24 tiles of 128 x 64 outputs.  Outputs must not overlap
  * inputs or each other.
  */
 typedef enum { RTL_ACT_RANGE_MIN_ = -0x7FFFFFFF - 1, RTL_ACT_SILU = 0, RTL_ACT_GELU = 1, RTL_ACT_RANGE_MAX_ = 0x7FFFFFFF } rtl_act;

@@ -160,7 +160,7 @@ GLU = [
     (dict(dt=9), "RTL_ERR_UNSUPPORTED"), (dict(M=0), "RTL_ERR_SHAPE"), (dict(K=0), "RTL_ERR_SHAPE"), (dict(H=-1), "RTL_ERR_SHAPE"),
     (dict(K=96), "RTL_ERR_UNSUPPORTED"), (dict(K=2 ** 22), "RTL_ERR_SHAPE"), (dict(M=2 ** 31), "RTL_ERR_SHAPE"),
     (dict(M=2 ** 62), "RTL_ERR_SHAPE"), (dict(M=2 ** 30, H=2 ** 30), "RTL_ERR_SHAPE"), (dict(X=None), "RTL_ERR_NULL"),
-    (dict(Wg=None), "RTL_ERR_NULL"), (dict(M=1, H=2 ** 28), "RTL_ERR_SHAPE"), (dict(M=2 ** 31 - 1, H=129), "RTL_ERR_SHAPE"),
+    (dict(Wg=None), "RTL_ERR_NULL"), (dict(M=1, H=2 ** 28 - 15), "RTL_ERR_SHAPE"), (dict(M=2 ** 20, H=2 ** 17), "RTL_ERR_SHAPE"), (dict(M=2 ** 31 - 1, H=129), "RTL_ERR_SHAPE"),
     (dict(X=lambda a: at(a["X"], 2)), "RTL_ERR_ALIGN"),
     (dict(U=lambda a: at(a["U"], 4)), "RTL_ERR_ALIGN"),
 ]
