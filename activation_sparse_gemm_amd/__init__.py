@@ -354,29 +354,16 @@ def rtl_linear_fused_fp8(X: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor, LA
     return Y
 
 
-class _Here:
-    """The context of a call whose tensors are on the current device."""
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE = _Here()
-
-
-def _one_device(first, *rest):
-    """The context in which the GPU that every given tensor is on is the current device, so that
-    a call without ``stream`` runs on that GPU's current stream."""
+def _elsewhere(first, *rest):
+    """None if every given tensor is on the current GPU; if they are on another one, the context in
+    which that is the current device, so that a call without ``stream`` runs on its current stream."""
     dev = first.get_device()
     for t in rest:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on one GPU, got {first.device} and {t.device}")
     if dev < 0:
         raise ValueError(f"tensors must be on one GPU, got {first.device}")
-    return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _mismatch(name, t, shape, dtype):
@@ -457,12 +444,15 @@ def rtl_rope_axes(X: torch.Tensor, pos: torch.Tensor, axis_dims, theta: float = 
     p + sum / 2.  ``inverse`` turns back, which is also the gradient.  ``Y`` may be X."""
     M, H, D = X.shape
     shape, dt = (M, H, D), X.dtype
-    with _one_device(X, pos, Y):
-        if Y is None:
-            Y = _new(stream, X, shape, dt)
-        _check(lib.rtl_rope_axes(_dt(X), M, H, D, *_heads("X", X, shape, dt),
-                                 *_rope_args(pos, axis_dims, theta, pairs, M), bool(inverse),
-                                 *_heads("Y", Y, shape, dt), _queue(stream, X)))
+    there = _elsewhere(X, pos, Y)
+    if there is not None:
+        with there:
+            return rtl_rope_axes(X, pos, axis_dims, theta, pairs, inverse, Y, stream)
+    if Y is None:
+        Y = _new(stream, X, shape, dt)
+    _check(lib.rtl_rope_axes(_dt(X), M, H, D, *_heads("X", X, shape, dt),
+                             *_rope_args(pos, axis_dims, theta, pairs, M), bool(inverse),
+                             *_heads("Y", Y, shape, dt), _queue(stream, X)))
     return Y
 
 
@@ -475,23 +465,27 @@ def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 
     M, Hq, D = Q.shape
     dt = Q.dtype
     qs, ks, ws = (M, Hq, D), (M, 0 if K is None else K.shape[1], D), (D,)
-    with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, Qo, Ko):
-        if Qo is None:
-            Qo = _new(stream, Q, qs, dt)
-        keys, keys_out, kw_at = _NO_HEADS, _NO_HEADS, None
-        if K is not None:
-            if Ko is None:
-                Ko = _new(stream, Q, ks, dt)
-            keys, keys_out, kw_at = _heads("K", K, ks, dt), _heads("Ko", Ko, ks, dt), _flat("kw", kw, ws, dt)
-        elif Ko is not None:
-            raise ValueError("Ko without K")
-        _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, ks[1], D, *_heads("Q", Q, qs, dt), *keys,
-                                    _flat("qw", qw, ws, dt), kw_at, eps,
-                                    *_rope_args(pos, axis_dims, theta, pairs, M), *_heads("Qo", Qo, qs, dt), *keys_out,
-                                    _queue(stream, Q)))
+    there = _elsewhere(Q, K, qw, kw, pos if len(axis_dims) else None, Qo, Ko)
+    if there is not None:
+        with there:
+            return rtl_qk_norm_rope(Q, K, qw, kw, pos, axis_dims, theta, eps, pairs, Qo, Ko, stream)
+    if Qo is None:
+        Qo = _new(stream, Q, qs, dt)
+    keys, keys_out, kw_at = _NO_HEADS, _NO_HEADS, None
+    if K is not None:
+        if Ko is None:
+            Ko = _new(stream, Q, ks, dt)
+        keys, keys_out, kw_at = _heads("K", K, ks, dt), _heads("Ko", Ko, ks, dt), _flat("kw", kw, ws, dt)
+    elif Ko is not None:
+        raise ValueError("Ko without K")
+    _check(lib.rtl_qk_norm_rope(_dt(Q), M, Hq, ks[1], D, *_heads("Q", Q, qs, dt), *keys,
+                                _flat("qw", qw, ws, dt), kw_at, eps,
+                                *_rope_args(pos, axis_dims, theta, pairs, M), *_heads("Qo", Qo, qs, dt), *keys_out,
+                                _queue(stream, Q)))
     return Qo, Ko
 
 
+@functools.lru_cache(maxsize=64)
 def rtl_qk_norm_rope_backward_workspace_bytes(D: int) -> int:
     return int(lib.rtl_qk_norm_rope_backward_workspace_bytes(D))
 
@@ -505,29 +499,33 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
     M, Hq, D = Q.shape
     dt = Q.dtype
     qs, ks, ws = (M, Hq, D), (M, 0 if K is None else K.shape[1], D), (D,)
-    with _one_device(Q, K, qw, kw, pos if len(axis_dims) else None, dQo, dKo, dQ, dK, dqw, dkw, workspace):
-        if dQ is None:
-            dQ = _new(stream, Q, qs, dt)
-        if dqw is None:
-            dqw = _new(stream, Q, (D,), torch.float32)
-        keys, grads, grads_out, kw_at, dkw_at = _NO_HEADS, _NO_HEADS, _NO_HEADS, None, None
-        if K is not None:
-            if dK is None:
-                dK = _new(stream, Q, ks, dt)
-            if dkw is None:
-                dkw = _new(stream, Q, (D,), torch.float32)
-            keys, grads, grads_out = _heads("K", K, ks, dt), _heads("dKo", dKo, ks, dt), _heads("dK", dK, ks, dt)
-            kw_at, dkw_at = _flat("kw", kw, ws, dt), _flat("dkw", dkw, ws, torch.float32)
-        elif dKo is not None or dK is not None or dkw is not None:
-            raise ValueError("dKo, dK or dkw without K")
-        if workspace is None:
-            workspace = _new(stream, Q, (max(rtl_qk_norm_rope_backward_workspace_bytes(D), 1),), torch.uint8)
-        _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, ks[1], D, *_heads("Q", Q, qs, dt), *keys,
-                                             _flat("qw", qw, ws, dt), kw_at, eps,
-                                             *_rope_args(pos, axis_dims, theta, pairs, M),
-                                             *_heads("dQo", dQo, qs, dt), *grads, *_heads("dQ", dQ, qs, dt), *grads_out,
-                                             _flat("dqw", dqw, ws, torch.float32), dkw_at, *_space(workspace),
-                                             _queue(stream, Q)))
+    there = _elsewhere(Q, K, qw, kw, pos if len(axis_dims) else None, dQo, dKo, dQ, dK, dqw, dkw, workspace)
+    if there is not None:
+        with there:
+            return rtl_qk_norm_rope_backward(Q, K, qw, kw, pos, axis_dims, dQo, dKo, theta, eps, pairs, dQ, dK, dqw, dkw,
+                                             workspace, stream)
+    if dQ is None:
+        dQ = _new(stream, Q, qs, dt)
+    if dqw is None:
+        dqw = _new(stream, Q, (D,), torch.float32)
+    keys, grads, grads_out, kw_at, dkw_at = _NO_HEADS, _NO_HEADS, _NO_HEADS, None, None
+    if K is not None:
+        if dK is None:
+            dK = _new(stream, Q, ks, dt)
+        if dkw is None:
+            dkw = _new(stream, Q, (D,), torch.float32)
+        keys, grads, grads_out = _heads("K", K, ks, dt), _heads("dKo", dKo, ks, dt), _heads("dK", dK, ks, dt)
+        kw_at, dkw_at = _flat("kw", kw, ws, dt), _flat("dkw", dkw, ws, torch.float32)
+    elif dKo is not None or dK is not None or dkw is not None:
+        raise ValueError("dKo, dK or dkw without K")
+    if workspace is None:
+        workspace = _new(stream, Q, (max(rtl_qk_norm_rope_backward_workspace_bytes(D), 1),), torch.uint8)
+    _check(lib.rtl_qk_norm_rope_backward(_dt(Q), M, Hq, ks[1], D, *_heads("Q", Q, qs, dt), *keys,
+                                         _flat("qw", qw, ws, dt), kw_at, eps,
+                                         *_rope_args(pos, axis_dims, theta, pairs, M),
+                                         *_heads("dQo", dQo, qs, dt), *grads, *_heads("dQ", dQ, qs, dt), *grads_out,
+                                         _flat("dqw", dqw, ws, torch.float32), dkw_at, *_space(workspace),
+                                         _queue(stream, Q)))
     return dQ, dK, dqw, dkw
 
 
@@ -538,12 +536,15 @@ def rtl_glu_fused(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: int 
     M, K = X.shape
     H = Wg.shape[0]
     xs, ws, ys, bf16 = (M, K), (H, K), (M, H), torch.bfloat16
-    with _one_device(X, Wg, Wu, Y, G, U):
-        if Y is None:
-            Y = _new(stream, X, ys, bf16)
-        _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _flat("X", X, xs, bf16), _flat("Wg", Wg, ws, bf16),
-                                 _flat("Wu", Wu, ws, bf16), _flat("Y", Y, ys, bf16), _flat("G", G, ys, bf16),
-                                 _flat("U", U, ys, bf16), _queue(stream, X)))
+    there = _elsewhere(X, Wg, Wu, Y, G, U)
+    if there is not None:
+        with there:
+            return rtl_glu_fused(X, Wg, Wu, act, Y, G, U, stream)
+    if Y is None:
+        Y = _new(stream, X, ys, bf16)
+    _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _flat("X", X, xs, bf16), _flat("Wg", Wg, ws, bf16),
+                             _flat("Wu", Wu, ws, bf16), _flat("Y", Y, ys, bf16), _flat("G", G, ys, bf16),
+                             _flat("U", U, ys, bf16), _queue(stream, X)))
     return Y
 
 
@@ -560,20 +561,23 @@ def rtl_glu_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: tor
     M, K = X.shape
     H = Wg.shape[0]
     xs, ws, ys, bf16 = (M, K), (H, K), (M, H), torch.bfloat16
-    with _one_device(X, Wg, Wu, G, U, dY, dX, dWg, dWu, workspace):
-        if not need_dx:
-            dX = None
-        elif dX is None:
-            dX = _new(stream, X, xs, bf16)
-        if not need_dw:
-            dWg = dWu = None
-        else:
-            dWg = _new(stream, X, ws, bf16) if dWg is None else dWg
-            dWu = _new(stream, X, ws, bf16) if dWu is None else dWu
-        if workspace is None:
-            workspace = _new(stream, X, (max(rtl_glu_backward_workspace_bytes(M, K, H), 1),), torch.uint8)
-        _check(lib.rtl_glu_backward(act, RTL_BF16, M, K, H, _flat("X", X, xs, bf16), _flat("Wg", Wg, ws, bf16),
-                                    _flat("Wu", Wu, ws, bf16), _flat("G", G, ys, bf16), _flat("U", U, ys, bf16),
-                                    _flat("dY", dY, ys, bf16), _flat("dX", dX, xs, bf16), _flat("dWg", dWg, ws, bf16),
-                                    _flat("dWu", dWu, ws, bf16), *_space(workspace), _queue(stream, X)))
+    there = _elsewhere(X, Wg, Wu, G, U, dY, dX, dWg, dWu, workspace)
+    if there is not None:
+        with there:
+            return rtl_glu_backward(X, Wg, Wu, G, U, dY, act, dX, dWg, dWu, workspace, need_dx, need_dw, stream)
+    if not need_dx:
+        dX = None
+    elif dX is None:
+        dX = _new(stream, X, xs, bf16)
+    if not need_dw:
+        dWg = dWu = None
+    else:
+        dWg = _new(stream, X, ws, bf16) if dWg is None else dWg
+        dWu = _new(stream, X, ws, bf16) if dWu is None else dWu
+    if workspace is None:
+        workspace = _new(stream, X, (max(rtl_glu_backward_workspace_bytes(M, K, H), 1),), torch.uint8)
+    _check(lib.rtl_glu_backward(act, RTL_BF16, M, K, H, _flat("X", X, xs, bf16), _flat("Wg", Wg, ws, bf16),
+                                _flat("Wu", Wu, ws, bf16), _flat("G", G, ys, bf16), _flat("U", U, ys, bf16),
+                                _flat("dY", dY, ys, bf16), _flat("dX", dX, xs, bf16), _flat("dWg", dWg, ws, bf16),
+                                _flat("dWu", dWu, ws, bf16), *_space(workspace), _queue(stream, X)))
     return dX, dWg, dWu

@@ -126,3 +126,38 @@ def test_training_step_of_the_new_operators():
     rx, rw, bx, bw = B.qk_backward(B.f64(Q), B.f64(w), phi, 0, 1e-6, B.f64(dq.view(M, heads, D)))
     B.check(dQ, rx, bx, BF, "dQ")
     B.check(dw, rw, bw, torch.float32, "dw")
+
+
+def test_calls_while_another_gpu_is_current(monkeypatch):
+    """Each call makes its tensors' GPU the current one first (here the current device's number and
+    the context that changes it stand in for a second GPU)."""
+    M, H, D, K, N = 5, 3, 64, 128, 40
+    q, k, g = rnd(1, M, H, D), rnd(2, M, H, D), rnd(3, M, H, D)
+    w, pos = rnd(4, D), torch.rand(M, 1, device="cuda")
+    x, wg, wu, dy = rnd(5, M, K), rnd(6, N, K), rnd(7, N, K), rnd(8, M, N)
+
+    def calls():
+        return (rtl.rtl_rope_axes(q, pos, (D,)), *rtl.rtl_qk_norm_rope(q, k, w, w, pos, (D,)),
+                *rtl.rtl_qk_norm_rope_backward(q, k, w, w, pos, (D,), g, g), rtl.rtl_glu_fused(x, wg, wu),
+                *rtl.rtl_glu_backward(x, wg, wu, dy, dy, dy))
+
+    want, here, entered = calls(), q.get_device(), []
+    current = [here + 1]
+
+    class There:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+            current[0] = self.device
+
+        def __exit__(self, *exc):
+            current[0] = here + 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", There)
+    got = calls()
+    monkeypatch.undo()
+    assert entered == [here] * 5
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
