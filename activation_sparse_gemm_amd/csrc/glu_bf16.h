@@ -89,7 +89,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // tile's 67 us the first loads and the stores of three outputs 17.  PAST: outputs bypass the caches,
 // which pays (4173 x 2560 x 6912 with G and U 257 us against 265, 24830 x 192 x 4672 223 against
 // 235) unless rows end inside a 64-byte piece, whose parts then go out one by one (24830 x 192 x
-// 4666 179 against 152, 4096 x 640 x 8196 with G and U 164 against 153).
+// 4666 179 against 152, 4096 x 640 x 8196 with G and U 164 against 153); the large tiles' Y gains
+// there too (4173 x 2560 x 6916 with G and U 279 against 281.5).
 template <int ACT, int RB, int NB, int WM, int WN, int DEPTH, bool PAST>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(RB == 8 ? 1 : 2, RB == 8 ? 1 : 2)))
 void glu_kernel(const GluArgs a) {
@@ -143,7 +144,7 @@ void glu_kernel(const GluArgs a) {
         u[e] = acc[rb][NC + e][j];
         y[e] = glu_act<ACT>(g[e]).v * u[e];
       }
-      store_cols<NC, PAST>(a.Y, M, H, row, col, y);
+      store_cols<NC, PAST || RB == 8>(a.Y, M, H, row, col, y);
       if (a.G != nullptr) store_cols<NC, PAST>(a.G, M, H, row, col, g);
       if (a.U != nullptr) store_cols<NC, PAST>(a.U, M, H, row, col, u);
     }
