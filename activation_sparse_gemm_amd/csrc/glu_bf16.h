@@ -85,7 +85,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // second up; row 16 nb + r16 of either half is output column NB / 2 r16 + nb, so that lane r16
 // holds NB / 2 consecutive columns over its blocks.  Measured: 32760 x 5120 x 13824 6.0-6.3 ms
 // (1.48-1.54 PFLOP/s; the matrix cores 78% busy at the 1.8 GHz that the power limit leaves), 4173 x
-// 2560 x 6916 with GELU, G and U kept 268 us (1.10): 935 tiles take four rounds of 256, and of a
+// 2560 x 6916 with GELU, G and U kept 270-280 us (1.05-1.09): 935 tiles take four rounds of 256, and of a
 // tile's 67 us the first loads and the stores of three outputs 17.  PAST: outputs bypass the caches,
 // which pays (4173 x 2560 x 6912 with G and U 257 us against 265, 24830 x 192 x 4672 223 against
 // 235) unless rows end inside a 64-byte piece, whose parts then go out one by one (24830 x 192 x
