@@ -333,11 +333,23 @@ hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void*
 // The rounding, 2^-8 of an element at most, adds to a gradient what the gradient's own rounding
 // to bf16 does, as long as many elements share the sum of squares; in a product of few of them
 // one large element's error shows in full.  Up to kGluFewElements of them (where the products
-// are held by the weights' bytes) what the rounding took is kept as well, rounded to bf16 in a
-// second P, and the products run over both: dG and dU then hold to 2^-16.
-// (Twice the products' steps: 1 x 5120 x 13824 takes 220 us instead of 170.)
+// are held by the weights' bytes) an element goes into two bf16 values, its leading digits in the
+// first P and what they leave, rounded, in a second one, and the products run over both: dG and dU
+// then hold to 2^-16.  (Twice the products' steps: 1 x 5120 x 13824 takes 220 us instead of 170.)
 constexpr int64_t kGluFewElements = 1 << 14;
 inline int glu_passes(int64_t M, int64_t H) { return M * H <= kGluFewElements ? 2 : 1; }
+// The two parts of v.  Each has v's sign and is 0 only where v is (down to 2^-102), so that with an
+// infinite weight or token both give the same infinity, where opposite ones, or a part of 0, would
+// give NaN: the first is v cut off towards zero, and the second 2^-24 of the first where nothing is
+// left.  An infinity or NaN is its own second part.
+struct GluParts {
+  __bf16 hi, lo;
+};
+__device__ __forceinline__ GluParts glu_parts(float v) {
+  if (!__builtin_isfinite(v)) return {(__bf16)v, (__bf16)v};
+  const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), lo = v - hi;
+  return {(__bf16)hi, (__bf16)(lo != 0.f ? lo : hi * 0x1p-24f)};
+}
 template <int ACT>
 __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int64_t Hp, const uint16_t* G,
                                                        const uint16_t* U, const uint16_t* dY, uint16_t* P, int passes) {
@@ -367,9 +379,13 @@ __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int
     const float v[2][2] = {{d0 * bf16lo(u[i]) * a0.slope, d1 * bf16hi(u[i]) * a1.slope}, {d0 * a0.v, d1 * a1.v}};
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-      const bf16x2_t hi = {(__bf16)v[k][0], (__bf16)v[k][1]};
-      p[0][k][i] = __builtin_bit_cast(uint32_t, hi);
-      p[1][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(v[k][0] - (float)hi[0]), (__bf16)(v[k][1] - (float)hi[1])});
+      if (passes == 1) {
+        p[0][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[k][0], (__bf16)v[k][1]});
+      } else {
+        const GluParts a = glu_parts(v[k][0]), b = glu_parts(v[k][1]);
+        p[0][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{a.hi, b.hi});
+        p[1][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{a.lo, b.lo});
+      }
     }
   }
   for (int pass = 0; pass < passes; pass++) {

@@ -1,0 +1,80 @@
+"""GPU tests of the block operators where their arithmetic leaves the ordinary: infinities, values
+at the ends of the types' ranges, tensors of no heads, and long sums."""
+import numpy as np
+import pytest
+import torch
+
+import _block as B
+
+pytestmark = pytest.mark.gpu
+
+rtl = pytest.importorskip("activation_sparse_gemm_amd")
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def setup_module(module):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def rnd(seed, *shape, std=1.0, dtype=BF):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype).cuda()
+
+
+def same_nonfinite(got, want, name):
+    """The same elements NaN, and the same infinite with the same sign."""
+    got = B.f64(got)
+    for what, a, b in (("NaN", np.isnan(got), np.isnan(want)), ("+inf", got == np.inf, want == np.inf),
+                       ("-inf", got == -np.inf, want == -np.inf)):
+        assert (a == b).all(), f"{name}: {what} at {np.argwhere(a)[:4]}, expected at {np.argwhere(b)[:4]}"
+
+
+def check_glu_gradient(args, kind, same=True):
+    """The gradient's outputs: infinite and NaN where the definition's are, the others within its
+    bounds (which the infinite operands do not enter: a finite element meets none of them)."""
+    got = rtl.rtl_glu_backward(*args, act=kind)
+    with np.errstate(invalid="ignore", over="ignore"):
+        want, _ = B.glu_backward(*map(B.f64, args), kind)
+        _, bounds = B.glu_backward(*(np.nan_to_num(B.f64(t), nan=0.0, posinf=0.0, neginf=0.0) for t in args), kind)
+    for t, w, b, name in zip(got, want, bounds, ("dX", "dWg", "dWu")):
+        same_nonfinite(t, w, name)
+        fine = np.isfinite(w)
+        B.check(torch.where(torch.isfinite(t), t, torch.zeros_like(t)), np.where(fine, w, 0.0), b, BF, name)
+
+
+# 2^14 elements of G at most (the gradient's two-part form), and more
+@pytest.mark.parametrize("M,H", ((1, 64), (3, 72), (40, 100), (200, 130)))
+@pytest.mark.parametrize("kind", (0, 1), ids=("silu", "gelu"))
+@pytest.mark.parametrize("where", ("dY", "U", "Wg", "Wu", "X"))
+def test_gradient_of_infinities(where, kind, M, H):
+    K = 128
+    args = [rnd(1, M, K), rnd(2, H, K, std=K ** -0.5), rnd(3, H, K, std=K ** -0.5), rnd(4, M, H, std=1.5),
+            rnd(5, M, H), rnd(6, M, H, std=0.1)]
+    m, h = M - 1, H // 2
+    # dG of 1/2 or 1 exactly, and dU of 0: what is left of them after one rounding is 0
+    args[3][:, 3], args[4][:, 3], args[5][:, 3] = 0.0, 1.0, 1.0
+    args[3][:, h], args[4][:, h] = 0.75, 1.25  # no zero meets an infinity
+    at = {"dY": (5, m, h), "U": (4, m, h), "Wg": (1, h, 7), "Wu": (2, h, 70), "X": (0, m, 9)}[where]
+    args[at[0]][at[1], at[2]] = float("-inf") if M == 3 else float("inf")
+    if where == "Wg":
+        args[1][3, 8] = float("inf")
+    check_glu_gradient(args, kind)
+
+
+@pytest.mark.parametrize("kind", (0, 1), ids=("silu", "gelu"))
+def test_gradient_past_bf16(kind):
+    """dU above the largest bf16 value but within fp32's, in the two-part form: its products with
+    small weights and tokens are finite."""
+    M, K, H = 3, 64, 40
+    X, Wg, Wu = rnd(1, M, K, std=2.0 ** -20), rnd(2, H, K, std=2.0 ** -20), rnd(3, H, K, std=2.0 ** -20)
+    G, U, dY = rnd(4, M, H, std=1.5), rnd(5, M, H, std=2.0 ** -30), rnd(6, M, H, std=0.1)
+    # a G whose activation times a dY of bf16 falls between the two types' ends
+    steps = torch.arange(1 << 14, dtype=torch.int32)
+    g = ((0x3F80 + steps[:256]).to(torch.int16)).view(BF).double().numpy()  # 1 to 4
+    d = ((0x7E80 + steps[:256]).to(torch.int16)).view(BF).double().numpy()  # 2^126 up to the largest
+    v = B.act(g, kind)[0][:, None] * d[None]
+    i, j = np.unravel_index(np.argmin(np.abs(v - 3.399e38)), v.shape)
+    assert 3.3965e38 < v[i, j] < 3.402e38
+    G[1, 7], dY[1, 7], U[1, 7] = float(g[i]), float(d[j]), 2.0 ** -30
+    check_glu_gradient([X, Wg, Wu, G, U, dY], kind)
