@@ -5,7 +5,7 @@
 //   phi_p = pos[m, axis(p)] f_p          one angle per token and channel pair p
 //   (x0, x1) -> (x0 cos - x1 sin, x1 cos + x0 sin)
 //   norm:  n = x r w,  r = 1 / sqrt(mean(x^2) + eps)
-//   back:  t = R^T dy,  dw = sum t x r,  dx = r w t - x r^3 / D sum(w t x)
+//   back:  t = R^T dy,  dw = sum t n0,  dx = r (w t - n0 / D sum(w t n0)),  n0 = x r
 //
 // Bound: memory (each element read once and written once; the gradient reads two and writes
 // one).  A group of GL lanes owns one head of one token, a lane eight channels (four pairs):
@@ -320,19 +320,19 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
       un.rotate(d, c, s);
       float q = 0.f, p = 0.f, wd[8];
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        wd[i] = d[i] * w[i];
-        q = fmaf(v[i], v[i], q);
-        p = fmaf(wd[i], v[i], p);
-      }
+      for (int i = 0; i < 8; i++) q = fmaf(v[i], v[i], q);
       const float r = __builtin_amdgcn_rsqf(fmaf(group_sum<GL>(q), a.inv_d, a.eps));
-      // dx = r w t - x r^3 / D sum(w t x)
-      const float k = r * r * r * a.inv_d * group_sum<GL>(p);
+      // with n = x r: dw = t n, dx = r (w t - n sum(w t n) / D), no factor larger than the result
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        dw[i] = fmaf(d[i], v[i] * r, dw[i]);
-        v[i] = fmaf(wd[i], r, -(v[i] * k));
+        v[i] *= r;
+        dw[i] = fmaf(d[i], v[i], dw[i]);
+        wd[i] = d[i] * w[i];
+        p = fmaf(wd[i], v[i], p);
       }
+      const float k = group_sum<GL>(p) * a.inv_d;
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] = r * fmaf(-v[i], k, wd[i]);
       if (lane) un.template store<true>(dx.p, at + j * dx.head, v);
     }
   };

@@ -78,3 +78,34 @@ def test_gradient_past_bf16(kind):
     assert 3.3965e38 < v[i, j] < 3.402e38
     G[1, 7], dY[1, 7], U[1, 7] = float(g[i]), float(d[j]), 2.0 ** -30
     check_glu_gradient([X, Wg, Wu, G, U, dY], kind)
+
+
+# eps and the heads' size: zero heads with a root of their eps, sizes whose cube leaves fp32
+RANGES = [(2.0 ** -126, 0.0, F32), (1e-30, 0.0, BF), (1e-30, 2.0 ** -45, F32), (2.0 ** -126, 2.0 ** -61, BF),
+          (1e-6, 2.0 ** 45, F32), (1e-6, 2.0 ** 45, BF), (1e-6, 2.0 ** 55, F32), (1e-6, 2.0 ** 55, BF), (1.0, 2.0 ** 58, F32)]
+
+
+@pytest.mark.parametrize("eps,size,dt", RANGES)
+@pytest.mark.parametrize("D", (32, 256))
+def test_head_norm_range(eps, size, dt, D):
+    """Norm and gradient wherever the squares lie in fp32's range."""
+    M, H, dims = 9, 3, (8, 16)
+    Q, w, dY, pos = rnd(1, M, H, D, std=size, dtype=dt), rnd(2, D, dtype=dt) + 1, rnd(3, M, H, D, dtype=dt), rnd(4, M, 2, dtype=F32)
+    Q[2] = 0
+    phi, e = B.angles(B.f64(pos), dims, 10000.0), float(np.float32(eps))
+    Qo, _ = rtl.rtl_qk_norm_rope(Q, None, w, None, pos, dims, eps=eps)
+    B.check(Qo, *B.qk_forward(B.f64(Q), B.f64(w), phi, 0, e), dt, "Qo")
+    dQ, _, dqw, _ = rtl.rtl_qk_norm_rope_backward(Q, None, w, None, pos, dims, dY, None, eps=eps)
+    dx, dw, bx, bw = B.qk_backward(B.f64(Q), B.f64(w), phi, 0, e, B.f64(dY))
+    B.check(dQ, dx, bx, dt, "dQ")
+    B.check(dqw, dw, bw, F32, "dqw")
+
+
+def test_head_norm_gradient_of_large_gradients():
+    """Large heads under a large gradient: their product leaves fp32's range, the gradient does not."""
+    M, H, D = 9, 3, 64
+    Q, w, dY = rnd(1, M, H, D, std=2.0 ** 58, dtype=F32), rnd(2, D, dtype=F32) + 1, rnd(3, M, H, D, std=2.0 ** 75, dtype=F32)
+    dQ, _, dqw, _ = rtl.rtl_qk_norm_rope_backward(Q, None, w, None, None, (), dY, None)
+    dx, dw, bx, bw = B.qk_backward(B.f64(Q), B.f64(w), np.zeros((M, 0)), 0, 1e-6, B.f64(dY))
+    B.check(dQ, dx, bx, F32, "dQ")
+    B.check(dqw, dw, bw, F32, "dqw")
