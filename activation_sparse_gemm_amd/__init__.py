@@ -494,8 +494,8 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
                               theta: float = 10000.0, eps: float = 1e-6, pairs: int = RTL_ROPE_ADJACENT, dQ=None,
                               dK=None, dqw=None, dkw=None, workspace=None, stream=None):
     """Gradient of rtl_qk_norm_rope: (dQ, dK, dqw, dkw) from its inputs and the gradients of its
-    outputs; dqw and dkw [D] are float32 sums over all tokens and heads.  Outputs given by the
-    caller are written in place; dQ and dK may be dQo and dKo, or Q and K."""
+    outputs; dqw and dkw [D] are float32 sums over all tokens and heads (zeros for a K of no heads).
+    Outputs given by the caller are written in place; dQ and dK may be dQo and dKo, or Q and K."""
     M, Hq, D = Q.shape
     dt = Q.dtype
     qs, ks, ws = (M, Hq, D), (M, 0 if K is None else K.shape[1], D), (D,)
@@ -526,6 +526,9 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
                                          *_heads("dQo", dQo, qs, dt), *grads, *_heads("dQ", dQ, qs, dt), *grads_out,
                                          _flat("dqw", dqw, ws, torch.float32), dkw_at, *_space(workspace),
                                          _queue(stream, Q)))
+    if K is not None and ks[1] == 0:  # to the library, no K: an empty sum is not written
+        with torch.cuda.stream(_torch_stream(stream)):
+            dkw.zero_()
     return dQ, dK, dqw, dkw
 
 

@@ -109,3 +109,24 @@ def test_head_norm_gradient_of_large_gradients():
     dx, dw, bx, bw = B.qk_backward(B.f64(Q), B.f64(w), np.zeros((M, 0)), 0, 1e-6, B.f64(dY))
     B.check(dQ, dx, bx, F32, "dQ")
     B.check(dqw, dw, bw, F32, "dqw")
+
+
+@pytest.mark.parametrize("given", (False, True))
+def test_no_key_heads(given):
+    """Keys of no heads: their outputs are empty, the gradient of their weights is an empty sum."""
+    M, H, D = 5, 2, 64
+    Q, K, w, dY, dK = rnd(1, M, H, D), rnd(2, M, 0, D), rnd(3, D), rnd(4, M, H, D), rnd(5, M, 0, D)
+    Qo, Ko = rtl.rtl_qk_norm_rope(Q, K, w, w, None, ())
+    assert Ko.shape == (M, 0, D) and torch.equal(Qo, rtl.rtl_qk_norm_rope(Q, None, w, None, None, ())[0])
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        held = torch.full((D,), 7.0, device="cuda")
+        if not given:  # the next allocation of its size is that memory
+            torch.cuda.synchronize()
+            del held
+        how = dict(dkw=held) if given else {}
+        want = rtl.rtl_qk_norm_rope_backward(Q, None, w, None, None, (), dY, None)
+        dQ, dKs, dqw, dkw = rtl.rtl_qk_norm_rope_backward(Q, K, w, w, None, (), dY, dK, stream=stream, **how)
+        torch.cuda.synchronize()
+        assert dKs.shape == (M, 0, D) and torch.equal(dQ, want[0]) and torch.equal(dqw, want[2])
+        assert bool((dkw == 0).all())
