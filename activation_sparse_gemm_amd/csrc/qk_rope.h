@@ -263,15 +263,18 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
 
 // Gradient of norm and rotation.  A fixed number of workgroups walks over the items, each on one
 // of the two tensors (shared out by their heads), the next item's loads in flight while one is
-// formed; each lane sums its channels' dw in fp32 over the items it meets, the workgroup adds its
-// groups in LDS, and qk_dw_kernel adds the workgroups: one order, the same result on every run.
+// formed; each lane sums its channels' dw in fp32 over kQkBackFlush items at a time, in double over
+// these in LDS (a lane meets up to 2^18 heads, of which a tensor with few of the heads has one
+// workgroup: one fp32 sum of 1700 alike terms was 400 half steps off), the workgroup adds its
+// groups, and qk_dw_kernel adds the workgroups: one order, the same result on every run.
 // Bound by memory and, nearly as much, by its vector instructions (the norm, two sums and the
 // rotation for every element of two inputs).  Measured: 4608 x 32 x 128 in bf16 22 us (5.2 TB/s).
+constexpr uint32_t kQkBackFlush = 16;  // even
 template <bool BF16, bool HALVES, int GL, int HC>
 __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a, const RopeTable t) {
   constexpr int NG = kRopeThreads / GL;
   typedef RopeUnit<BF16, HALVES> Unit;
-  __shared__ float red[NG * GL * 8];
+  __shared__ double sums[8][kRopeThreads + 8];  // 64 columns of the last sum fall in different banks
   const int u = threadIdx.x % GL, g = threadIdx.x / GL;
   const Unit un(u, a.pairs);
   const bool lane = 8 * u < a.D;
@@ -282,7 +285,10 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
   const RopeTensor x = a.x[which], y = a.y[which], dx = a.dx[which];
   float w[8], dw[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) w[i] = dw[i] = 0.f;
+  for (int i = 0; i < 8; i++) {
+    w[i] = dw[i] = 0.f;
+    sums[i][threadIdx.x] = 0.0;
+  }
   if (lane) rope_weights<BF16, HALVES>(un, a.w[which], w);
 
   const RopeFreq<BF16, HALVES> freq(a, t, u);
@@ -336,6 +342,13 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
       if (lane) un.template store<true>(dx.p, at + j * dx.head, v);
     }
   };
+  auto flush = [&]() {  // the lane's own sums: nothing to wait for
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      sums[i][threadIdx.x] += (double)dw[i];
+      dw[i] = 0.f;
+    }
+  };
   Item one, two;
   uint32_t item = block * NG + g;
   const uint32_t rounds = (items + stride - 1) / stride;  // the same for every lane: the sums are exchanged
@@ -347,15 +360,15 @@ __global__ __launch_bounds__(kRopeThreads) void qk_back_kernel(const RopeArgs a,
     fetch(item + 2 * stride, one);
     form(two);
     item += 2 * stride;
+    if (r % kQkBackFlush == kQkBackFlush - 2) flush();
   }
-#pragma unroll
-  for (int i = 0; i < 8; i++) red[(g * GL + u) * 8 + i] = dw[i];
+  flush();
   __syncthreads();
   for (int at = threadIdx.x; at < a.D; at += kRopeThreads) {
-    float sum = 0.f;
-    for (int j = 0; j < NG; j++) sum += red[j * GL * 8 + at];
+    double sum = 0.0;
+    for (int j = 0; j < NG; j++) sum += sums[at % 8][j * GL + at / 8];
     const Unit ue(at / 8, a.pairs);
-    a.part[(int64_t)blockIdx.x * a.D + (at % 8 < 4 ? ue.lo + at % 8 : ue.hi + at % 8 - 4)] = sum;
+    a.part[(int64_t)blockIdx.x * a.D + (at % 8 < 4 ? ue.lo + at % 8 : ue.hi + at % 8 - 4)] = (float)sum;
   }
 }
 

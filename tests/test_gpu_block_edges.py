@@ -130,3 +130,18 @@ def test_no_key_heads(given):
         torch.cuda.synchronize()
         assert dKs.shape == (M, 0, D) and torch.equal(dQ, want[0]) and torch.equal(dqw, want[2])
         assert bool((dkw == 0).all())
+
+
+@pytest.mark.parametrize("dt", (BF, F32))
+def test_long_sums(dt):
+    """Norm weights' gradients over 14 million heads of one sign, most of which one lane adds one
+    after another: all heads alike, so that every addition to a sum rounds the same way."""
+    M, H, D = 40_000, 350, 256
+    x, dy, w = rnd(1, D, dtype=dt).abs() + 0.25, rnd(2, D, dtype=dt).abs() + 0.25, rnd(3, D, dtype=dt)
+    spread = lambda t, n: t.view(1, 1, D).expand(M, n, D)
+    dx = torch.empty(M, H, D, dtype=dt, device="cuda")
+    _, _, dqw, dkw = rtl.rtl_qk_norm_rope_backward(spread(x, H), spread(x, 1), w, w, None, (), spread(dy, H), spread(dy, 1),
+                                                   dQ=dx)
+    one = B.f64(dy) * B.f64(x) / np.sqrt((B.f64(x) ** 2).mean() + 1e-6)
+    B.check(dqw, one * M * H, 128 * B.U * one * M * H, F32, "dqw")
+    B.check(dkw, one * M, 128 * B.U * one * M, F32, "dkw")
