@@ -338,17 +338,17 @@ hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void*
 // then hold to 2^-16.  (Twice the products' steps: 1 x 5120 x 13824 takes 220 us instead of 170.)
 constexpr int64_t kGluFewElements = 1 << 14;
 inline int glu_passes(int64_t M, int64_t H) { return M * H <= kGluFewElements ? 2 : 1; }
-// The two parts of v.  Each has v's sign and is 0 only where v is (down to 2^-102), so that with an
-// infinite weight or token both give the same infinity, where opposite ones, or a part of 0, would
-// give NaN: the first is v cut off towards zero, and the second 2^-24 of the first where nothing is
-// left.  An infinity or NaN is its own second part.
+// The two parts of v: the next bf16 value towards zero (below v, also where v is one) and the rest (a
+// bf16 value is exact in its two parts).  Each has v's sign and is 0 only where v is (down to
+// 2^-102), so that with an infinite weight or token both give the same infinity, where opposite
+// ones, or a part of 0, would give NaN.  An infinity or NaN is its own second part.
 struct GluParts {
   __bf16 hi, lo;
 };
 __device__ __forceinline__ GluParts glu_parts(float v) {
-  if (!__builtin_isfinite(v)) return {(__bf16)v, (__bf16)v};
-  const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), lo = v - hi;
-  return {(__bf16)hi, (__bf16)(lo != 0.f ? lo : hi * 0x1p-24f)};
+  if (!__builtin_isfinite(v) || v == 0.f) return {(__bf16)v, (__bf16)v};
+  const float hi = __uint_as_float((__float_as_uint(v) - 1) & 0xFFFF0000u);
+  return {(__bf16)hi, (__bf16)(v - hi)};
 }
 template <int ACT>
 __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int64_t Hp, const uint16_t* G,

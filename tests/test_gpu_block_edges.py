@@ -145,3 +145,41 @@ def test_long_sums(dt):
     one = B.f64(dy) * B.f64(x) / np.sqrt((B.f64(x) ** 2).mean() + 1e-6)
     B.check(dqw, one * M * H, 128 * B.U * one * M * H, F32, "dqw")
     B.check(dkw, one * M, 128 * B.U * one * M, F32, "dkw")
+
+
+# the sizes whose gradients take the larger tiles, parts of a tile's sum, and the few-element form
+EXACT = [(1, 1344, 333), (15, 640, 130), (64, 64, 11000), (400, 320, 6000), (100, 1344, 1500), (140, 832, 5000),
+         (3100, 4096, 70), (90, 3200, 2049), (257, 320, 516), (1029, 192, 4100), (2050, 768, 3001)]
+
+
+def label(c):
+    return "x".join(map(str, c))
+
+
+def exact_inputs(M, K, H, gen):
+    """Gates of 0 and 64, whose activation is 0 and 64 with slopes 1/2 and 1; all else -1, 0, 1."""
+    def three(*shape):
+        return torch.randint(-1, 2, shape, generator=gen, device="cuda", dtype=torch.int8).to(BF)
+
+    G = torch.randint(0, 2, (M, H), generator=gen, device="cuda", dtype=torch.int8).to(BF) * 64
+    return three(M, K), three(H, K), three(H, K), G, three(M, H), three(M, H)
+
+
+def exact_parts(G, U, dY):
+    return dY.double() * U.double() * torch.where(G == 0, 0.5, 1.0), dY.double() * G.double()
+
+
+# GELU's Phi(0) is off by its approximation's error, which only the rounding to one part takes away
+@pytest.mark.parametrize("kind,c", [(k, c) for k in (0, 1) for c in EXACT if k == 0 or c[0] * c[2] > 2 ** 14],
+                         ids=lambda v: label(v) if isinstance(v, tuple) else ("silu", "gelu")[v])
+def test_gradient_sums_exact(kind, c):
+    """Every term of every sum: inputs whose products and sums are halves of whole numbers below
+    2^24, so that each output is its exact value rounded once (a lost or repeated step of a sum
+    shows, where a bound on the roundings of all its terms leaves room for it)."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    X, Wg, Wu, G, U, dY = exact_inputs(*c, gen)
+    got = rtl.rtl_glu_backward(X, Wg, Wu, G, U, dY, act=kind)
+    dg, du = (t.cpu() for t in exact_parts(G, U, dY))
+    x, wg, wu = (t.double().cpu() for t in (X, Wg, Wu))
+    for t, want, name in zip(got, (dg @ wg + du @ wu, dg.t() @ x, du.t() @ x), ("dX", "dWg", "dWu")):
+        assert torch.equal(t.cpu(), want.to(BF)), f"{name}: off by {(t.cpu().double() - want).abs().max()}"
