@@ -183,3 +183,79 @@ def test_gradient_sums_exact(kind, c):
     x, wg, wu = (t.double().cpu() for t in (X, Wg, Wu))
     for t, want, name in zip(got, (dg @ wg + du @ wu, dg.t() @ x, du.t() @ x), ("dX", "dWg", "dWu")):
         assert torch.equal(t.cpu(), want.to(BF)), f"{name}: off by {(t.cpu().double() - want).abs().max()}"
+
+
+@pytest.mark.parametrize("c", [(1_020_000, 2112, 96), (1_020_000, 64, 2112)], ids=label)
+def test_gradient_sums_exact_far(c):
+    """The same where P, X or dX pass 2^32 bytes, every token with terms of its own: the weights'
+    gradients in full, the tokens' at both ends and in the middle."""
+    M, K, H = c
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    X, Wg, Wu, G, U, dY = exact_inputs(M, K, H, gen)
+    dX, dWg, dWu = rtl.rtl_glu_backward(X, Wg, Wu, G, U, dY)
+    want = [torch.zeros(H, K, dtype=torch.float64, device="cuda") for _ in range(2)]
+    n = 1 << 16
+    for m in range(0, M, n):
+        x = X[m:m + n].double()
+        for w, p in zip(want, exact_parts(G[m:m + n], U[m:m + n], dY[m:m + n])):
+            w += torch.mm(p.t().contiguous(), x)
+    assert torch.equal(dWg, want[0].to(BF)) and torch.equal(dWu, want[1].to(BF))
+    for m in (0, M // 2, M - 300):
+        dg, du = exact_parts(G[m:m + 300], U[m:m + 300], dY[m:m + 300])
+        assert torch.equal(dX[m:m + 300], (torch.mm(dg, Wg.double()) + torch.mm(du, Wu.double())).to(BF))
+    del X, dX, G, U, dY, x, p
+    torch.cuda.empty_cache()
+
+
+# every bf16 value to 40 in magnitude as a pre-activation: rows of the streamed and of the tiled kernels
+@pytest.mark.parametrize("kind", (0, 1), ids=("silu", "gelu"))
+@pytest.mark.parametrize("rows", (16, 1 << 15))
+def test_activation_sweep(kind, rows):
+    """Value and slope of the activation by themselves, through weights of one 1: relative bounds on
+    the negative side, where both fall off.
+
+    SiLU: exp(-g) is within (2 |g| + 4) u, a sum, a reciprocal and a product add under 8 u: value
+    within (2 |g| + 12) u of itself, slope likewise of p (1 + |g|).  GELU: the published polynomial
+    P(t) exp(-x^2) / 2 stands for Phi(-|g|); the argument x^2 = g^2 / 2 is within 7 u of itself, exp within 4 g^2 + 8 u,
+    the polynomial (five steps, coefficients up to 1.5, a result of 0.1 or more) within 40 u: (4 g^2
+    + 60) u of it, 1 - tail adds u.  The polynomial itself is within 1.5e-7 of erf, and of its tail
+    within 6e-5 to g = -3, 5e-4 to -4, 1.1% to -8 and 4% to -13.2; past that exp(-x^2) lies below fp32's normal numbers
+    (exp(-87.8) = 7.5e-39 < 2^-126) and may be 0: 2^-126 of it."""
+    bits = torch.arange(0x4221, dtype=torch.int32)
+    g = torch.cat([bits, bits - 0x8000]).to(torch.int16).view(BF)
+    g = g[(g == 0) | (g.abs().float() > 2.0 ** -100)]
+    if rows == 16:
+        g = g[torch.linspace(0, len(g) - 1, rows).long()]
+    M, K, u = len(g), 64, B.U
+    X = torch.zeros(M, K, dtype=BF)
+    X[:, 0], X[:, 1] = g, 1.0
+    Wg, Wu = torch.zeros(1, K, dtype=BF), torch.zeros(1, K, dtype=BF)
+    Wg[0, 0], Wu[0, 1] = 1.0, 1.0
+    X, Wg, Wu, gd = X.cuda(), Wg.cuda(), Wu.cuda(), g.cuda().view(M, 1)
+    one = torch.ones_like(gd)
+    G, U = torch.empty_like(gd), torch.empty_like(gd)
+    Y = rtl.rtl_glu_fused(X, Wg, Wu, act=kind, G=G, U=U)
+    assert torch.equal(G, gd) and torch.equal(U, one)
+    dX = rtl.rtl_glu_backward(X, Wg, Wu, gd, one, one, act=kind, need_dw=False)[0]
+    x = B.f64(g)
+    a = np.abs(x)
+    if kind == 0:
+        value, slope = B.act(x, 0)
+        p = 1 / (1 + np.exp(-x))
+        bv, bs = (2 * a + 12) * u * np.abs(value), (2 * a + 12) * u * p * (1 + a)
+    else:
+        phi = np.exp(-x * x / 2) / np.sqrt(2 * np.pi)
+        tail = 0.5 * torch.special.erfc(torch.from_numpy(a / np.sqrt(2))).numpy()
+        cut = np.select([a <= 3, a <= 4, a <= 8, a <= 13.2], [6e-5, 5e-4, 1.1e-2, 4e-2], 0.4)
+        p = np.where(x < 0, tail, 1 - tail)
+        value, slope = x * p, p + x * phi
+        end = torch.finfo(F32).tiny
+        bp = end + np.minimum(0.75e-7, cut * tail) + (4 * x * x + 60) * u * tail + np.where(x < 0, 0, 2 * u)
+        bv = a * bp + 2 * u * np.abs(value)
+        bs = bp + a * end + (4 * x * x + 8) * u * a * phi + 2 * u * (p + a * phi)
+    few = 2.0 ** -16 if M <= 2 ** 14 else 2.0 ** -8  # the gradient's operands, rounded
+    zero = np.zeros_like(x)
+    B.check(Y[:, 0], value, bv, BF, "Y")
+    B.check(dX[:, 0], slope, bs + few * (np.abs(slope) + bs), BF, "slope")
+    B.check(dX[:, 1], value, bv + few * (np.abs(value) + bv), BF, "value in the gradient")
+    assert not dX[:, 2:].any()
