@@ -421,6 +421,14 @@ def _queue(stream, like):
     return _stream(stream)
 
 
+def _changed(given):
+    """Counts outputs that the caller gave as changed (torch's in-place operations do), so that autograd
+    refuses to use one that it kept for a backward pass."""
+    for t in given:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 @functools.lru_cache(maxsize=64)
 def _dims(axis_dims):
     if any(not 0 <= d < 2 ** 31 for d in axis_dims):
@@ -448,11 +456,13 @@ def rtl_rope_axes(X: torch.Tensor, pos: torch.Tensor, axis_dims, theta: float = 
     if there is not None:
         with there:
             return rtl_rope_axes(X, pos, axis_dims, theta, pairs, inverse, Y, stream)
+    given = (Y,)
     if Y is None:
         Y = _new(stream, X, shape, dt)
     _check(lib.rtl_rope_axes(_dt(X), M, H, D, *_heads("X", X, shape, dt),
                              *_rope_args(pos, axis_dims, theta, pairs, M), bool(inverse),
                              *_heads("Y", Y, shape, dt), _queue(stream, X)))
+    _changed(given)
     return Y
 
 
@@ -469,6 +479,7 @@ def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 
     if there is not None:
         with there:
             return rtl_qk_norm_rope(Q, K, qw, kw, pos, axis_dims, theta, eps, pairs, Qo, Ko, stream)
+    given = Qo, Ko
     if Qo is None:
         Qo = _new(stream, Q, qs, dt)
     keys, keys_out, kw_at = _NO_HEADS, _NO_HEADS, None
@@ -482,6 +493,7 @@ def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 
                                 _flat("qw", qw, ws, dt), kw_at, eps,
                                 *_rope_args(pos, axis_dims, theta, pairs, M), *_heads("Qo", Qo, qs, dt), *keys_out,
                                 _queue(stream, Q)))
+    _changed(given)
     return Qo, Ko
 
 
@@ -504,6 +516,7 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
         with there:
             return rtl_qk_norm_rope_backward(Q, K, qw, kw, pos, axis_dims, dQo, dKo, theta, eps, pairs, dQ, dK, dqw, dkw,
                                              workspace, stream)
+    given = dQ, dK, dqw, dkw
     if dQ is None:
         dQ = _new(stream, Q, qs, dt)
     if dqw is None:
@@ -529,6 +542,7 @@ def rtl_qk_norm_rope_backward(Q: torch.Tensor, K, qw, kw, pos, axis_dims, dQo: t
     if K is not None and ks[1] == 0:  # to the library, no K: an empty sum is not written
         with torch.cuda.stream(_torch_stream(stream)):
             dkw.zero_()
+    _changed(given)
     return dQ, dK, dqw, dkw
 
 
@@ -543,11 +557,13 @@ def rtl_glu_fused(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: int 
     if there is not None:
         with there:
             return rtl_glu_fused(X, Wg, Wu, act, Y, G, U, stream)
+    given = Y, G, U
     if Y is None:
         Y = _new(stream, X, ys, bf16)
     _check(lib.rtl_glu_fused(act, RTL_BF16, M, K, H, _flat("X", X, xs, bf16), _flat("Wg", Wg, ws, bf16),
                              _flat("Wu", Wu, ws, bf16), _flat("Y", Y, ys, bf16), _flat("G", G, ys, bf16),
                              _flat("U", U, ys, bf16), _queue(stream, X)))
+    _changed(given)
     return Y
 
 
@@ -570,11 +586,12 @@ def rtl_glu_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: tor
             return rtl_glu_backward(X, Wg, Wu, G, U, dY, act, dX, dWg, dWu, workspace, need_dx, need_dw, stream)
     if not need_dx:
         dX = None
-    elif dX is None:
-        dX = _new(stream, X, xs, bf16)
     if not need_dw:
         dWg = dWu = None
-    else:
+    given = dX, dWg, dWu
+    if need_dx and dX is None:
+        dX = _new(stream, X, xs, bf16)
+    if need_dw:
         dWg = _new(stream, X, ws, bf16) if dWg is None else dWg
         dWu = _new(stream, X, ws, bf16) if dWu is None else dWu
     if workspace is None:
@@ -583,4 +600,5 @@ def rtl_glu_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: tor
                                 _flat("Wu", Wu, ws, bf16), _flat("G", G, ys, bf16), _flat("U", U, ys, bf16),
                                 _flat("dY", dY, ys, bf16), _flat("dX", dX, xs, bf16), _flat("dWg", dWg, ws, bf16),
                                 _flat("dWu", dWu, ws, bf16), *_space(workspace), _queue(stream, X)))
+    _changed(given)
     return dX, dWg, dWu

@@ -259,3 +259,37 @@ def test_activation_sweep(kind, rows):
     B.check(dX[:, 0], slope, bs + few * (np.abs(slope) + bs), BF, "slope")
     B.check(dX[:, 1], value, bv + few * (np.abs(value) + bv), BF, "value in the gradient")
     assert not dX[:, 2:].any()
+
+
+def test_outputs_given_by_the_caller_count_as_changed():
+    """Tensors that a call writes in place have a new version, so that torch's autograd refuses to use
+    them where it kept them for a backward pass."""
+    M, H, D, K = 3, 2, 64, 128
+    pos, w = rnd(1, M, 1, dtype=F32), rnd(2, D)
+    q, k, dq, dk, y = (rnd(3 + i, M, H, D) for i in range(5))
+    x, wg, wu, s, t = rnd(9, M, K), rnd(10, K, K), rnd(11, K, K), rnd(12, M, K), rnd(13, M, K)
+    dqw, dkw = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    out = [torch.empty_like(wg) for _ in range(2)] + [torch.empty_like(x) for _ in range(3)]
+
+    def grows(call, *written, kept=()):
+        before = [a._version for a in (*written, *kept)]
+        call()
+        after = [a._version for a in (*written, *kept)]
+        n = len(written)
+        assert all(b > a for a, b in zip(before[:n], after[:n])) and after[n:] == before[n:]
+
+    grows(lambda: rtl.rtl_rope_axes(y, pos, (D,), Y=y), y, kept=(pos,))
+    grows(lambda: rtl.rtl_qk_norm_rope(q, k, w, w, pos, (D,), Qo=q, Ko=k), q, k, kept=(w,))
+    grows(lambda: rtl.rtl_qk_norm_rope_backward(q, k, w, w, pos, (D,), dq, dk, dQ=dq, dK=dk, dqw=dqw, dkw=dkw),
+          dq, dk, dqw, dkw, kept=(q, k))
+    grows(lambda: rtl.rtl_glu_fused(x, wg, wu, Y=out[2], G=s, U=t), out[2], s, t, kept=(x, wg))
+    grows(lambda: rtl.rtl_glu_backward(x, wg, wu, s, t, out[2], dX=out[3], dWg=out[0], dWu=out[1]), out[3], out[0], out[1],
+          kept=(x, s, t))
+    scale = torch.ones(M, H, D, dtype=BF, device="cuda", requires_grad=True)
+    loss = (y * scale).sum()  # keeps y
+    rtl.rtl_rope_axes(y, pos, (D,), Y=y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        z = torch.zeros(M, H, D, dtype=BF, device="cuda")
+        assert rtl.rtl_rope_axes(z, pos, (D,), Y=z) is z
