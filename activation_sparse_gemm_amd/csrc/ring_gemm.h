@@ -110,8 +110,12 @@ struct KCols {
 
 // acc += A B^T on one 16 x 16 block, K = 32.  The sum stays in its accumulation registers: in
 // the compiler's form of the instruction it may land in others, and with 64 blocks, which fill
-// all 256, two register moves then go with every product.  Nothing but another product, at least
-// four further on, reads an accumulator before settle().
+// all 256, two register moves then go with every product.  Before settle() nothing but the next
+// product on the same block touches an accumulator, RB products further on (two at least).  That
+// one needs no distance: the hardware holds it back until exactly these registers are written (the
+// compiler, too, puts its own products on one accumulator next to each other).  The compiler sees no
+// matrix instruction here and keeps no wait states for it: tests/test_matrix_operands.py holds the
+// compiled kernels to them.
 __device__ __forceinline__ void mfma_acc(f32x4& acc, u32x4 a, u32x4 b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
