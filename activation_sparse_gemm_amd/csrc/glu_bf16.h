@@ -92,7 +92,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // 4666 179 against 152, 4096 x 640 x 8196 with G and U 164 against 153); the large tiles' Y gains
 // there too (4173 x 2560 x 6916 with G and U 279 against 281.5).
 template <int ACT, int RB, int NB, int WM, int WN, int DEPTH, bool PAST>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(RB == 8 ? 1 : 2, RB == 8 ? 1 : 2)))
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
+                          amdgpu_waves_per_eu(RB == 8 || DEPTH == 4 ? 1 : 2, RB == 8 || DEPTH == 4 ? 1 : 2)))
 void glu_kernel(const GluArgs a) {
   static_assert(WM * WN == kRingWaves, "four waves");
   constexpr int BM = 16 * RB * WM, BN = 16 * NB * WN, NC = NB / 2;
