@@ -89,8 +89,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // tile's 67 us the first loads and the stores of three outputs 17.  PAST: outputs bypass the caches,
 // which pays (4173 x 2560 x 6912 with G and U 257 us against 265, 24830 x 192 x 4672 223 against
 // 235) unless rows end inside a 64-byte piece, whose parts then go out one by one (24830 x 192 x
-// 4666 179 against 152, 4096 x 640 x 8196 with G and U 164 against 153); the large tiles' Y gains
-// there too (4173 x 2560 x 6916 with G and U 279 against 281.5).
+// 4666 179 against 152, 4096 x 640 x 8196 with G and U 164 against 153).  The large tiles' Y goes past
+// them at every width: 14 shapes with such rows, odd ones among them, from 4096 x 640 x 8193 to 8192 x
+// 5120 x 13828, gain up to 4% alone (113 against 118, 20000 x 256 x 6000 223 against 231) and 5% with G
+// and U kept (8000 x 1024 x 7000 248 against 261), and lose 1% at most (16000 x 640 x 6913 with G and U).
 template <int ACT, int RB, int NB, int WM, int WN, int DEPTH, bool PAST>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
                           amdgpu_waves_per_eu(RB == 8 || DEPTH == 4 ? 1 : 2, RB == 8 || DEPTH == 4 ? 1 : 2)))
