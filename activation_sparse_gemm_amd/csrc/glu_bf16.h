@@ -295,10 +295,11 @@ inline bool glu_small(int64_t M, int64_t K, int64_t H) {
 //    against 33; 100 x 10000, K = 5120: 41 against 53);
 //  - at most two to a CU, or more where glu_small says so; else 256 x 128 tiles (900 x 5000, 640
 //    tiles: 52 against 65).
-// Waves of 32 x 128 store whole 128-byte lines, waves of 64 x 64 read a fifth less from LDS: the
-// former but for one tile to a CU and K above 1280 (128 x 13824 at K = 640 with G and U 15 against
-// 17, 564 x 12712 at K = 128 22 against 26, 500 x 6912 43 against 42.5; four ahead 200 x 6912 26.5
-// against 25, 100 x 10000 at K = 5120 43 against 40).
+// Waves of 32 x 128 store whole 128-byte lines, waves of 64 x 64 read a fifth less from LDS, which
+// tells the more steps there are.  One tile to a CU, means over three to nine shapes of 100 to 1000
+// rows, 64 x 64 against 32 x 128: K = 640 9.4 and 8.9, 1280 13.7 and 13.4, 1920 17.9 and 17.7, 2560 22.1
+// and 22.2, 4096 31.3 and 32.1, 5120 39.4 and 41.5.  More than one to a CU: 32 x 128 (128 x 13824 at K =
+// 640 with G and U 15 against 17, 564 x 12712 at K = 128 22 against 26, 500 x 6912 43 against 42.5).
 template <int ACT>
 void glu_launch(const GluArgs& a, hipStream_t stream) {
   const int64_t tiles = ((a.M + 127) / 128) * ((a.H + 63) / 64);
@@ -307,7 +308,7 @@ void glu_launch(const GluArgs& a, hipStream_t stream) {
   else if (a.M <= 32 || groups(32) <= 256) glu_rows<ACT, 2>(a, stream);
   else if ((a.M <= 64 && tiles < 171) || groups(64) <= 256) glu_rows<ACT, 4>(a, stream);
   else if (tiles <= 128) glu_tiles<ACT, 2, 4, 4, 1, 4>(a, stream);
-  else if (tiles <= 256 && a.K > 1280) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
+  else if (tiles <= 256 && a.K > 1920) glu_tiles<ACT, 4, 4, 2, 2, 4>(a, stream);
   else if (tiles <= 256) glu_tiles<ACT, 2, 8, 4, 1, 4>(a, stream);
   else if (tiles <= 512 || glu_small(a.M, a.K, a.H)) glu_tiles<ACT, 2, 8, 4, 1, 2>(a, stream);
   else glu_tiles<ACT, 8, 8, 2, 2, 2>(a, stream);

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import _block as B
+from _gpu import Guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -259,6 +260,21 @@ def test_activation_sweep(kind, rows):
     B.check(dX[:, 0], slope, bs + few * (np.abs(slope) + bs), BF, "slope")
     B.check(dX[:, 1], value, bv + few * (np.abs(value) + bv), BF, "value in the gradient")
     assert not dX[:, 2:].any()
+
+
+# one forward tile to a CU, on either side of the K from which its waves are square: rows that end on a
+# 128-byte line, inside one, and at an odd address
+@pytest.mark.parametrize("c", [(200, 1920, 5001), (200, 1984, 5001), (300, 1984, 4000), (257, 2112, 3844)], ids=label)
+@pytest.mark.parametrize("kind", (0, 1), ids=("silu", "gelu"))
+def test_one_tile_to_a_cu(c, kind):
+    M, K, H = c
+    X, Wg, Wu = rnd(1, M, K), rnd(2, H, K, std=K ** -0.5), rnd(3, H, K, std=K ** -0.5)
+    outs = [Guarded((M, H), BF) for _ in range(3)]
+    rtl.rtl_glu_fused(X, Wg, Wu, act=kind, Y=outs[0].t, G=outs[1].t, U=outs[2].t)
+    want = B.glu_forward(B.f64(X), B.f64(Wg), B.f64(Wu), kind)
+    for o, w, bound, name in zip(outs, want[:3], want[3:], "YGU"):
+        B.check(o.t, w, bound, BF, name)
+        o.check(name)
 
 
 def test_outputs_given_by_the_caller_count_as_changed():
