@@ -4,7 +4,8 @@ Thin Python binding of the C ABI in ``include/rtl.h`` (``librtl.so``, gfx950 HIP
 kernels).  Every function here only marshals arguments: tensors stay on the GPU, the
 work runs in the library's kernels on the current torch stream, and nothing falls back
 to the CPU.  If the library is missing the import fails loudly; build it with
-``python activation_sparse_gemm_amd/build.py``.
+``python activation_sparse_gemm_amd/build.py``.  No call records an autograd graph, whatever its
+inputs require: gradients are the ``_backward`` calls' and the caller's to chain.
 
 Method: "RT-Lynx: Putting the GEMM Sparsity In a Right Way for Diffusion Models"
 (summary page, method steps 1, 2 and 4):
@@ -19,7 +20,8 @@ import os
 
 import torch
 
-try:  # the allocation alone, without the parsing of torch.empty_strided's arguments (half the time)
+try:  # the allocation alone, without torch.empty_strided's parsing of arguments and dispatch (half the
+    # time): every element of these tensors is written, so deterministic mode's fill is not missed
     from torch._C._dynamo.guards import _empty_strided_cuda as _empty_cuda
 except ImportError:
     def _empty_cuda(shape, stride, dtype):
@@ -426,7 +428,7 @@ def _changed(given):
     refuses to use one that it kept for a backward pass."""
     for t in given:
         if t is not None:
-            torch.autograd.graph.increment_version(t)
+            return torch.autograd.graph.increment_version([t for t in given if t is not None])
 
 
 @functools.lru_cache(maxsize=64)
@@ -470,7 +472,7 @@ def rtl_qk_norm_rope(Q: torch.Tensor, K, qw, kw, pos, axis_dims, theta: float = 
                      pairs: int = RTL_ROPE_ADJACENT, Qo=None, Ko=None, stream=None):
     """RMS norm of every head of Q [M,Hq,D] and K [M,Hk,D] (weights ``qw`` and ``kw`` [D], None:
     ones), then the rotation of rtl_rope_axes (``axis_dims`` empty: none), in one pass.  K None:
-    queries only.  Q and K may be views of a packed projection.  Returns (Qo, Ko); outputs given
+    queries only (``kw`` is not read).  Q and K may be views of a packed projection.  Returns (Qo, Ko); outputs given
     by the caller are written in place and may be Q and K."""
     M, Hq, D = Q.shape
     dt = Q.dtype

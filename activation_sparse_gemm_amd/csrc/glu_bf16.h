@@ -27,7 +27,8 @@ struct GluArgs {
 // Phi(g) + g phi(g), with Phi from Abramowitz and Stegun 7.1.26 (erf within 1.5e-7): for x = |g| /
 // sqrt 2, t = 1 / (1 + 0.3275911 x), Phi(-|g|) = (a1 t + .. + a5 t^5) exp(-x^2) / 2, whose exp(-x^2)
 // is also that of phi(g).  A fifth of the instructions of the library's erf, which took a sixth
-// of a tile's time at K = 2560.
+// of a tile's time at K = 2560.  Relative to Phi(g) itself it is within 6e-5 to g = -3, 5e-4 to -4 and
+// 1.1% to -8, where 1 + erf in fp32 has nothing left.
 struct ActValue {
   float v, slope;
 };
@@ -83,9 +84,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_if(bool live, const void*
 // The tiled product: WM x WN waves of RB x NB blocks, 16 RB WM rows and 16 NB WN weight rows (8 NB
 // WN outputs) a tile.  Of a wave column's 16 NB weight rows the first half are gate rows, the
 // second up; row 16 nb + r16 of either half is output column NB / 2 r16 + nb, so that lane r16
-// holds NB / 2 consecutive columns over its blocks.  Measured: 32760 x 5120 x 13824 6.0-6.3 ms
-// (1.48-1.54 PFLOP/s; the matrix cores 78% busy at the 1.8 GHz that the power limit leaves), 4173 x
-// 2560 x 6916 with GELU, G and U kept 270-280 us (1.05-1.09): 935 tiles take four rounds of 256, and of a
+// holds NB / 2 consecutive columns over its blocks.  Measured: 32760 x 5120 x 13824 6.0-6.5 ms
+// (1.43-1.54 PFLOP/s; the matrix cores 78% busy at the 1.8 GHz that the power limit leaves), 4173 x
+// 2560 x 6916 with GELU, G and U kept 255-290 us (1.02-1.16): 935 tiles take four rounds of 256, and of a
 // tile's 67 us the first loads and the stores of three outputs 17.  PAST: outputs bypass the caches,
 // which pays (4173 x 2560 x 6912 with G and U 257 us against 265, 24830 x 192 x 4672 223 against
 // 235) unless rows end inside a 64-byte piece, whose parts then go out one by one (24830 x 192 x
@@ -339,7 +340,8 @@ hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void*
 // one large element's error shows in full.  Up to kGluFewElements of them (where the products
 // are held by the weights' bytes) an element goes into two bf16 values, its leading digits in the
 // first P and what they leave, rounded, in a second one, and the products run over both: dG and dU
-// then hold to 2^-16.  (Twice the products' steps: 1 x 5120 x 13824 takes 220 us instead of 170.)
+// then hold to 2^-16.  (Twice the products' steps: 1 x 5120 x 13824 takes 192 us instead of 149, 2 x
+// 2560 x 6912 56 instead of 42.)
 constexpr int64_t kGluFewElements = 1 << 14;
 inline int glu_passes(int64_t M, int64_t H) { return M * H <= kGluFewElements ? 2 : 1; }
 // The two parts of v: the next bf16 value towards zero (below v, also where v is one) and the rest (a
@@ -430,8 +432,8 @@ __device__ __forceinline__ void store_rows(const f32x4 (&acc)[NB], uint8_t* blk,
 // would leave idle.  A job is a tile over all of k, or, where a product has few tiles, a part of a
 // tile's k: the parts' fp32 sums go to `part` in accumulator order and are added in split order by
 // glu_join_kernel.  Bound by the matrix cores and the power they draw (71% busy at 1.75 GHz) where
-// both sides are large: 8190 x 5120 x 13824 3.5-3.65 ms (1.27-1.33 PFLOP/s); by the tiles' first
-// loads and stores where few tokens meet whole weights: 333 x 2560 x 6912 80 us.
+// both sides are large: 8190 x 5120 x 13824 3.5-3.8 ms (1.22-1.33 PFLOP/s); by the tiles' first
+// loads and stores where few tokens meet whole weights: 333 x 2560 x 6912 79-80 us.
 struct GluJobs {
   int tiles_m, tiles_n, splits;
   int steps, per;  // K steps of a tile, of a part

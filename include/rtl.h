@@ -350,7 +350,8 @@ rtl_status rtl_qk_norm_rope_backward(rtl_dtype dt, int64_t M, int64_t Hq, int64_
  *   X [M,K], Wg [H,K], Wu [H,K], Y [M,H]; G and U [M,H] are optional outputs (NULL to skip),
  *   the pre-activations that rtl_glu_backward takes.
  * act: RTL_ACT_SILU g / (1 + exp(-g)) or RTL_ACT_GELU g Phi(g) (the erf form, Phi within
- * 4e-7), evaluated on the fp32 accumulators; every output is rounded once.  Limits: K % 64 == 0,
+ * 4e-7; relative to its own size, 5e-5 at g = -3, 5e-4 at -4, 1% at -8), evaluated on the fp32
+ * accumulators; every output is rounded once.  Limits: K % 64 == 0,
  * K < 2^22, H <= 2^28 - 16, fewer than 2^24 tiles of 128 x 64 outputs.  Outputs must not overlap
  * inputs or each other.
  */
