@@ -63,6 +63,24 @@ def test_gradient_of_infinities(where, kind, M, H):
     check_glu_gradient(args, kind)
 
 
+# the streamed kernel, small tiles, large tiles
+@pytest.mark.parametrize("M,K,H", ((2, 128, 70), (150, 192, 700), (1100, 640, 4003)))
+@pytest.mark.parametrize("kind", (0, 1), ids=("silu", "gelu"))
+@pytest.mark.parametrize("where", ("X", "Wg", "Wu"))
+def test_forward_of_infinities(where, kind, M, K, H):
+    """An infinite token or weight gives infinities and NaN in its own row or column, as defined."""
+    args = dict(X=rnd(1, M, K), Wg=rnd(2, H, K, std=K ** -0.5), Wu=rnd(3, H, K, std=K ** -0.5))
+    fine = B.glu_forward(*map(B.f64, args.values()), kind)
+    args[where][1, 5] = float("inf")
+    G, U = torch.empty(M, H, dtype=BF, device="cuda"), torch.empty(M, H, dtype=BF, device="cuda")
+    Y = rtl.rtl_glu_fused(**args, act=kind, G=G, U=U)
+    with np.errstate(invalid="ignore"):
+        want = B.glu_forward(*map(B.f64, args.values()), kind)[:3]
+    for t, w, b, name in zip((Y, G, U), want, fine[3:], "YGU"):
+        same_nonfinite(t, w, name)
+        B.check(torch.where(torch.isfinite(t), t, torch.zeros_like(t)), np.where(np.isfinite(w), w, 0.0), b, BF, name)
+
+
 @pytest.mark.parametrize("kind", (0, 1), ids=("silu", "gelu"))
 def test_gradient_past_bf16(kind):
     """dU above the largest bf16 value but within fp32's, in the two-part form: its products with
