@@ -263,10 +263,10 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a, co
 
 // Gradient of norm and rotation.  A fixed number of workgroups walks over the items, each on one
 // of the two tensors (shared out by their heads), the next item's loads in flight while one is
-// formed; each lane sums its channels' dw in fp32 over kQkBackFlush items at a time, in double over
-// these in LDS (a lane meets up to 2^18 heads, of which a tensor with few of the heads has one
-// workgroup: one fp32 sum of 1700 alike terms was 400 half steps off), the workgroup adds its
-// groups, and qk_dw_kernel adds the workgroups: one order, the same result on every run.
+// formed; each lane sums its channels' dw in fp32 over kQkBackFlush items at a time and these in
+// double, in LDS (it can meet 2^18 heads, where a tensor's share is one workgroup; as one fp32 sum
+// 1700 alike terms were 400 half steps off), the workgroup adds its groups, and qk_dw_kernel adds the
+// workgroups: one order, the same result on every run.
 // Bound by memory and, nearly as much, by its vector instructions (the norm, two sums and the
 // rotation for every element of two inputs).  Measured: 4608 x 32 x 128 in bf16 22 us (5.2 TB/s).
 constexpr uint32_t kQkBackFlush = 16;  // even
