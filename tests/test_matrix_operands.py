@@ -101,7 +101,7 @@ def functions(text):
     return out
 
 
-def test_checker():
+def test_distances():
     """The distances, on code that keeps them and on code that does not."""
     def bad(*lines):
         return len(faults(Code(lines)))
