@@ -39,6 +39,10 @@ __all__ = [
     "RTL_ROPE_ADJACENT", "RTL_ROPE_HALVES", "rtl_rope_axes", "rtl_qk_norm_rope", "rtl_qk_norm_rope_backward",
     "rtl_qk_norm_rope_backward_workspace_bytes",
     "RTL_ACT_SILU", "RTL_ACT_GELU", "rtl_glu_fused", "rtl_glu_backward", "rtl_glu_backward_workspace_bytes",
+    "rtl_layer_norm", "rtl_layer_norm_backward", "rtl_layer_norm_backward_workspace_bytes",
+    "rtl_adapters_plan", "rtl_adapters_plan_bytes", "rtl_adapters", "rtl_adapters_workspace_bytes",
+    "rtl_adapters_backward", "rtl_adapters_backward_workspace_bytes",
+    "RTL_STATES_8", "RTL_STATES_32", "AdamWTensors", "rtl_adamw_tensors", "rtl_adamw",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +57,7 @@ RTL_NOALLOC_SCRATCH_BYTES = 192 << 20  # include/rtl.h
 RTL_MLP_AUTO, RTL_MLP_PRODUCER, RTL_MLP_CONSUMER = 0, 1, 2
 RTL_ROPE_ADJACENT, RTL_ROPE_HALVES = 0, 1
 RTL_ACT_SILU, RTL_ACT_GELU = 0, 1
+RTL_STATES_8, RTL_STATES_32 = 8, 32
 STATUS = {0: "RTL_OK", 1: "RTL_ERR_NULL", 2: "RTL_ERR_SHAPE", 3: "RTL_ERR_ALIGN", 4: "RTL_ERR_UNSUPPORTED",
           5: "RTL_ERR_ARG", 6: "RTL_ERR_WORKSPACE", 7: "RTL_ERR_HIP"}
 
@@ -62,7 +67,10 @@ EXPORTS = ["rtl_sparsify", "rtl_linear_fused_workspace_bytes", "rtl_linear_fused
            "rtl_mlp_fused_workspace_bytes", "rtl_mlp_fused", "rtl_quantize_weight_fp8",
            "rtl_linear_fused_fp8_workspace_bytes", "rtl_linear_fused_fp8", "rtl_rope_axes", "rtl_qk_norm_rope",
            "rtl_qk_norm_rope_backward_workspace_bytes", "rtl_qk_norm_rope_backward", "rtl_glu_fused",
-           "rtl_glu_backward_workspace_bytes", "rtl_glu_backward", "rtl_status_string",
+           "rtl_glu_backward_workspace_bytes", "rtl_glu_backward", "rtl_layer_norm",
+           "rtl_layer_norm_backward_workspace_bytes", "rtl_layer_norm_backward", "rtl_adapters_plan_bytes",
+           "rtl_adapters_plan", "rtl_adapters_workspace_bytes", "rtl_adapters",
+           "rtl_adapters_backward_workspace_bytes", "rtl_adapters_backward", "rtl_adamw", "rtl_status_string",
            "rtl_last_error", "rtl_version"]
 
 
@@ -70,6 +78,11 @@ class RtlError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
         self.status = status
+
+
+class _AdamWTensor(ctypes.Structure):
+    """rtl_adamw_tensor of include/rtl.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "master", "m", "v", "m_scale", "v_scale")] + [("n", ctypes.c_int64)]
 
 
 def _load() -> ctypes.CDLL:
@@ -122,6 +135,27 @@ def _load() -> ctypes.CDLL:
     L.rtl_glu_backward_workspace_bytes.restype = sz
     L.rtl_glu_backward.argtypes = [i32, i32, i64, i64, i64, p, p, p, p, p, p, p, p, p, p, sz, p]
     L.rtl_glu_backward.restype = i32
+    rows = [p, i64]  # pointer, row stride
+    L.rtl_layer_norm.argtypes = [i32, i64, i64, *rows, p, p, i64, p, *rows, *rows, f32, *rows, p, p]
+    L.rtl_layer_norm.restype = i32
+    L.rtl_layer_norm_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.rtl_layer_norm_backward_workspace_bytes.restype = sz
+    L.rtl_layer_norm_backward.argtypes = [i32, i64, i64, *rows, p, *rows, p, p, i64, p, *rows, *rows, p, p, p, p, p, sz, p]
+    L.rtl_layer_norm_backward.restype = i32
+    L.rtl_adapters_plan_bytes.argtypes = [i64, i64]
+    L.rtl_adapters_plan_bytes.restype = sz
+    L.rtl_adapters_plan.argtypes = [i64, i64, p, p, sz, p]
+    L.rtl_adapters_plan.restype = i32
+    for name in ("rtl_adapters_workspace_bytes", "rtl_adapters_backward_workspace_bytes"):
+        getattr(L, name).argtypes = [i64] * 5
+        getattr(L, name).restype = sz
+    L.rtl_adapters.argtypes = [i32, i64, i64, i64, i64, i64, *rows, p, p, p, p, sz, *rows, *rows, p, p, sz, p]
+    L.rtl_adapters.restype = i32
+    L.rtl_adapters_backward.argtypes = [i32, i64, i64, i64, i64, i64, *rows, p, p, p, p, sz, p, *rows, *rows, *rows, p, p, p, sz,
+                                        p]
+    L.rtl_adapters_backward.restype = i32
+    L.rtl_adamw.argtypes = [i32, i32, i32, i64, ctypes.POINTER(_AdamWTensor), i64, p, f64, p, f64, f64, f64, f64, p, p]
+    L.rtl_adamw.restype = i32
     L.rtl_status_string.argtypes = [i32]
     L.rtl_status_string.restype = ctypes.c_char_p
     L.rtl_last_error.argtypes = []
@@ -604,3 +638,275 @@ def rtl_glu_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: tor
                                 _flat("dWu", dWu, ws, bf16), *_space(workspace), _queue(stream, X)))
     _changed(given)
     return dX, dWg, dWu
+
+
+_NO_ROWS = None, 0
+
+
+def _rows(name, t, shape, dtype):
+    """Address and row stride of a tensor of `shape` [M, C] and `dtype` whose channels are contiguous
+    (None: null)."""
+    if t is None:
+        return _NO_ROWS
+    if t.shape != shape or t.dtype is not dtype:
+        _mismatch(name, t, shape, dtype)
+    row, channel = t.stride()
+    if channel != 1 and shape[1] > 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return t.data_ptr(), row
+
+
+def _groups(groups, scale):
+    """Number of groups, and the address of their offsets."""
+    if groups is None:
+        return (0 if scale is None else scale.shape[0]), None
+    if groups.dim() != 1 or groups.numel() < 2:
+        raise ValueError(f"groups must hold G + 1 offsets, got shape {tuple(groups.shape)}")
+    return groups.numel() - 1, _flat("groups", groups, groups.shape, torch.int32)
+
+
+def rtl_layer_norm(X: torch.Tensor, weight=None, bias=None, scale=None, shift=None, groups=None, eps: float = 1e-6,
+                   Y=None, stats=None, stream=None) -> torch.Tensor:
+    """Layer norm of every row of X [M,D] (any row stride): y = (n weight + bias) (1 + scale_g) + shift_g.
+
+    ``weight`` and ``bias`` [D] (None: ones, zeros).  ``scale`` and ``shift`` [G,D] (any row stride; both or
+    neither) belong to groups of rows: ``groups`` int32 [G+1] on the GPU holds ascending offsets, rows outside
+    them are left as they were; None: all rows are one group.  ``stats`` [M,2] float32, when given, receives
+    each row's mean and 1 / deviation (rtl_layer_norm_backward takes them).  ``Y`` may be X."""
+    M, D = X.shape
+    shape, dt, ws = (M, D), X.dtype, (D,)
+    there = _elsewhere(X, weight, bias, scale, shift, groups, Y, stats)
+    if there is not None:
+        with there:
+            return rtl_layer_norm(X, weight, bias, scale, shift, groups, eps, Y, stats, stream)
+    given = Y, stats
+    if Y is None:
+        Y = _new(stream, X, shape, dt)
+    G, at = _groups(groups, scale)
+    _check(lib.rtl_layer_norm(_dt(X), M, D, *_rows("X", X, shape, dt), _flat("weight", weight, ws, dt),
+                              _flat("bias", bias, ws, dt), G, at, *_rows("scale", scale, (G, D), dt),
+                              *_rows("shift", shift, (G, D), dt), eps, *_rows("Y", Y, shape, dt),
+                              _flat("stats", stats, (M, 2), torch.float32), _queue(stream, X)))
+    _changed(given)
+    return Y
+
+
+@functools.lru_cache(maxsize=64)
+def rtl_layer_norm_backward_workspace_bytes(M: int, D: int, G: int) -> int:
+    return int(lib.rtl_layer_norm_backward_workspace_bytes(M, D, G))
+
+
+def rtl_layer_norm_backward(X: torch.Tensor, stats: torch.Tensor, dY: torch.Tensor, weight=None, bias=None, scale=None,
+                            groups=None, dX=None, dweight=None, dbias=None, dscale=None, dshift=None, workspace=None,
+                            need_dw: bool = True, stream=None):
+    """Gradient of rtl_layer_norm: (dX, dweight, dbias, dscale, dshift) from its inputs, the ``stats`` it
+    left and dY.  The sums are float32, dweight and dbias [D] for a weight or bias that is given, dscale and
+    dshift [G,D] for a scale that is (else None; all None with ``need_dw`` False).  Rows outside the groups are
+    left as they were in dX and count in no sum.  Outputs given by the caller are written in place; dX may be dY or X."""
+    M, D = X.shape
+    shape, dt, ws, f32 = (M, D), X.dtype, (D,), torch.float32
+    there = _elsewhere(X, stats, dY, weight, bias, scale, groups, dX, dweight, dbias, dscale, dshift, workspace)
+    if there is not None:
+        with there:
+            return rtl_layer_norm_backward(X, stats, dY, weight, bias, scale, groups, dX, dweight, dbias, dscale, dshift,
+                                           workspace, need_dw, stream)
+    G, at = _groups(groups, scale)
+    if not need_dw:
+        dweight = dbias = dscale = dshift = None
+    if scale is None and (dscale is not None or dshift is not None):
+        raise ValueError("dscale or dshift without scale")
+    given = dX, dweight, dbias, dscale, dshift
+    if dX is None:
+        dX = _new(stream, X, shape, dt)
+    if need_dw:
+        if weight is not None and dweight is None:
+            dweight = _new(stream, X, ws, f32)
+        if bias is not None and dbias is None:
+            dbias = _new(stream, X, ws, f32)
+        if scale is not None:
+            dscale = _new(stream, X, (G, D), f32) if dscale is None else dscale
+            dshift = _new(stream, X, (G, D), f32) if dshift is None else dshift
+    if workspace is None:
+        workspace = _new(stream, X, (max(rtl_layer_norm_backward_workspace_bytes(M, D, G), 1),), torch.uint8)
+    _check(lib.rtl_layer_norm_backward(
+        _dt(X), M, D, *_rows("X", X, shape, dt), _flat("stats", stats, (M, 2), f32), *_rows("dY", dY, shape, dt),
+        _flat("weight", weight, ws, dt), _flat("bias", bias, ws, dt), G, at, *_rows("scale", scale, (G, D), dt),
+        *_rows("dX", dX, shape, dt), _flat("dweight", dweight, ws, f32), _flat("dbias", dbias, ws, f32),
+        _flat("dscale", dscale, (G, D), f32), _flat("dshift", dshift, (G, D), f32), *_space(workspace), _queue(stream, X)))
+    _changed(given)
+    return dX, dweight, dbias, dscale, dshift
+
+
+@functools.lru_cache(maxsize=64)
+def rtl_adapters_plan_bytes(M: int, A: int) -> int:
+    return int(lib.rtl_adapters_plan_bytes(M, A))
+
+
+def rtl_adapters_plan(ids: torch.Tensor, A: int, plan=None, stream=None) -> torch.Tensor:
+    """The plan of a batch whose row m has adapter ids[m] (int32 [M] on the GPU; outside 0..A-1: none), for
+    rtl_adapters and rtl_adapters_backward: a uint8 tensor, written in place when given (a captured call
+    then takes the next batch of M rows)."""
+    M, = ids.shape
+    there = _elsewhere(ids, plan)
+    if there is not None:
+        with there:
+            return rtl_adapters_plan(ids, A, plan, stream)
+    given = (plan,)
+    if plan is None:
+        plan = _new(stream, ids, (max(rtl_adapters_plan_bytes(M, A), 1),), torch.uint8)
+    _check(lib.rtl_adapters_plan(M, A, _flat("ids", ids, (M,), torch.int32), *_space(plan), _queue(stream, ids)))
+    _changed(given)
+    return plan
+
+
+@functools.lru_cache(maxsize=64)
+def rtl_adapters_workspace_bytes(M: int, N: int, K: int, R: int, A: int) -> int:
+    return int(lib.rtl_adapters_workspace_bytes(M, N, K, R, A))
+
+
+def _factors(LA, LB):
+    """A, N, R and K of LA [A,N,R] and LB [A,R,K]."""
+    if LA.dim() != 3 or LB.dim() != 3 or LA.shape[0] != LB.shape[0] or LA.shape[2] != LB.shape[1]:
+        raise ValueError(f"LA and LB must be [A,N,R] and [A,R,K], got {tuple(LA.shape)} and {tuple(LB.shape)}")
+    return *LA.shape, LB.shape[2]
+
+
+def rtl_adapters(X: torch.Tensor, LA: torch.Tensor, LB: torch.Tensor, plan: torch.Tensor, alpha=None, Y0=None, Y=None,
+                 T=None, workspace=None, stream=None) -> torch.Tensor:
+    """Y = Y0 + alpha_a (X LB_a^T) LA_a^T, each row with its own adapter a of LA [A,N,R] and LB [A,R,K] (bf16).
+
+    X [M,K] and Y0 [M,N] (what the shared projection made of X; None: zeros) may be parts of wider rows.
+    ``plan`` is rtl_adapters_plan's of the batch, ``alpha`` [A] float32 (None: ones).  ``Y`` may be Y0, and then
+    rows without an adapter are not touched.  ``T`` [M,R] float32, when given, receives X LB_a^T
+    (rtl_adapters_backward takes it)."""
+    M = X.shape[0]
+    A, N, R, K = _factors(LA, LB)
+    bf16 = torch.bfloat16
+    there = _elsewhere(X, LA, LB, plan, alpha, Y0, Y, T, workspace)
+    if there is not None:
+        with there:
+            return rtl_adapters(X, LA, LB, plan, alpha, Y0, Y, T, workspace, stream)
+    given = Y, T
+    if Y is None:
+        Y = _new(stream, X, (M, N), bf16)
+    if workspace is None:
+        workspace = _new(stream, X, (max(rtl_adapters_workspace_bytes(M, N, K, R, A), 1),), torch.uint8)
+    _check(lib.rtl_adapters(RTL_BF16, M, N, K, R, A, *_rows("X", X, (M, K), bf16), _flat("LA", LA, (A, N, R), bf16),
+                            _flat("LB", LB, (A, R, K), bf16), _flat("alpha", alpha, (A,), torch.float32), *_space(plan),
+                            *_rows("Y0", Y0, (M, N), bf16), *_rows("Y", Y, (M, N), bf16),
+                            _flat("T", T, (M, R), torch.float32), *_space(workspace), _queue(stream, X)))
+    _changed(given)
+    return Y
+
+
+@functools.lru_cache(maxsize=64)
+def rtl_adapters_backward_workspace_bytes(M: int, N: int, K: int, R: int, A: int) -> int:
+    return int(lib.rtl_adapters_backward_workspace_bytes(M, N, K, R, A))
+
+
+def rtl_adapters_backward(X: torch.Tensor, LA: torch.Tensor, LB: torch.Tensor, plan: torch.Tensor, T, dY: torch.Tensor,
+                          alpha=None, dX0=None, dX=None, dLA=None, dLB=None, workspace=None, need_dx: bool = True,
+                          need_dw: bool = True, stream=None):
+    """Gradient of rtl_adapters: (dX, dLA, dLB) from its inputs, the ``T`` it left and dY [M,N].
+
+    dX = dX0 + alpha_a (dY LA_a) LB_a [M,K] (``dX0``: what came through the shared projection, None: zeros;
+    ``dX`` may be dX0); dLA [A,N,R] and dLB [A,R,K] are float32, zeros for an adapter without rows.
+    ``need_dx`` or ``need_dw`` False leaves those out (None).  Outputs given by the caller are written in place."""
+    M = X.shape[0]
+    A, N, R, K = _factors(LA, LB)
+    bf16, f32 = torch.bfloat16, torch.float32
+    there = _elsewhere(X, LA, LB, plan, T, dY, alpha, dX0, dX, dLA, dLB, workspace)
+    if there is not None:
+        with there:
+            return rtl_adapters_backward(X, LA, LB, plan, T, dY, alpha, dX0, dX, dLA, dLB, workspace, need_dx, need_dw,
+                                         stream)
+    if not need_dx:
+        dX = None
+    if not need_dw:
+        dLA = dLB = None
+    given = dX, dLA, dLB
+    if need_dx and dX is None:
+        dX = _new(stream, X, (M, K), bf16)
+    if need_dw:
+        dLA = _new(stream, X, (A, N, R), f32) if dLA is None else dLA
+        dLB = _new(stream, X, (A, R, K), f32) if dLB is None else dLB
+    if workspace is None:
+        workspace = _new(stream, X, (max(rtl_adapters_backward_workspace_bytes(M, N, K, R, A), 1),), torch.uint8)
+    _check(lib.rtl_adapters_backward(
+        RTL_BF16, M, N, K, R, A, *_rows("X", X, (M, K), bf16), _flat("LA", LA, (A, N, R), bf16),
+        _flat("LB", LB, (A, R, K), bf16), _flat("alpha", alpha, (A,), f32), *_space(plan), _flat("T", T, (M, R), f32),
+        *_rows("dY", dY, (M, N), bf16), *_rows("dX0", dX0, (M, K), bf16), *_rows("dX", dX, (M, K), bf16),
+        _flat("dLA", dLA, (A, N, R), f32), _flat("dLB", dLB, (A, R, K), f32), *_space(workspace), _queue(stream, X)))
+    _changed(given)
+    return dX, dLA, dLB
+
+
+class AdamWTensors:
+    """The tensors that an rtl_adamw call steps, checked and listed once (rtl_adamw_tensors).  It holds
+    them: their memory stays as long as it does, and a tensor that is replaced needs a new list."""
+
+    def __init__(self, params, grads, m, v, masters, m_scales, v_scales):
+        kinds = dict(p=params, g=grads, master=masters, m=m, v=v, m_scale=m_scales, v_scale=v_scales)
+        kinds = {n: [t.detach() for t in ts] for n, ts in kinds.items() if ts is not None}
+        if not kinds["p"]:
+            raise ValueError("no tensors")
+        if any(len(ts) != len(kinds["p"]) for ts in kinds.values()):
+            raise ValueError("the lists differ in length: " + ", ".join(f"{n} {len(ts)}" for n, ts in kinds.items()))
+        self.p_dt, self.g_dt = _dt(kinds["p"][0]), _dt(kinds["g"][0])
+        self.states = RTL_STATES_32 if kinds["m"][0].dtype is torch.float32 else RTL_STATES_8
+        if (self.p_dt == RTL_BF16) != ("master" in kinds):
+            raise ValueError("bf16 parameters need fp32 masters, fp32 ones take none")
+        if any((self.states == RTL_STATES_8) != (n in kinds) for n in ("m_scale", "v_scale")):
+            raise ValueError("8-bit states need m_scales and v_scales, 32-bit ones take none")
+        state = torch.float32 if self.states == RTL_STATES_32 else torch.float8_e4m3fn
+        types = dict(p=kinds["p"][0].dtype, g=kinds["g"][0].dtype, master=torch.float32, m=state, v=state,
+                     m_scale=torch.float32, v_scale=torch.float32)
+        self.like = kinds["p"][0]
+        _elsewhere(self.like, *(t for ts in kinds.values() for t in ts))
+        self.array = (_AdamWTensor * len(kinds["p"]))()
+        for i, entry in enumerate(self.array):
+            shape = kinds["p"][i].shape
+            entry.n = kinds["p"][i].numel()
+            blocks = ((entry.n + 255) // 256,)
+            for n, ts in kinds.items():
+                setattr(entry, n, _flat(f"{n}[{i}]", ts[i], blocks if n.endswith("scale") else shape, types[n]))
+        self.held = kinds
+        self.changed = [t for n, ts in kinds.items() if n != "g" for t in ts]
+
+
+def rtl_adamw_tensors(params, grads, m, v, masters=None, m_scales=None, v_scales=None) -> AdamWTensors:
+    """The list that rtl_adamw steps: tensors of equal shapes at equal places of ``params``, ``grads``, ``m``, ``v`` and,
+    where ``params`` are bf16, ``masters`` (float32).  m and v are float32, or torch.float8_e4m3fn with
+    ``m_scales`` and ``v_scales`` float32 [(n + 255) // 256] (all zeros to start)."""
+    return AdamWTensors(params, grads, m, v, masters, m_scales, v_scales)
+
+
+def _number(name, x, dtype, like):
+    """A number, or the address of one on the GPU: (number, address)."""
+    if not isinstance(x, torch.Tensor):
+        return x, None
+    if x.numel() != 1 or x.dtype is not dtype:
+        raise ValueError(f"{name} must be one {dtype}, got {x.dtype} of shape {tuple(x.shape)}")
+    _elsewhere(like, x)
+    return 1, x.data_ptr()
+
+
+def rtl_adamw(tensors: AdamWTensors, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+              weight_decay: float = 0.01, grad_scale=None, stream=None) -> None:
+    """One AdamW step of all ``tensors`` in place (rtl_adamw_tensors), on the gradients they hold then:
+    m += (1 - beta1) (g - m), v = beta2 v + (1 - beta2) g^2, and the parameters (their masters, where bf16) less
+    lr (m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps) + weight_decay p).
+
+    ``step`` counts from 1.  ``step`` (int64), ``lr`` and ``grad_scale`` (float32; a factor of the gradients) may be tensors of
+    one element on the GPU, which a captured call reads anew with every replay."""
+    like = tensors.like
+    there = _elsewhere(like)
+    if there is not None:
+        with there:
+            return rtl_adamw(tensors, step, lr, beta1, beta2, eps, weight_decay, grad_scale, stream)
+    step, step_at = _number("step", step, torch.int64, like)
+    lr, lr_at = _number("lr", lr, torch.float32, like)
+    scale_at = None if grad_scale is None else _number("grad_scale", torch.as_tensor(grad_scale), torch.float32, like)[1]
+    _check(lib.rtl_adamw(tensors.p_dt, tensors.g_dt, tensors.states, len(tensors.array), tensors.array, step, step_at, lr,
+                         lr_at, beta1, beta2, eps, weight_decay, scale_at, _queue(stream, like)))
+    _changed(tensors.changed)

@@ -344,18 +344,6 @@ hipError_t launch_glu_bf16(int act, int64_t M, int64_t K, int64_t H, const void*
 // 2560 x 6912 56 instead of 42.)
 constexpr int64_t kGluFewElements = 1 << 14;
 inline int glu_passes(int64_t M, int64_t H) { return M * H <= kGluFewElements ? 2 : 1; }
-// The two parts of v: the next bf16 value towards zero (below v, also where v is one) and the rest (a
-// bf16 value is exact in its two parts).  Each has v's sign and is 0 only where v is (down to
-// 2^-102), so that with an infinite weight or token both give the same infinity, where opposite
-// ones, or a part of 0, would give NaN.  An infinity or NaN is its own second part.
-struct GluParts {
-  __bf16 hi, lo;
-};
-__device__ __forceinline__ GluParts glu_parts(float v) {
-  if (!__builtin_isfinite(v) || v == 0.f) return {(__bf16)v, (__bf16)v};
-  const float hi = __uint_as_float((__float_as_uint(v) - 1) & 0xFFFF0000u);
-  return {(__bf16)hi, (__bf16)(v - hi)};
-}
 template <int ACT>
 __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int64_t Hp, const uint16_t* G,
                                                        const uint16_t* U, const uint16_t* dY, uint16_t* P, int passes) {
@@ -388,7 +376,7 @@ __global__ __launch_bounds__(256) void glu_back_kernel(int64_t M, int64_t H, int
       if (passes == 1) {
         p[0][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)v[k][0], (__bf16)v[k][1]});
       } else {
-        const GluParts a = glu_parts(v[k][0]), b = glu_parts(v[k][1]);
+        const Bf16Parts a = two_parts(v[k][0]), b = two_parts(v[k][1]);
         p[0][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{a.hi, b.hi});
         p[1][k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{a.lo, b.lo});
       }

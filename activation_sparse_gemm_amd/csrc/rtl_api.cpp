@@ -3,9 +3,11 @@
 // and a call that fails validation launches nothing and writes no output.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 
 #include "../../include/rtl.h"
@@ -718,6 +720,401 @@ rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int
   return hip_status(rtl::launch_glu_back_bf16(act == RTL_ACT_SILU ? rtl::kActSilu : rtl::kActGelu, M, K, H, X, Wg, Wu, G,
                                               U, dY, dX, dWg, dWu, workspace, (hipStream_t)stream),
                     "rtl_glu_backward launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// A [M, D] tensor with a row stride, aligned to its elements; the stride of one row counts as 0.
+View rows_of(const void* p, int64_t M, int64_t D, int64_t row, size_t es) { return View(p, M, 1, D, row, 0, es); }
+
+rtl_status check_rows(const View& v, const char* name, bool output) {
+  if (!v.p) return fail(RTL_ERR_NULL, "%s is required", name);
+  if (v.row < 0 || (__int128)(v.M - 1) * v.row > ((int64_t)1 << 48))
+    return fail(RTL_ERR_SHAPE, "row stride of %s out of range (%lld)", name, (long long)v.row);
+  if ((uintptr_t)v.p % v.es != 0) return fail(RTL_ERR_ALIGN, "%s must be aligned to its elements", name);
+  if (output && v.M > 1 && v.row < v.D) return fail(RTL_ERR_ARG, "the rows of %s overlap", name);
+  return RTL_OK;
+}
+
+// What the layer norm and its gradient share; fills the call but for y, dy and stats.
+rtl_status check_norm(rtl_dtype dt, int64_t M, int64_t D, const View& x, const void* w, const void* b, int64_t G,
+                      const int32_t* groups, const View& scale, rtl::NormCall& c) {
+  rtl_status st;
+  const size_t es = elem_size(dt);
+  if ((st = check_rows(x, "X", false)) != RTL_OK) return st;
+  if ((uintptr_t)w % es != 0 || (uintptr_t)b % es != 0 || (uintptr_t)groups % 4 != 0)
+    return fail(RTL_ERR_ALIGN, "w, b and groups must be aligned to their elements");
+  if (groups == nullptr && G > 1) return fail(RTL_ERR_NULL, "groups is required for G = %lld", (long long)G);
+  if (groups != nullptr && G < 1) return fail(RTL_ERR_SHAPE, "groups of G = %lld", (long long)G);
+  if (scale.p != nullptr && G < 1) return fail(RTL_ERR_SHAPE, "scale and shift of G = %lld", (long long)G);
+  c = rtl::NormCall{};
+  c.dt = dt == RTL_BF16 ? rtl::kDtBF16 : rtl::kDtF32;
+  c.M = M;
+  c.D = D;
+  c.G = G;
+  c.x = rtl::RowsView{x.p, x.row};
+  c.scale = rtl::RowsView{scale.p, scale.row};
+  c.w = w;
+  c.b = b;
+  c.groups = groups;
+  return RTL_OK;
+}
+
+rtl_status check_norm_sizes(rtl_dtype dt, int64_t M, int64_t D, int64_t G) {
+  rtl_status st;
+  if ((st = check_dtype(dt)) != RTL_OK) return st;
+  if (M <= 0 || D <= 0 || G < 0)
+    return fail(RTL_ERR_SHAPE, "need M, D > 0 and G >= 0 (M=%lld D=%lld G=%lld)", (long long)M, (long long)D, (long long)G);
+  if (M > INT32_MAX || G >= INT32_MAX) return fail(RTL_ERR_SHAPE, "M or G is too large (M=%lld G=%lld)", (long long)M, (long long)G);
+  if (!rtl::norm_fits(dt == RTL_BF16 ? rtl::kDtBF16 : rtl::kDtF32, D, true))
+    return fail(RTL_ERR_UNSUPPORTED, "D is too large (D=%lld)", (long long)D);
+  return RTL_OK;
+}
+
+rtl_status check_norm_width(const rtl::NormCall& c) {
+  if (!rtl::norm_fits(c.dt, c.D, rtl::norm_is_wide(c)))
+    return fail(RTL_ERR_UNSUPPORTED, "D above %lld needs 16-byte aligned rows (D=%lld)", (long long)rtl::kNormMaxDNarrow,
+                (long long)c.D);
+  return RTL_OK;
+}
+
+// Flat outputs and a workspace against strided and flat inputs and against each other.
+struct Flat {
+  const void* p;
+  size_t bytes;
+};
+template <int NO, int NI>
+rtl_status check_flat_apart(const Flat (&outs)[NO], const Flat (&ins)[NI]) {
+  for (int o = 0; o < NO; o++) {
+    for (int i = 0; i < NI; i++)
+      if (overlap(outs[o].p, outs[o].bytes, ins[i].p, ins[i].bytes))
+        return fail(RTL_ERR_ARG, "an output or the workspace overlaps an input");
+    for (int k = o + 1; k < NO; k++)
+      if (overlap(outs[o].p, outs[o].bytes, outs[k].p, outs[k].bytes))
+        return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+  }
+  return RTL_OK;
+}
+Flat range_of(const View& v) { return Flat{v.p, v.p ? (size_t)v.span() * v.es : 0}; }
+
+}  // namespace
+
+extern "C" {
+
+rtl_status rtl_layer_norm(rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const void* w, const void* b,
+                          int64_t G, const int32_t* groups, const void* scale, int64_t scale_row, const void* shift,
+                          int64_t shift_row, float eps, void* Y, int64_t y_row, float* stats, void* stream) {
+  rtl_status st;
+  if ((st = check_norm_sizes(dt, M, D, G)) != RTL_OK || (st = check_norm_eps(eps)) != RTL_OK) return st;
+  const size_t es = elem_size(dt);
+  const View x = rows_of(X, M, D, x_row, es), y = rows_of(Y, M, D, y_row, es);
+  const View sc = rows_of(scale, G, D, scale_row, es), sh = rows_of(shift, G, D, shift_row, es);
+  rtl::NormCall c;
+  if ((st = check_norm(dt, M, D, x, w, b, G, groups, sc, c)) != RTL_OK || (st = check_rows(y, "Y", true)) != RTL_OK) return st;
+  if ((scale == nullptr) != (shift == nullptr)) return fail(RTL_ERR_NULL, "scale and shift go together");
+  if (scale != nullptr &&
+      ((st = check_rows(sc, "scale", false)) != RTL_OK || (st = check_rows(sh, "shift", false)) != RTL_OK))
+    return st;
+  if ((uintptr_t)stats % 8 != 0) return fail(RTL_ERR_ALIGN, "stats must be 8-byte aligned");
+  c.y = rtl::RowsView{y.p, y.row};
+  c.shift = rtl::RowsView{sh.p, sh.row};
+  c.eps = eps;
+  c.stats = stats;
+  if ((st = check_norm_width(c)) != RTL_OK) return st;
+  const Flat small[3] = {{w, (size_t)D * es}, {b, (size_t)D * es}, {groups, (size_t)(G + 1) * 4}};
+  const Flat wide[2] = {scale ? range_of(sc) : Flat{nullptr, 0}, shift ? range_of(sh) : Flat{nullptr, 0}};
+  if (!x.same(y) && !apart(x, y)) return fail(RTL_ERR_ARG, "Y overlaps an input");
+  for (const Flat& f : small)
+    if (!apart_flat(y, f.p, f.bytes)) return fail(RTL_ERR_ARG, "Y overlaps an input");
+  for (const Flat& f : wide)
+    if (!apart_flat(y, f.p, f.bytes)) return fail(RTL_ERR_ARG, "Y overlaps an input");
+  const Flat outs[1] = {{stats, (size_t)M * 8}};
+  const Flat ins[6] = {small[0], small[1], small[2], wide[0], wide[1], range_of(x)};
+  if ((st = check_flat_apart(outs, ins)) != RTL_OK) return st;
+  if (!apart_flat(y, stats, (size_t)M * 8)) return fail(RTL_ERR_ARG, "outputs overlap each other");
+  return hip_status(rtl::launch_norm(c, (hipStream_t)stream), "rtl_layer_norm launch");
+}
+
+size_t rtl_layer_norm_backward_workspace_bytes(int64_t M, int64_t D, int64_t G) {
+  if (M <= 0 || D <= 0 || G < 0 || M > INT32_MAX || D > rtl::kNormMaxD || G >= INT32_MAX || G * D >= (int64_t)1 << 29) return 0;
+  return rtl::norm_back_workspace(M, D, G);
+}
+
+rtl_status rtl_layer_norm_backward(rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const float* stats,
+                                   const void* dY, int64_t dy_row, const void* w, const void* b, int64_t G,
+                                   const int32_t* groups, const void* scale, int64_t scale_row, void* dX, int64_t dx_row,
+                                   float* dw, float* db, float* dscale, float* dshift, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  rtl_status st;
+  if ((st = check_norm_sizes(dt, M, D, G)) != RTL_OK) return st;
+  if (G * D >= (int64_t)1 << 29) return fail(RTL_ERR_SHAPE, "G x D is too large (G=%lld D=%lld)", (long long)G, (long long)D);
+  const size_t es = elem_size(dt);
+  const View x = rows_of(X, M, D, x_row, es), dy = rows_of(dY, M, D, dy_row, es), dx = rows_of(dX, M, D, dx_row, es);
+  const View sc = rows_of(scale, G, D, scale_row, es);
+  rtl::NormCall c;
+  if ((st = check_norm(dt, M, D, x, w, b, G, groups, sc, c)) != RTL_OK || (st = check_rows(dy, "dY", false)) != RTL_OK ||
+      (st = check_rows(dx, "dX", true)) != RTL_OK)
+    return st;
+  if (scale != nullptr && (st = check_rows(sc, "scale", false)) != RTL_OK) return st;
+  if (!stats) return fail(RTL_ERR_NULL, "stats is required");
+  if (scale == nullptr && (dscale != nullptr || dshift != nullptr))
+    return fail(RTL_ERR_ARG, "dscale and dshift without scale");
+  if ((uintptr_t)stats % 8 != 0 || misaligned(dw) || misaligned(db) || misaligned(dscale) || misaligned(dshift) ||
+      misaligned(workspace))
+    return fail(RTL_ERR_ALIGN, "stats must be 8-byte aligned, the sums and the workspace 16-byte aligned");
+  c.y = rtl::RowsView{dx.p, dx.row};
+  c.dy = rtl::RowsView{dy.p, dy.row};
+  c.stats = stats;
+  if ((st = check_norm_width(c)) != RTL_OK) return st;
+  const size_t need = rtl::norm_back_workspace(M, D, G), wb = (size_t)D * 4, gb = (size_t)(G > 0 ? G : 1) * D * 4;
+  const Flat outs[5] = {{dw, wb}, {db, wb}, {dscale, gb}, {dshift, gb}, {workspace, need}};
+  const Flat ins[7] = {{w, (size_t)D * es}, {b, (size_t)D * es}, {groups, (size_t)(G + 1) * 4}, {stats, (size_t)M * 8},
+                       scale ? range_of(sc) : Flat{nullptr, 0}, range_of(x), range_of(dy)};
+  if ((st = check_flat_apart(outs, ins)) != RTL_OK) return st;
+  for (const Flat& f : outs)
+    if (!apart_flat(dx, f.p, f.bytes)) return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+  for (int i = 0; i < 5; i++)
+    if (!apart_flat(dx, ins[i].p, ins[i].bytes)) return fail(RTL_ERR_ARG, "an output overlaps an input");
+  if ((!x.same(dx) && !apart(x, dx)) || (!dy.same(dx) && !apart(dy, dx)))
+    return fail(RTL_ERR_ARG, "an output overlaps an input");
+  if (!workspace || ws_bytes < need)
+    return fail(RTL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  return hip_status(rtl::launch_norm_back(c, dw, db, dscale, dshift, workspace, (hipStream_t)stream),
+                    "rtl_layer_norm_backward launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+bool adapters_fit(int64_t M, int64_t A) { return M > 0 && M <= 1 << 24 && A > 0 && A <= 4096; }
+bool adapters_fit(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
+  return adapters_fit(M, A) && N > 0 && N <= kMaxK && K > 0 && K <= kMaxK && R > 0 && R <= 128 && N % 8 == 0 && K % 8 == 0 &&
+         R % 8 == 0 && A * R * (N > K ? N : K) <= (int64_t)1 << 40;
+}
+
+rtl_status check_plan_sizes(int64_t M, int64_t A) {
+  if (M <= 0 || A <= 0) return fail(RTL_ERR_SHAPE, "need M, A > 0 (M=%lld A=%lld)", (long long)M, (long long)A);
+  if (!adapters_fit(M, A)) return fail(RTL_ERR_SHAPE, "M or A is too large (M=%lld A=%lld)", (long long)M, (long long)A);
+  return RTL_OK;
+}
+
+rtl_status check_adapters(rtl_dtype dt, int64_t M, int64_t N, int64_t K, int64_t R, int64_t A, const void* LA, const void* LB,
+                          const void* plan, size_t plan_bytes, const float* alpha) {
+  rtl_status st;
+  if ((st = check_dtype(dt)) != RTL_OK) return st;
+  if (dt != RTL_BF16) return fail(RTL_ERR_UNSUPPORTED, "adapters are bf16 only");
+  if ((st = check_plan_sizes(M, A)) != RTL_OK) return st;
+  if (N <= 0 || K <= 0 || R <= 0 || N > kMaxK || K > kMaxK)
+    return fail(RTL_ERR_SHAPE, "need N, K in 1 .. 2^22 and R > 0 (N=%lld K=%lld R=%lld)", (long long)N, (long long)K, (long long)R);
+  if (N % 8 != 0 || K % 8 != 0 || R % 8 != 0 || R > 128)
+    return fail(RTL_ERR_UNSUPPORTED, "adapters need N, K, R multiples of 8 and R <= 128 (N=%lld K=%lld R=%lld)", (long long)N,
+                (long long)K, (long long)R);
+  if (!adapters_fit(M, N, K, R, A)) return fail(RTL_ERR_SHAPE, "the factors are too large (A=%lld R=%lld)", (long long)A, (long long)R);
+  if (!LA || !LB || !plan) return fail(RTL_ERR_NULL, "LA, LB and the plan are required");
+  if (misaligned(LA) || misaligned(LB) || misaligned(plan)) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  if ((uintptr_t)alpha % 4 != 0) return fail(RTL_ERR_ALIGN, "alpha must be aligned to its elements");
+  if (plan_bytes != rtl::adapters_plan_bytes(M, A))
+    return fail(RTL_ERR_ARG, "the plan has %zu bytes, one for M=%lld and A=%lld has %zu", plan_bytes, (long long)M, (long long)A,
+                rtl::adapters_plan_bytes(M, A));
+  return RTL_OK;
+}
+
+// A [M, C] tensor of bf16 rows that 16-byte accesses reach.
+rtl_status check_bf16_rows(const View& v, const char* name, bool output) {
+  rtl_status st = check_rows(v, name, output);
+  if (st != RTL_OK) return st;
+  if (misaligned(v.p) || v.row % 8 != 0) return fail(RTL_ERR_ALIGN, "%s and its rows must be 16-byte aligned", name);
+  return RTL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rtl_adapters_plan_bytes(int64_t M, int64_t A) { return adapters_fit(M, A) ? rtl::adapters_plan_bytes(M, A) : 0; }
+
+rtl_status rtl_adapters_plan(int64_t M, int64_t A, const int32_t* ids, void* plan, size_t plan_bytes, void* stream) {
+  rtl_status st;
+  if ((st = check_plan_sizes(M, A)) != RTL_OK) return st;
+  if (!ids || !plan) return fail(RTL_ERR_NULL, "ids and the plan are required");
+  if ((uintptr_t)ids % 4 != 0 || misaligned(plan)) return fail(RTL_ERR_ALIGN, "the plan must be 16-byte aligned, ids to its elements");
+  const size_t need = rtl::adapters_plan_bytes(M, A);
+  if (plan_bytes != need) return fail(RTL_ERR_ARG, "the plan needs %zu bytes, got %zu", need, plan_bytes);
+  if (overlap(plan, need, ids, (size_t)M * 4)) return fail(RTL_ERR_ARG, "the plan overlaps ids");
+  return hip_status(rtl::launch_adapters_plan(ids, M, A, plan, (hipStream_t)stream), "rtl_adapters_plan launch");
+}
+
+size_t rtl_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
+  return adapters_fit(M, N, K, R, A) ? rtl::adapters_workspace(M, N, K, R, A) : 0;
+}
+
+rtl_status rtl_adapters(rtl_dtype dt, int64_t M, int64_t N, int64_t K, int64_t R, int64_t A, const void* X, int64_t x_row,
+                        const void* LA, const void* LB, const float* alpha, const void* plan, size_t plan_bytes,
+                        const void* Y0, int64_t y0_row, void* Y, int64_t y_row, float* T, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  rtl_status st;
+  if ((st = check_adapters(dt, M, N, K, R, A, LA, LB, plan, plan_bytes, alpha)) != RTL_OK) return st;
+  const View x = rows_of(X, M, K, x_row, 2), y0 = rows_of(Y0, M, N, y0_row, 2), y = rows_of(Y, M, N, y_row, 2);
+  if ((st = check_bf16_rows(x, "X", false)) != RTL_OK || (st = check_bf16_rows(y, "Y", true)) != RTL_OK) return st;
+  if (Y0 != nullptr && (st = check_bf16_rows(y0, "Y0", false)) != RTL_OK) return st;
+  if (misaligned(T) || misaligned(workspace)) return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  const size_t need = rtl::adapters_workspace(M, N, K, R, A), tb = (size_t)M * R * 4;
+  const Flat ins[6] = {{LA, (size_t)A * N * R * 2}, {LB, (size_t)A * K * R * 2}, {plan, plan_bytes}, {alpha, (size_t)A * 4},
+                       range_of(x), Y0 ? range_of(y0) : Flat{nullptr, 0}};
+  const Flat outs[2] = {{T, tb}, {workspace, need}};
+  if ((st = check_flat_apart(outs, ins)) != RTL_OK) return st;
+  for (const Flat& f : outs)
+    if (!apart_flat(y, f.p, f.bytes)) return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+  for (int i = 0; i < 4; i++)
+    if (!apart_flat(y, ins[i].p, ins[i].bytes)) return fail(RTL_ERR_ARG, "Y overlaps an input");
+  if (!apart(x, y) || (Y0 != nullptr && !y0.same(y) && !apart(y0, y))) return fail(RTL_ERR_ARG, "Y overlaps an input");
+  if (!workspace || ws_bytes < need)
+    return fail(RTL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  const rtl::AdapterCall c{M, N, K, R, A, X, x.row, LA, LB, plan, alpha};
+  return hip_status(rtl::launch_adapters(c, Y0, y0.row, Y, y.row, T, workspace, (hipStream_t)stream), "rtl_adapters launch");
+}
+
+size_t rtl_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
+  return adapters_fit(M, N, K, R, A) ? rtl::adapters_back_workspace(M, N, K, R, A) : 0;
+}
+
+rtl_status rtl_adapters_backward(rtl_dtype dt, int64_t M, int64_t N, int64_t K, int64_t R, int64_t A, const void* X,
+                                 int64_t x_row, const void* LA, const void* LB, const float* alpha, const void* plan,
+                                 size_t plan_bytes, const float* T, const void* dY, int64_t dy_row, const void* dX0,
+                                 int64_t dx0_row, void* dX, int64_t dx_row, float* dLA, float* dLB, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  rtl_status st;
+  if ((st = check_adapters(dt, M, N, K, R, A, LA, LB, plan, plan_bytes, alpha)) != RTL_OK) return st;
+  if (!dX && !dLA && !dLB) return fail(RTL_ERR_NULL, "one of dX, dLA and dLB is required");
+  if (!dX) dX0 = nullptr;
+  if (!dLB) X = nullptr;
+  if (!dLA) T = nullptr;
+  const View x = rows_of(X, M, K, x_row, 2), dy = rows_of(dY, M, N, dy_row, 2), dx0 = rows_of(dX0, M, K, dx0_row, 2),
+             dx = rows_of(dX, M, K, dx_row, 2);
+  if ((st = check_bf16_rows(dy, "dY", false)) != RTL_OK || (dLB && (st = check_bf16_rows(x, "X", false)) != RTL_OK) ||
+      (dX && (st = check_bf16_rows(dx, "dX", true)) != RTL_OK) || (dX0 && (st = check_bf16_rows(dx0, "dX0", false)) != RTL_OK))
+    return st;
+  if (dLA && !T) return fail(RTL_ERR_NULL, "T is required");
+  if (misaligned(T) || misaligned(dLA) || misaligned(dLB) || misaligned(workspace))
+    return fail(RTL_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  const size_t need = rtl::adapters_back_workspace(M, N, K, R, A);
+  const Flat none{nullptr, 0};
+  const Flat ins[8] = {{LA, (size_t)A * N * R * 2}, {LB, (size_t)A * K * R * 2}, {plan, plan_bytes}, {alpha, (size_t)A * 4},
+                       {T, (size_t)M * R * 4}, range_of(dy), X ? range_of(x) : none, dX0 ? range_of(dx0) : none};
+  const Flat outs[3] = {{dLA, (size_t)A * N * R * 4}, {dLB, (size_t)A * K * R * 4}, {workspace, need}};
+  if ((st = check_flat_apart(outs, ins)) != RTL_OK) return st;
+  if (dX != nullptr) {
+    for (const Flat& f : outs)
+      if (!apart_flat(dx, f.p, f.bytes)) return fail(RTL_ERR_ARG, "outputs overlap each other or the workspace");
+    for (int i = 0; i < 5; i++)
+      if (!apart_flat(dx, ins[i].p, ins[i].bytes)) return fail(RTL_ERR_ARG, "dX overlaps an input");
+    if (!apart(dy, dx) || (X && !apart(x, dx)) || (dX0 && !dx0.same(dx) && !apart(dx0, dx)))
+      return fail(RTL_ERR_ARG, "dX overlaps an input");
+  }
+  if (!workspace || ws_bytes < need)
+    return fail(RTL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  const rtl::AdapterCall c{M, N, K, R, A, X, x.row, LA, LB, plan, alpha};
+  return hip_status(rtl::launch_adapters_back(c, T, dY, dy.row, dX0, dx0.row, dX, dx.row, dLA, dLB, workspace, (hipStream_t)stream),
+                    "rtl_adapters_backward launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Memory ranges of a list of tensors, sorted, so that one pass finds those that overlap.
+struct Range {
+  uintptr_t from, to;
+  bool output;
+  bool operator<(const Range& o) const { return from < o.from; }
+};
+
+}  // namespace
+
+extern "C" {
+
+rtl_status rtl_adamw(rtl_dtype p_dt, rtl_dtype g_dt, rtl_states states, int64_t count, const rtl_adamw_tensor* tensors,
+                     int64_t step, const int64_t* step_at, double lr, const float* lr_at, double beta1, double beta2,
+                     double eps, double weight_decay, const float* grad_scale, void* stream) {
+  rtl_status st;
+  if ((st = check_dtype(p_dt)) != RTL_OK || (st = check_dtype(g_dt)) != RTL_OK) return st;
+  if (states != RTL_STATES_8 && states != RTL_STATES_32) return fail(RTL_ERR_UNSUPPORTED, "unsupported states %d", (int)states);
+  if (count <= 0 || count > 1 << 20) return fail(RTL_ERR_SHAPE, "need 1 to 2^20 tensors (%lld)", (long long)count);
+  if (!tensors) return fail(RTL_ERR_NULL, "tensors is required");
+  if (!step_at && step < 1) return fail(RTL_ERR_ARG, "step counts from 1 (got %lld)", (long long)step);
+  if ((!lr_at && !std::isfinite((float)lr)) || !std::isfinite((float)weight_decay) || !(beta1 >= 0 && (float)beta1 < 1) || !(beta2 >= 0 && (float)beta2 < 1) ||
+      !(eps >= 0 && eps <= 1))
+    return fail(RTL_ERR_ARG, "need finite lr and weight_decay, betas in [0, 1), eps in [0, 1] (lr=%g betas=%g,%g eps=%g decay=%g)", lr,
+                beta1, beta2, eps, weight_decay);
+  if ((uintptr_t)step_at % 8 != 0 || (uintptr_t)lr_at % 4 != 0 || (uintptr_t)grad_scale % 4 != 0)
+    return fail(RTL_ERR_ALIGN, "step_at, lr_at and grad_scale must be aligned to their elements");
+  const bool eight = states == RTL_STATES_8, bf16 = p_dt == RTL_BF16;
+  const size_t ps = elem_size(p_dt), gs = elem_size(g_dt), ss = eight ? 1 : 4;
+  for (int64_t i = 0; i < count; i++) {
+    const rtl_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n > rtl::kAdamMaxN) return fail(RTL_ERR_SHAPE, "tensor %lld has %lld elements", (long long)i, (long long)t.n);
+    if (t.n == 0) continue;
+    if (!t.p || !t.g || !t.m || !t.v || bf16 != (t.master != nullptr) || eight != (t.m_scale != nullptr) ||
+        eight != (t.v_scale != nullptr))
+      return fail(RTL_ERR_NULL, "tensor %lld needs p, g, m, v, a master beside bf16 parameters alone and scales beside 8-bit states alone",
+                  (long long)i);
+    if (misaligned(t.p) || misaligned(t.g) || misaligned(t.master) || misaligned(t.m) || misaligned(t.v) ||
+        (uintptr_t)t.m_scale % 4 != 0 || (uintptr_t)t.v_scale % 4 != 0)
+      return fail(RTL_ERR_ALIGN, "tensor %lld must be 16-byte aligned", (long long)i);
+  }
+  Range* all = (Range*)malloc(sizeof(Range) * (size_t)(7 * count + 3));
+  if (all == nullptr) return fail(RTL_ERR_HIP, "no host memory for %lld tensors", (long long)count);
+  size_t k = 0;
+  auto add = [&](const void* p, size_t bytes, bool output) {
+    if (p != nullptr && bytes > 0) all[k++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, output};
+  };
+  for (int64_t i = 0; i < count; i++) {
+    const rtl_adamw_tensor& t = tensors[i];
+    const size_t n = (size_t)t.n, blocks = (n + 255) / 256 * 4;
+    add(t.p, n * ps, true);
+    add(t.g, n * gs, false);
+    add(t.master, bf16 ? n * 4 : 0, true);
+    add(t.m, n * ss, true);
+    add(t.v, n * ss, true);
+    add(t.m_scale, eight ? blocks : 0, true);
+    add(t.v_scale, eight ? blocks : 0, true);
+  }
+  add(step_at, 8, false);
+  add(lr_at, 4, false);
+  add(grad_scale, 4, false);
+  std::sort(all, all + k);
+  uintptr_t end = 0, out_end = 0;
+  bool clash = false;
+  for (size_t i = 0; i < k; i++) {
+    clash |= all[i].from < (all[i].output ? end : out_end);
+    end = std::max(end, all[i].to);
+    if (all[i].output) out_end = std::max(out_end, all[i].to);
+  }
+  free(all);
+  if (clash) return fail(RTL_ERR_ARG, "tensors overlap each other");
+  rtl::AdamRates r{};
+  r.beta1 = beta1;
+  r.beta2 = beta2;
+  r.step_at = step_at;
+  r.lr_at = lr_at;
+  r.grad_scale = grad_scale;
+  r.lr = (float)lr;
+  r.c1 = (float)(1.0 - beta1);
+  r.b2 = (float)beta2;
+  r.c2 = (float)(1.0 - beta2);
+  if (!step_at) {
+    r.m_up = (float)(1.0 / (1.0 - std::pow(beta1, (double)step)));
+    r.u_up = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+  }
+  r.eps = (float)eps;
+  r.decay = (float)weight_decay;
+  static_assert(sizeof(rtl::AdamTensor) == sizeof(rtl_adamw_tensor), "one layout");
+  return hip_status(rtl::launch_adamw(bf16, g_dt == RTL_BF16, eight, reinterpret_cast<const rtl::AdamTensor*>(tensors), count, r,
+                                      (hipStream_t)stream),
+                    "rtl_adamw launch");
 }
 
 }  // extern "C"

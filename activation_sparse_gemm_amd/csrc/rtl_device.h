@@ -86,6 +86,29 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
 
+// The two parts of v: the next bf16 value towards zero (below v, also where v is one) and the rest (a
+// bf16 value is exact in its two parts).  Each has v's sign and is 0 only where v is (down to
+// 2^-102), so that with an infinite weight or token both give the same infinity, where opposite
+// ones, or a part of 0, would give NaN.  An infinity or NaN is its own second part.
+struct Bf16Parts {
+  __bf16 hi, lo;
+};
+__device__ __forceinline__ Bf16Parts two_parts(float v) {
+  if (!__builtin_isfinite(v) || v == 0.f) return {(__bf16)v, (__bf16)v};
+  const float hi = __uint_as_float((__float_as_uint(v) - 1) & 0xFFFF0000u);
+  return {(__bf16)hi, (__bf16)(v - hi)};
+}
+// Three parts, which hold all of an fp32 value's digits (down to 2^-102), each of its sign likewise.
+__device__ __forceinline__ void three_parts(float v, __bf16 (&part)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; i++) {
+    const bool whole = i == 2 || !__builtin_isfinite(v) || v == 0.f;
+    const float p = whole ? v : __uint_as_float((__float_as_uint(v) - 1) & 0xFFFF0000u);
+    part[i] = (__bf16)p;
+    if (__builtin_isfinite(v)) v -= p;
+  }
+}
+
 // Squared-norm accumulation of the two bf16 values packed in d, in double precision: the
 // square of any finite bf16 (or fp32) value and sums of up to 2^40 of them stay inside the
 // double range, so no row norm underflows or overflows.

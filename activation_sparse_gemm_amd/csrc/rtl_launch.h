@@ -104,6 +104,72 @@ hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const 
                                 const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
                                 void* dWu, void* ws, hipStream_t stream);
 
+// Layer norm with weights and per-group scale and shift, and its gradient (layer_norm.hip).
+struct RowsView {
+  const void* p;  // rows of D contiguous elements
+  int64_t row;    // stride in elements
+};
+struct NormCall {
+  int dt;
+  int64_t M, D, G;          // G: groups, 0 without scale and shift
+  RowsView x, y, dy;        // gradient: dy, and y is dx
+  RowsView scale, shift;    // [G, D] or null
+  const void *w, *b;        // [D] or null
+  const int32_t* groups;    // [G + 1] or null
+  float eps;
+  const float* stats;       // [M, 2]: forward writes them (null: not wanted), the gradient reads them
+};
+constexpr int64_t kNormMaxD = 32768;       // bf16 rows in 16-byte pieces (fp32: half)
+constexpr int64_t kNormMaxDNarrow = 8192;  // rows taken by the element
+bool norm_is_wide(const NormCall& c);
+bool norm_fits(int dt, int64_t D, bool wide);
+hipError_t launch_norm(const NormCall& c, hipStream_t stream);
+size_t norm_back_workspace(int64_t M, int64_t D, int64_t G);
+hipError_t launch_norm_back(const NormCall& c, float* dw, float* db, float* dscale, float* dshift, void* ws,
+                            hipStream_t stream);
+
+// Low-rank adapters of many requests and their gradient (adapters.hip).
+struct AdapterCall {
+  int64_t M, N, K, R, A;
+  const void* x;
+  int64_t x_row;
+  const void *LA, *LB;  // [A, N, R], [A, R, K]
+  const void* plan;
+  const float* alpha;   // [A] or null
+};
+size_t adapters_plan_bytes(int64_t M, int64_t A);
+hipError_t launch_adapters_plan(const int32_t* ids, int64_t M, int64_t A, void* plan, hipStream_t stream);
+size_t adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A);
+hipError_t launch_adapters(const AdapterCall& c, const void* y0, int64_t y0_row, void* y, int64_t y_row, float* t, void* ws,
+                           hipStream_t stream);
+size_t adapters_back_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A);
+hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void* dy, int64_t dy_row, const void* dx0,
+                                int64_t dx0_row, void* dx, int64_t dx_row, float* dla, float* dlb, void* ws,
+                                hipStream_t stream);
+
+// AdamW over many tensors (adamw.hip).
+struct AdamTensor {
+  void* p;               // parameters: fp32, or bf16 beside `master`
+  const void* g;         // gradients
+  float* master;         // fp32 copies of bf16 parameters, else null
+  void *m, *v;           // states: fp32, or E4M3 codes of m and of sqrt(v)
+  float *m_scale, *v_scale;  // one for 256 codes
+  int64_t n;
+};
+struct AdamRates {
+  double beta1, beta2;
+  const int64_t* step_at;   // device: the step's number, null: m_up and u_up hold its corrections
+  const float* lr_at;       // device: the learning rate, null: lr
+  const float* grad_scale;  // device: a factor of the gradients, or null
+  float lr, c1, b2, c2;     // c1 = 1 - beta1, b2 = beta2, c2 = 1 - beta2
+  float m_up, u_up;         // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  float eps, decay;
+};
+constexpr int64_t kAdamMaxN = (int64_t)1 << 35;
+constexpr uint32_t kAdamMaxBlocks = 1u << 23;  // of 256 threads: below 2^32
+hipError_t launch_adamw(bool p_bf16, bool g_bf16, bool eight, const AdamTensor* t, int64_t count, const AdamRates& r,
+                        hipStream_t stream);
+
 // Allocation-free workspace: the per-device scratch array (noalloc.hip).  `mismatch` is set
 // when `stream` does not belong to the current device (no address is resolved then).
 size_t noalloc_scratch_bytes();

@@ -374,6 +374,119 @@ rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int
                             const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
                             void* dWu, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * Layer norm of every row, with the layer's weights and with the scale and shift that a request
+ * brings (what stands in front of each projection of a diffusion transformer's block):
+ *   n = (x - mean) r,  r = 1 / sqrt(mean((x - mean)^2) + eps),  y = (n w + b) (1 + scale_g) + shift_g
+ *
+ * X and Y are [M, D] with D contiguous and a row stride in elements (that of one row is ignored); Y may
+ * be X (same pointer and stride), else it overlaps no input.  w and b [D] may be NULL (ones, zeros).
+ * groups [G + 1] (device, int32): ascending offsets, rows groups[g] .. groups[g + 1] - 1 are group g,
+ * which may be empty; rows before groups[0] and from groups[G] on are not read and left as they were.
+ * groups NULL: all rows are one group (G 0 or 1).  scale and shift [G, D] with a row stride, both or
+ * neither (NULL).  What groups holds is not checked, but no call goes past its tensors for it.
+ * stats [M, 2] fp32 (NULL to skip) receives each row's mean and r, which the gradient takes.
+ *
+ * dt is bf16 or fp32, of all tensors but groups and stats; all arithmetic is fp32, rounded once.  The
+ * squares are summed in fp32 and must lie in its range.  Pointers are aligned to their elements.
+ * Limits: where pointers, strides and D allow 16-byte accesses D <= 32768 (bf16) or 16384 (fp32), else
+ * D <= 8192; M below 2^31, G below 2^31 - 1; eps in [2^-126, 1].
+ */
+rtl_status rtl_layer_norm(rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const void* w, const void* b,
+                          int64_t G, const int32_t* groups, const void* scale, int64_t scale_row, const void* shift,
+                          int64_t shift_row, float eps, void* Y, int64_t y_row, float* stats, void* stream);
+
+/*
+ * Gradient of rtl_layer_norm from its inputs, the stats it left and the gradient dY: dX [M, D] (which
+ * may be dY or X), and fp32 sums, each NULL to skip: dw and db [D] over all rows of the groups,
+ * dscale and dshift [G, D] (without scale: NULL) over each group's rows (zeros for an empty group, and
+ * for dw and db without rows).  Rows of no group are left as they were in dX.  A sum runs in fp32 over at
+ * most 32 rows, in double from there, in one order: the same result on every run.  Calls that share
+ * a workspace must be serialised.  Limits besides rtl_layer_norm's: G * D below 2^29.
+ */
+size_t rtl_layer_norm_backward_workspace_bytes(int64_t M, int64_t D, int64_t G);
+rtl_status rtl_layer_norm_backward(rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const float* stats,
+                                   const void* dY, int64_t dy_row, const void* w, const void* b, int64_t G,
+                                   const int32_t* groups, const void* scale, int64_t scale_row, void* dX, int64_t dx_row,
+                                   float* dw, float* db, float* dscale, float* dshift, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection (bf16).  Row m of a batch has adapter
+ * ids[m] of A (below 0 or from A on: none); adapter a has the factors LB[a] [R, K] and LA[a] [N, R] and a
+ * factor alpha[a] (fp32; NULL: ones):
+ *   T = X LB[a]^T,  Y = Y0 + alpha[a] T LA[a]^T
+ * Y0 [M, N] is the output of the projection that all requests share, whichever layer computed it
+ * (NULL: zeros); Y may be Y0 (same pointer and stride), and then rows without an adapter are left alone.
+ * X, Y0 and Y have row strides in elements, multiples of 8 (that of one row is ignored), so that Y0 can be
+ * a part of a packed projection.  T [M, R] fp32 (NULL to skip; zeros for rows without an adapter) is
+ * what the gradient takes.
+ *
+ * The plan of a batch (rtl_adapters_plan_bytes bytes of device memory, made from ids [M], int32)
+ * serves all calls with that M and A, forward and back, until it is written again.  What it holds is
+ * not checked, but no call goes past its tensors for it.
+ *
+ * Both products accumulate in fp32; T enters the second in two bf16 parts (2^-16 of it); one rounding at
+ * the end.  Limits: K, N and R multiples of 8, R <= 128, K and N <= 2^22, A <= 4096, M <= 2^24, and
+ * A * R * max(K, N) <= 2^40.  Outputs overlap no input but Y0 as said.  Calls that share a workspace must be
+ * serialised.
+ */
+size_t rtl_adapters_plan_bytes(int64_t M, int64_t A);
+rtl_status rtl_adapters_plan(int64_t M, int64_t A, const int32_t* ids, void* plan, size_t plan_bytes, void* stream);
+size_t rtl_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A);
+rtl_status rtl_adapters(rtl_dtype dt, int64_t M, int64_t N, int64_t K, int64_t R, int64_t A, const void* X, int64_t x_row,
+                        const void* LA, const void* LB, const float* alpha, const void* plan, size_t plan_bytes,
+                        const void* Y0, int64_t y0_row, void* Y, int64_t y_row, float* T, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of rtl_adapters from its inputs, the T it left and the gradient dY [M, N]:
+ *   dT = alpha[a] dY LA[a],  dX = dX0 + dT LB[a] [M, K],
+ *   dLB[a] = the sum over a's rows of dT^T X [R, K],  dLA[a] = alpha[a] times that of dY^T T [N, R]
+ * dLA and dLB are fp32 (zeros for an adapter without rows); dX0 (NULL: zeros) is the gradient that came
+ * through the shared projection, and dX may be dX0.  dX may be NULL, dLA and dLB too, not all three.  Sums
+ * run in one order: the same result on every run.  X is not read without dLB, T not without dLA.
+ */
+size_t rtl_adapters_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A);
+rtl_status rtl_adapters_backward(rtl_dtype dt, int64_t M, int64_t N, int64_t K, int64_t R, int64_t A, const void* X,
+                                 int64_t x_row, const void* LA, const void* LB, const float* alpha, const void* plan,
+                                 size_t plan_bytes, const float* T, const void* dY, int64_t dy_row, const void* dX0,
+                                 int64_t dx0_row, void* dX, int64_t dx_row, float* dLA, float* dLB, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * The AdamW step over many tensors (the low-rank factors and norm weights that the gradients above
+ * belong to), of any sizes, in few launches:
+ *   g' = g * grad_scale,  m += (1 - beta1) (g' - m),  v = beta2 v + (1 - beta2) g'^2
+ *   p -= lr (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay p)
+ * computed in fp32 in that order.  p_dt RTL_F32: p is fp32, master NULL.  p_dt RTL_BF16: the step is taken
+ * on the fp32 master, and p is its rounding.  g is g_dt.
+ * RTL_STATES_32: m and v are fp32.  RTL_STATES_8: m and v hold E4M3 codes [n], of m and of sqrt(v), and
+ * m_scale and v_scale [(n + 255) / 256] fp32 the scale of each 256 codes (zeros start a run): the largest
+ * magnitude a of the 256 gives the codes e4m3(x * fl32(448 / a)) (0 where 448 / a is not finite) and the
+ * scale fl32(a / 448); a sqrt(v) that is not 0 takes the code 2^-9 at least.
+ *
+ * tensors (HOST pointer, `count` of them; n may be 0); the call keeps nothing of it.  t is `step` >= 1, or,
+ * where step_at (device, int64) is not NULL, what that holds; lr likewise, lr_at (device, fp32).
+ * grad_scale (device, fp32) may be NULL (1): a clipping or an unscaling factor.  Tensors overlap no other's;
+ * gradients may repeat.  Each pointer is 16-byte aligned, the scales' and the device numbers' to
+ * their elements.  Limits: n <= 2^35; lr finite, beta1 and beta2 in [0, 1), eps in [0, 1], weight_decay finite.
+ */
+typedef enum { RTL_STATES_RANGE_MIN_ = -0x7FFFFFFF - 1, RTL_STATES_8 = 8, RTL_STATES_32 = 32, RTL_STATES_RANGE_MAX_ = 0x7FFFFFFF } rtl_states;
+typedef struct {
+  void* p;
+  const void* g;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+} rtl_adamw_tensor;
+rtl_status rtl_adamw(rtl_dtype p_dt, rtl_dtype g_dt, rtl_states states, int64_t count, const rtl_adamw_tensor* tensors,
+                     int64_t step, const int64_t* step_at, double lr, const float* lr_at, double beta1, double beta2,
+                     double eps, double weight_decay, const float* grad_scale, void* stream);
+
 const char* rtl_status_string(rtl_status st);
 const char* rtl_last_error(void); /* message of this thread's last failed call, or "" */
 int rtl_version(void);            /* major * 10000 + minor * 100 + patch */
