@@ -15,11 +15,10 @@
 // the largest error of an adapter's share, and the products are too small to hold the kernels.
 // The gradients' sums of few rows take three (kFewRows).
 //
-//   down:   T's parts over K, one tile and split of K a workgroup, the waves taking K in turn
-//   join:   the parts' sum; T as operand fragments (and transposed ones for the gradients)
-//   up:     Y0 + T L_A^T, a tile's 64 rows by strips of 32 columns a wave
+//   down:   T in pieces over K, the waves taking 64 of K in turn
+//   up:     Y0 + T L_A^T, strips of 64 columns a wave, T's pieces summed on the way
 //   turn:   factors transposed, which makes dT a `down` and dX an `up`
-//   grad:   dL_B and dL_A, 128 (64) columns by R a workgroup, over a share of an adapter's rows
+//   grad:   dL_B and dL_A, tiles of 128 (64) columns by R over runs of an adapter's rows
 #include <algorithm>
 #include <type_traits>
 
@@ -170,117 +169,49 @@ __device__ __forceinline__ Tile tile_of(const Plan& p, int64_t index) {
   t.rows = (int)min((int64_t)min(max(__builtin_amdgcn_readfirstlane(v.z), 0), kTile), p.M - t.pos);
   return t;
 }
+// Work in equal shares: `tiles` tiles of `steps` steps each, one after another, are dealt out to `groups`
+// workgroups, `least` steps each at the least; a workgroup goes through its pieces of tiles.  All workgroups
+// run at once and end together, where whole tiles, one a workgroup, left half the chip idle in the last
+// round (down at 32760 x 5120, 514 tiles on 512 places: 141 us).  The piece of a tile that workgroup w
+// has is number w + tile (pieces in order raise one or the other).
+struct Stream {
+  int64_t steps;
+  int groups, least;
+  __device__ __forceinline__ int64_t len(int64_t tiles) const {
+    return max((tiles * steps + groups - 1) / groups, (int64_t)least);
+  }
+  // First and last workgroup of a tile.
+  __device__ __forceinline__ void of(int64_t tile, int64_t len, int64_t& first, int64_t& last) const {
+    first = min(tile * steps / len, (int64_t)groups - 1);
+    last = min((tile * steps + steps - 1) / len, (int64_t)groups - 1);
+  }
+};
+// Tiles of rows with an adapter (they come first), and all of them.
+__device__ __forceinline__ int64_t used_tiles(const Plan& p) { return min(max((int64_t)p.tbase[p.A], (int64_t)0), p.most); }
+__device__ __forceinline__ int64_t all_tiles(const Plan& p) { return min(max((int64_t)*p.count, (int64_t)0), p.most); }
+
 __device__ __forceinline__ int64_t row_at(const Plan& p, int64_t pos) {
   return min(max(p.order[pos], 0), (int)p.M - 1);
 }
+
+// Keeps the loads of the next step ahead of this step's products: the compiler would move them to
+// where they are used, to save registers (down at 32760 x 5120: 150 us without).
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// down: part[split][position][r] = sum over the split's K of X[row][k] W[adapter][r][k].  A workgroup
-// takes one tile and one split; its waves take 64 of K in turn, each with all 64 rows and all R, so that
-// nothing is loaded twice, and their sums are added in LDS in one order.  Blocks of 16 r by 16 rows: lane
-// (r16, q) of a block holds row r16 and r = 4q .. 4q + 3.
-struct DownArgs {
-  Plan plan;
-  const uint16_t *x, *w;  // [M, K] with a row stride, [A, R, K]
-  int64_t x_row, K, part_stride;
-  int R, steps;           // steps of 64 a split
-  float* part;
+// A tile's T, scaled by alpha, in bf16 parts: as up's operand (row_operand: two parts; lane (r16, q): row r16 of
+// a block, r = 8q .. 8q + 7 of 32), and as grad's, `cols` (lane (r16, q): r = r16 of a block, rows 8q ..
+// 8q + 7 of 32); T itself, unscaled, to `t`.
+struct Emit {
+  const float* alpha;  // [A] or null
+  float* t;            // [M, R] by row, or null
+  u32x4* cols;         // or null
+  int R, RB, width, parts;  // RB: R in 16s as grad takes them; width: of the tile in LDS; parts of cols
 };
-template <int RB>
-__global__ __launch_bounds__(kThreads) void down_kernel(const DownArgs a) {
-  constexpr int BLOCKS = 4 * RB, ROUND = BLOCKS < 16 ? BLOCKS : 16;
-  __shared__ f32x4 sums[kWaves][ROUND][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
-  const Tile t = tile_of(a.plan, blockIdx.x);
-  if (t.rows == 0 || t.adapter >= a.plan.A) return;
-  const int blocks = (t.rows + 15) / 16;
-  const uint16_t *xp[4], *wp[RB];
-#pragma unroll
-  for (int b = 0; b < 4; b++)  // rows past the last repeat it: their sums are dropped
-    xp[b] = a.x + row_at(a.plan, t.pos + min(16 * b + r16, t.rows - 1)) * a.x_row + 8 * q;
-#pragma unroll
-  for (int b = 0; b < RB; b++) wp[b] = a.w + ((int64_t)t.adapter * a.R + min(16 * b + r16, a.R - 1)) * a.K + 8 * q;
-  f32x4 acc[4][RB];
-#pragma unroll
-  for (int b = 0; b < 4; b++)
-#pragma unroll
-    for (int c = 0; c < RB; c++) acc[b][c] = f32x4{};
-  struct Step {
-    u32x4 x[2][4], w[2][RB];
-  };
-  const int64_t first = (int64_t)blockIdx.y * a.steps, last = min(first + a.steps, (a.K + 63) / 64);
-  auto fetch = [&](int64_t s, Step& it) {
-    if (s >= last) return;
-    const int64_t k = s * 64;
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const bool in = k + 32 * h + 8 * q < a.K;
-#pragma unroll
-      for (int b = 0; b < 4; b++) {
-        it.x[h][b] = u32x4{};
-        if (b < blocks && in) it.x[h][b] = *reinterpret_cast<const u32x4*>(xp[b] + k + 32 * h);
-      }
-#pragma unroll
-      for (int b = 0; b < RB; b++) {
-        it.w[h][b] = u32x4{};
-        if (in) it.w[h][b] = *reinterpret_cast<const u32x4*>(wp[b] + k + 32 * h);
-      }
-    }
-  };
-  auto form = [&](const Step& it) {
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-      for (int b = 0; b < 4; b++)
-        if (b < blocks)
-#pragma unroll
-          for (int c = 0; c < RB; c++) acc[b][c] = mfma16(it.w[h][c], it.x[h][b], acc[b][c]);
-  };
-  Step one, two;
-  fetch(first + wave, one);
-  for (int64_t s = first + wave; s < last; s += 2 * kWaves) {
-    fetch(s + kWaves, two);
-    form(one);
-    if (s + kWaves >= last) break;
-    fetch(s + 2 * kWaves, one);
-    form(two);
-  }
-  float* part = a.part + blockIdx.y * a.part_stride;
-#pragma unroll
-  for (int round = 0; round < BLOCKS; round += ROUND) {
-    if (round > 0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ROUND; i++) sums[wave][i][lane] = acc[(round + i) / RB][(round + i) % RB];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ROUND / kWaves; i++) {
-      const int at = i * kWaves + wave, b = (round + at) / RB, c = (round + at) % RB;
-      f32x4 v = sums[0][at][lane];
-#pragma unroll
-      for (int w = 1; w < kWaves; w++) v += sums[w][at][lane];
-      const int m = 16 * b + r16, r = 16 * c + 4 * q;
-      if (m < t.rows && r < a.R) *reinterpret_cast<f32x4*>(part + (t.pos + m) * a.R + r) = v;
-    }
-  }
-}
-
-// join: a tile's sum over the splits (or a kept T's rows), scaled by alpha, in two bf16 parts, as
-// operands: `rows` for up (lane (r16, q): row r16 of a block, r = 8q .. 8q + 7 of 32) and `cols` for
-// grad (lane (r16, q): r = r16 of a block, rows 8q .. 8q + 7 of 32); T itself to `t`.
-struct JoinArgs {
-  Plan plan;
-  const float* part;  // [splits][M][R] by position
-  const float* kept;  // [M, R] by row, in its place
-  int64_t part_stride;
-  int splits, R, RK, RB, width;  // RK: R in 32s, RB: in 16s as grad takes them; width: the wider of the two
-  const float* alpha;
-  float* t;           // [M, R] by row, or null
-  u32x4 *rows, *cols; // or null
-  int parts;          // of cols
-};
+__device__ __forceinline__ int pitch_of(const Emit& e) { return e.width + 4; }
 __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4& hi, u32x4& lo) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
@@ -290,187 +221,448 @@ __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4& hi, u32x4& 
     lo[i] = __builtin_bit_cast(uint32_t, bf16x2_t{x.lo, y.lo});
   }
 }
-__global__ __launch_bounds__(kThreads) void join_kernel(const JoinArgs a) {
-  extern __shared__ float tile[];  // [64][pitch]
-  const int pitch = a.width + 4, quads = a.width / 4;
-  const Tile t = tile_of(a.plan, blockIdx.x);
-  if (t.rows == 0) return;
-  const bool bare = t.adapter >= a.plan.A;
-  if (bare && a.t == nullptr) return;
-  const float alpha = bare || a.alpha == nullptr ? 1.f : a.alpha[t.adapter];
-  for (int id = threadIdx.x; id < kTile * quads; id += kThreads) {
-    const int m = id / quads, r = id % quads * 4;
-    f32x4 v{};
-    if (m < t.rows && r < a.R) {
-      const int64_t row = row_at(a.plan, t.pos + m);
-      if (a.kept != nullptr) {
-        v = *reinterpret_cast<const f32x4*>(a.kept + row * a.R + r);
-      } else if (!bare) {
-        const float* p = a.part + (t.pos + m) * a.R + r;
-#pragma unroll 4
-        for (int s = 0; s < a.splits; s++) v += *reinterpret_cast<const f32x4*>(p + s * a.part_stride);
-      }
-      if (a.t != nullptr) *reinterpret_cast<f32x4*>(a.t + row * a.R + r) = v;
-    }
-    *reinterpret_cast<f32x4*>(tile + m * pitch + r) = v * alpha;
-  }
-  if (bare) return;
-  __syncthreads();
-  if (a.rows != nullptr) {
-    const int n = 4 * a.RK * 64;
-    u32x4* to = a.rows + (int64_t)blockIdx.x * 2 * n;
-    for (int id = threadIdx.x; id < n; id += kThreads) {
-      const int lane = id & 63, kk = (id >> 6) % a.RK, mb = (id >> 6) / a.RK;
-      const float* p = tile + (16 * mb + (lane & 15)) * pitch + 32 * kk + 8 * (lane >> 4);
-      float v[8];
-      u32x4 hi, lo;
+// Lane's row operand of block mb and 32 r kk, from the tile [64][pitch] in LDS.
+__device__ __forceinline__ void row_operand(const float* tile, int pitch, int mb, int kk, int lane, u32x4& hi, u32x4& lo) {
+  const float* p = tile + (16 * mb + (lane & 15)) * pitch + 32 * kk + 8 * (lane >> 4);
+  float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = p[i];
+  for (int i = 0; i < 8; i++) v[i] = p[i];
+  parts_of(v, hi, lo);
+}
+__device__ __forceinline__ void emit_cols(const Emit& a, const float* tile, int64_t index) {
+  const int pitch = pitch_of(a);
+  const int n = 2 * a.RB * 64;
+  u32x4* to = a.cols + index * a.parts * n;
+  for (int id = threadIdx.x; id < n; id += kThreads) {
+    const int lane = id & 63, rb = (id >> 6) % a.RB, half = (id >> 6) / a.RB;
+    const float* p = tile + (32 * half + 8 * (lane >> 4)) * pitch + 16 * rb + (lane & 15);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = p[i * pitch];
+    if (a.parts == 3) {
+      u32x4 w[3];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+        __bf16 x[3], y[3];
+        three_parts(v[2 * i], x);
+        three_parts(v[2 * i + 1], y);
+#pragma unroll
+        for (int k = 0; k < 3; k++) w[k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{x[k], y[k]});
+      }
+#pragma unroll
+      for (int k = 0; k < 3; k++) to[k * n + id] = w[k];
+    } else {
+      u32x4 hi, lo;
       parts_of(v, hi, lo);
       to[id] = hi;
       to[n + id] = lo;
     }
   }
-  if (a.cols != nullptr) {
-    const int n = 2 * a.RB * 64;
-    u32x4* to = a.cols + (int64_t)blockIdx.x * a.parts * n;
-    for (int id = threadIdx.x; id < n; id += kThreads) {
-      const int lane = id & 63, rb = (id >> 6) % a.RB, half = (id >> 6) / a.RB;
-      const float* p = tile + (32 * half + 8 * (lane >> 4)) * pitch + 16 * rb + (lane & 15);
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = p[i * pitch];
-      if (a.parts == 3) {
-        u32x4 w[3];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-          __bf16 x[3], y[3];
-          three_parts(v[2 * i], x);
-          three_parts(v[2 * i + 1], y);
-#pragma unroll
-          for (int k = 0; k < 3; k++) w[k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{x[k], y[k]});
-        }
-#pragma unroll
-        for (int k = 0; k < 3; k++) to[k * n + id] = w[k];
+}
+// T of a tile to LDS, scaled: the sum of down's pieces, or, `kept`, its rows as they are; and unscaled to a.t
+// (put).  Rows and r past the tile's are zeros, rows without an adapter too.
+__device__ __forceinline__ void join_tile(const Emit& a, const Plan& plan, const Tile& t, int64_t index, const float* part,
+                                          const Stream& down, int64_t down_len, const float* kept, bool put, float* tile) {
+  const bool bare = t.adapter >= plan.A;
+  const int pitch = pitch_of(a), quads = a.width / 4;
+  const float alpha = bare || a.alpha == nullptr ? 1.f : a.alpha[t.adapter];
+  int64_t first = 0, last = -1;
+  if (!bare && kept == nullptr) down.of(index, down_len, first, last);
+  for (int id = threadIdx.x; id < kTile * quads; id += kThreads) {
+    const int m = id / quads, r = id % quads * 4;
+    f32x4 v{};
+    if (m < t.rows && r < a.R) {
+      if (kept != nullptr) {
+        v = *reinterpret_cast<const f32x4*>(kept + row_at(plan, t.pos + m) * a.R + r);
       } else {
-        u32x4 hi, lo;
-        parts_of(v, hi, lo);
-        to[id] = hi;
-        to[n + id] = lo;
+        const float* p = part + ((first + index) * kTile + m) * a.R + r;
+#pragma unroll 4
+        for (int64_t w = first; w <= last; w++, p += kTile * a.R) v += *reinterpret_cast<const f32x4*>(p);
       }
+      if (put) *reinterpret_cast<f32x4*>(a.t + row_at(plan, t.pos + m) * a.R + r) = v;
     }
+    *reinterpret_cast<f32x4*>(tile + m * pitch + r) = v * alpha;
   }
 }
 
-// up: Y[row][n] = Y0[row][n] + sum over r of T[row][r] W[adapter][n][r].  The waves of a workgroup take
-// strips of 32 columns in turn, with the tile's T in registers.  The two blocks of a strip take the
-// columns 8 (i / 4) + 4 b + i % 4, so that lane (r16, q) ends with columns 8q .. 8q + 7 of row r16: one
-// 16-byte access to Y0 and Y.
+// Memory is met in whole lines, eight rows of 128 bytes an access with a row's eight chunks in neighbouring lanes, and
+// passes through the wave's own LDS to and from the matrix instructions' layout (lane (r16, q): chunks q and 4 + q
+// of row r16; line_at is free of bank conflicts both ways).  Read as the instructions have it, neighbouring lanes on
+// different rows, every lane is an access of its own: 63 of them an instruction instead of 16, the address and data
+// units 85% busy, and down and up at 32760 x 5120, R = 64, took 105 and 170 us instead of XX and XX.  The LDS
+// is the wave's own and its instructions run in order: no barrier.
+__device__ __forceinline__ int line_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+// down: piece[row][r] of a tile = sum over the piece's K of X[row][k] W[adapter][r][k].  The waves take 64 of
+// K in turn, each with all the rows and all R, so that nothing is loaded twice, and their sums are added in LDS in one
+// order.  Blocks of 16 r by 16 rows: lane (r16, q) of a block holds row r16 and r = 4q .. 4q + 3.
+// The loop has no condition but its count: the last loads repeat.
+struct DownArgs {
+  Plan plan;
+  const uint16_t *x, *w;  // [M, K] with a row stride, [A, R, K]
+  int64_t x_row, K;
+  int R;
+  Stream stream;
+  float* part;            // [pieces][64][R]
+};
+// Workgroups a CU, by their registers.
+constexpr int down_per_cu(int RB) { return RB == 8 ? 1 : RB == 4 ? 2 : 3; }  // and LDS
+template <int RB, int MB>  // MB: blocks of rows
+__device__ __forceinline__ void down_piece(const DownArgs& a, const Tile& t, int64_t first, int64_t last, float* part, uint8_t* lds) {
+  constexpr int BLOCKS = MB * RB, ROUND = BLOCKS < 8 ? BLOCKS : 8;
+  static_assert(BLOCKS % ROUND == 0, "whole rounds");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
+  const int64_t whole = a.K / 64, end = min(last, whole);
+  const int row = lane >> 3, chunk = lane & 7;  // of an access
+  const uint16_t* xp[MB][2];
+#pragma unroll
+  for (int b = 0; b < MB; b++)
+#pragma unroll
+    for (int i = 0; i < 2; i++)  // rows past the last repeat it: their sums are dropped
+      xp[b][i] = a.x + row_at(a.plan, t.pos + min(16 * b + 8 * i + row, t.rows - 1)) * a.x_row + (first + wave) * 64 + 8 * chunk;
+  // eight r past R repeat R's last eight
+  const uint16_t* w0 = a.w + (int64_t)t.adapter * a.R * a.K + (first + wave) * 64;
+  const uint32_t w_lane = (uint32_t)(row * a.K + 8 * chunk);
+  auto wp = [&](int b, int i) { return w0 + (int64_t)min(16 * b + 8 * i, a.R - 8) * a.K; };
+  uint8_t* mine = lds + wave * ((4 + RB) * 2048);  // blocks of X, then of W
+  f32x4 acc[MB][RB];
+#pragma unroll
+  for (int b = 0; b < MB; b++)
+#pragma unroll
+    for (int c = 0; c < RB; c++) acc[b][c] = f32x4{};
+  u32x4 x[MB][2], w[RB][2];
+  const int64_t count = max((end - first - wave + kWaves - 1) / kWaves, (int64_t)0);
+  auto fetch = [&](int64_t i) {
+    const int64_t k = min(i, count - 1) * (64 * kWaves);
+#pragma unroll
+    for (int b = 0; b < RB; b++)
+#pragma unroll
+      for (int i = 0; i < 2; i++) w[b][i] = *reinterpret_cast<const u32x4*>(wp(b, i) + k + w_lane);
+#pragma unroll
+    for (int b = 0; b < MB; b++)
+#pragma unroll
+      for (int i = 0; i < 2; i++) x[b][i] = *reinterpret_cast<const u32x4*>(xp[b][i] + k);
+  };
+  auto put = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+#pragma unroll
+      for (int b = 0; b < RB; b++) *reinterpret_cast<u32x4*>(mine + (4 + b) * 2048 + line_at(8 * i + row, chunk)) = w[b][i];
+#pragma unroll
+      for (int b = 0; b < MB; b++) *reinterpret_cast<u32x4*>(mine + b * 2048 + line_at(8 * i + row, chunk)) = x[b][i];
+    }
+  };
+  auto form = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      u32x4 f[RB];
+#pragma unroll
+      for (int c = 0; c < RB; c++) f[c] = *reinterpret_cast<const u32x4*>(mine + (4 + c) * 2048 + line_at(r16, 4 * h + q));
+#pragma unroll
+      for (int b = 0; b < MB; b++) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(mine + b * 2048 + line_at(r16, 4 * h + q));
+#pragma unroll
+        for (int c = 0; c < RB; c++) acc[b][c] = mfma16(f[c], v, acc[b][c]);
+      }
+    }
+  };
+  __syncthreads();  // the sums that lie there are read
+  if (count > 0) {
+    fetch(0);
+    for (int64_t i = 0; i < count; i++) {
+      put();
+      hold();
+      fetch(i + 1);
+      hold();
+      form();
+      hold();
+    }
+  }
+  // what K leaves past its whole steps, by the wave whose turn it is
+  if (last > whole && (whole - first) % kWaves == wave) {
+    const int64_t k = (whole - first - wave) * 64;
+    const bool in = whole * 64 + 8 * chunk < a.K;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+#pragma unroll
+      for (int b = 0; b < MB; b++) x[b][i] = in ? *reinterpret_cast<const u32x4*>(xp[b][i] + k) : u32x4{};
+#pragma unroll
+      for (int b = 0; b < RB; b++) w[b][i] = in ? *reinterpret_cast<const u32x4*>(wp(b, i) + k + w_lane) : u32x4{};
+    }
+    put();
+    form();
+  }
+  f32x4(*sums)[ROUND][64] = reinterpret_cast<f32x4(*)[ROUND][64]>(lds);
+#pragma unroll
+  for (int round = 0; round < BLOCKS; round += ROUND) {
+    __syncthreads();  // what lay there is read
+#pragma unroll
+    for (int i = 0; i < ROUND; i++) sums[wave][i][lane] = acc[(round + i) / RB][(round + i) % RB];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < (ROUND + kWaves - 1) / kWaves; i++) {
+      const int at = i * kWaves + wave, b = (round + at) / RB, c = (round + at) % RB;
+      const int m = 16 * b + r16, r = 16 * c + 4 * q;
+      if (at >= ROUND) continue;
+      f32x4 v = sums[0][at][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; w++) v += sums[w][at][lane];
+      if (m < t.rows && r < a.R) *reinterpret_cast<f32x4*>(part + m * a.R + r) = v;
+    }
+  }
+}
+template <int RB>
+__global__ __launch_bounds__(kThreads, down_per_cu(RB)) void down_kernel(const DownArgs a) {
+  __shared__ __align__(16) uint8_t lds[kWaves * (4 + RB) * 2048];  // the waves' lines, then their sums
+  const int64_t tiles = used_tiles(a.plan), len = a.stream.len(tiles);
+  int64_t at = blockIdx.x * len;
+  const int64_t end = min(at + len, tiles * a.stream.steps);
+  while (at < end) {
+    const int64_t index = at / a.stream.steps, first = at - index * a.stream.steps, last = min(a.stream.steps, first + end - at);
+    at += last - first;
+    const Tile t = tile_of(a.plan, index);
+    if (t.rows == 0 || t.adapter >= a.plan.A) continue;
+    float* part = a.part + (blockIdx.x + index) * (int64_t)(kTile * a.R);
+    if (t.rows <= 16) down_piece<RB, 1>(a, t, first, last, part, lds);
+    else down_piece<RB, 4>(a, t, first, last, part, lds);
+  }
+}
+
+// join: a tile's T as grad's operand, from down's pieces or from a kept T.
+struct JoinArgs {
+  Plan plan;
+  const float *part, *kept;
+  Stream down;
+  Emit e;
+};
+__device__ __forceinline__ void join_cols(const JoinArgs& a, int64_t index, float* tile) {
+  const Tile t = tile_of(a.plan, index);
+  if (t.rows == 0 || t.adapter >= a.plan.A) return;
+  join_tile(a.e, a.plan, t, index, a.part, a.down, a.kept != nullptr ? 1 : a.down.len(used_tiles(a.plan)), a.kept, false, tile);
+  __syncthreads();
+  emit_cols(a.e, tile, index);
+}
+__global__ __launch_bounds__(kThreads) void join_kernel(const JoinArgs a) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  join_cols(a, blockIdx.x, reinterpret_cast<float*>(dynamic));
+}
+
+// up: Y[row][n] = Y0[row][n] + sum over r of T[row][r] W[adapter][n][r].  The waves of a workgroup take the
+// strips of 64 columns of its piece of a tile in turn, with the tile's T, which they sum from down's pieces, in
+// LDS.  A strip is four blocks of columns: half s takes columns 32 s + 8 (i / 4) + 4 b + i % 4 into its
+// blocks b = 0, 1, so that lane (r16, q) ends with columns 32 s + 8q .. + 7 of row r16.  Y0, Y and the factors pass in whole
+// lines.  The workgroup that has a tile's first strip also leaves its T and grad's operand.
 struct UpArgs {
   Plan plan;
-  const u32x4* t;          // join's rows
   const uint16_t *w, *y0;  // [A, N, R]; [M, N] with a row stride, or null
   uint16_t* y;
   int64_t y0_row, y_row, N;
-  int R, strips;           // strips of a workgroup
+  Stream stream, down;
+  const float* part;
+  Emit e;
 };
-template <int RK>
-__global__ __launch_bounds__(kThreads) void up_kernel(const UpArgs a) {
+// Workgroups a CU, by their registers.
+constexpr int up_per_cu(int RK) { return RK <= 2 ? 2 : 1; }  // and LDS
+// A wave's LDS: two blocks of rows and a strip's factors.
+constexpr int up_lines(int RK) { return 2 * 2048 + RK * 4096; }
+// MB: blocks of rows.  `prepare` puts T's operands into LDS, behind the first loads.
+template <int RK, bool ADD, int MB, typename Prepare>
+__device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t first, int64_t last, const u32x4* operands,
+                                         uint8_t* lines, Prepare prepare) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  constexpr int PER = 4 * RK, WL = 64 * PER / 64;  // chunks of a factor's row, accesses of a strip's factors
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
-  const Tile t = tile_of(a.plan, blockIdx.x);
-  if (t.rows == 0) return;
-  const bool bare = t.adapter >= a.plan.A;
-  if (bare && a.y0 == a.y) return;
-  const int blocks = (t.rows + 15) / 16;
-  u32x4 tv[2][4][RK];
-  int64_t row[4];
+  const int R = a.e.R, l8 = lane >> 3, chunk = lane & 7;
+  const u32x4* tv = operands + lane;
+  uint8_t *mine = lines + wave * up_lines(RK), *mine_w = mine + 2 * 2048;
+  const int64_t whole = a.N / 64, end = min(last, whole), n0 = (first + wave) * 64;
+  // Factors: access j takes chunks 64 j + lane of the strip's 64 columns, PER each; r past R as zeros.  In LDS column n's
+  // chunk c lies so that the columns of 8 neighbouring lanes of a block fall in different banks.
+  auto w_at = [](int n, int c) {
+    const int g = RK % 2 ? n >> 3 & 1 : (n & 3) | (n >> 3 & 1) << 2;
+    return n * (PER * 16) + ((c ^ g) << 4);
+  };
+  const uint16_t* w0 = a.w + ((int64_t)t.adapter * a.N + n0) * R;
+  int w_off[WL];  // -1: past R
+  int w_to[WL];
 #pragma unroll
-  for (int b = 0; b < 4; b++) {
-    row[b] = 16 * b + r16 < t.rows ? row_at(a.plan, t.pos + 16 * b + r16) : -1;
+  for (int j = 0; j < WL; j++) {
+    const int n = (64 * j + lane) / PER, c = (64 * j + lane) % PER;
+    w_off[j] = 8 * c < R ? n * R + 8 * c : -1;
+    w_to[j] = w_at(n, c);
+  }
+  const uint16_t* yp[MB][2];
+  int row[MB][2];  // -1: past the last, which is repeated and not stored
+#pragma unroll
+  for (int b = 0; b < MB; b++)
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int m = 16 * b + 8 * i + l8, at = (int)row_at(a.plan, t.pos + min(m, t.rows - 1));
+      yp[b][i] = ADD ? a.y0 + at * a.y0_row + n0 + 8 * chunk : nullptr;
+      row[b][i] = m < t.rows ? at : -1;
+    }
+  uint16_t* op = a.y + n0 + 8 * chunk;
+  u32x4 y[MB][2], w[WL];
+  const int64_t count = max((end - first - wave + kWaves - 1) / kWaves, (int64_t)0);
+  auto place = [&](int64_t i) { return min(i, count - 1) * (64 * kWaves); };
+  auto fetch_y = [&](int64_t n, int b) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) y[b][k] = ADD ? *reinterpret_cast<const u32x4*>(yp[b][k] + n) : u32x4{};
+  };
+  auto fetch_w = [&](int64_t n) {
+#pragma unroll
+    for (int j = 0; j < WL; j++) w[j] = w_off[j] >= 0 ? *reinterpret_cast<const u32x4*>(w0 + n * R + w_off[j]) : u32x4{};
+  };
+  u32x4 f[4][RK];
+  auto ready = [&]() {
+#pragma unroll
+    for (int j = 0; j < WL; j++) *reinterpret_cast<u32x4*>(mine_w + w_to[j]) = w[j];
+#pragma unroll
+    for (int c = 0; c < 4; c++)
+#pragma unroll
+      for (int k = 0; k < RK; k++)
+        f[c][k] = *reinterpret_cast<const u32x4*>(mine_w + w_at(32 * (c >> 1) + 8 * (r16 >> 2) + 4 * (c & 1) + (r16 & 3), 4 * k + q));
+  };
+  auto form = [&](int64_t n, int b, bool in) {
+    uint8_t* block = mine + (b & 1) * 2048;
+    u32x4 v[2], tb[2][RK];
+    if (ADD) {
+#pragma unroll
+      for (int i = 0; i < 2; i++) *reinterpret_cast<u32x4*>(block + line_at(8 * i + l8, chunk)) = y[b][i];
+#pragma unroll
+      for (int s = 0; s < 2; s++) v[s] = *reinterpret_cast<const u32x4*>(block + line_at(r16, 4 * s + q));
+    } else {
+      v[0] = v[1] = u32x4{};
+    }
 #pragma unroll
     for (int k = 0; k < RK; k++)
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        tv[h][b][k] = u32x4{};
-        if (!bare && b < blocks) tv[h][b][k] = a.t[(((int64_t)blockIdx.x * 2 + h) * 4 + b) * RK * 64 + k * 64 + lane];
-      }
-  }
-  const uint16_t* w = a.w + (int64_t)(bare ? 0 : t.adapter) * a.N * a.R;
-  struct Strip {
-    u32x4 y[4], w[2][RK];
-  };
-  const int64_t all = (a.N + 31) / 32, first = (int64_t)blockIdx.y * a.strips, last = min(first + a.strips, all);
-  auto fetch = [&](int64_t s, Strip& it) {
-    if (s >= last) return;
-    const int64_t n = s * 32 + 8 * q;
+      for (int h = 0; h < 2; h++) tb[h][k] = tv[((h * 4 + b) * RK + k) * 64];
 #pragma unroll
-    for (int b = 0; b < 4; b++) {
-      it.y[b] = u32x4{};
-      if (a.y0 != nullptr && row[b] >= 0 && n < a.N) it.y[b] = *reinterpret_cast<const u32x4*>(a.y0 + row[b] * a.y0_row + n);
-    }
-#pragma unroll
-    for (int b = 0; b < 2; b++) {
-      const int64_t col = s * 32 + 8 * (r16 >> 2) + 4 * b + (r16 & 3);
-#pragma unroll
-      for (int k = 0; k < RK; k++) {
-        it.w[b][k] = u32x4{};
-        if (!bare && col < a.N && 32 * k + 8 * q < a.R) it.w[b][k] = *reinterpret_cast<const u32x4*>(w + col * a.R + 32 * k + 8 * q);
-      }
-    }
-  };
-  auto form = [&](int64_t s, const Strip& it) {
-    const int64_t n = s * 32 + 8 * q;
-#pragma unroll
-    for (int b = 0; b < 4; b++) {
-      if (b >= blocks) break;
-      f32x4 c[2];
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        c[i] = f32x4{};
-#pragma unroll
-        for (int k = 0; k < RK; k++) {
-          c[i] = mfma16(it.w[i][k], tv[0][b][k], c[i]);
-          c[i] = mfma16(it.w[i][k], tv[1][b][k], c[i]);
-        }
-      }
-      if (row[b] < 0 || n >= a.N) continue;
+    for (int s = 0; s < 2; s++) {
       u32x4 out;
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        out[i] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)(bf16lo(it.y[b][i]) + c[i >> 1][2 * (i & 1)]),
-                                                      (__bf16)(bf16hi(it.y[b][i]) + c[i >> 1][2 * (i & 1) + 1])});
-      *reinterpret_cast<u32x4*>(a.y + row[b] * a.y_row + n) = out;
+      for (int c = 0; c < 2; c++) {
+        f32x4 z = {bf16lo(v[s][2 * c]), bf16hi(v[s][2 * c]), bf16lo(v[s][2 * c + 1]), bf16hi(v[s][2 * c + 1])};
+#pragma unroll
+        for (int k = 0; k < RK; k++) {
+          z = mfma16(f[2 * s + c][k], tb[0][k], z);
+          z = mfma16(f[2 * s + c][k], tb[1][k], z);
+        }
+        out[2 * c] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)z[0], (__bf16)z[1]});
+        out[2 * c + 1] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)z[2], (__bf16)z[3]});
+      }
+      *reinterpret_cast<u32x4*>(block + line_at(r16, 4 * s + q)) = out;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const u32x4 out = *reinterpret_cast<const u32x4*>(block + line_at(8 * k + l8, chunk));
+      if (row[b][k] >= 0 && in) *reinterpret_cast<u32x4*>(op + (int64_t)row[b][k] * a.y_row + n) = out;
     }
   };
-  Strip one, two;
-  fetch(first + wave, one);
-  for (int64_t s = first + wave; s < last; s += 2 * kWaves) {
-    fetch(s + kWaves, two);
-    form(s, one);
-    if (s + kWaves >= last) break;
-    fetch(s + 2 * kWaves, one);
-    form(s + kWaves, two);
+  if (count > 0) {
+    fetch_w(0);
+#pragma unroll
+    for (int b = 0; b < MB; b++) fetch_y(0, b);
+  }
+  prepare();
+  // The next strip's factors go out first, each block of rows when this strip's is done with: every load has a
+  // whole strip's time, and none waits for one that is not needed yet (they return in order).
+  for (int64_t i = 0; i < count; i++) {
+    const int64_t n = place(i + 1);
+    ready();
+    hold();
+    fetch_w(n);
+    hold();
+#pragma unroll
+    for (int b = 0; b < MB; b++) {
+      form(i * (64 * kWaves), b, true);
+      hold();
+      fetch_y(n, b);
+      hold();
+    }
+  }
+  // the columns past the whole strips, by the wave whose turn it is
+  if (last > whole && (whole - first) % kWaves == wave) {
+    const int64_t n = (whole - first - wave) * 64;
+    const bool in = whole * 64 + 8 * chunk < a.N;
+#pragma unroll
+    for (int b = 0; b < MB; b++)
+#pragma unroll
+      for (int k = 0; k < 2; k++) y[b][k] = ADD && in ? *reinterpret_cast<const u32x4*>(yp[b][k] + n) : u32x4{};
+#pragma unroll
+    for (int j = 0; j < WL; j++)
+      w[j] = w_off[j] >= 0 && whole * 64 + (64 * j + lane) / PER < a.N ? *reinterpret_cast<const u32x4*>(w0 + n * R + w_off[j]) : u32x4{};
+    ready();
+#pragma unroll
+    for (int b = 0; b < MB; b++) form(n, b, in);
+  }
+}
+template <int RK, bool ADD>
+__global__ __launch_bounds__(kThreads, up_per_cu(RK)) void up_kernel(const UpArgs a) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  u32x4* operands = reinterpret_cast<u32x4*>(dynamic);  // [2][4][RK][64]
+  uint8_t* lines = dynamic + 8 * RK * 1024;             // the waves' lines, and in `prepare` T
+  float* tile = reinterpret_cast<float*>(lines);
+  const int64_t used = used_tiles(a.plan), tiles = a.y0 == a.y && a.e.t == nullptr ? used : all_tiles(a.plan);
+  const int64_t len = a.stream.len(tiles), down_len = a.down.len(used);
+  int64_t at = blockIdx.x * len;
+  const int64_t end = min(at + len, tiles * a.stream.steps);
+  while (at < end) {
+    const int64_t index = at / a.stream.steps, first = at - index * a.stream.steps, last = min(a.stream.steps, first + end - at);
+    at += last - first;
+    const Tile t = tile_of(a.plan, index);
+    if (t.rows == 0) continue;
+    const bool bare = t.adapter >= a.plan.A, put = a.e.t != nullptr && first == 0;
+    auto prepare = [&]() {
+      __syncthreads();  // the tile and the operands before are read
+      join_tile(a.e, a.plan, t, index, a.part, a.down, down_len, nullptr, put, tile);
+      __syncthreads();
+      for (int id = threadIdx.x; id < 4 * RK * 64; id += kThreads)
+        row_operand(tile, pitch_of(a.e), id / (64 * RK), id / 64 % RK, id & 63, operands[id], operands[4 * RK * 64 + id]);
+      if (a.e.cols != nullptr && first == 0 && !bare) emit_cols(a.e, tile, index);
+      __syncthreads();
+    };
+    if (bare) {  // Y0 as it is, T zeros
+      if (put) prepare();
+      if (a.y0 == a.y) continue;
+      const int64_t c0 = first * 64, wide = (min(last * 64, a.N) - c0) / 8;
+      for (int64_t id = threadIdx.x; id < wide * t.rows; id += kThreads) {
+        const int64_t row = row_at(a.plan, t.pos + id / wide), n = c0 + id % wide * 8;
+        *reinterpret_cast<u32x4*>(a.y + row * a.y_row + n) = ADD ? *reinterpret_cast<const u32x4*>(a.y0 + row * a.y0_row + n) : u32x4{};
+      }
+      continue;
+    }
+    if (t.rows <= 16) up_piece<RK, ADD, 1>(a, t, first, last, operands, lines, prepare);
+    else up_piece<RK, ADD, 4>(a, t, first, last, operands, lines, prepare);
   }
 }
 
 // turn: in [A][rows][cols] to out [A][cols][rows], 64 x 64 elements a workgroup, for the adapters that
-// have rows.
+// have rows; and, in the same launch, a kept T's operands.
 struct TurnArgs {
   Plan plan;
   const uint16_t* in[2];
   uint16_t* out[2];
   int64_t rows[2], cols[2];
-  uint32_t tiles[2];  // workgroups of each
+  uint32_t tiles[2];  // workgroups of each, for an adapter
+  uint32_t turns;     // all of them; the others take a tile each of the kept T
+  JoinArgs kept;
 };
 __global__ __launch_bounds__(kThreads) void turn_kernel(const TurnArgs a) {
-  __shared__ uint16_t block[64][72];
-  const int64_t adapter = blockIdx.y;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  if (blockIdx.x >= a.turns) {
+    join_cols(a.kept, blockIdx.x - a.turns, reinterpret_cast<float*>(dynamic));
+    return;
+  }
+  uint16_t(*block)[72] = reinterpret_cast<uint16_t(*)[72]>(dynamic);
+  const uint32_t per = a.tiles[0] + a.tiles[1], place = blockIdx.x % per;
+  const int64_t adapter = blockIdx.x / per;
   if (a.plan.start[adapter] >= a.plan.start[adapter + 1]) return;
-  const int k = blockIdx.x >= a.tiles[0];
+  const int k = place >= a.tiles[0];
   const int64_t rows = a.rows[k], cols = a.cols[k], wide = (cols + 63) / 64;
-  const int64_t at = blockIdx.x - (k ? a.tiles[0] : 0), r0 = at / wide * 64, c0 = at % wide * 64;
+  const int64_t at = place - (k ? a.tiles[0] : 0), r0 = at / wide * 64, c0 = at % wide * 64;
   const uint16_t* in = a.in[k] + adapter * rows * cols;
   uint16_t* out = a.out[k] + adapter * rows * cols;
 #pragma unroll
@@ -492,11 +684,11 @@ __global__ __launch_bounds__(kThreads) void turn_kernel(const TurnArgs a) {
   }
 }
 
-// grad: for C columns of Z (X for dL_B, dY for dL_A) and all R, the sum over a share of an adapter's rows
-// of Z[row][c] S[row][r], S = dT or alpha T in parts (join's cols).  Share j of the launch is rows
-// [i share, (i + 1) share) of adapter a where j = start[a] / share + a + i: every adapter, one
-// without rows among them, has its own.  A share that is all of an adapter's rows goes to the
-// output, the others to `part`, which grad_join adds.  The waves take 32 rows in turn: Z's rows go
+// grad: for C columns of Z (X for dL_B, dY for dL_A) and all R, the sum over an adapter's rows of Z[row][c]
+// S[row][r], S = dT or alpha T in parts (join's cols).  Column tiles, each with all tiles of rows, are dealt out as
+// Stream says; a workgroup goes through its runs of tiles of one adapter and one column tile.  A run
+// that is all of the adapter's goes to the output, else to `part`: the first run of a workgroup, begun by the
+// one before, to 2 w, the last to 2 w + 1; grad_join adds them.  The waves take 32 rows in turn: Z's rows go
 // through the wave's own LDS, to be read with the rows along a lane (the transposing read), their
 // 32-byte blocks swizzled so that the eight rows that half a wave reads lie in different banks.
 struct GradArgs {
@@ -506,37 +698,23 @@ struct GradArgs {
   uint32_t tiles[2];     // column tiles of each; 0 if its gradient is not wanted
   const u32x4* s[2];
   float* out[2];         // dL_B [A, R, K], dL_A [A, N, R]
-  float* part[2];        // the same for each share
-  int R, share;
+  float* part;           // [2 workgroups][C R]: [R][C] of dL_B, [C][R] of dL_A
+  int R, groups;
 };
 template <int RB>
 struct GradSize {
   static constexpr int CB = RB == 8 ? 4 : 8, C = 16 * CB;  // 32 blocks of 16 x 16 at the most
 };
-
-// Adapter of share j, and which of its shares.
-__device__ __forceinline__ int share_of(const Plan& p, int64_t j, int share, int64_t& i) {
-  int lo = 0, n = p.A;  // the last adapter whose first share is at or below j
-  while (n > 1) {
-    const int half = n / 2;
-    if ((int64_t)p.start[lo + half] / share + lo + half <= j) {
-      lo += half;
-      n -= half;
-    } else {
-      n = half;
-    }
-  }
-  i = j - ((int64_t)p.start[lo] / share + lo);
-  return lo;
+__device__ __forceinline__ int64_t grad_len(const GradArgs& a, int64_t tiles) {
+  return max(((int64_t)(a.tiles[0] + a.tiles[1]) * tiles + a.groups - 1) / a.groups, (int64_t)2);
 }
 
 template <int RB, int PARTS, bool LA>
-__device__ __forceinline__ void grad_tile(const GradArgs& a, uint8_t* lds, int64_t c0, int64_t j, int adapter, int64_t i,
-                                          int64_t from, int64_t rows) {
+__device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_t c0, int64_t tile, int64_t from, int64_t rows,
+                                         float* out, int64_t out_row) {
   constexpr int CB = GradSize<RB>::CB, C = GradSize<RB>::C, PER = C / 8, LOADS = 32 * PER / 64, BLOCKS = CB * RB;
   constexpr int ROUND = BLOCKS < 16 ? BLOCKS : 16, STEP = 32 * kWaves;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
-  const int64_t n = a.plan.start[adapter + 1] - a.plan.start[adapter];
   f32x4 acc[CB][RB];
 #pragma unroll
   for (int c = 0; c < CB; c++)
@@ -546,11 +724,9 @@ __device__ __forceinline__ void grad_tile(const GradArgs& a, uint8_t* lds, int64
   const int sub = lane / PER, p = lane % PER;
   const bool in = c0 + 8 * p < a.cols[LA];
   const uint16_t* z = a.z[LA] + c0 + 8 * p;
-  // the share's first tile
-  const int64_t tile = min(max(a.plan.tbase[adapter] + i * (a.share / kTile), (int64_t)0), a.plan.most - (rows + kTile - 1) / kTile);
   const u32x4* s = a.s[LA] + tile * PARTS * 2 * RB * 64 + lane;
   u32x4 zv[LOADS], sv[PARTS][RB];
-  auto index = [&](int64_t r0) {  // lane l: row r0 + l % 32 of the share
+  auto index = [&](int64_t r0) {  // lane l: row r0 + l % 32 of the run
     return r0 + (lane & 31) < rows ? (int)row_at(a.plan, from + r0 + (lane & 31)) : -1;
   };
   auto fetch_z = [&](int rows32) {
@@ -584,8 +760,10 @@ __device__ __forceinline__ void grad_tile(const GradArgs& a, uint8_t* lds, int64
     // the next rows' loads go out ahead of this step's products, those of S behind them, into the
     // registers that the products have read
     const bool more = r0 + STEP < rows;
+    hold();
     if (more) fetch_z(ahead);
     ahead = index(r0 + 2 * STEP);
+    hold();
     const int jr = (lane & 15) >> 2, f = C == 128 ? jr | (q & 1) << 2 : jr >> 1 | (q & 1) << 1;
     const uint8_t* at = mine + (8 * q + jr) * C * 2 + (lane & 3) * 8;
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -602,14 +780,12 @@ __device__ __forceinline__ void grad_tile(const GradArgs& a, uint8_t* lds, int64
 #pragma unroll
         for (int b = 0; b < RB; b++) acc[c][b] = LA ? mfma16(sv[h][b], v, acc[c][b]) : mfma16(v, sv[h][b], acc[c][b]);
     }
-    __builtin_amdgcn_sched_barrier(0);
+    hold();
     if (more) fetch_s(r0 + STEP);
   }
   // the waves' sums, in one order; block (c, b): lane (r16, q) holds r = 16 b + r16 and columns 16 c +
   // 4q .. + 3 (dL_B), or column 16 c + r16 and r = 16 b + 4q .. + 3 (dL_A)
   f32x4(*sums)[ROUND][64] = reinterpret_cast<f32x4(*)[ROUND][64]>(lds);
-  const int64_t cols = a.cols[LA];
-  float* out = n <= a.share ? a.out[LA] + (int64_t)adapter * a.R * cols : a.part[LA] + j * a.R * cols;
 #pragma unroll
   for (int round = 0; round < BLOCKS; round += ROUND) {
     __syncthreads();
@@ -622,69 +798,95 @@ __device__ __forceinline__ void grad_tile(const GradArgs& a, uint8_t* lds, int64
       f32x4 v = sums[0][at][lane];
 #pragma unroll
       for (int w = 1; w < kWaves; w++) v += sums[w][at][lane];
-      const int64_t col = c0 + 16 * c + (LA ? r16 : 4 * q);
-      const int r = 16 * b + (LA ? 4 * q : r16);
-      if (col < cols && r < a.R) *reinterpret_cast<f32x4*>(out + (LA ? col * a.R + r : r * cols + col)) = v;
+      const int col = 16 * c + (LA ? r16 : 4 * q), r = 16 * b + (LA ? 4 * q : r16);
+      if (c0 + col < a.cols[LA] && r < a.R) *reinterpret_cast<f32x4*>(out + (LA ? col * out_row + r : r * out_row + col)) = v;
     }
   }
+  __syncthreads();  // before the next run's rows
 }
 template <int RB, int PARTS>
 __global__ __launch_bounds__(kThreads, 2) void grad_kernel(const GradArgs a) {
   constexpr int C = GradSize<RB>::C, ROUND = GradSize<RB>::CB * RB < 16 ? GradSize<RB>::CB * RB : 16;
   __shared__ __align__(16) uint8_t lds[kWaves * (ROUND * 1024 > 64 * C ? ROUND * 1024 : 64 * C)];
-  int64_t i;
-  const int64_t j = blockIdx.y;
-  const int adapter = __builtin_amdgcn_readfirstlane(share_of(a.plan, j, a.share, i));
-  const int64_t first = a.plan.start[adapter], n = a.plan.start[adapter + 1] - first;
-  if (i < 0 || i * a.share >= max(n, (int64_t)1)) return;
-  const int64_t from = first + i * a.share, rows = max(min(n - i * a.share, (int64_t)a.share), (int64_t)0);
-  if (first < 0 || from + rows > a.plan.M) return;
-  if (blockIdx.x >= a.tiles[0]) grad_tile<RB, PARTS, true>(a, lds, (int64_t)(blockIdx.x - a.tiles[0]) * C, j, adapter, i, from, rows);
-  else grad_tile<RB, PARTS, false>(a, lds, (int64_t)blockIdx.x * C, j, adapter, i, from, rows);
+  const int64_t tiles = used_tiles(a.plan), len = grad_len(a, tiles);
+  int64_t at = blockIdx.x * len;
+  const int64_t end = min(at + len, (a.tiles[0] + a.tiles[1]) * tiles);
+  while (at < end) {
+    const int64_t column = at / tiles, tile = at - column * tiles;
+    const int adapter = min(max(__builtin_amdgcn_readfirstlane(a.plan.tiles[tile].x), 0), a.plan.A - 1);
+    const int64_t t0 = a.plan.tbase[adapter], t1 = a.plan.tbase[adapter + 1], p0 = a.plan.start[adapter], p1 = a.plan.start[adapter + 1];
+    const int64_t stop = min(tile + end - at, min(max(t1, tile + 1), tiles));  // first tile past the run
+    at += stop - tile;
+    // positions of the run; a plan that was not made leaves none
+    const int64_t from = p0 + (tile - t0) * kTile, rows = min(p1, p0 + (stop - t0) * kTile) - from;
+    if (from < 0 || rows <= 0 || rows > (stop - tile) * kTile || from + rows > a.plan.M) continue;
+    const bool la = column >= a.tiles[0], whole = tile <= t0 && stop >= t1;
+    const int64_t c0 = (la ? column - a.tiles[0] : column) * C;
+    float* part = a.part + (2 * (int64_t)blockIdx.x + (tile > t0 ? 0 : 1)) * C * a.R;
+    if (la) grad_run<RB, PARTS, true>(a, lds, c0, tile, from, rows, whole ? a.out[1] + (adapter * a.cols[1] + c0) * a.R : part, a.R);
+    else grad_run<RB, PARTS, false>(a, lds, c0, tile, from, rows, whole ? a.out[0] + adapter * a.R * a.cols[0] + c0 : part, whole ? a.cols[0] : C);
+  }
 }
 
-// The shares of the adapters that have several, added in their order.
+// The runs of each adapter and column tile that has several, added in their order; zeros for an adapter without
+// rows.
+template <int C>
 __global__ __launch_bounds__(kThreads) void grad_join_kernel(const GradArgs a) {
-  const int adapter = blockIdx.y, k = blockIdx.z;
-  const int64_t first = a.plan.start[adapter], n = a.plan.start[adapter + 1] - first, size = a.R * a.cols[k];
-  if (a.out[k] == nullptr || n <= a.share || first < 0 || first + n > a.plan.M) return;
-  const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (at >= size) return;
-  const float* p = a.part[k] + (first / a.share + adapter) * size + at;
-  f32x4 v{};
-  const int64_t shares = (n + a.share - 1) / a.share;
+  const int64_t column = blockIdx.x, adapter = blockIdx.y;
+  const bool la = column >= a.tiles[0];
+  const int64_t c0 = (la ? column - a.tiles[0] : column) * C, cols = a.cols[la];
+  const int64_t tiles = used_tiles(a.plan), len = grad_len(a, tiles), t0 = a.plan.tbase[adapter], t1 = a.plan.tbase[adapter + 1];
+  int64_t first = 0, last = -1;
+  if (t0 >= 0 && t1 > t0 && t1 <= tiles) {
+    first = (column * tiles + t0) / len;
+    last = (column * tiles + t1 - 1) / len;
+    if (first == last || last >= a.groups) return;
+  }
+  for (int id = threadIdx.x; id < C * a.R / 4; id += kThreads) {
+    // four of a row of the run's sums
+    const int wide = (la ? a.R : C) / 4, row = id / wide, x = id % wide * 4, col = la ? row : x;
+    if (c0 + col >= cols) continue;
+    f32x4 v{};
 #pragma unroll 4
-  for (int64_t i = 0; i < shares; i++) v += *reinterpret_cast<const f32x4*>(p + i * size);
-  *reinterpret_cast<f32x4*>(a.out[k] + adapter * size + at) = v;
+    for (int64_t w = first; w <= last; w++)
+      v += *reinterpret_cast<const f32x4*>(a.part + (2 * w + (w == first)) * C * a.R + (int64_t)id * 4);
+    float* out = a.out[la] + adapter * a.R * cols + (la ? (c0 + row) * a.R + x : row * cols + c0 + x);
+    *reinterpret_cast<f32x4*>(out) = v;
+  }
 }
 
 // ---------------------------------------------------------------- launches
 
-// Splits of a `down` over C channels: about two workgroups a CU, each with eight steps of 64 at least.
-struct Splits {
-  int count, steps;
-};
-Splits down_splits(int64_t tiles, int64_t C) {
-  const int64_t steps = (C + 63) / 64;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 8));
-  const int64_t per = (steps + want - 1) / want;
-  return Splits{(int)((steps + per - 1) / per), (int)per};
-}
-
 int rank_blocks(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 int rank_steps(int64_t R) { return (int)((R + 31) / 32); }
-size_t rows_bytes(int64_t M, int64_t A, int64_t R) { return (size_t)max_tiles(M, A) * 2 * 4 * rank_steps(R) * 1024; }
 // Parts of S in the gradients' sums.  Two hold it to 2^-16 of each element, 5e-6 of a sum of many rows; where
 // rows are few and one may be most of a sum, three hold all of it, at half as many products again.
 constexpr int64_t kFewRows = 1024;
 int sum_parts(int64_t M) { return M <= kFewRows ? 3 : 2; }
 size_t cols_bytes(int64_t M, int64_t A, int64_t R) { return (size_t)max_tiles(M, A) * sum_parts(M) * 2 * rank_blocks(R) * 1024; }
 
+// The workgroups that the chip's 256 CUs hold at once, by their registers and LDS.
+constexpr int kCus = 256;
+Stream stream_of(int64_t most, int64_t steps, int per_cu, int least) {
+  return Stream{steps, (int)std::min<int64_t>(per_cu * kCus, (most * steps + least - 1) / least), least};
+}
+Stream down_stream(int64_t most, int64_t C, int64_t R) {
+  return stream_of(most, (C + 63) / 64, down_per_cu(rank_blocks(R)), kWaves);
+}
+size_t align(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t part_bytes(int64_t M, int64_t A, int64_t R, int64_t C) {
+  const int64_t most = max_tiles(M, A);
+  return align((size_t)(most + down_stream(most, C, R).groups) * kTile * R * 4);
+}
+
+Emit emit_of(int64_t M, int64_t R, const float* alpha, float* t, void* cols) {
+  return Emit{alpha, t, (u32x4*)cols, (int)R, rank_blocks(R), std::max(32 * rank_steps(R), 16 * rank_blocks(R)), sum_parts(M)};
+}
+size_t tile_bytes(const Emit& e) { return (size_t)kTile * (e.width + 4) * 4; }
+
 void down(const Plan& plan, const void* x, int64_t x_row, const void* w, int64_t C, int64_t R, float* part, hipStream_t stream) {
-  const int64_t tiles = max_tiles(plan.M, plan.A);
-  const Splits sp = down_splits(tiles, C);
-  DownArgs a{plan, (const uint16_t*)x, (const uint16_t*)w, x_row, C, plan.M * R, (int)R, sp.steps, part};
-  const dim3 grid((unsigned)tiles, (unsigned)sp.count);
+  const DownArgs a{plan, (const uint16_t*)x, (const uint16_t*)w, x_row, C, (int)R, down_stream(plan.most, C, R), part};
+  const dim3 grid((unsigned)a.stream.groups);
   switch (rank_blocks(R)) {
     case 1: hipLaunchKernelGGL(down_kernel<1>, grid, dim3(kThreads), 0, stream, a); break;
     case 2: hipLaunchKernelGGL(down_kernel<2>, grid, dim3(kThreads), 0, stream, a); break;
@@ -693,45 +895,29 @@ void down(const Plan& plan, const void* x, int64_t x_row, const void* w, int64_t
   }
 }
 
-void join(const Plan& plan, const float* part, const float* kept, int splits, int64_t R, const float* alpha, float* t,
-          void* rows, void* cols, hipStream_t stream) {
-  const int width = std::max(32 * rank_steps(R), 16 * rank_blocks(R));
-  JoinArgs a{plan, part, kept, plan.M * R, splits, (int)R, rank_steps(R), rank_blocks(R), width, alpha, t, (u32x4*)rows, (u32x4*)cols,
-             sum_parts(plan.M)};
-  hipLaunchKernelGGL(join_kernel, dim3((unsigned)max_tiles(plan.M, plan.A)), dim3(kThreads),
-                     (size_t)kTile * (width + 4) * 4, stream, a);
-}
-
-void up(const Plan& plan, const void* t, const void* w, const void* y0, int64_t y0_row, void* y, int64_t y_row, int64_t N,
-        int64_t R, hipStream_t stream) {
-  const int64_t tiles = max_tiles(plan.M, plan.A), all = (N + 31) / 32;
-  // about four workgroups a CU, each wave with two strips at least
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((1024 + tiles - 1) / tiles, all / 8));
-  const int64_t strips = (all + want - 1) / want;
-  UpArgs a{plan, (const u32x4*)t, (const uint16_t*)w, (const uint16_t*)y0, (uint16_t*)y, y0_row, y_row, N, (int)R, (int)strips};
-  const dim3 grid((unsigned)tiles, (unsigned)((all + strips - 1) / strips));
-  switch (rank_steps(R)) {
-    case 1: hipLaunchKernelGGL(up_kernel<1>, grid, dim3(kThreads), 0, stream, a); break;
-    case 2: hipLaunchKernelGGL(up_kernel<2>, grid, dim3(kThreads), 0, stream, a); break;
-    case 3: hipLaunchKernelGGL(up_kernel<3>, grid, dim3(kThreads), 0, stream, a); break;
-    default: hipLaunchKernelGGL(up_kernel<4>, grid, dim3(kThreads), 0, stream, a); break;
+// C: the channels that down summed over.
+void up(const Plan& plan, const void* w, const void* y0, int64_t y0_row, void* y, int64_t y_row, int64_t N, int64_t C,
+        const float* part, const Emit& e, hipStream_t stream) {
+  const int rk = rank_steps(e.R);
+  const UpArgs a{plan, (const uint16_t*)w, (const uint16_t*)y0, (uint16_t*)y, y0_row, y_row, N,
+                 stream_of(plan.most, (N + 63) / 64, up_per_cu(rk), kWaves), down_stream(plan.most, C, e.R), part, e};
+  const dim3 grid((unsigned)a.stream.groups);
+  auto go = [&](auto k) {
+    constexpr int RK = decltype(k)::value;
+    const size_t lds = 8 * RK * 1024 + std::max<size_t>(tile_bytes(e), kWaves * up_lines(RK));
+    if (y0 != nullptr) hipLaunchKernelGGL((up_kernel<RK, true>), grid, dim3(kThreads), lds, stream, a);
+    else hipLaunchKernelGGL((up_kernel<RK, false>), grid, dim3(kThreads), lds, stream, a);
+  };
+  switch (rk) {
+    case 1: go(std::integral_constant<int, 1>()); break;
+    case 2: go(std::integral_constant<int, 2>()); break;
+    case 3: go(std::integral_constant<int, 3>()); break;
+    default: go(std::integral_constant<int, 4>()); break;
   }
 }
 
-size_t align(size_t n) { return (n + 255) & ~(size_t)255; }
-
-size_t part_bytes(int64_t M, int64_t A, int64_t R, int64_t C) {
-  return align((size_t)down_splits(max_tiles(M, A), C).count * M * R * 4);
-}
-
-// Rows of a share: enough shares to fill the chip with column tiles, each of 256 rows at least.
-int64_t grad_share(int64_t M, int64_t A, int64_t R, int64_t K, int64_t N) {
-  const int64_t C = rank_blocks(R) == 8 ? 64 : 128, tiles = (K + C - 1) / C + (N + C - 1) / C;
-  const int64_t want = std::max<int64_t>(1, 768 / tiles);
-  return std::max<int64_t>(256, ((M + want - 1) / want + 63) / 64 * 64);
-}
-int64_t grad_shares(int64_t M, int64_t A, int64_t share) { return M / share + A; }
-bool grad_splits(int64_t M, int64_t share) { return M > share; }
+constexpr int kGradGroups = 2 * kCus;
+int64_t grad_columns(int64_t R) { return rank_blocks(R) == 8 ? 64 : 128; }
 
 }  // namespace
 
@@ -749,33 +935,28 @@ hipError_t launch_adapters_plan(const int32_t* ids, int64_t M, int64_t A, void* 
   return hipGetLastError();
 }
 
-size_t adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
-  return part_bytes(M, A, R, K) + align(rows_bytes(M, A, R));
-}
+// Workspace: down's pieces.
+size_t adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) { return part_bytes(M, A, R, K); }
 
 hipError_t launch_adapters(const AdapterCall& c, const void* y0, int64_t y0_row, void* y, int64_t y_row, float* t, void* ws,
                            hipStream_t stream) {
   const Plan plan = plan_of(c.plan, c.M, c.A);
   float* part = (float*)ws;
-  void* rows = (uint8_t*)ws + part_bytes(c.M, c.A, c.R, c.K);
   down(plan, c.x, c.x_row, c.LB, c.K, c.R, part, stream);
-  join(plan, part, nullptr, down_splits(max_tiles(c.M, c.A), c.K).count, c.R, c.alpha, t, rows, nullptr, stream);
-  up(plan, rows, c.LA, y0, y0_row, y, y_row, c.N, c.R, stream);
+  up(plan, c.LA, y0, y0_row, y, y_row, c.N, c.K, part, emit_of(c.M, c.R, c.alpha, t, nullptr), stream);
   return hipGetLastError();
 }
 
-// Workspace of the gradient: L_A^T, L_B^T | parts of dT | operands of dT, of dT and T transposed | shares.
+// Workspace of the gradient: L_A^T, L_B^T | down's pieces | operands of dT and T for grad | grad's runs.
 size_t adapters_back_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
-  const int64_t share = grad_share(M, A, R, K, N);
-  return align((size_t)A * N * R * 2) + align((size_t)A * K * R * 2) + part_bytes(M, A, R, N) + align(rows_bytes(M, A, R)) +
-         2 * align(cols_bytes(M, A, R)) + (grad_splits(M, share) ? align((size_t)grad_shares(M, A, share) * R * (K + N) * 4) : 0);
+  return align((size_t)A * N * R * 2) + align((size_t)A * K * R * 2) + part_bytes(M, A, R, N) + 2 * align(cols_bytes(M, A, R)) +
+         align((size_t)2 * kGradGroups * grad_columns(R) * R * 4);
 }
 
 hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void* dy, int64_t dy_row, const void* dx0,
                                 int64_t dx0_row, void* dx, int64_t dx_row, float* dla, float* dlb, void* ws,
                                 hipStream_t stream) {
   const Plan plan = plan_of(c.plan, c.M, c.A);
-  const int64_t share = grad_share(c.M, c.A, c.R, c.K, c.N);
   uint8_t* at = (uint8_t*)ws;
   auto take = [&](size_t bytes) {
     void* p = at;
@@ -785,12 +966,14 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
   void* lat = take((size_t)c.A * c.N * c.R * 2);
   void* lbt = take((size_t)c.A * c.K * c.R * 2);
   float* part = (float*)take(part_bytes(c.M, c.A, c.R, c.N));
-  void* rows = take(rows_bytes(c.M, c.A, c.R));
   void* dcols = take(cols_bytes(c.M, c.A, c.R));
   void* tcols = take(cols_bytes(c.M, c.A, c.R));
-  float* shares = (float*)at;
+  float* runs = (float*)at;
+  const Stream ds = down_stream(plan.most, c.N, c.R);
   const bool dt = dx != nullptr || dlb != nullptr;
-  if (dt) {
+  const Emit de = emit_of(c.M, c.R, c.alpha, nullptr, dlb != nullptr ? dcols : nullptr);
+  const Emit te = emit_of(c.M, c.R, c.alpha, nullptr, tcols);
+  {
     TurnArgs a{};
     a.plan = plan;
     a.in[0] = (const uint16_t*)c.LA;
@@ -801,17 +984,24 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     a.out[1] = (uint16_t*)lbt;
     a.rows[1] = c.R;
     a.cols[1] = c.K;
-    a.tiles[0] = (uint32_t)(((c.N + 63) / 64) * ((c.R + 63) / 64));
+    a.tiles[0] = dt ? (uint32_t)(((c.N + 63) / 64) * ((c.R + 63) / 64)) : 0;
     a.tiles[1] = dx != nullptr ? (uint32_t)(((c.K + 63) / 64) * ((c.R + 63) / 64)) : 0;
-    hipLaunchKernelGGL(turn_kernel, dim3(a.tiles[0] + a.tiles[1], (unsigned)c.A), dim3(kThreads), 0, stream, a);
-    down(plan, dy, dy_row, lat, c.N, c.R, part, stream);
-    join(plan, part, nullptr, down_splits(max_tiles(c.M, c.A), c.N).count, c.R, c.alpha, nullptr, dx != nullptr ? rows : nullptr,
-         dlb != nullptr ? dcols : nullptr, stream);
+    a.turns = (uint32_t)(c.A * (a.tiles[0] + a.tiles[1]));
+    a.kept = JoinArgs{plan, nullptr, t, ds, te};
+    const size_t lds = std::max<size_t>(tile_bytes(te), 64 * 72 * 2);
+    hipLaunchKernelGGL(turn_kernel, dim3(a.turns + (dla != nullptr ? (unsigned)plan.most : 0)), dim3(kThreads), lds, stream, a);
   }
-  if (dla != nullptr) join(plan, nullptr, t, 0, c.R, c.alpha, nullptr, nullptr, tcols, stream);
-  if (dx != nullptr) up(plan, rows, lbt, dx0, dx0_row, dx, dx_row, c.K, c.R, stream);
+  if (dt) {
+    down(plan, dy, dy_row, lat, c.N, c.R, part, stream);
+    if (dx != nullptr) {
+      up(plan, lbt, dx0, dx0_row, dx, dx_row, c.K, c.N, part, de, stream);
+    } else {
+      const JoinArgs a{plan, part, nullptr, ds, de};
+      hipLaunchKernelGGL(join_kernel, dim3((unsigned)plan.most), dim3(kThreads), tile_bytes(de), stream, a);
+    }
+  }
   if (dla != nullptr || dlb != nullptr) {
-    const int64_t C = rank_blocks(c.R) == 8 ? 64 : 128;
+    const int64_t C = grad_columns(c.R);
     GradArgs a{};
     a.plan = plan;
     a.z[0] = (const uint16_t*)c.x;
@@ -826,11 +1016,10 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     a.out[1] = dla;
     a.tiles[0] = dlb != nullptr ? (uint32_t)((c.K + C - 1) / C) : 0;
     a.tiles[1] = dla != nullptr ? (uint32_t)((c.N + C - 1) / C) : 0;
-    a.part[0] = shares;
-    a.part[1] = shares + grad_shares(c.M, c.A, share) * c.R * c.K;
+    a.part = runs;
     a.R = (int)c.R;
-    a.share = (int)share;
-    const dim3 grid(a.tiles[0] + a.tiles[1], (unsigned)grad_shares(c.M, c.A, share));
+    a.groups = kGradGroups;
+    const dim3 grid((unsigned)kGradGroups), columns(a.tiles[0] + a.tiles[1], (unsigned)c.A);
     auto go = [&](auto parts) {
       constexpr int P = decltype(parts)::value;
       switch (rank_blocks(c.R)) {
@@ -842,11 +1031,8 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     };
     if (sum_parts(c.M) == 3) go(std::integral_constant<int, 3>());
     else go(std::integral_constant<int, 2>());
-    if (grad_splits(c.M, share)) {
-      const int64_t most = c.R * std::max(c.K, c.N) / 4;
-      hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)((most + kThreads - 1) / kThreads), (unsigned)c.A, 2), dim3(kThreads), 0,
-                         stream, a);
-    }
+    if (C == 64) hipLaunchKernelGGL(grad_join_kernel<64>, columns, dim3(kThreads), 0, stream, a);
+    else hipLaunchKernelGGL(grad_join_kernel<128>, columns, dim3(kThreads), 0, stream, a);
   }
   return hipGetLastError();
 }

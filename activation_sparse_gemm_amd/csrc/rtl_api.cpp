@@ -892,7 +892,7 @@ namespace {
 bool adapters_fit(int64_t M, int64_t A) { return M > 0 && M <= 1 << 24 && A > 0 && A <= 4096; }
 bool adapters_fit(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
   return adapters_fit(M, A) && N > 0 && N <= kMaxK && K > 0 && K <= kMaxK && R > 0 && R <= 128 && N % 8 == 0 && K % 8 == 0 &&
-         R % 8 == 0 && A * R * (N > K ? N : K) <= (int64_t)1 << 40;
+         R % 8 == 0 && A * (N > K ? N : K) <= (int64_t)1 << 27;
 }
 
 rtl_status check_plan_sizes(int64_t M, int64_t A) {

@@ -428,7 +428,7 @@ rtl_status rtl_layer_norm_backward(rtl_dtype dt, int64_t M, int64_t D, const voi
  *
  * Both products accumulate in fp32; T enters the second in two bf16 parts (2^-16 of it); one rounding at
  * the end.  Limits: K, N and R multiples of 8, R <= 128, K and N <= 2^22, A <= 4096, M <= 2^24, and
- * A * R * max(K, N) <= 2^40.  Outputs overlap no input but Y0 as said.  Calls that share a workspace must be
+ * A * max(K, N) <= 2^27.  Outputs overlap no input but Y0 as said.  Calls that share a workspace must be
  * serialised.
  */
 size_t rtl_adapters_plan_bytes(int64_t M, int64_t A);

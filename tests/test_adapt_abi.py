@@ -92,7 +92,7 @@ ADAPTERS = [
     (dict(N=0), "RTL_ERR_SHAPE"), (dict(K=-8), "RTL_ERR_SHAPE"), (dict(R=0), "RTL_ERR_SHAPE"), (dict(A=0), "RTL_ERR_SHAPE"),
     (dict(M=2 ** 24 + 1), "RTL_ERR_SHAPE"), (dict(A=4097), "RTL_ERR_SHAPE"), (dict(K=2 ** 22 + 8), "RTL_ERR_SHAPE"),
     (dict(N=2 ** 62), "RTL_ERR_SHAPE"), (dict(N=44), "RTL_ERR_UNSUPPORTED"), (dict(K=60), "RTL_ERR_UNSUPPORTED"),
-    (dict(R=12), "RTL_ERR_UNSUPPORTED"), (dict(R=136), "RTL_ERR_UNSUPPORTED"), (dict(A=4096, R=128, K=2 ** 22), "RTL_ERR_SHAPE"),
+    (dict(R=12), "RTL_ERR_UNSUPPORTED"), (dict(R=136), "RTL_ERR_UNSUPPORTED"), (dict(A=64, K=2 ** 22), "RTL_ERR_SHAPE"),
     (dict(X=None), "RTL_ERR_NULL"), (dict(LA=None), "RTL_ERR_NULL"), (dict(LB=None), "RTL_ERR_NULL"), (dict(plan=None), "RTL_ERR_NULL"),
     (dict(pb=16), "RTL_ERR_ARG"), (dict(pb=lambda a: a["pb"] + 4), "RTL_ERR_ARG"), (dict(xr=68), "RTL_ERR_ALIGN"),
     (dict(xr=-64), "RTL_ERR_SHAPE"), (dict(LB=lambda a: at(a["LB"], 8)), "RTL_ERR_ALIGN"), (dict(al=lambda a: at(a["al"], 2)), "RTL_ERR_ALIGN"),
@@ -178,7 +178,7 @@ def test_sizes_of_plans_and_workspaces():
     assert rtl.rtl_adapters_plan_bytes(1, 4097) == 0
     # tables of two numbers an adapter, four words a tile, one a row
     assert rtl.rtl_adapters_plan_bytes(2 ** 24, 4096) == 4 * (8200 + 4 * (2 ** 18 + 4097) + 2 ** 24)
-    for bad in ((0, 8, 8, 8, 1), (1, 4, 8, 8, 1), (1, 8, 12, 8, 1), (1, 8, 8, 136, 1), (1, 2 ** 22, 8, 128, 4096)):
+    for bad in ((0, 8, 8, 8, 1), (1, 4, 8, 8, 1), (1, 8, 12, 8, 1), (1, 8, 8, 136, 1), (1, 2 ** 22, 8, 128, 33)):
         assert rtl.rtl_adapters_workspace_bytes(*bad) == rtl.rtl_adapters_backward_workspace_bytes(*bad) == 0
     for M, K, N, R, A in ((1, 8, 8, 8, 1), (2 ** 24, 8, 8, 8, 4096), (70, 2 ** 22, 2 ** 22, 8, 2)):
         assert 0 < rtl.rtl_adapters_workspace_bytes(M, N, K, R, A)
