@@ -16,7 +16,8 @@
 // The gradients' sums of few rows take three (kFewRows).
 //
 //   down:   T in pieces over K, the waves taking 64 of K in turn
-//   up:     Y0 + T L_A^T, strips of 64 columns a wave, T's pieces summed on the way
+//   join:   T's pieces summed, T in the layouts of the products that it enters
+//   up:     Y0 + T L_A^T, strips of 64 columns a wave
 //   turn:   factors transposed, which makes dT a `down` and dX an `up`
 //   grad:   dL_B and dL_A, tiles of 128 (64) columns by R over runs of an adapter's rows
 #include <algorithm>
@@ -202,16 +203,6 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// A tile's T, scaled by alpha, in bf16 parts: as up's operand (row_operand: two parts; lane (r16, q): row r16 of
-// a block, r = 8q .. 8q + 7 of 32), and as grad's, `cols` (lane (r16, q): r = r16 of a block, rows 8q ..
-// 8q + 7 of 32); T itself, unscaled, to `t`.
-struct Emit {
-  const float* alpha;  // [A] or null
-  float* t;            // [M, R] by row, or null
-  u32x4* cols;         // or null
-  int R, RB, width, parts;  // RB: R in 16s as grad takes them; width: of the tile in LDS; parts of cols
-};
-__device__ __forceinline__ int pitch_of(const Emit& e) { return e.width + 4; }
 __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4& hi, u32x4& lo) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
@@ -221,69 +212,104 @@ __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4& hi, u32x4& 
     lo[i] = __builtin_bit_cast(uint32_t, bf16x2_t{x.lo, y.lo});
   }
 }
-// Lane's row operand of block mb and 32 r kk, from the tile [64][pitch] in LDS.
-__device__ __forceinline__ void row_operand(const float* tile, int pitch, int mb, int kk, int lane, u32x4& hi, u32x4& lo) {
-  const float* p = tile + (16 * mb + (lane & 15)) * pitch + 32 * kk + 8 * (lane >> 4);
-  float v[8];
+__device__ __forceinline__ void parts_of(const float (&v)[8], u32x4 (&w)[3]) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = p[i];
-  parts_of(v, hi, lo);
+  for (int i = 0; i < 4; i++) {
+    __bf16 x[3], y[3];
+    three_parts(v[2 * i], x);
+    three_parts(v[2 * i + 1], y);
+#pragma unroll
+    for (int k = 0; k < 3; k++) w[k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{x[k], y[k]});
+  }
 }
-__device__ __forceinline__ void emit_cols(const Emit& a, const float* tile, int64_t index) {
-  const int pitch = pitch_of(a);
-  const int n = 2 * a.RB * 64;
-  u32x4* to = a.cols + index * a.parts * n;
-  for (int id = threadIdx.x; id < n; id += kThreads) {
-    const int lane = id & 63, rb = (id >> 6) % a.RB, half = (id >> 6) / a.RB;
-    const float* p = tile + (32 * half + 8 * (lane >> 4)) * pitch + 16 * rb + (lane & 15);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = p[i * pitch];
-    if (a.parts == 3) {
-      u32x4 w[3];
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-        __bf16 x[3], y[3];
-        three_parts(v[2 * i], x);
-        three_parts(v[2 * i + 1], y);
-#pragma unroll
-        for (int k = 0; k < 3; k++) w[k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{x[k], y[k]});
+
+// join: T of half a tile, 32 rows, the sum of down's pieces or (kept) its rows as they are; unscaled to `t`, and scaled
+// by alpha in bf16 parts as the products take it: `rows`, up's operand, [tile][part][block of 16 rows][RK][lane]
+// (lane (r16, q): row r16, r = 8q .. 8q + 7 of 32), and `cols`, grad's, [tile][part][half][RB][lane] (r =
+// r16 of a block, rows 8q .. 8q + 7 of the half).  Rows and r past the tile's are zeros.
+// A launch of its own: summed by each workgroup of up that needed it, T cost 8 to 19 us of up's time
+// (4608 rows of 5120, R = 64, 72 tiles of 8 pieces on 512 workgroups: 53 us for 35; this takes 6).
+struct JoinArgs {
+  Plan plan;
+  const float *part, *kept;  // one of them
+  Stream down;
+  const float* alpha;        // [A] or null
+  float* t;                  // [M, R] by row, or null
+  u32x4 *rows, *cols;        // or null
+  int R, RB, RK, parts;      // R in 16s as grad takes them, in 32s as up does; parts of cols
+};
+constexpr int kJoinThreads = 512;
+constexpr int join_pitch(int RK) { return 32 * RK + 4; }
+template <int THREADS>
+__device__ __forceinline__ void join_half(const JoinArgs& a, int64_t index, int half, float* lds) {
+  const Tile t = tile_of(a.plan, index);
+  const int left = t.rows - 32 * half, R = a.R, wide = 8 * a.RK, pitch = join_pitch(a.RK);
+  const bool bare = t.adapter >= a.plan.A;
+  if (t.rows == 0 || (bare && (a.t == nullptr || left <= 0))) return;
+  const float alpha = bare || a.alpha == nullptr ? 1.f : a.alpha[t.adapter];
+  int64_t first = 0, last = -1;
+  if (a.kept != nullptr) last = 0;
+  else if (!bare) a.down.of(index, a.down.len(used_tiles(a.plan)), first, last);
+  for (int id = threadIdx.x; id < 32 * wide; id += THREADS) {
+    const int m = id / wide, r = id % wide * 4;
+    const bool in = m < left && r < R;
+    f32x4 v{};
+    if (in) {
+      const int64_t row = row_at(a.plan, t.pos + 32 * half + m);
+      if (a.kept != nullptr) {
+        v = *reinterpret_cast<const f32x4*>(a.kept + row * R + r);
+      } else {
+        const float* p = a.part + ((first + index) * kTile + 32 * half + m) * R + r;
+#pragma unroll 8
+        for (int64_t w = first; w <= last; w++, p += kTile * R) v += *reinterpret_cast<const f32x4*>(p);
       }
+      if (a.t != nullptr) *reinterpret_cast<f32x4*>(a.t + row * R + r) = v;
+    }
+    *reinterpret_cast<f32x4*>(lds + m * pitch + r) = v * alpha;
+  }
+  if (bare) return;
+  __syncthreads();
+  if (a.rows != nullptr) {
+    u32x4* to = a.rows + (index * 8 + 2 * half) * a.RK * 64;
+    for (int id = threadIdx.x; id < 2 * a.RK * 64; id += THREADS) {
+      const int lane = id & 63, k = (id >> 6) % a.RK, block = (id >> 6) / a.RK;
+      const float* p = lds + (16 * block + (lane & 15)) * pitch + 32 * k + 8 * (lane >> 4);
+      float v[8];
 #pragma unroll
-      for (int k = 0; k < 3; k++) to[k * n + id] = w[k];
-    } else {
+      for (int i = 0; i < 8; i++) v[i] = p[i];
       u32x4 hi, lo;
       parts_of(v, hi, lo);
       to[id] = hi;
-      to[n + id] = lo;
+      to[id + 4 * a.RK * 64] = lo;
+    }
+  }
+  if (a.cols != nullptr) {
+    const int n = 2 * a.RB * 64;
+    u32x4* to = a.cols + index * a.parts * n + half * a.RB * 64;
+    for (int id = threadIdx.x; id < a.RB * 64; id += THREADS) {
+      const int lane = id & 63;
+      const float* p = lds + 8 * (lane >> 4) * pitch + 16 * (id >> 6) + (lane & 15);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] = p[i * pitch];
+      if (a.parts == 3) {
+        u32x4 w[3];
+        parts_of(v, w);
+#pragma unroll
+        for (int k = 0; k < 3; k++) to[k * n + id] = w[k];
+      } else {
+        u32x4 hi, lo;
+        parts_of(v, hi, lo);
+        to[id] = hi;
+        to[id + n] = lo;
+      }
     }
   }
 }
-// T of a tile to LDS, scaled: the sum of down's pieces, or, `kept`, its rows as they are; and unscaled to a.t
-// (put).  Rows and r past the tile's are zeros, rows without an adapter too.
-__device__ __forceinline__ void join_tile(const Emit& a, const Plan& plan, const Tile& t, int64_t index, const float* part,
-                                          const Stream& down, int64_t down_len, const float* kept, bool put, float* tile) {
-  const bool bare = t.adapter >= plan.A;
-  const int pitch = pitch_of(a), quads = a.width / 4;
-  const float alpha = bare || a.alpha == nullptr ? 1.f : a.alpha[t.adapter];
-  int64_t first = 0, last = -1;
-  if (!bare && kept == nullptr) down.of(index, down_len, first, last);
-  for (int id = threadIdx.x; id < kTile * quads; id += kThreads) {
-    const int m = id / quads, r = id % quads * 4;
-    f32x4 v{};
-    if (m < t.rows && r < a.R) {
-      if (kept != nullptr) {
-        v = *reinterpret_cast<const f32x4*>(kept + row_at(plan, t.pos + m) * a.R + r);
-      } else {
-        const float* p = part + ((first + index) * kTile + m) * a.R + r;
-#pragma unroll 4
-        for (int64_t w = first; w <= last; w++, p += kTile * a.R) v += *reinterpret_cast<const f32x4*>(p);
-      }
-      if (put) *reinterpret_cast<f32x4*>(a.t + row_at(plan, t.pos + m) * a.R + r) = v;
-    }
-    *reinterpret_cast<f32x4*>(tile + m * pitch + r) = v * alpha;
-  }
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const JoinArgs a) {
+  __shared__ __align__(16) float lds[32 * join_pitch(4)];
+  join_half<kJoinThreads>(a, blockIdx.x >> 1, blockIdx.x & 1, lds);
 }
 
 // Memory is met in whole lines, eight rows of 128 bytes an access with a row's eight chunks in neighbouring lanes, and
@@ -429,51 +455,31 @@ __global__ __launch_bounds__(kThreads, down_per_cu(RB)) void down_kernel(const D
   }
 }
 
-// join: a tile's T as grad's operand, from down's pieces or from a kept T.
-struct JoinArgs {
-  Plan plan;
-  const float *part, *kept;
-  Stream down;
-  Emit e;
-};
-__device__ __forceinline__ void join_cols(const JoinArgs& a, int64_t index, float* tile) {
-  const Tile t = tile_of(a.plan, index);
-  if (t.rows == 0 || t.adapter >= a.plan.A) return;
-  join_tile(a.e, a.plan, t, index, a.part, a.down, a.kept != nullptr ? 1 : a.down.len(used_tiles(a.plan)), a.kept, false, tile);
-  __syncthreads();
-  emit_cols(a.e, tile, index);
-}
-__global__ __launch_bounds__(kThreads) void join_kernel(const JoinArgs a) {
-  extern __shared__ __align__(16) uint8_t dynamic[];
-  join_cols(a, blockIdx.x, reinterpret_cast<float*>(dynamic));
-}
-
 // up: Y[row][n] = Y0[row][n] + sum over r of T[row][r] W[adapter][n][r].  The waves of a workgroup take the
-// strips of 64 columns of its piece of a tile in turn, with the tile's T, which they sum from down's pieces, in
-// LDS.  A strip is four blocks of columns: half s takes columns 32 s + 8 (i / 4) + 4 b + i % 4 into its
+// strips of 64 columns of its piece of a tile in turn, with the tile's T (join's rows) in LDS.  A strip is four blocks of columns: half s takes columns 32 s + 8 (i / 4) + 4 b + i % 4 into its
 // blocks b = 0, 1, so that lane (r16, q) ends with columns 32 s + 8q .. + 7 of row r16.  Y0, Y and the factors pass in whole
-// lines.  The workgroup that has a tile's first strip also leaves its T and grad's operand.
+// lines.
 struct UpArgs {
   Plan plan;
   const uint16_t *w, *y0;  // [A, N, R]; [M, N] with a row stride, or null
   uint16_t* y;
   int64_t y0_row, y_row, N;
-  Stream stream, down;
-  const float* part;
-  Emit e;
+  int R;
+  Stream stream;
+  const u32x4* t;
 };
 // Workgroups a CU, by their registers.
 constexpr int up_per_cu(int RK) { return RK <= 2 ? 2 : 1; }  // and LDS
 // A wave's LDS: two blocks of rows and a strip's factors.
 constexpr int up_lines(int RK) { return 2 * 2048 + RK * 4096; }
-// MB: blocks of rows.  `prepare` puts T's operands into LDS, behind the first loads.
-template <int RK, bool ADD, int MB, typename Prepare>
-__device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t first, int64_t last, const u32x4* operands,
-                                         uint8_t* lines, Prepare prepare) {
+// MB: blocks of rows.
+template <int RK, bool ADD, int MB>
+__device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t first, int64_t last, const u32x4* t_from,
+                                         u32x4* operands, uint8_t* lines) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
   constexpr int PER = 4 * RK, WL = 64 * PER / 64;  // chunks of a factor's row, accesses of a strip's factors
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
-  const int R = a.e.R, l8 = lane >> 3, chunk = lane & 7;
+  const int R = a.R, l8 = lane >> 3, chunk = lane & 7;
   const u32x4* tv = operands + lane;
   uint8_t *mine = lines + wave * up_lines(RK), *mine_w = mine + 2 * 2048;
   const int64_t whole = a.N / 64, end = min(last, whole), n0 = (first + wave) * 64;
@@ -566,7 +572,15 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
 #pragma unroll
     for (int b = 0; b < MB; b++) fetch_y(0, b);
   }
-  prepare();
+  {  // T, behind the first loads
+    u32x4 v[2 * RK];
+#pragma unroll
+    for (int j = 0; j < 2 * RK; j++) v[j] = t_from[threadIdx.x + j * kThreads];
+    __syncthreads();  // the tile before is read
+#pragma unroll
+    for (int j = 0; j < 2 * RK; j++) operands[threadIdx.x + j * kThreads] = v[j];
+    __syncthreads();
+  }
   // The next strip's factors go out first, each block of rows when this strip's is done with: every load has a
   // whole strip's time, and none waits for one that is not needed yet (they return in order).
   for (int64_t i = 0; i < count; i++) {
@@ -603,10 +617,8 @@ template <int RK, bool ADD>
 __global__ __launch_bounds__(kThreads, up_per_cu(RK)) void up_kernel(const UpArgs a) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   u32x4* operands = reinterpret_cast<u32x4*>(dynamic);  // [2][4][RK][64]
-  uint8_t* lines = dynamic + 8 * RK * 1024;             // the waves' lines, and in `prepare` T
-  float* tile = reinterpret_cast<float*>(lines);
-  const int64_t used = used_tiles(a.plan), tiles = a.y0 == a.y && a.e.t == nullptr ? used : all_tiles(a.plan);
-  const int64_t len = a.stream.len(tiles), down_len = a.down.len(used);
+  uint8_t* lines = dynamic + 8 * RK * 1024;             // the waves' lines
+  const int64_t tiles = a.y0 == a.y ? used_tiles(a.plan) : all_tiles(a.plan), len = a.stream.len(tiles);
   int64_t at = blockIdx.x * len;
   const int64_t end = min(at + len, tiles * a.stream.steps);
   while (at < end) {
@@ -614,19 +626,7 @@ __global__ __launch_bounds__(kThreads, up_per_cu(RK)) void up_kernel(const UpArg
     at += last - first;
     const Tile t = tile_of(a.plan, index);
     if (t.rows == 0) continue;
-    const bool bare = t.adapter >= a.plan.A, put = a.e.t != nullptr && first == 0;
-    auto prepare = [&]() {
-      __syncthreads();  // the tile and the operands before are read
-      join_tile(a.e, a.plan, t, index, a.part, a.down, down_len, nullptr, put, tile);
-      __syncthreads();
-      for (int id = threadIdx.x; id < 4 * RK * 64; id += kThreads)
-        row_operand(tile, pitch_of(a.e), id / (64 * RK), id / 64 % RK, id & 63, operands[id], operands[4 * RK * 64 + id]);
-      if (a.e.cols != nullptr && first == 0 && !bare) emit_cols(a.e, tile, index);
-      __syncthreads();
-    };
-    if (bare) {  // Y0 as it is, T zeros
-      if (put) prepare();
-      if (a.y0 == a.y) continue;
+    if (t.adapter >= a.plan.A) {  // Y0 as it is
       const int64_t c0 = first * 64, wide = (min(last * 64, a.N) - c0) / 8;
       for (int64_t id = threadIdx.x; id < wide * t.rows; id += kThreads) {
         const int64_t row = row_at(a.plan, t.pos + id / wide), n = c0 + id % wide * 8;
@@ -634,8 +634,9 @@ __global__ __launch_bounds__(kThreads, up_per_cu(RK)) void up_kernel(const UpArg
       }
       continue;
     }
-    if (t.rows <= 16) up_piece<RK, ADD, 1>(a, t, first, last, operands, lines, prepare);
-    else up_piece<RK, ADD, 4>(a, t, first, last, operands, lines, prepare);
+    const u32x4* from = a.t + index * (8 * RK * 64);
+    if (t.rows <= 16) up_piece<RK, ADD, 1>(a, t, first, last, from, operands, lines);
+    else up_piece<RK, ADD, 4>(a, t, first, last, from, operands, lines);
   }
 }
 
@@ -647,16 +648,18 @@ struct TurnArgs {
   uint16_t* out[2];
   int64_t rows[2], cols[2];
   uint32_t tiles[2];  // workgroups of each, for an adapter
-  uint32_t turns;     // all of them; the others take a tile each of the kept T
+  uint32_t turns;     // all of them; the others take half a tile each of the kept T
   JoinArgs kept;
 };
 __global__ __launch_bounds__(kThreads) void turn_kernel(const TurnArgs a) {
-  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ __align__(16) float lds[32 * join_pitch(4)];
   if (blockIdx.x >= a.turns) {
-    join_cols(a.kept, blockIdx.x - a.turns, reinterpret_cast<float*>(dynamic));
+    const uint32_t at = blockIdx.x - a.turns;
+    join_half<kThreads>(a.kept, at >> 1, at & 1, lds);
     return;
   }
-  uint16_t(*block)[72] = reinterpret_cast<uint16_t(*)[72]>(dynamic);
+  uint16_t(*block)[72] = reinterpret_cast<uint16_t(*)[72]>(lds);
+  static_assert(sizeof(lds) >= 64 * sizeof(*block), "a block's LDS");
   const uint32_t per = a.tiles[0] + a.tiles[1], place = blockIdx.x % per;
   const int64_t adapter = blockIdx.x / per;
   if (a.plan.start[adapter] >= a.plan.start[adapter + 1]) return;
@@ -879,10 +882,21 @@ size_t part_bytes(int64_t M, int64_t A, int64_t R, int64_t C) {
   return align((size_t)(most + down_stream(most, C, R).groups) * kTile * R * 4);
 }
 
-Emit emit_of(int64_t M, int64_t R, const float* alpha, float* t, void* cols) {
-  return Emit{alpha, t, (u32x4*)cols, (int)R, rank_blocks(R), std::max(32 * rank_steps(R), 16 * rank_blocks(R)), sum_parts(M)};
+size_t rows_bytes(int64_t M, int64_t A, int64_t R) { return (size_t)max_tiles(M, A) * 8 * rank_steps(R) * 1024; }
+
+JoinArgs join_of(const Plan& plan, int64_t R, const float* alpha) {
+  JoinArgs a{};
+  a.plan = plan;
+  a.alpha = alpha;
+  a.R = (int)R;
+  a.RB = rank_blocks(R);
+  a.RK = rank_steps(R);
+  a.parts = sum_parts(plan.M);
+  return a;
 }
-size_t tile_bytes(const Emit& e) { return (size_t)kTile * (e.width + 4) * 4; }
+void join(const JoinArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(join_kernel, dim3((unsigned)(2 * a.plan.most)), dim3(kJoinThreads), 0, stream, a);
+}
 
 void down(const Plan& plan, const void* x, int64_t x_row, const void* w, int64_t C, int64_t R, float* part, hipStream_t stream) {
   const DownArgs a{plan, (const uint16_t*)x, (const uint16_t*)w, x_row, C, (int)R, down_stream(plan.most, C, R), part};
@@ -895,16 +909,15 @@ void down(const Plan& plan, const void* x, int64_t x_row, const void* w, int64_t
   }
 }
 
-// C: the channels that down summed over.
-void up(const Plan& plan, const void* w, const void* y0, int64_t y0_row, void* y, int64_t y_row, int64_t N, int64_t C,
-        const float* part, const Emit& e, hipStream_t stream) {
-  const int rk = rank_steps(e.R);
-  const UpArgs a{plan, (const uint16_t*)w, (const uint16_t*)y0, (uint16_t*)y, y0_row, y_row, N,
-                 stream_of(plan.most, (N + 63) / 64, up_per_cu(rk), kWaves), down_stream(plan.most, C, e.R), part, e};
+void up(const Plan& plan, const void* w, const void* y0, int64_t y0_row, void* y, int64_t y_row, int64_t N, int64_t R, const void* t,
+        hipStream_t stream) {
+  const int rk = rank_steps(R);
+  const UpArgs a{plan, (const uint16_t*)w, (const uint16_t*)y0, (uint16_t*)y, y0_row, y_row, N, (int)R,
+                 stream_of(plan.most, (N + 63) / 64, up_per_cu(rk), kWaves), (const u32x4*)t};
   const dim3 grid((unsigned)a.stream.groups);
   auto go = [&](auto k) {
     constexpr int RK = decltype(k)::value;
-    const size_t lds = 8 * RK * 1024 + std::max<size_t>(tile_bytes(e), kWaves * up_lines(RK));
+    constexpr size_t lds = 8 * RK * 1024 + kWaves * up_lines(RK);
     if (y0 != nullptr) hipLaunchKernelGGL((up_kernel<RK, true>), grid, dim3(kThreads), lds, stream, a);
     else hipLaunchKernelGGL((up_kernel<RK, false>), grid, dim3(kThreads), lds, stream, a);
   };
@@ -935,21 +948,29 @@ hipError_t launch_adapters_plan(const int32_t* ids, int64_t M, int64_t A, void* 
   return hipGetLastError();
 }
 
-// Workspace: down's pieces.
-size_t adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) { return part_bytes(M, A, R, K); }
+// Workspace: down's pieces | up's operands.
+size_t adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
+  return part_bytes(M, A, R, K) + align(rows_bytes(M, A, R));
+}
 
 hipError_t launch_adapters(const AdapterCall& c, const void* y0, int64_t y0_row, void* y, int64_t y_row, float* t, void* ws,
                            hipStream_t stream) {
   const Plan plan = plan_of(c.plan, c.M, c.A);
   float* part = (float*)ws;
   down(plan, c.x, c.x_row, c.LB, c.K, c.R, part, stream);
-  up(plan, c.LA, y0, y0_row, y, y_row, c.N, c.K, part, emit_of(c.M, c.R, c.alpha, t, nullptr), stream);
+  JoinArgs j = join_of(plan, c.R, c.alpha);
+  j.part = part;
+  j.down = down_stream(plan.most, c.K, c.R);
+  j.t = t;
+  j.rows = (u32x4*)((uint8_t*)ws + part_bytes(c.M, c.A, c.R, c.K));
+  join(j, stream);
+  up(plan, c.LA, y0, y0_row, y, y_row, c.N, c.R, j.rows, stream);
   return hipGetLastError();
 }
 
-// Workspace of the gradient: L_A^T, L_B^T | down's pieces | operands of dT and T for grad | grad's runs.
+// Workspace of the gradient: L_A^T, L_B^T | down's pieces | dT as up's operand | dT and T as grad's | grad's runs.
 size_t adapters_back_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
-  return align((size_t)A * N * R * 2) + align((size_t)A * K * R * 2) + part_bytes(M, A, R, N) + 2 * align(cols_bytes(M, A, R)) +
+  return align((size_t)A * N * R * 2) + align((size_t)A * K * R * 2) + part_bytes(M, A, R, N) + align(rows_bytes(M, A, R)) + 2 * align(cols_bytes(M, A, R)) +
          align((size_t)2 * kGradGroups * grad_columns(R) * R * 4);
 }
 
@@ -966,13 +987,11 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
   void* lat = take((size_t)c.A * c.N * c.R * 2);
   void* lbt = take((size_t)c.A * c.K * c.R * 2);
   float* part = (float*)take(part_bytes(c.M, c.A, c.R, c.N));
+  void* drows = take(rows_bytes(c.M, c.A, c.R));
   void* dcols = take(cols_bytes(c.M, c.A, c.R));
   void* tcols = take(cols_bytes(c.M, c.A, c.R));
   float* runs = (float*)at;
-  const Stream ds = down_stream(plan.most, c.N, c.R);
   const bool dt = dx != nullptr || dlb != nullptr;
-  const Emit de = emit_of(c.M, c.R, c.alpha, nullptr, dlb != nullptr ? dcols : nullptr);
-  const Emit te = emit_of(c.M, c.R, c.alpha, nullptr, tcols);
   {
     TurnArgs a{};
     a.plan = plan;
@@ -987,18 +1006,20 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     a.tiles[0] = dt ? (uint32_t)(((c.N + 63) / 64) * ((c.R + 63) / 64)) : 0;
     a.tiles[1] = dx != nullptr ? (uint32_t)(((c.K + 63) / 64) * ((c.R + 63) / 64)) : 0;
     a.turns = (uint32_t)(c.A * (a.tiles[0] + a.tiles[1]));
-    a.kept = JoinArgs{plan, nullptr, t, ds, te};
-    const size_t lds = std::max<size_t>(tile_bytes(te), 64 * 72 * 2);
-    hipLaunchKernelGGL(turn_kernel, dim3(a.turns + (dla != nullptr ? (unsigned)plan.most : 0)), dim3(kThreads), lds, stream, a);
+    a.kept = join_of(plan, c.R, c.alpha);
+    a.kept.kept = t;
+    a.kept.cols = (u32x4*)tcols;
+    hipLaunchKernelGGL(turn_kernel, dim3(a.turns + (dla != nullptr ? 2 * (unsigned)plan.most : 0)), dim3(kThreads), 0, stream, a);
   }
   if (dt) {
     down(plan, dy, dy_row, lat, c.N, c.R, part, stream);
-    if (dx != nullptr) {
-      up(plan, lbt, dx0, dx0_row, dx, dx_row, c.K, c.N, part, de, stream);
-    } else {
-      const JoinArgs a{plan, part, nullptr, ds, de};
-      hipLaunchKernelGGL(join_kernel, dim3((unsigned)plan.most), dim3(kThreads), tile_bytes(de), stream, a);
-    }
+    JoinArgs j = join_of(plan, c.R, c.alpha);
+    j.part = part;
+    j.down = down_stream(plan.most, c.N, c.R);
+    j.rows = dx != nullptr ? (u32x4*)drows : nullptr;
+    j.cols = dlb != nullptr ? (u32x4*)dcols : nullptr;
+    join(j, stream);
+    if (dx != nullptr) up(plan, lbt, dx0, dx0_row, dx, dx_row, c.K, c.R, drows, stream);
   }
   if (dla != nullptr || dlb != nullptr) {
     const int64_t C = grad_columns(c.R);
