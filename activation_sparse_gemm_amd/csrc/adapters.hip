@@ -19,7 +19,7 @@
 //   join:   T's pieces summed, T in the layouts of the products that it enters
 //   up:     Y0 + T L_A^T, strips of 64 columns a wave
 //   turn:   factors transposed, which makes dT a `down` and dX an `up`
-//   grad:   dL_B and dL_A, tiles of 128 (64) columns by R over runs of an adapter's rows
+//   grad:   dL_B and dL_A, tiles of 256 (128) columns by R over runs of an adapter's rows
 #include <algorithm>
 #include <type_traits>
 
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const JoinArgs a) {
 // passes through the wave's own LDS to and from the matrix instructions' layout (lane (r16, q): chunks q and 4 + q
 // of row r16; line_at is free of bank conflicts both ways).  Read as the instructions have it, neighbouring lanes on
 // different rows, every lane is an access of its own: 63 of them an instruction instead of 16, the address and data
-// units 85% busy, and down and up at 32760 x 5120, R = 64, took 105 and 170 us instead of XX and XX.  The LDS
+// units 85% busy, and down and up at 32760 x 5120, R = 64, took 105 and 170 us instead of 99 and 142.  The LDS
 // is the wave's own and its instructions run in order: no barrier.
 __device__ __forceinline__ int line_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
@@ -691,9 +691,12 @@ __global__ __launch_bounds__(kThreads) void turn_kernel(const TurnArgs a) {
 // S[row][r], S = dT or alpha T in parts (join's cols).  Column tiles, each with all tiles of rows, are dealt out as
 // Stream says; a workgroup goes through its runs of tiles of one adapter and one column tile.  A run
 // that is all of the adapter's goes to the output, else to `part`: the first run of a workgroup, begun by the
-// one before, to 2 w, the last to 2 w + 1; grad_join adds them.  The waves take 32 rows in turn: Z's rows go
-// through the wave's own LDS, to be read with the rows along a lane (the transposing read), their
-// 32-byte blocks swizzled so that the eight rows that half a wave reads lie in different banks.
+// one before, to 2 w, the last to 2 w + 1; grad_join adds them.  Of eight waves, four take 32
+// rows in turn and two take half the columns each: the two read the same lines of S, which L1 then holds once
+// (16380 rows of 5120 and 5120, R = 64: 107 us with the waves along the rows alone, 90 with two across, 74 with S not read
+// again; four across gain 1 us here and lose 3 in grad_join).  Z's rows go through the wave's own LDS, to be
+// read with the rows along a lane (the transposing read), their 32-byte blocks swizzled so that the
+// eight rows that half a wave reads lie in different banks.
 struct GradArgs {
   Plan plan;
   const uint16_t* z[2];  // X, dY
@@ -704,9 +707,11 @@ struct GradArgs {
   float* part;           // [2 workgroups][C R]: [R][C] of dL_B, [C][R] of dL_A
   int R, groups;
 };
+constexpr int kGradWaves = 8, kAcross = 2, kAlong = kGradWaves / kAcross, kGradThreads = 64 * kGradWaves;
 template <int RB>
 struct GradSize {
-  static constexpr int CB = RB == 8 ? 4 : 8, C = 16 * CB;  // 32 blocks of 16 x 16 at the most
+  static constexpr int CB = RB == 8 ? 4 : 8, C = 16 * CB;  // a wave's: 32 blocks of 16 x 16 at the most
+  static constexpr int BLOCKS = CB * RB, ROUND = BLOCKS < 8 ? BLOCKS : 8;
 };
 __device__ __forceinline__ int64_t grad_len(const GradArgs& a, int64_t tiles) {
   return max(((int64_t)(a.tiles[0] + a.tiles[1]) * tiles + a.groups - 1) / a.groups, (int64_t)2);
@@ -715,9 +720,12 @@ __device__ __forceinline__ int64_t grad_len(const GradArgs& a, int64_t tiles) {
 template <int RB, int PARTS, bool LA>
 __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_t c0, int64_t tile, int64_t from, int64_t rows,
                                          float* out, int64_t out_row) {
-  constexpr int CB = GradSize<RB>::CB, C = GradSize<RB>::C, PER = C / 8, LOADS = 32 * PER / 64, BLOCKS = CB * RB;
-  constexpr int ROUND = BLOCKS < 16 ? BLOCKS : 16, STEP = 32 * kWaves;
+  constexpr int CB = GradSize<RB>::CB, C = GradSize<RB>::C, PER = C / 8, LOADS = 32 * PER / 64;
+  constexpr int BLOCKS = GradSize<RB>::BLOCKS, ROUND = GradSize<RB>::ROUND, STEP = 32 * kAlong;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
+  const int along = wave / kAcross, across = wave % kAcross;
+  c0 += across * C;
+  out += across * C * (LA ? out_row : 1);
   f32x4 acc[CB][RB];
 #pragma unroll
   for (int c = 0; c < CB; c++)
@@ -725,19 +733,16 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     for (int b = 0; b < RB; b++) acc[c][b] = f32x4{};
   uint8_t* mine = lds + wave * 32 * C * 2;
   const int sub = lane / PER, p = lane % PER;
-  const bool in = c0 + 8 * p < a.cols[LA];
-  const uint16_t* z = a.z[LA] + c0 + 8 * p;
+  const uint16_t* z = a.z[LA] + (c0 + 8 * p < a.cols[LA] ? c0 + 8 * p : 0);  // columns past the last: dropped
   const u32x4* s = a.s[LA] + tile * PARTS * 2 * RB * 64 + lane;
   u32x4 zv[LOADS], sv[PARTS][RB];
-  auto index = [&](int64_t r0) {  // lane l: row r0 + l % 32 of the run
-    return r0 + (lane & 31) < rows ? (int)row_at(a.plan, from + r0 + (lane & 31)) : -1;
+  auto index = [&](int64_t r0) {  // lane l: row r0 + l % 32 of the run, or its last
+    return (int)row_at(a.plan, from + min(r0 + (lane & 31), rows - 1));
   };
   auto fetch_z = [&](int rows32) {
 #pragma unroll
     for (int l = 0; l < LOADS; l++) {
-      const int m = __shfl(rows32, l * (64 / PER) + sub, 64);
-      zv[l] = u32x4{};
-      if (m >= 0 && in) zv[l] = *reinterpret_cast<const u32x4*>(z + m * a.z_row[LA]);
+      zv[l] = *reinterpret_cast<const u32x4*>(z + __shfl(rows32, l * (64 / PER) + sub, 64) * a.z_row[LA]);
     }
   };
   auto fetch_s = [&](int64_t r0) {
@@ -747,7 +752,7 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
 #pragma unroll
       for (int b = 0; b < RB; b++) sv[h][b] = t[(h * 2 * RB + b) * 64];
   };
-  int64_t r0 = 32 * wave;
+  int64_t r0 = 32 * along;
   int ahead = index(r0);
   if (r0 < rows) {
     fetch_z(ahead);
@@ -755,6 +760,11 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
   }
   ahead = index(r0 + STEP);
   for (; r0 < rows; r0 += STEP) {
+    if (r0 + 32 > rows) {  // nothing of the last row again, which may hold what no zero of S takes away
+#pragma unroll
+      for (int l = 0; l < LOADS; l++)
+        if (r0 + l * (64 / PER) + sub >= rows) zv[l] = u32x4{};
+    }
 #pragma unroll
     for (int l = 0; l < LOADS; l++) {
       const int r = l * (64 / PER) + sub, f = C == 128 ? (r & 3) | (r >> 3 & 1) << 2 : (r >> 1 & 1) | (r >> 3 & 1) << 1;
@@ -796,11 +806,11 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     for (int k = 0; k < ROUND; k++) sums[wave][k][lane] = acc[(round + k) / RB][(round + k) % RB];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < ROUND / kWaves; k++) {
-      const int at = k * kWaves + wave, c = (round + at) / RB, b = (round + at) % RB;
-      f32x4 v = sums[0][at][lane];
+    for (int k = 0; k < ROUND / kAlong; k++) {
+      const int at = k * kAlong + along, c = (round + at) / RB, b = (round + at) % RB;
+      f32x4 v = sums[across][at][lane];
 #pragma unroll
-      for (int w = 1; w < kWaves; w++) v += sums[w][at][lane];
+      for (int w = 1; w < kAlong; w++) v += sums[w * kAcross + across][at][lane];
       const int col = 16 * c + (LA ? r16 : 4 * q), r = 16 * b + (LA ? 4 * q : r16);
       if (c0 + col < a.cols[LA] && r < a.R) *reinterpret_cast<f32x4*>(out + (LA ? col * out_row + r : r * out_row + col)) = v;
     }
@@ -808,9 +818,9 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
   __syncthreads();  // before the next run's rows
 }
 template <int RB, int PARTS>
-__global__ __launch_bounds__(kThreads, 2) void grad_kernel(const GradArgs a) {
-  constexpr int C = GradSize<RB>::C, ROUND = GradSize<RB>::CB * RB < 16 ? GradSize<RB>::CB * RB : 16;
-  __shared__ __align__(16) uint8_t lds[kWaves * (ROUND * 1024 > 64 * C ? ROUND * 1024 : 64 * C)];
+__global__ __launch_bounds__(kGradThreads, 1) void grad_kernel(const GradArgs a) {
+  constexpr int C = kAcross * GradSize<RB>::C, LINES = 64 * GradSize<RB>::C, SUMS = 1024 * GradSize<RB>::ROUND;
+  __shared__ __align__(16) uint8_t lds[kGradWaves * (LINES > SUMS ? LINES : SUMS)];
   const int64_t tiles = used_tiles(a.plan), len = grad_len(a, tiles);
   int64_t at = blockIdx.x * len;
   const int64_t end = min(at + len, (a.tiles[0] + a.tiles[1]) * tiles);
@@ -845,7 +855,7 @@ __global__ __launch_bounds__(kThreads) void grad_join_kernel(const GradArgs a) {
     last = (column * tiles + t1 - 1) / len;
     if (first == last || last >= a.groups) return;
   }
-  for (int id = threadIdx.x; id < C * a.R / 4; id += kThreads) {
+  for (int id = blockIdx.z * kThreads + threadIdx.x; id < C * a.R / 4; id += gridDim.z * kThreads) {
     // four of a row of the run's sums
     const int wide = (la ? a.R : C) / 4, row = id / wide, x = id % wide * 4, col = la ? row : x;
     if (c0 + col >= cols) continue;
@@ -929,8 +939,8 @@ void up(const Plan& plan, const void* w, const void* y0, int64_t y0_row, void* y
   }
 }
 
-constexpr int kGradGroups = 2 * kCus;
-int64_t grad_columns(int64_t R) { return rank_blocks(R) == 8 ? 64 : 128; }
+constexpr int kGradGroups = kCus;
+int64_t grad_columns(int64_t R) { return rank_blocks(R) == 8 ? 128 : 256; }
 
 }  // namespace
 
@@ -1040,20 +1050,22 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     a.part = runs;
     a.R = (int)c.R;
     a.groups = kGradGroups;
-    const dim3 grid((unsigned)kGradGroups), columns(a.tiles[0] + a.tiles[1], (unsigned)c.A);
+    const dim3 grid((unsigned)kGradGroups);
+    const int64_t joins = (int64_t)(a.tiles[0] + a.tiles[1]) * c.A, most = C * c.R / 4 / kThreads;
+    const dim3 columns(a.tiles[0] + a.tiles[1], (unsigned)c.A, (unsigned)std::max<int64_t>(1, std::min(most, 4 * kCus / joins)));
     auto go = [&](auto parts) {
       constexpr int P = decltype(parts)::value;
       switch (rank_blocks(c.R)) {
-        case 1: hipLaunchKernelGGL((grad_kernel<1, P>), grid, dim3(kThreads), 0, stream, a); break;
-        case 2: hipLaunchKernelGGL((grad_kernel<2, P>), grid, dim3(kThreads), 0, stream, a); break;
-        case 4: hipLaunchKernelGGL((grad_kernel<4, P>), grid, dim3(kThreads), 0, stream, a); break;
-        default: hipLaunchKernelGGL((grad_kernel<8, P>), grid, dim3(kThreads), 0, stream, a); break;
+        case 1: hipLaunchKernelGGL((grad_kernel<1, P>), grid, dim3(kGradThreads), 0, stream, a); break;
+        case 2: hipLaunchKernelGGL((grad_kernel<2, P>), grid, dim3(kGradThreads), 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((grad_kernel<4, P>), grid, dim3(kGradThreads), 0, stream, a); break;
+        default: hipLaunchKernelGGL((grad_kernel<8, P>), grid, dim3(kGradThreads), 0, stream, a); break;
       }
     };
     if (sum_parts(c.M) == 3) go(std::integral_constant<int, 3>());
     else go(std::integral_constant<int, 2>());
-    if (C == 64) hipLaunchKernelGGL(grad_join_kernel<64>, columns, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL(grad_join_kernel<128>, columns, dim3(kThreads), 0, stream, a);
+    if (C == 128) hipLaunchKernelGGL(grad_join_kernel<128>, columns, dim3(kThreads), 0, stream, a);
+    else hipLaunchKernelGGL(grad_join_kernel<256>, columns, dim3(kThreads), 0, stream, a);
   }
   return hipGetLastError();
 }
