@@ -13,7 +13,7 @@
 // Bound: memory (X, Y0 and Y pass once, 2 R flops a byte of them).  T and dT are held in fp32 and enter
 // the next product in two bf16 parts (two_parts), 16 digits: its rounding to one, 2^-9, would be
 // the largest error of an adapter's share, and the products are too small to hold the kernels.
-// The gradients' sums of few rows take three (kFewRows).
+// The gradients leave in fp32, and their sums take three parts, all 24 digits: with two they were 5e-6 off.
 //
 //   down:   T in pieces over K, the waves taking 64 of K in turn
 //   join:   T's pieces summed, T in the layouts of the products that it enters
@@ -32,6 +32,7 @@ namespace {
 constexpr int kTile = 64;     // rows of a tile
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
+constexpr int kParts = 3;     // of T and dT in the gradients' sums
 
 struct Plan {
   const int32_t *start, *tbase;  // [A + 2]: first position, first tile of each adapter; A: the rows without one
@@ -212,7 +213,7 @@ __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4& hi, u32x4& 
     lo[i] = __builtin_bit_cast(uint32_t, bf16x2_t{x.lo, y.lo});
   }
 }
-__device__ __forceinline__ void parts_of(const float (&v)[8], u32x4 (&w)[3]) {
+__device__ __forceinline__ void parts_of(const float (&v)[8], u32x4 (&w)[kParts]) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -220,7 +221,7 @@ __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4 (&w)[3]) {
     three_parts(v[2 * i], x);
     three_parts(v[2 * i + 1], y);
 #pragma unroll
-    for (int k = 0; k < 3; k++) w[k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{x[k], y[k]});
+    for (int k = 0; k < kParts; k++) w[k][i] = __builtin_bit_cast(uint32_t, bf16x2_t{x[k], y[k]});
   }
 }
 
@@ -237,7 +238,7 @@ struct JoinArgs {
   const float* alpha;        // [A] or null
   float* t;                  // [M, R] by row, or null
   u32x4 *rows, *cols;        // or null
-  int R, RB, RK, parts;      // R in 16s as grad takes them, in 32s as up does; parts of cols
+  int R, RB, RK;             // R in 16s as grad takes them, in 32s as up does
 };
 constexpr int kJoinThreads = 512;
 constexpr int join_pitch(int RK) { return 32 * RK + 4; }
@@ -286,24 +287,17 @@ __device__ __forceinline__ void join_half(const JoinArgs& a, int64_t index, int 
   }
   if (a.cols != nullptr) {
     const int n = 2 * a.RB * 64;
-    u32x4* to = a.cols + index * a.parts * n + half * a.RB * 64;
+    u32x4* to = a.cols + index * kParts * n + half * a.RB * 64;
     for (int id = threadIdx.x; id < a.RB * 64; id += THREADS) {
       const int lane = id & 63;
       const float* p = lds + 8 * (lane >> 4) * pitch + 16 * (id >> 6) + (lane & 15);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; i++) v[i] = p[i * pitch];
-      if (a.parts == 3) {
-        u32x4 w[3];
-        parts_of(v, w);
+      u32x4 w[kParts];
+      parts_of(v, w);
 #pragma unroll
-        for (int k = 0; k < 3; k++) to[k * n + id] = w[k];
-      } else {
-        u32x4 hi, lo;
-        parts_of(v, hi, lo);
-        to[id] = hi;
-        to[id + n] = lo;
-      }
+      for (int k = 0; k < kParts; k++) to[k * n + id] = w[k];
     }
   }
 }
@@ -717,7 +711,7 @@ __device__ __forceinline__ int64_t grad_len(const GradArgs& a, int64_t tiles) {
   return max(((int64_t)(a.tiles[0] + a.tiles[1]) * tiles + a.groups - 1) / a.groups, (int64_t)2);
 }
 
-template <int RB, int PARTS, bool LA>
+template <int RB, bool LA>
 __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_t c0, int64_t tile, int64_t from, int64_t rows,
                                          float* out, int64_t out_row) {
   constexpr int CB = GradSize<RB>::CB, C = GradSize<RB>::C, PER = C / 8, LOADS = 32 * PER / 64;
@@ -734,8 +728,8 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
   uint8_t* mine = lds + wave * 32 * C * 2;
   const int sub = lane / PER, p = lane % PER;
   const uint16_t* z = a.z[LA] + (c0 + 8 * p < a.cols[LA] ? c0 + 8 * p : 0);  // columns past the last: dropped
-  const u32x4* s = a.s[LA] + tile * PARTS * 2 * RB * 64 + lane;
-  u32x4 zv[LOADS], sv[PARTS][RB];
+  const u32x4* s = a.s[LA] + tile * kParts * 2 * RB * 64 + lane;
+  u32x4 zv[LOADS], sv[kParts][RB];
   auto index = [&](int64_t r0) {  // lane l: row r0 + l % 32 of the run, or its last
     return (int)row_at(a.plan, from + min(r0 + (lane & 31), rows - 1));
   };
@@ -746,9 +740,9 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     }
   };
   auto fetch_s = [&](int64_t r0) {
-    const u32x4* t = s + (r0 / kTile * PARTS * 2 + r0 / 32 % 2) * RB * 64;
+    const u32x4* t = s + (r0 / kTile * kParts * 2 + r0 / 32 % 2) * RB * 64;
 #pragma unroll
-    for (int h = 0; h < PARTS; h++)
+    for (int h = 0; h < kParts; h++)
 #pragma unroll
       for (int b = 0; b < RB; b++) sv[h][b] = t[(h * 2 * RB + b) * 64];
   };
@@ -789,7 +783,7 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
           (__attribute__((address_space(3))) bf16x4*)(block + 4 * C * 2)));
       const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-      for (int h = 0; h < PARTS; h++)
+      for (int h = 0; h < kParts; h++)
 #pragma unroll
         for (int b = 0; b < RB; b++) acc[c][b] = LA ? mfma16(sv[h][b], v, acc[c][b]) : mfma16(v, sv[h][b], acc[c][b]);
     }
@@ -817,7 +811,7 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
   }
   __syncthreads();  // before the next run's rows
 }
-template <int RB, int PARTS>
+template <int RB>
 __global__ __launch_bounds__(kGradThreads, 1) void grad_kernel(const GradArgs a) {
   constexpr int C = kAcross * GradSize<RB>::C, LINES = 64 * GradSize<RB>::C, SUMS = 1024 * GradSize<RB>::ROUND;
   __shared__ __align__(16) uint8_t lds[kGradWaves * (LINES > SUMS ? LINES : SUMS)];
@@ -836,8 +830,8 @@ __global__ __launch_bounds__(kGradThreads, 1) void grad_kernel(const GradArgs a)
     const bool la = column >= a.tiles[0], whole = tile <= t0 && stop >= t1;
     const int64_t c0 = (la ? column - a.tiles[0] : column) * C;
     float* part = a.part + (2 * (int64_t)blockIdx.x + (tile > t0 ? 0 : 1)) * C * a.R;
-    if (la) grad_run<RB, PARTS, true>(a, lds, c0, tile, from, rows, whole ? a.out[1] + (adapter * a.cols[1] + c0) * a.R : part, a.R);
-    else grad_run<RB, PARTS, false>(a, lds, c0, tile, from, rows, whole ? a.out[0] + adapter * a.R * a.cols[0] + c0 : part, whole ? a.cols[0] : C);
+    if (la) grad_run<RB, true>(a, lds, c0, tile, from, rows, whole ? a.out[1] + (adapter * a.cols[1] + c0) * a.R : part, a.R);
+    else grad_run<RB, false>(a, lds, c0, tile, from, rows, whole ? a.out[0] + adapter * a.R * a.cols[0] + c0 : part, whole ? a.cols[0] : C);
   }
 }
 
@@ -872,11 +866,7 @@ __global__ __launch_bounds__(kThreads) void grad_join_kernel(const GradArgs a) {
 
 int rank_blocks(int64_t R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 int rank_steps(int64_t R) { return (int)((R + 31) / 32); }
-// Parts of S in the gradients' sums.  Two hold it to 2^-16 of each element, 5e-6 of a sum of many rows; where
-// rows are few and one may be most of a sum, three hold all of it, at half as many products again.
-constexpr int64_t kFewRows = 1024;
-int sum_parts(int64_t M) { return M <= kFewRows ? 3 : 2; }
-size_t cols_bytes(int64_t M, int64_t A, int64_t R) { return (size_t)max_tiles(M, A) * sum_parts(M) * 2 * rank_blocks(R) * 1024; }
+size_t cols_bytes(int64_t M, int64_t A, int64_t R) { return (size_t)max_tiles(M, A) * kParts * 2 * rank_blocks(R) * 1024; }
 
 // The workgroups that the chip's 256 CUs hold at once, by their registers and LDS.
 constexpr int kCus = 256;
@@ -901,7 +891,6 @@ JoinArgs join_of(const Plan& plan, int64_t R, const float* alpha) {
   a.R = (int)R;
   a.RB = rank_blocks(R);
   a.RK = rank_steps(R);
-  a.parts = sum_parts(plan.M);
   return a;
 }
 void join(const JoinArgs& a, hipStream_t stream) {
@@ -1053,17 +1042,12 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     const dim3 grid((unsigned)kGradGroups);
     const int64_t joins = (int64_t)(a.tiles[0] + a.tiles[1]) * c.A, most = C * c.R / 4 / kThreads;
     const dim3 columns(a.tiles[0] + a.tiles[1], (unsigned)c.A, (unsigned)std::max<int64_t>(1, std::min(most, 4 * kCus / joins)));
-    auto go = [&](auto parts) {
-      constexpr int P = decltype(parts)::value;
-      switch (rank_blocks(c.R)) {
-        case 1: hipLaunchKernelGGL((grad_kernel<1, P>), grid, dim3(kGradThreads), 0, stream, a); break;
-        case 2: hipLaunchKernelGGL((grad_kernel<2, P>), grid, dim3(kGradThreads), 0, stream, a); break;
-        case 4: hipLaunchKernelGGL((grad_kernel<4, P>), grid, dim3(kGradThreads), 0, stream, a); break;
-        default: hipLaunchKernelGGL((grad_kernel<8, P>), grid, dim3(kGradThreads), 0, stream, a); break;
-      }
-    };
-    if (sum_parts(c.M) == 3) go(std::integral_constant<int, 3>());
-    else go(std::integral_constant<int, 2>());
+    switch (rank_blocks(c.R)) {
+      case 1: hipLaunchKernelGGL(grad_kernel<1>, grid, dim3(kGradThreads), 0, stream, a); break;
+      case 2: hipLaunchKernelGGL(grad_kernel<2>, grid, dim3(kGradThreads), 0, stream, a); break;
+      case 4: hipLaunchKernelGGL(grad_kernel<4>, grid, dim3(kGradThreads), 0, stream, a); break;
+      default: hipLaunchKernelGGL(grad_kernel<8>, grid, dim3(kGradThreads), 0, stream, a); break;
+    }
     if (C == 128) hipLaunchKernelGGL(grad_join_kernel<128>, columns, dim3(kThreads), 0, stream, a);
     else hipLaunchKernelGGL(grad_join_kernel<256>, columns, dim3(kThreads), 0, stream, a);
   }

@@ -64,8 +64,8 @@ def norm_backward(x, stats, w, b, scale, group, G, dy):
 
 
 # T enters the second product in two bf16 parts, the second rounded by half of its 2^-8 steps where the
-# first leaves up to 2^-7: 2^-16.  The gradients' sums take three up to FEW rows, which hold all of fp32's digits.
-PARTS, FEW = 2.0 ** -16, 1024
+# first leaves up to 2^-7: 2^-16.  The gradients' sums take three, which hold all of fp32's digits.
+PARTS = 2.0 ** -16
 
 
 def adapters_forward(x, la, lb, alpha, ids, y0):
@@ -97,7 +97,7 @@ def adapters_backward(x, la, lb, alpha, ids, t, dy, dx0):
         dx[m] += dt @ lb[a]
         bx[m] = (bt + (PARTS + 4 * (R + 32) * U) * (np.abs(dt) + bt)) @ np.abs(lb[a])
         dlb[a], dla[a] = dt.T @ x[m], s * (dy[m].T @ t[m])
-        off = 6 * n * U + (0 if len(x) <= FEW else PARTS)
+        off = 6 * n * U
         bb[a] = (bt + off * (np.abs(dt) + bt)).T @ np.abs(x[m])
         ba[a] = off * abs(s) * (np.abs(dy[m]).T @ np.abs(t[m]))
     return (dx, dla, dlb), (bx + U * (np.abs(dx) + bx), ba, bb)
