@@ -702,24 +702,27 @@ struct GradArgs {
   int R, groups;
 };
 constexpr int kGradWaves = 8, kAcross = 2, kAlong = kGradWaves / kAcross, kGradThreads = 64 * kGradWaves;
-template <int RB>
+// RB: R in 16s of a wave.  SPLIT: the waves across take half of R each (R > 64), not half of the columns.
+template <int RB, bool SPLIT>
 struct GradSize {
-  static constexpr int CB = RB == 8 ? 4 : 8, C = 16 * CB;  // a wave's: 32 blocks of 16 x 16 at the most
-  static constexpr int BLOCKS = CB * RB, ROUND = BLOCKS < 8 ? BLOCKS : 8;
+  static constexpr int CB = 8, C = 16 * CB, COLUMNS = SPLIT ? C : kAcross * C;  // a wave's, the workgroup's
+  static constexpr int BLOCKS = CB * RB, ROUND = 8;
 };
 __device__ __forceinline__ int64_t grad_len(const GradArgs& a, int64_t tiles) {
   return max(((int64_t)(a.tiles[0] + a.tiles[1]) * tiles + a.groups - 1) / a.groups, (int64_t)2);
 }
 
-template <int RB, bool LA>
+template <int RB, bool SPLIT, bool LA>
 __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_t c0, int64_t tile, int64_t from, int64_t rows,
                                          float* out, int64_t out_row) {
-  constexpr int CB = GradSize<RB>::CB, C = GradSize<RB>::C, PER = C / 8, LOADS = 32 * PER / 64;
-  constexpr int BLOCKS = GradSize<RB>::BLOCKS, ROUND = GradSize<RB>::ROUND, STEP = 32 * kAlong;
+  typedef GradSize<RB, SPLIT> Size;
+  constexpr int CB = Size::CB, C = Size::C, PER = C / 8, LOADS = 32 * PER / 64, BLOCKS = Size::BLOCKS, ROUND = Size::ROUND;
+  constexpr int STEP = 32 * kAlong, ALL = SPLIT ? kAcross * RB : RB;  // blocks of r of S
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
   const int along = wave / kAcross, across = wave % kAcross;
-  c0 += across * C;
-  out += across * C * (LA ? out_row : 1);
+  const int at0 = across * (SPLIT ? 16 * RB : C), r_end = a.R - (SPLIT ? at0 : 0);  // first r or column of the wave
+  if (!SPLIT) c0 += at0;
+  out += at0 * (LA != SPLIT ? out_row : 1);
   f32x4 acc[CB][RB];
 #pragma unroll
   for (int c = 0; c < CB; c++)
@@ -728,7 +731,7 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
   uint8_t* mine = lds + wave * 32 * C * 2;
   const int sub = lane / PER, p = lane % PER;
   const uint16_t* z = a.z[LA] + (c0 + 8 * p < a.cols[LA] ? c0 + 8 * p : 0);  // columns past the last: dropped
-  const u32x4* s = a.s[LA] + tile * kParts * 2 * RB * 64 + lane;
+  const u32x4* s = a.s[LA] + (tile * kParts * 2 * ALL + (SPLIT ? across * RB : 0)) * 64 + lane;
   u32x4 zv[LOADS], sv[kParts][RB];
   auto index = [&](int64_t r0) {  // lane l: row r0 + l % 32 of the run, or its last
     return (int)row_at(a.plan, from + min(r0 + (lane & 31), rows - 1));
@@ -740,11 +743,11 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     }
   };
   auto fetch_s = [&](int64_t r0) {
-    const u32x4* t = s + (r0 / kTile * kParts * 2 + r0 / 32 % 2) * RB * 64;
+    const u32x4* t = s + (r0 / kTile * kParts * 2 + r0 / 32 % 2) * ALL * 64;
 #pragma unroll
     for (int h = 0; h < kParts; h++)
 #pragma unroll
-      for (int b = 0; b < RB; b++) sv[h][b] = t[(h * 2 * RB + b) * 64];
+      for (int b = 0; b < RB; b++) sv[h][b] = t[(h * 2 * ALL + b) * 64];
   };
   int64_t r0 = 32 * along;
   int ahead = index(r0);
@@ -761,7 +764,7 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     }
 #pragma unroll
     for (int l = 0; l < LOADS; l++) {
-      const int r = l * (64 / PER) + sub, f = C == 128 ? (r & 3) | (r >> 3 & 1) << 2 : (r >> 1 & 1) | (r >> 3 & 1) << 1;
+      const int r = l * (64 / PER) + sub, f = (r & 3) | (r >> 3 & 1) << 2;
       *reinterpret_cast<u32x4*>(mine + r * C * 2 + ((((p >> 1) ^ f) << 1) | (p & 1)) * 16) = zv[l];
     }
     // the next rows' loads go out ahead of this step's products, those of S behind them, into the
@@ -771,7 +774,7 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     if (more) fetch_z(ahead);
     ahead = index(r0 + 2 * STEP);
     hold();
-    const int jr = (lane & 15) >> 2, f = C == 128 ? jr | (q & 1) << 2 : jr >> 1 | (q & 1) << 1;
+    const int jr = (lane & 15) >> 2, f = jr | (q & 1) << 2;
     const uint8_t* at = mine + (8 * q + jr) * C * 2 + (lane & 3) * 8;
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
@@ -806,14 +809,14 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
 #pragma unroll
       for (int w = 1; w < kAlong; w++) v += sums[w * kAcross + across][at][lane];
       const int col = 16 * c + (LA ? r16 : 4 * q), r = 16 * b + (LA ? 4 * q : r16);
-      if (c0 + col < a.cols[LA] && r < a.R) *reinterpret_cast<f32x4*>(out + (LA ? col * out_row + r : r * out_row + col)) = v;
+      if (c0 + col < a.cols[LA] && r < r_end) *reinterpret_cast<f32x4*>(out + (LA ? col * out_row + r : r * out_row + col)) = v;
     }
   }
   __syncthreads();  // before the next run's rows
 }
-template <int RB>
+template <int RB, bool SPLIT>
 __global__ __launch_bounds__(kGradThreads, 1) void grad_kernel(const GradArgs a) {
-  constexpr int C = kAcross * GradSize<RB>::C, LINES = 64 * GradSize<RB>::C, SUMS = 1024 * GradSize<RB>::ROUND;
+  constexpr int C = GradSize<RB, SPLIT>::COLUMNS, LINES = 64 * GradSize<RB, SPLIT>::C, SUMS = 1024 * GradSize<RB, SPLIT>::ROUND;
   __shared__ __align__(16) uint8_t lds[kGradWaves * (LINES > SUMS ? LINES : SUMS)];
   const int64_t tiles = used_tiles(a.plan), len = grad_len(a, tiles);
   int64_t at = blockIdx.x * len;
@@ -830,8 +833,8 @@ __global__ __launch_bounds__(kGradThreads, 1) void grad_kernel(const GradArgs a)
     const bool la = column >= a.tiles[0], whole = tile <= t0 && stop >= t1;
     const int64_t c0 = (la ? column - a.tiles[0] : column) * C;
     float* part = a.part + (2 * (int64_t)blockIdx.x + (tile > t0 ? 0 : 1)) * C * a.R;
-    if (la) grad_run<RB, true>(a, lds, c0, tile, from, rows, whole ? a.out[1] + (adapter * a.cols[1] + c0) * a.R : part, a.R);
-    else grad_run<RB, false>(a, lds, c0, tile, from, rows, whole ? a.out[0] + adapter * a.R * a.cols[0] + c0 : part, whole ? a.cols[0] : C);
+    if (la) grad_run<RB, SPLIT, true>(a, lds, c0, tile, from, rows, whole ? a.out[1] + (adapter * a.cols[1] + c0) * a.R : part, a.R);
+    else grad_run<RB, SPLIT, false>(a, lds, c0, tile, from, rows, whole ? a.out[0] + adapter * a.R * a.cols[0] + c0 : part, whole ? a.cols[0] : C);
   }
 }
 
@@ -1043,10 +1046,10 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     const int64_t joins = (int64_t)(a.tiles[0] + a.tiles[1]) * c.A, most = C * c.R / 4 / kThreads;
     const dim3 columns(a.tiles[0] + a.tiles[1], (unsigned)c.A, (unsigned)std::max<int64_t>(1, std::min(most, 4 * kCus / joins)));
     switch (rank_blocks(c.R)) {
-      case 1: hipLaunchKernelGGL(grad_kernel<1>, grid, dim3(kGradThreads), 0, stream, a); break;
-      case 2: hipLaunchKernelGGL(grad_kernel<2>, grid, dim3(kGradThreads), 0, stream, a); break;
-      case 4: hipLaunchKernelGGL(grad_kernel<4>, grid, dim3(kGradThreads), 0, stream, a); break;
-      default: hipLaunchKernelGGL(grad_kernel<8>, grid, dim3(kGradThreads), 0, stream, a); break;
+      case 1: hipLaunchKernelGGL((grad_kernel<1, false>), grid, dim3(kGradThreads), 0, stream, a); break;
+      case 2: hipLaunchKernelGGL((grad_kernel<2, false>), grid, dim3(kGradThreads), 0, stream, a); break;
+      case 4: hipLaunchKernelGGL((grad_kernel<4, false>), grid, dim3(kGradThreads), 0, stream, a); break;
+      default: hipLaunchKernelGGL((grad_kernel<4, true>), grid, dim3(kGradThreads), 0, stream, a); break;
     }
     if (C == 128) hipLaunchKernelGGL(grad_join_kernel<128>, columns, dim3(kThreads), 0, stream, a);
     else hipLaunchKernelGGL(grad_join_kernel<256>, columns, dim3(kThreads), 0, stream, a);
