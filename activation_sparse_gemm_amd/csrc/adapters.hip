@@ -62,33 +62,42 @@ Plan plan_of(const void* p, int64_t M, int64_t A) {
 // ---------------------------------------------------------------- the plan
 
 // Every workgroup counts all rows (in LDS, whole numbers: no order) and then places the rows of its
-// own adapters in their order.
-__global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* ids, int64_t M, int A, int32_t* head, int4* tiles,
+// own adapters in their order, a thread four rows at a time.  Bound: the two passes' latency (32760 rows: 97 us
+// with 256 threads of a row each, 34 so).
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64, kPlanRows = 4;
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* ids, int64_t M, int A, int32_t* head, int4* tiles,
                                                         int32_t* order) {
   extern __shared__ int32_t lds[];
   int32_t* count = lds;           // [A + 1], then the first positions
   int32_t* first = lds + A + 1;   // [A + 2] first tiles
-  __shared__ int32_t wave_sum[kWaves][2];
+  __shared__ int32_t wave_sum[2][kPlanWaves][2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int a = threadIdx.x; a <= A; a += kThreads) count[a] = 0;
+  for (int a = threadIdx.x; a <= A; a += kPlanThreads) count[a] = 0;
   __syncthreads();
   auto key = [&](int64_t m) {
     const int a = ids[m];
     return a < 0 || a >= A ? A : a;
   };
-  for (int64_t m0 = 0; m0 < M; m0 += kThreads) {
-    const int64_t m = m0 + threadIdx.x;
-    const int k = m < M ? key(m) : -1;
-    // one count for a wave of one adapter
-    const int k0 = __builtin_amdgcn_readfirstlane(k);
-    const uint64_t same = __ballot(k == k0);
-    if (k0 >= 0 && lane == 0) atomicAdd(&count[k0], __popcll(same));
-    if (k >= 0 && k != k0) atomicAdd(&count[k], 1);
+  for (int64_t m0 = 0; m0 < M; m0 += kPlanThreads * kPlanRows) {
+    int of[kPlanRows];
+#pragma unroll
+    for (int i = 0; i < kPlanRows; i++) {
+      const int64_t m = m0 + i * kPlanThreads + threadIdx.x;
+      of[i] = m < M ? key(m) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanRows; i++) {
+      // one count for a wave of one adapter
+      const int k0 = __builtin_amdgcn_readfirstlane(of[i]);
+      const uint64_t same = __ballot(of[i] == k0);
+      if (k0 >= 0 && lane == 0) atomicAdd(&count[k0], __popcll(same));
+      if (of[i] >= 0 && of[i] != k0) atomicAdd(&count[of[i]], 1);
+    }
   }
   __syncthreads();
-  // first positions and tiles: sums over the adapters before, kThreads at a time
+  // first positions and tiles: sums over the adapters before, kPlanThreads at a time
   int32_t rows_before = 0, tiles_before = 0;
-  for (int a0 = 0; a0 <= A; a0 += kThreads) {
+  for (int a0 = 0; a0 <= A; a0 += kPlanThreads) {
     const int a = a0 + threadIdx.x;
     const int n = a <= A ? count[a] : 0, t = (n + kTile - 1) / kTile;
     int sn = n, st = t;  // inclusive sums over the wave
@@ -101,26 +110,26 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* ids, int6
       }
     }
     if (lane == 63) {
-      wave_sum[wave][0] = sn;
-      wave_sum[wave][1] = st;
+      wave_sum[0][wave][0] = sn;
+      wave_sum[0][wave][1] = st;
     }
     __syncthreads();
     for (int w = 0; w < wave; w++) {
-      sn += wave_sum[w][0];
-      st += wave_sum[w][1];
+      sn += wave_sum[0][w][0];
+      st += wave_sum[0][w][1];
     }
     if (a <= A) {
       count[a] = rows_before + sn - n;
       first[a] = tiles_before + st - t;
     }
-    for (int w = 0; w < kWaves; w++) {
-      rows_before += wave_sum[w][0];
-      tiles_before += wave_sum[w][1];
+    for (int w = 0; w < kPlanWaves; w++) {
+      rows_before += wave_sum[0][w][0];
+      tiles_before += wave_sum[0][w][1];
     }
     __syncthreads();
   }
   if (blockIdx.x == 0) {
-    for (int a = threadIdx.x; a <= A; a += kThreads) {
+    for (int a = threadIdx.x; a <= A; a += kPlanThreads) {
       head[4 + a] = count[a];
       head[4 + A + 2 + a] = first[a];
     }
@@ -134,24 +143,40 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* ids, int6
   for (int a = blockIdx.x; a <= A; a += gridDim.x) {
     const int from = count[a], n = (a < A ? count[a + 1] : (int32_t)M) - from;
     if (n <= 0) continue;
-    for (int t = threadIdx.x; t * kTile < n; t += kThreads) tiles[first[a] + t] = make_int4(a, from + t * kTile, min(kTile, n - t * kTile), 0);
+    for (int t = threadIdx.x; t * kTile < n; t += kPlanThreads) tiles[first[a] + t] = make_int4(a, from + t * kTile, min(kTile, n - t * kTile), 0);
     int32_t at = from;
-    for (int64_t m0 = 0; m0 < M && at < from + n; m0 += kThreads) {  // at: the same in all threads
-      const int64_t m = m0 + threadIdx.x;
-      const bool mine = m < M && key(m) == a;
-      const uint64_t which = __ballot(mine);
-      if (lane == 0) wave_sum[wave][0] = __popcll(which);
-      __syncthreads();
-      int before = 0, all = 0;
-      for (int w = 0; w < kWaves; w++) {
-        if (w < wave) before += wave_sum[w][0];
-        all += wave_sum[w][0];
+    int turn = 0;
+    for (int64_t m0 = 0; m0 < M && at < from + n; m0 += kPlanThreads * kPlanRows) {  // at: the same in all threads
+      const int64_t m = m0 + threadIdx.x * kPlanRows;
+      bool mine[kPlanRows];
+      int sum = 0;
+#pragma unroll
+      for (int i = 0; i < kPlanRows; i++) {
+        mine[i] = m + i < M && key(m + i) == a;
+        sum += mine[i];
       }
-      const int to = at + before + __popcll(which & ((1ull << lane) - 1));
-      if (mine && to < from + n) order[to] = (int32_t)m;
-      at += all;
+      int to = sum;  // inclusive sum over the wave
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(to, o, 64);
+        if (lane >= o) to += up;
+      }
+      if (lane == 63) wave_sum[turn][wave][0] = to;
       __syncthreads();
+      to += at - sum;
+      for (int w = 0; w < kPlanWaves; w++) {
+        const int of_wave = wave_sum[turn][w][0];
+        if (w < wave) to += of_wave;
+        at += of_wave;
+      }
+      turn ^= 1;  // two sets: the next sums are written while a wave may still read these
+#pragma unroll
+      for (int i = 0; i < kPlanRows; i++) {
+        if (mine[i] && to < from + n) order[to] = (int32_t)(m + i);
+        to += mine[i];
+      }
     }
+    __syncthreads();
   }
 }
 
@@ -945,7 +970,7 @@ hipError_t launch_adapters_plan(const int32_t* ids, int64_t M, int64_t A, void* 
   size_t tiles, order;
   plan_words(M, A, &tiles, &order);
   int32_t* w = (int32_t*)plan;
-  hipLaunchKernelGGL(plan_kernel, dim3((unsigned)(A + 1)), dim3(kThreads), (size_t)(2 * A + 3) * 4, stream, ids, M, (int)A, w,
+  hipLaunchKernelGGL(plan_kernel, dim3((unsigned)(A + 1)), dim3(kPlanThreads), (size_t)(2 * A + 3) * 4, stream, ids, M, (int)A, w,
                      (int4*)(w + tiles), w + order);
   return hipGetLastError();
 }
