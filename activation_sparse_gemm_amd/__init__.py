@@ -897,8 +897,8 @@ def rtl_adamw(tensors: AdamWTensors, step, lr, beta1: float = 0.9, beta2: float 
     m += (1 - beta1) (g - m), v = beta2 v + (1 - beta2) g^2, and the parameters (their masters, where bf16) less
     lr (m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps) + weight_decay p).
 
-    ``step`` counts from 1.  ``step`` (int64), ``lr`` and ``grad_scale`` (float32; a factor of the gradients) may be tensors of
-    one element on the GPU, which a captured call reads anew with every replay."""
+    ``step`` counts from 1.  ``step`` (int64) and ``lr`` (float32) may be tensors of one element on the GPU, which a captured
+    call reads anew with every replay; so is ``grad_scale`` (float32, None: 1), a factor of the gradients."""
     like = tensors.like
     there = _elsewhere(like)
     if there is not None:
@@ -906,7 +906,9 @@ def rtl_adamw(tensors: AdamWTensors, step, lr, beta1: float = 0.9, beta2: float 
             return rtl_adamw(tensors, step, lr, beta1, beta2, eps, weight_decay, grad_scale, stream)
     step, step_at = _number("step", step, torch.int64, like)
     lr, lr_at = _number("lr", lr, torch.float32, like)
-    scale_at = None if grad_scale is None else _number("grad_scale", torch.as_tensor(grad_scale), torch.float32, like)[1]
+    if grad_scale is not None and not isinstance(grad_scale, torch.Tensor):
+        raise ValueError("grad_scale must be a tensor on the GPU")
+    scale_at = None if grad_scale is None else _number("grad_scale", grad_scale, torch.float32, like)[1]
     _check(lib.rtl_adamw(tensors.p_dt, tensors.g_dt, tensors.states, len(tensors.array), tensors.array, step, step_at, lr,
                          lr_at, beta1, beta2, eps, weight_decay, scale_at, _queue(stream, like)))
     _changed(tensors.changed)

@@ -6,22 +6,27 @@ method step 2: L_A and L_B are trained so that X (L_A L_B)^T reproduces the resi
 sparsification leaves, i.e. they minimise ||X W^T - S(X) W^T - X (L_A L_B)^T||^2 over the
 calibration activations X (the page reports convergence in 2k steps of training).  That
 objective is a reduced-rank regression of the residual E = X W^T - S(X) W^T on X, whose
-minimiser has a closed form, computed here instead of running gradient steps:
+minimiser has a closed form (fit_lowrank):
 
     C = (X^T X)^-1 X^T E          least-squares coefficients, K x N
     X C = U S V^T                 SVD of the fitted residual
     L_A = V_R,  L_B = (C V_R)^T   so that L_A L_B = V_R V_R^T C^T  (rank R)
 
+train_lowrank takes the page's way, gradient steps on batches of rows, for calibration sets
+whose X^T X or residual is not to be had in one piece.
+
 Every layer output used here (dense, norm-compensated sparse, and the full layer) comes
-from the library's kernels; the fit itself is host-side linear algebra in float64.
+from the library's kernels, as do the gradients and steps of train_lowrank; the closed-form
+fit is host-side linear algebra in float64.
 """
 from __future__ import annotations
 
 import torch
 
-from . import EPS, rtl_linear_dense_ref, rtl_linear_fused
+from . import (EPS, rtl_adamw, rtl_adamw_tensors, rtl_adapters, rtl_adapters_backward, rtl_adapters_plan, rtl_linear_dense_ref,
+               rtl_linear_fused)
 
-__all__ = ["fit_lowrank", "residual", "ablation"]
+__all__ = ["fit_lowrank", "train_lowrank", "lowrank_gradient", "residual", "ablation"]
 
 
 def fit_lowrank(X: torch.Tensor, E: torch.Tensor, R: int, ridge: float = 0.0):
@@ -42,6 +47,48 @@ def fit_lowrank(X: torch.Tensor, E: torch.Tensor, R: int, ridge: float = 0.0):
     _, _, Vh = torch.linalg.svd(X @ C, full_matrices=False)
     V = Vh[:R].T.contiguous()
     return V, (C @ V).T.contiguous()
+
+
+def lowrank_gradient(X: torch.Tensor, E: torch.Tensor, LA: torch.Tensor, LB: torch.Tensor, plan=None, dLA=None, dLB=None):
+    """(dLA, dLB): half the gradient of ||E - X (L_A L_B)^T||_F^2 in float32, for bf16 X [M,K], E [M,N], LA [N,R] and
+    LB [R,K]; the difference X (L_A L_B)^T - E that it starts from is rounded to bf16.  `plan`: of M rows with adapter
+    0."""
+    if plan is None:
+        plan = rtl_adapters_plan(torch.zeros((X.shape[0],), dtype=torch.int32, device=X.device), 1)
+    T = torch.empty((X.shape[0], LB.shape[0]), dtype=torch.float32, device=X.device)
+    off = rtl_adapters(X, LA[None], LB[None], plan, Y0=-E, T=T)
+    _, dLA, dLB = rtl_adapters_backward(X, LA[None], LB[None], plan, T, off, need_dx=False,
+                                        dLA=None if dLA is None else dLA[None], dLB=None if dLB is None else dLB[None])
+    return dLA[0], dLB[0]
+
+
+def train_lowrank(X: torch.Tensor, E: torch.Tensor, R: int, steps: int = 2000, rows: int = 4096, lr: float = 1e-3,
+                  LA=None, LB=None, seed: int = 0):
+    """Rank-R factors (L_A [N,R], L_B [R,K], float32) after `steps` AdamW steps (no decay) on the mean of
+    (E - X (L_A L_B)^T)^2 over batches of `rows` rows of X [M,K] and E [M,N] (bf16 on the GPU), one
+    batch after another.  They start from L_A = 0 and a random L_B, or from those given."""
+    if X.dim() != 2 or E.dim() != 2 or X.shape[0] != E.shape[0] or X.dtype != torch.bfloat16 or E.dtype != torch.bfloat16:
+        raise ValueError("X and E are [M,K] and [M,N] in bf16")
+    M, K, N = X.shape[0], X.shape[1], E.shape[1]
+    if not 0 < R <= min(K, N) or rows < 1 or steps < 0:
+        raise ValueError(f"rank {R} outside 1..{min(K, N)}, or no rows, or fewer than no steps")
+    if (LA is None) != (LB is None):
+        raise ValueError("L_A and L_B go together")
+    rows = min(rows, M)
+    if LA is None:
+        LA = torch.zeros((N, R), device=X.device)
+        LB = torch.randn((R, K), generator=torch.Generator(device=X.device).manual_seed(seed), device=X.device) * K ** -0.5
+    masters = [LA.to(torch.float32).clone(), LB.to(torch.float32).clone()]
+    params = [t.to(torch.bfloat16) for t in masters]
+    grads, m, v = ([torch.zeros_like(t) for t in masters] for _ in range(3))
+    tensors = rtl_adamw_tensors(params, grads, m, v, masters=masters)
+    plan = rtl_adapters_plan(torch.zeros((rows,), dtype=torch.int32, device=X.device), 1)
+    scale = torch.full((1,), 2.0 / (rows * N), dtype=torch.float32, device=X.device)
+    for step in range(steps):
+        at = step * rows % (M - rows + 1)
+        lowrank_gradient(X[at:at + rows], E[at:at + rows], *params, plan, *grads)
+        rtl_adamw(tensors, step + 1, lr, weight_decay=0.0, grad_scale=scale)
+    return masters[0], masters[1]
 
 
 def residual(X: torch.Tensor, W: torch.Tensor) -> torch.Tensor:

@@ -8,8 +8,9 @@ layers is too large for the rank-64 branch, so FLUX keeps the attention output p
 and MLP-down of its single-stream blocks dense and Z-Image keeps the attention output
 projection and MLP-up dense; every other layer uses the sparse layer.
 
-Beside the projections, what such a block runs on their outputs: the queries' and keys' head norms
-and rotary positions (AttentionInput) and the gated feed-forward block (GatedMLP).
+Beside the projections, what such a block runs around them: the layer norm in front, with each request's scale
+and shift (AdaptiveNorm), the low-rank adapters of a batch's requests beside a projection (AdaptedLinear), the queries'
+and keys' head norms and rotary positions (AttentionInput) and the gated feed-forward block (GatedMLP).
 
 Reading taken where the page is silent: Qwen-Image's attention output projection, which the
 page does not list, stays dense; FLUX's double-stream blocks sparsify all four projections.
@@ -18,10 +19,12 @@ from __future__ import annotations
 
 import torch
 
-from . import (EPS, RTL_ACT_SILU, RTL_ROPE_ADJACENT, rtl_glu_fused, rtl_linear_dense_ref, rtl_linear_fused,
-               rtl_linear_fused_workspace_bytes, rtl_qk_norm_rope, _dt)
+from . import (EPS, RTL_ACT_SILU, RTL_ROPE_ADJACENT, rtl_adapters, rtl_adapters_backward, rtl_adapters_plan,
+               rtl_adapters_workspace_bytes, rtl_glu_fused, rtl_layer_norm, rtl_layer_norm_backward, rtl_linear_dense_ref,
+               rtl_linear_fused, rtl_linear_fused_workspace_bytes, rtl_qk_norm_rope, _dt)
 
-__all__ = ["LAYER_KINDS", "MODELS", "dense_layers", "is_sparse", "Linear", "build_block", "AttentionInput", "GatedMLP"]
+__all__ = ["LAYER_KINDS", "MODELS", "dense_layers", "is_sparse", "Linear", "build_block", "AdaptiveNorm", "AdaptedLinear",
+           "AttentionInput", "GatedMLP"]
 
 LAYER_KINDS = ("attn.qkv", "attn.o_proj", "mlp.up", "mlp.down")
 
@@ -92,6 +95,63 @@ def build_block(model: str, stream: str, weights: dict) -> dict:
         sp = is_sparse(model, stream, kind)
         out[kind] = Linear(W, LA if sp else None, LB if sp else None, sparse=sp)
     return out
+
+
+class AdaptiveNorm:
+    """The layer norm in front of a block's projections, with weights [D] (None: ones, zeros) and, a
+    call, each request's scale and shift."""
+
+    def __init__(self, weight=None, bias=None, eps: float = 1e-6):
+        if weight is not None and bias is not None and weight.shape != bias.shape:
+            raise ValueError("the weight and the bias have one length")
+        self.weight, self.bias, self.eps = weight, bias, eps
+
+    def __call__(self, X: torch.Tensor, scale=None, shift=None, groups=None, stats=None, Y=None, stream=None) -> torch.Tensor:
+        """Rows groups[g] .. groups[g + 1] - 1 of X [M,D] are request g's (rtl_layer_norm); `stats` [M,2] float32
+        receives what `backward` needs."""
+        return rtl_layer_norm(X, self.weight, self.bias, scale, shift, groups, self.eps, Y=Y, stats=stats, stream=stream)
+
+    def backward(self, X: torch.Tensor, stats: torch.Tensor, dY: torch.Tensor, scale=None, groups=None, stream=None):
+        """(dX, dweight, dbias, dscale, dshift) of rtl_layer_norm_backward."""
+        return rtl_layer_norm_backward(X, stats, dY, self.weight, self.bias, scale, groups, stream=stream)
+
+
+class AdaptedLinear:
+    """A projection that a batch's requests share, and beside it the low-rank adapters that they bring: Y = linear(X)
+    + alpha_a (X LB_a^T) LA_a^T, a row's adapter a of LA [A,N,R] and LB [A,R,K] (bf16) as its batch's plan says.  The
+    adapters add to the projection's output in place: rows without one are the projection's own, to the bit.  Like
+    Linear it keeps one workspace for a number of rows, so two streams need two objects."""
+
+    def __init__(self, linear: Linear, LA: torch.Tensor, LB: torch.Tensor, alpha=None):
+        N, K = linear.W.shape
+        if LA.dim() != 3 or LB.dim() != 3 or tuple(LA.shape) != (LB.shape[0], N, LB.shape[1]) or LB.shape[2] != K:
+            raise ValueError(f"LA and LB are [A,{N},R] and [A,R,{K}], got {tuple(LA.shape)} and {tuple(LB.shape)}")
+        if alpha is not None and tuple(alpha.shape) != (LA.shape[0],):
+            raise ValueError(f"alpha is [{LA.shape[0]}], got {tuple(alpha.shape)}")
+        self.linear, self.LA, self.LB, self.alpha = linear, LA, LB, alpha
+        self._ws = {}
+
+    def plan(self, ids: torch.Tensor, plan=None, stream=None) -> torch.Tensor:
+        """The plan of a batch whose row m has adapter ids[m] (int32; outside 0..A-1: none)."""
+        return rtl_adapters_plan(ids, self.LA.shape[0], plan, stream=stream)
+
+    def workspace(self, M: int):
+        if M not in self._ws:
+            A, N, R = self.LA.shape
+            need = rtl_adapters_workspace_bytes(M, N, self.LB.shape[2], R, A)
+            self._ws[M] = torch.empty((max(need, 1),), dtype=torch.uint8, device=self.LA.device)
+        return self._ws[M]
+
+    def __call__(self, X: torch.Tensor, plan: torch.Tensor, T=None, Y=None, stream=None) -> torch.Tensor:
+        """`T` [M,R] float32 receives what `backward` needs."""
+        Y = self.linear(X, Y=Y, stream=stream)
+        return rtl_adapters(X, self.LA, self.LB, plan, self.alpha, Y0=Y, Y=Y, T=T, workspace=self.workspace(X.shape[0]),
+                            stream=stream)
+
+    def backward(self, X: torch.Tensor, plan: torch.Tensor, T: torch.Tensor, dY: torch.Tensor, dX0=None, need_dx: bool = True,
+                 stream=None):
+        """(dX, dLA, dLB) of rtl_adapters_backward; `dX0`: what came through the projection."""
+        return rtl_adapters_backward(X, self.LA, self.LB, plan, T, dY, self.alpha, dX0=dX0, need_dx=need_dx, stream=stream)
 
 
 class AttentionInput:

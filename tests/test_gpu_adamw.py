@@ -193,3 +193,12 @@ def test_autograd_sees_the_change():
     rtl.rtl_adamw(rtl.rtl_adamw_tensors([p], [t[0]], [t[1]], [t[2]]), step=1, lr=0.1)
     with pytest.raises(RuntimeError):
         y.backward()
+
+
+def test_gradient_factor_is_a_tensor_on_the_gpu():
+    t = Tensors((300,), F32, F32, False)
+    tensors = rtl.rtl_adamw_tensors(**t.dev)
+    for bad in (0.5, torch.tensor([0.5]), torch.tensor([0.5], device="cuda", dtype=torch.float64), torch.ones(2, device="cuda")):
+        with pytest.raises(ValueError):
+            rtl.rtl_adamw(tensors, step=1, grad_scale=bad, **HOW)
+    t.check()  # as they were
