@@ -781,7 +781,13 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     fetch_s(r0);
   }
   ahead = index(r0 + STEP);
+  // A lane's place in the wave's rows as it writes and as it reads them, made anew each step: kept, the sixteen
+  // addresses that come of them are more registers than there are, and what spills waits for the loads.
+  const int jr = (lane & 15) >> 2;
+  int put_at = (sub * C + ((p >> 1) ^ (sub & 3)) * 16 + (p & 1) * 8) * 2;
+  int get_at = (8 * q + jr) * C * 2 + ((jr | (q & 1) << 2) << 5) + (lane & 3) * 8;
   for (; r0 < rows; r0 += STEP) {
+    asm volatile("" : "+v"(put_at), "+v"(get_at));
     if (r0 + 32 > rows) {  // nothing of the last row again, which may hold what no zero of S takes away
 #pragma unroll
       for (int l = 0; l < LOADS; l++)
@@ -789,8 +795,7 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     }
 #pragma unroll
     for (int l = 0; l < LOADS; l++) {
-      const int r = l * (64 / PER) + sub, f = (r & 3) | (r >> 3 & 1) << 2;
-      *reinterpret_cast<u32x4*>(mine + r * C * 2 + ((((p >> 1) ^ f) << 1) | (p & 1)) * 16) = zv[l];
+      *reinterpret_cast<u32x4*>(mine + ((put_at ^ (l >> 1 & 1) << 7) + l * (64 / PER) * C * 2)) = zv[l];
     }
     // the next rows' loads go out ahead of this step's products, those of S behind them, into the
     // registers that the products have read
@@ -799,12 +804,10 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
     if (more) fetch_z(ahead);
     ahead = index(r0 + 2 * STEP);
     hold();
-    const int jr = (lane & 15) >> 2, f = jr | (q & 1) << 2;
-    const uint8_t* at = mine + (8 * q + jr) * C * 2 + (lane & 3) * 8;
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int c = 0; c < CB; c++) {
-      const uint8_t* block = at + ((c ^ f) << 5);
+      const uint8_t* block = mine + (get_at ^ c << 5);
       const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
           (__attribute__((address_space(3))) bf16x4*)block));
       const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
