@@ -52,8 +52,8 @@ struct Piece {
       for (int i = 0; i < 4; i++) v[i] = __uint_as_float(r[i]);
     }
   }
-  // PAST: by stores that bypass the caches.
-  template <bool PAST>
+  // Plain stores: hinted to leave the caches first they make the norm faster (32760 x 2560: 65 -> 55 us) and
+  // the product that reads its result slower (norm and a copy of 32760 x 5120: 241 -> 252 us).
   __device__ __forceinline__ static void store(void* p, int64_t at, const float (&v)[V]) {
     if constexpr (V == 1) {
       if constexpr (BF16) ((__bf16*)p)[at] = (__bf16)v[0];
@@ -68,9 +68,7 @@ struct Piece {
 #pragma unroll
         for (int i = 0; i < 4; i++) w[i] = __float_as_uint(v[i]);
       }
-      u32x4* to = reinterpret_cast<u32x4*>((uint8_t*)p + at * (BF16 ? 2 : 4));
-      if constexpr (PAST) __builtin_nontemporal_store(w, to);
-      else *to = w;
+      *reinterpret_cast<u32x4*>((uint8_t*)p + at * (BF16 ? 2 : 4)) = w;
     }
   }
 };
@@ -128,8 +126,8 @@ dim3 norm_grid(int64_t blocks) {
 __device__ __forceinline__ int64_t norm_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
 // Forward: W waves a row, J pieces a lane.
-template <bool BF16, int V, int W, int J, bool PAST>
-__global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormArgs a) {
+template <bool BF16, int V, int W, int J>
+__global__ __launch_bounds__(W == 1 ? kNormThreads : W * 64) void norm_kernel(const NormArgs a) {
   typedef Piece<BF16, V> P;
   __shared__ float sums[W > 1 ? 3 : 1][W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = W > 1 ? wave : 0;
@@ -230,7 +228,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormArgs a) {
 #pragma unroll
       for (int i = 0; i < V; i++) v[i] = fmaf(v[i], 1.f + u[i], h[i]);
     }
-    P::template store<PAST>(a.y, row * a.y_row + at, v);
+    P::store(a.y, row * a.y_row + at, v);
   }
 }
 
@@ -366,7 +364,7 @@ __global__ __launch_bounds__(W == 1 ? kNormThreads : W * 64) void norm_back_kern
         const float n = (v[i] - it.mean) * it.r;
         v[i] = it.r * fmaf(-n, c1, fmaf(d[i], up[j][i], -c0));
       }
-      P::template store<true>(a.y, row * a.y_row + at, v);
+      P::store(a.y, row * a.y_row + at, v);
     }
   };
   Row one, two;
@@ -546,8 +544,11 @@ NormArgs norm_args(const NormCall& c) {
   return a;
 }
 
-// Rows that take a wave each from here on; fewer spread over four waves, for their latency.
-constexpr int64_t kNormWaveRows = 1024;
+// A row takes a wave of its own where there are many (from kNormWaveRows on) and it is no wider than kNormWavePieces
+// pieces a lane: no wait for other waves.  Few rows take four waves each for their latency, wide ones for
+// the rows in flight.  bf16, us with one wave and with four: 512 rows of 5120 7.0 and 4.8; 4096 of 512 4.0 and
+// 6.7, of 5120 21.7 and 17.7; 32760 of 1024 24 and 40, of 2560 65 and 76, of 4096 102 and 98, of 5120 134 and 122.
+constexpr int64_t kNormWaveRows = 1024, kNormWavePieces = 6;
 
 template <bool BF16>
 void norm_forward(const NormCall& c, hipStream_t stream) {
@@ -555,14 +556,15 @@ void norm_forward(const NormCall& c, hipStream_t stream) {
   const NormArgs a = norm_args(c);
   auto go = [&](auto v, auto w, auto j) {
     constexpr int VV = decltype(v)::value, W = decltype(w)::value, J = decltype(j)::value;
-    hipLaunchKernelGGL((norm_kernel<BF16, VV, W, J, false>), norm_grid(W > 1 ? c.M : (c.M + 3) / 4), dim3(kNormThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_kernel<BF16, VV, W, J>), norm_grid(W > 1 ? c.M : (c.M + 3) / 4), dim3(W == 1 ? kNormThreads : W * 64), 0, stream, a);
   };
   if (!norm_wide(c)) {
-    pick<1, 2, 4, 8, 16, 32>((c.D + 255) / 256, [&](auto j) { go(Int<1>(), Int<4>(), j); });
+    if (c.D <= 2048) pick<1, 2, 4, 8>((c.D + 255) / 256, [&](auto j) { go(Int<1>(), Int<4>(), j); });
+    else pick<4, 8>((c.D + 1023) / 1024, [&](auto j) { go(Int<1>(), Int<16>(), j); });
     return;
   }
   const int64_t pieces = c.D / V, one = (pieces + 63) / 64;
-  if (c.M >= kNormWaveRows && one <= 16) pick<1, 2, 3, 4, 6, 8, 10, 12, 16>(one, [&](auto j) { go(Int<V>(), Int<1>(), j); });
+  if (c.M >= kNormWaveRows && one <= kNormWavePieces) pick<1, 2, 3, 4, 6>(one, [&](auto j) { go(Int<V>(), Int<1>(), j); });
   else pick<1, 2, 3, 4, 6, 8, 12, 16>((pieces + 255) / 256, [&](auto j) { go(Int<V>(), Int<4>(), j); });
 }
 
