@@ -1,4 +1,4 @@
-// adamw.hip -- the AdamW step over many tensors in few launches, states in 32 or in 8 bits.
+// adamw.h -- the AdamW step over many tensors in few launches, states in 32 or in 8 bits.
 //
 //   g' = g gs,  m += (1 - b1) (g' - m),  v = b2 v + (1 - b2) g'^2
 //   p -= lr ((m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps) + decay p)
@@ -13,6 +13,7 @@
 // Bound: memory (28 bytes an element with 32-bit states, 16 with 8-bit ones, 2 less where parameters or
 // gradients are bf16 beside fp32 masters).  A launch takes up to kAdamTensors tensors, their addresses in
 // its arguments, so that nothing is copied to the device first and a captured call holds them.
+#pragma once
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -20,7 +21,7 @@
 
 namespace rtl {
 
-namespace {
+namespace adam {
 
 constexpr int kAdamThreads = 256;
 constexpr int kAdamTensors = 56;  // of 64 bytes: the arguments stay below 4 KB
@@ -254,10 +255,11 @@ hipError_t adamw_launch(const AdamTensor* t, int64_t count, const AdamRates& r, 
   return go();
 }
 
-}  // namespace
+}  // namespace adam
 
 hipError_t launch_adamw(bool p_bf16, bool g_bf16, bool eight, const AdamTensor* t, int64_t count, const AdamRates& r,
                         hipStream_t stream) {
+  using namespace adam;
   static_assert(kAdamMaxN <= (int64_t)kAdamMaxBlocks * kAdamChunk, "a tensor fits one launch");
   if (p_bf16)
     return g_bf16 ? (eight ? adamw_launch<true, true, true>(t, count, r, stream) : adamw_launch<true, true, false>(t, count, r, stream))

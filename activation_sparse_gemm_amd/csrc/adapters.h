@@ -1,4 +1,4 @@
-// adapters.hip -- low-rank adapters of many requests beside a shared projection, and their gradient.
+// adapters.h -- low-rank adapters of many requests beside a shared projection, and their gradient.
 // Row m of a batch belongs to a request whose adapter a (or none) has factors L_B[a] [R, K] and L_A[a]
 // [N, R] and a factor alpha[a]:
 //
@@ -20,6 +20,7 @@
 //   up:     Y0 + T L_A^T, strips of 64 columns a wave
 //   turn:   factors transposed, which makes dT a `down` and dX an `up`
 //   grad:   dL_B and dL_A, tiles of 256 (128) columns by R over runs of an adapter's rows
+#pragma once
 #include <algorithm>
 #include <type_traits>
 
@@ -27,7 +28,7 @@
 
 namespace rtl {
 
-namespace {
+namespace lora {
 
 constexpr int kTile = 64;     // rows of a tile
 constexpr int kThreads = 256;
@@ -977,14 +978,16 @@ void up(const Plan& plan, const void* w, const void* y0, int64_t y0_row, void* y
 constexpr int kGradGroups = kCus;
 int64_t grad_columns(int64_t R) { return rank_blocks(R) == 8 ? 128 : 256; }
 
-}  // namespace
+}  // namespace lora
 
 size_t adapters_plan_bytes(int64_t M, int64_t A) {
+  using namespace lora;
   size_t tiles, order;
   return plan_words(M, A, &tiles, &order) * 4;
 }
 
 hipError_t launch_adapters_plan(const int32_t* ids, int64_t M, int64_t A, void* plan, hipStream_t stream) {
+  using namespace lora;
   size_t tiles, order;
   plan_words(M, A, &tiles, &order);
   int32_t* w = (int32_t*)plan;
@@ -995,11 +998,13 @@ hipError_t launch_adapters_plan(const int32_t* ids, int64_t M, int64_t A, void* 
 
 // Workspace: down's pieces | up's operands.
 size_t adapters_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
+  using namespace lora;
   return part_bytes(M, A, R, K) + align(rows_bytes(M, A, R));
 }
 
 hipError_t launch_adapters(const AdapterCall& c, const void* y0, int64_t y0_row, void* y, int64_t y_row, float* t, void* ws,
                            hipStream_t stream) {
+  using namespace lora;
   const Plan plan = plan_of(c.plan, c.M, c.A);
   float* part = (float*)ws;
   down(plan, c.x, c.x_row, c.LB, c.K, c.R, part, stream);
@@ -1015,6 +1020,7 @@ hipError_t launch_adapters(const AdapterCall& c, const void* y0, int64_t y0_row,
 
 // Workspace of the gradient: L_A^T, L_B^T | down's pieces | dT as up's operand | dT and T as grad's | grad's runs.
 size_t adapters_back_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t A) {
+  using namespace lora;
   return align((size_t)A * N * R * 2) + align((size_t)A * K * R * 2) + part_bytes(M, A, R, N) + align(rows_bytes(M, A, R)) + 2 * align(cols_bytes(M, A, R)) +
          align((size_t)2 * kGradGroups * grad_columns(R) * R * 4);
 }
@@ -1022,6 +1028,7 @@ size_t adapters_back_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64
 hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void* dy, int64_t dy_row, const void* dx0,
                                 int64_t dx0_row, void* dx, int64_t dx_row, float* dla, float* dlb, void* ws,
                                 hipStream_t stream) {
+  using namespace lora;
   const Plan plan = plan_of(c.plan, c.M, c.A);
   uint8_t* at = (uint8_t*)ws;
   auto take = [&](size_t bytes) {

@@ -18,6 +18,9 @@
 //                    compressed operand straight to registers one K step ahead; the
 //                    epilogue scales by sw and s sx, then adds the rank-R slice
 //                    T L_A^T before the single store of Y.
+//
+// The AdamW step, whose 8-bit states are E4M3 codes too, is compiled in this unit.
+#include "adamw.h"
 #include "fp8_common.h"
 #include "lora_lds.h"
 

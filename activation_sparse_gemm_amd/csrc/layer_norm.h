@@ -1,4 +1,4 @@
-// layer_norm.hip -- layer norm of every row with the weights of the layer and the scale and shift of
+// layer_norm.h -- layer norm of every row with the weights of the layer and the scale and shift of
 // the row's request, and its gradient with the sums over rows that the weights', the scales' and
 // the shifts' gradients are.
 //
@@ -14,6 +14,7 @@
 // A row is held in the registers of W waves, so that it is read once for mean, squares and result.
 // Groups are ascending offsets in device memory: a row finds its group there, and rows outside
 // every group are left as they were.  Whatever the offsets hold, no access leaves the arrays.
+#pragma once
 #include <algorithm>
 #include <type_traits>
 
@@ -22,7 +23,7 @@
 
 namespace rtl {
 
-namespace {
+namespace norm {
 
 // V elements of a row: 16 bytes, or one element where rows are not 16-byte aligned.
 template <bool BF16, int V>
@@ -605,14 +606,19 @@ size_t norm_part_bytes(int64_t M, int64_t D, int64_t G) {
   return (((size_t)((M + rows - 1) / rows + std::max<int64_t>(G, 1)) * 2 * D * 4) + 255) & ~(size_t)255;
 }
 
-}  // namespace
+}  // namespace norm
 
 bool norm_fits(int dt, int64_t D, bool wide) {
+  using namespace norm;
   return wide ? D <= (dt == kDtBF16 ? kNormMaxD : kNormMaxD / 2) : D <= kNormMaxDNarrow;
 }
-bool norm_is_wide(const NormCall& c) { return norm_wide(c); }
+bool norm_is_wide(const NormCall& c) {
+  using namespace norm;
+  return norm_wide(c);
+}
 
 hipError_t launch_norm(const NormCall& c, hipStream_t stream) {
+  using namespace norm;
   if (c.dt == kDtBF16) norm_forward<true>(c, stream);
   else norm_forward<false>(c, stream);
   return hipGetLastError();
@@ -620,11 +626,13 @@ hipError_t launch_norm(const NormCall& c, hipStream_t stream) {
 
 // Workspace: the chunks' sums, then the groups'.
 size_t norm_back_workspace(int64_t M, int64_t D, int64_t G) {
+  using namespace norm;
   return norm_part_bytes(M, D, G) + (size_t)std::max<int64_t>(G, 1) * 2 * D * 8;
 }
 
 hipError_t launch_norm_back(const NormCall& c, float* dw, float* db, float* dscale, float* dshift, void* ws,
                             hipStream_t stream) {
+  using namespace norm;
   NormArgs a = norm_args(c);
   a.rows = norm_chunk(c.M);
   const bool sums = dw != nullptr || db != nullptr || dscale != nullptr || dshift != nullptr;

@@ -5,6 +5,9 @@
 // double precision), the 2-of-4 selection and s; for the pre-compressed variant it also
 // writes the kept values and their 2-bit positions in the register order of the sparse
 // MFMA's A operand.
+//
+// The low-rank adapters of many requests are compiled in this unit too.
+#include "adapters.h"
 #include "bf16_common.h"
 #include "fp8_common.h"
 

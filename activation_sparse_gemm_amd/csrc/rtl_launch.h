@@ -104,7 +104,7 @@ hipError_t launch_glu_back_bf16(int act, int64_t M, int64_t K, int64_t H, const 
                                 const void* Wu, const void* G, const void* U, const void* dY, void* dX, void* dWg,
                                 void* dWu, void* ws, hipStream_t stream);
 
-// Layer norm with weights and per-group scale and shift, and its gradient (layer_norm.hip).
+// Layer norm with weights and per-group scale and shift, and its gradient (layer_norm.h).
 struct RowsView {
   const void* p;  // rows of D contiguous elements
   int64_t row;    // stride in elements
@@ -128,7 +128,7 @@ size_t norm_back_workspace(int64_t M, int64_t D, int64_t G);
 hipError_t launch_norm_back(const NormCall& c, float* dw, float* db, float* dscale, float* dshift, void* ws,
                             hipStream_t stream);
 
-// Low-rank adapters of many requests and their gradient (adapters.hip).
+// Low-rank adapters of many requests and their gradient (adapters.h).
 struct AdapterCall {
   int64_t M, N, K, R, A;
   const void* x;
@@ -147,7 +147,7 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
                                 int64_t dx0_row, void* dx, int64_t dx_row, float* dla, float* dlb, void* ws,
                                 hipStream_t stream);
 
-// AdamW over many tensors (adamw.hip).
+// AdamW over many tensors (adamw.h).
 struct AdamTensor {
   void* p;               // parameters: fp32, or bf16 beside `master`
   const void* g;         // gradients

@@ -3,8 +3,9 @@
 // page, method step 1).  Memory-bound: one wave per row streams the row once.  The squared
 // norms are summed in double precision (no finite row underflows or overflows them).
 //
-// The other memory-bound row passes, rotary positions and the per-head norms of queries and
-// keys, are compiled in this unit too.
+// The other memory-bound row passes, rotary positions, the per-head norms of queries and keys
+// and the layer norm, are compiled in this unit too.
+#include "layer_norm.h"
 #include "qk_rope.h"
 #include "rtl_device.h"
 #include "rtl_launch.h"
