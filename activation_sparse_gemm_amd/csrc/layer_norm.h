@@ -10,7 +10,8 @@
 //     dshift_g = S0_g,  dscale_g = w S1_g + b S0_g,
 //     dw = sum_g (1 + scale_g) S1_g,  db = sum_g (1 + scale_g) S0_g
 //
-// Bound: memory (each element read once and written once; the gradient reads two and writes one).
+// Bound: memory (each element read once and written once; the gradient reads two and writes one).  32760 x 5120 in
+// bf16: forward 122 us, 5.5 TB/s; the gradient's pass 210, 5.0 with its chunks' sums, and 26 to join them.
 // A row is held in the registers of W waves, so that it is read once for mean, squares and result.
 // Groups are ascending offsets in device memory: a row finds its group there, and rows outside
 // every group are left as they were.  Whatever the offsets hold, no access leaves the arrays.
@@ -237,7 +238,8 @@ __global__ __launch_bounds__(W == 1 ? kNormThreads : W * 64) void norm_kernel(co
 // row's loads in flight while one is formed, and hold the sums of their columns; at the end of a
 // group in the chunk, and of the chunk, the sums go to slot chunk + group (rows in order raise one or the
 // other, so each pair has a slot of its own).  A sum in fp32 runs over at most kNormChunk rows; what follows is
-// in double.
+// in double.  Longer chunks halve the sums' bytes and end unevenly: 32760 x 5120 in chunks of 32 rows 209 + 21 us
+// (sums), of 64 301 + 11, of 16 216 + 39.
 constexpr int kNormChunk = 32;
 template <bool BF16, int V, int W, int J>
 __global__ __launch_bounds__(W == 1 ? kNormThreads : W * 64) void norm_back_kernel(const NormArgs a) {
