@@ -268,52 +268,62 @@ struct JoinArgs {
   int R, RB, RK;             // R in 16s as grad takes them, in 32s as up does
 };
 constexpr int kJoinThreads = 512;
+constexpr int kJoinHere = 16;  // rows of a batch up to which up joins (join_here)
 constexpr int join_pitch(int RK) { return 32 * RK + 4; }
-template <int THREADS>
-__device__ __forceinline__ void join_half(const JoinArgs& a, int64_t index, int half, float* lds) {
-  const Tile t = tile_of(a.plan, index);
-  const int left = t.rows - 32 * half, R = a.R, wide = 8 * a.RK, pitch = join_pitch(a.RK);
+// T of ROWS rows of a tile from row m0 on, scaled to `lds`, unscaled to a.t (put).
+template <int THREADS, int ROWS>
+__device__ __forceinline__ void sum_rows(const JoinArgs& a, const Tile& t, int64_t index, int m0, int64_t down_len, bool put, float* lds) {
+  const int left = t.rows - m0, R = a.R, wide = 8 * a.RK, pitch = join_pitch(a.RK);
   const bool bare = t.adapter >= a.plan.A;
-  if (t.rows == 0 || (bare && (a.t == nullptr || left <= 0))) return;
   const float alpha = bare || a.alpha == nullptr ? 1.f : a.alpha[t.adapter];
   int64_t first = 0, last = -1;
   if (a.kept != nullptr) last = 0;
-  else if (!bare) a.down.of(index, a.down.len(used_tiles(a.plan)), first, last);
-  for (int id = threadIdx.x; id < 32 * wide; id += THREADS) {
+  else if (!bare) a.down.of(index, down_len, first, last);
+  for (int id = threadIdx.x; id < ROWS * wide; id += THREADS) {
     const int m = id / wide, r = id % wide * 4;
-    const bool in = m < left && r < R;
     f32x4 v{};
-    if (in) {
-      const int64_t row = row_at(a.plan, t.pos + 32 * half + m);
+    if (m < left && r < R) {
+      const int64_t row = row_at(a.plan, t.pos + m0 + m);
       if (a.kept != nullptr) {
         v = *reinterpret_cast<const f32x4*>(a.kept + row * R + r);
       } else {
-        const float* p = a.part + ((first + index) * kTile + 32 * half + m) * R + r;
+        const float* p = a.part + ((first + index) * kTile + m0 + m) * R + r;
 #pragma unroll 8
         for (int64_t w = first; w <= last; w++, p += kTile * R) v += *reinterpret_cast<const f32x4*>(p);
       }
-      if (a.t != nullptr) *reinterpret_cast<f32x4*>(a.t + row * R + r) = v;
+      if (put) *reinterpret_cast<f32x4*>(a.t + row * R + r) = v;
     }
     *reinterpret_cast<f32x4*>(lds + m * pitch + r) = v * alpha;
   }
+}
+// up's operand of BLOCKS blocks of 16 rows; its parts lie 4 RK 64 apart.
+template <int THREADS, int BLOCKS>
+__device__ __forceinline__ void form_rows(int RK, const float* lds, u32x4* to) {
+  const int pitch = join_pitch(RK);
+  for (int id = threadIdx.x; id < BLOCKS * RK * 64; id += THREADS) {
+    const int lane = id & 63, k = (id >> 6) % RK, block = (id >> 6) / RK;
+    const float* p = lds + (16 * block + (lane & 15)) * pitch + 32 * k + 8 * (lane >> 4);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = p[i];
+    u32x4 hi, lo;
+    parts_of(v, hi, lo);
+    to[id] = hi;
+    to[id + 4 * RK * 64] = lo;
+  }
+}
+template <int THREADS>
+__device__ __forceinline__ void join_half(const JoinArgs& a, int64_t index, int half, float* lds) {
+  const Tile t = tile_of(a.plan, index);
+  const bool bare = t.adapter >= a.plan.A;
+  if (t.rows == 0 || (bare && (a.t == nullptr || t.rows <= 32 * half))) return;
+  sum_rows<THREADS, 32>(a, t, index, 32 * half, a.kept != nullptr ? 1 : a.down.len(used_tiles(a.plan)), a.t != nullptr, lds);
   if (bare) return;
   __syncthreads();
-  if (a.rows != nullptr) {
-    u32x4* to = a.rows + (index * 8 + 2 * half) * a.RK * 64;
-    for (int id = threadIdx.x; id < 2 * a.RK * 64; id += THREADS) {
-      const int lane = id & 63, k = (id >> 6) % a.RK, block = (id >> 6) / a.RK;
-      const float* p = lds + (16 * block + (lane & 15)) * pitch + 32 * k + 8 * (lane >> 4);
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = p[i];
-      u32x4 hi, lo;
-      parts_of(v, hi, lo);
-      to[id] = hi;
-      to[id + 4 * a.RK * 64] = lo;
-    }
-  }
+  if (a.rows != nullptr) form_rows<THREADS, 2>(a.RK, lds, a.rows + (index * 8 + 2 * half) * a.RK * 64);
   if (a.cols != nullptr) {
     const int n = 2 * a.RB * 64;
+    const int pitch = join_pitch(a.RK);
     u32x4* to = a.cols + index * kParts * n + half * a.RB * 64;
     for (int id = threadIdx.x; id < a.RB * 64; id += THREADS) {
       const int lane = id & 63;
@@ -488,15 +498,16 @@ struct UpArgs {
   int R;
   Stream stream;
   const u32x4* t;
+  JoinArgs join;  // JOIN
 };
 // Workgroups a CU, by their registers.
 constexpr int up_per_cu(int RK) { return RK <= 2 ? 2 : 1; }  // and LDS
 // A wave's LDS: two blocks of rows and a strip's factors.
 constexpr int up_lines(int RK) { return 2 * 2048 + RK * 4096; }
-// MB: blocks of rows.
-template <int RK, bool ADD, int MB>
-__device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t first, int64_t last, const u32x4* t_from,
-                                         u32x4* operands, uint8_t* lines) {
+// MB: blocks of rows.  JOIN: T is summed here, in place of join's launch.
+template <int RK, bool ADD, bool JOIN, int MB>
+__device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t index, int64_t first, int64_t last,
+                                         int64_t down_len, u32x4* operands, uint8_t* lines) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
   constexpr int PER = 4 * RK, WL = 64 * PER / 64;  // chunks of a factor's row, accesses of a strip's factors
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q = lane >> 4;
@@ -593,7 +604,15 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
 #pragma unroll
     for (int b = 0; b < MB; b++) fetch_y(0, b);
   }
-  {  // T, behind the first loads
+  if constexpr (JOIN) {
+    float* tile = reinterpret_cast<float*>(lines);
+    __syncthreads();  // the tile before is read
+    sum_rows<kThreads, 16 * MB>(a.join, t, index, 0, down_len, a.join.t != nullptr && first == 0, tile);
+    __syncthreads();
+    form_rows<kThreads, MB>(RK, tile, operands);
+    __syncthreads();
+  } else {  // T, behind the first loads
+    const u32x4* t_from = a.t + index * (8 * RK * 64);
     u32x4 v[2 * RK];
 #pragma unroll
     for (int j = 0; j < 2 * RK; j++) v[j] = t_from[threadIdx.x + j * kThreads];
@@ -653,12 +672,14 @@ __device__ __forceinline__ void copy_piece(const UpArgs& a, const Tile& t, int64
       if (r + 8 * i < t.rows) *reinterpret_cast<u32x4*>(a.y + row[i] * a.y_row + n) = v[i];
   }
 }
-template <int RK, bool ADD>
+template <int RK, bool ADD, bool JOIN>
 __global__ __launch_bounds__(kThreads, up_per_cu(RK)) void up_kernel(const UpArgs a) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   u32x4* operands = reinterpret_cast<u32x4*>(dynamic);  // [2][4][RK][64]
   uint8_t* lines = dynamic + 8 * RK * 1024;             // the waves' lines
-  const int64_t tiles = a.y0 == a.y ? used_tiles(a.plan) : all_tiles(a.plan), len = a.stream.len(tiles);
+  const bool zeros = JOIN && a.join.t != nullptr;  // T of rows without an adapter
+  const int64_t used = used_tiles(a.plan), tiles = a.y0 == a.y && !zeros ? used : all_tiles(a.plan), len = a.stream.len(tiles);
+  const int64_t down_len = JOIN ? a.join.down.len(used) : 0;
   int64_t at = blockIdx.x * len;
   const int64_t end = min(at + len, tiles * a.stream.steps);
   while (at < end) {
@@ -667,12 +688,15 @@ __global__ __launch_bounds__(kThreads, up_per_cu(RK)) void up_kernel(const UpArg
     const Tile t = tile_of(a.plan, index);
     if (t.rows == 0) continue;
     if (t.adapter >= a.plan.A) {  // Y0 as it is
-      copy_piece<ADD>(a, t, first * 64, min(last * 64, a.N));
+      if (zeros && first == 0) {
+        __syncthreads();  // the tile before is read
+        sum_rows<kThreads, kJoinHere>(a.join, t, index, 0, down_len, true, reinterpret_cast<float*>(lines));
+      }
+      if (a.y0 != a.y) copy_piece<ADD>(a, t, first * 64, min(last * 64, a.N));
       continue;
     }
-    const u32x4* from = a.t + index * (8 * RK * 64);
-    if (t.rows <= 16) up_piece<RK, ADD, 1>(a, t, first, last, from, operands, lines);
-    else up_piece<RK, ADD, 4>(a, t, first, last, from, operands, lines);
+    if (JOIN || t.rows <= 16) up_piece<RK, ADD, JOIN, 1>(a, t, index, first, last, down_len, operands, lines);
+    else if constexpr (!JOIN) up_piece<RK, ADD, JOIN, 4>(a, t, index, first, last, down_len, operands, lines);
   }
 }
 
@@ -941,6 +965,9 @@ JoinArgs join_of(const Plan& plan, int64_t R, const float* alpha) {
   a.RK = rank_steps(R);
   return a;
 }
+// One block of rows at the most: up sums T itself, each workgroup what it needs, a launch less (5120 -> 5120, R = 128: one
+// row 15.5 us and 14.0 so, 8 rows of 8 adapters 17.0 and 15.1, 64 rows of one 24 and 58).
+bool join_here(int64_t M) { return M <= kJoinHere; }
 void join(const JoinArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(join_kernel, dim3((unsigned)(2 * a.plan.most)), dim3(kJoinThreads), 0, stream, a);
 }
@@ -956,17 +983,22 @@ void down(const Plan& plan, const void* x, int64_t x_row, const void* w, int64_t
   }
 }
 
+// t: join's rows, or null: summed as `j` says.
 void up(const Plan& plan, const void* w, const void* y0, int64_t y0_row, void* y, int64_t y_row, int64_t N, int64_t R, const void* t,
-        hipStream_t stream) {
+        const JoinArgs& j, hipStream_t stream) {
   const int rk = rank_steps(R);
   const UpArgs a{plan, (const uint16_t*)w, (const uint16_t*)y0, (uint16_t*)y, y0_row, y_row, N, (int)R,
-                 stream_of(plan.most, (N + 63) / 64, up_per_cu(rk), kWaves), (const u32x4*)t};
+                 stream_of(plan.most, (N + 63) / 64, up_per_cu(rk), kWaves), (const u32x4*)t, j};
   const dim3 grid((unsigned)a.stream.groups);
   auto go = [&](auto k) {
     constexpr int RK = decltype(k)::value;
     constexpr size_t lds = 8 * RK * 1024 + kWaves * up_lines(RK);
-    if (y0 != nullptr) hipLaunchKernelGGL((up_kernel<RK, true>), grid, dim3(kThreads), lds, stream, a);
-    else hipLaunchKernelGGL((up_kernel<RK, false>), grid, dim3(kThreads), lds, stream, a);
+    static_assert(kWaves * up_lines(RK) >= kJoinHere * join_pitch(RK) * 4, "a tile's T in the lines' place");
+    auto run = [&](auto add, auto here) {
+      hipLaunchKernelGGL((up_kernel<RK, decltype(add)::value, decltype(here)::value>), grid, dim3(kThreads), lds, stream, a);
+    };
+    if (y0 != nullptr) t == nullptr ? run(std::true_type(), std::true_type()) : run(std::true_type(), std::false_type());
+    else t == nullptr ? run(std::false_type(), std::true_type()) : run(std::false_type(), std::false_type());
   };
   switch (rk) {
     case 1: go(std::integral_constant<int, 1>()); break;
@@ -1014,8 +1046,10 @@ hipError_t launch_adapters(const AdapterCall& c, const void* y0, int64_t y0_row,
   j.down = down_stream(plan.most, c.K, c.R);
   j.t = t;
   j.rows = (u32x4*)((uint8_t*)ws + part_bytes(c.M, c.A, c.R, c.K));
-  join(j, stream);
-  up(plan, c.LA, y0, y0_row, y, y_row, c.N, c.R, j.rows, stream);
+  const bool here = join_here(c.M);
+  if (here) j.rows = nullptr;
+  else join(j, stream);
+  up(plan, c.LA, y0, y0_row, y, y_row, c.N, c.R, j.rows, j, stream);
   return hipGetLastError();
 }
 
@@ -1072,7 +1106,7 @@ hipError_t launch_adapters_back(const AdapterCall& c, const float* t, const void
     j.rows = dx != nullptr ? (u32x4*)drows : nullptr;
     j.cols = dlb != nullptr ? (u32x4*)dcols : nullptr;
     join(j, stream);
-    if (dx != nullptr) up(plan, lbt, dx0, dx0_row, dx, dx_row, c.K, c.R, drows, stream);
+    if (dx != nullptr) up(plan, lbt, dx0, dx0_row, dx, dx_row, c.K, c.R, drows, j, stream);
   }
   if (dla != nullptr || dlb != nullptr) {
     const int64_t C = grad_columns(c.R);

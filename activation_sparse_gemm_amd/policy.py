@@ -136,9 +136,9 @@ class AdaptedLinear:
         return rtl_adapters_plan(ids, self.LA.shape[0], plan, stream=stream)
 
     def workspace(self, M: int):
-        if M not in self._ws:
-            A, N, R = self.LA.shape
-            need = rtl_adapters_workspace_bytes(M, N, self.LB.shape[2], R, A)
+        A, N, R = self.LA.shape
+        need = rtl_adapters_workspace_bytes(M, N, self.LB.shape[2], R, A)
+        if M not in self._ws or self._ws[M].numel() < need:
             self._ws[M] = torch.empty((max(need, 1),), dtype=torch.uint8, device=self.LA.device)
         return self._ws[M]
 

@@ -289,3 +289,27 @@ def test_plan_of_garbage_stays_in_bounds():
         rtl.rtl_adapters_backward(c.X, c.LA, c.LB, plan, T.t, c.dY, c.alpha, dX=out[0].t, dLA=out[1].t, dLB=out[2].t)
         for o in (Y, T, *out):
             o.check(f"garbage {seed}")
+
+
+@pytest.mark.parametrize("M", (1, 2, 15, 16, 17))
+@pytest.mark.parametrize("R", (8, 40, 72, 128))
+@pytest.mark.parametrize("kind", ("one", "mixed", "none", "few"))
+def test_few_rows_in_place(M, R, kind):
+    """Single rows of requests, Y in Y0's place: T of every row, zeros without an adapter, whose Y is not touched."""
+    K, N, n = 328, 1032, 5
+    c = Case(M, K, N, R, n, kind, seed=60 + M)
+    x, la, lb, a = c.host()
+    y, t, by, bt = A.adapters_forward(x, la, lb, a, c.ids, B.f64(c.Y0))
+    Y, T = Guarded((M, N), BF), Guarded((M, R), F32)
+    Y.t.copy_(c.Y0)
+    rtl.rtl_adapters(c.X, c.LA, c.LB, c.plan, c.alpha, Y0=Y.t, Y=Y.t, T=T.t)
+    B.check(T.t, t, bt, F32, f"{M} {R} {kind} T")
+    B.check(Y.t, y, by, BF, f"{M} {R} {kind} Y")
+    bare = torch.from_numpy((c.ids < 0) | (c.ids >= n)).cuda()
+    assert torch.equal(Y.t[bare], c.Y0[bare]) and not bool(T.t[bare].any())
+    Y.check(kind)
+    T.check(kind)
+    # the same without T, into a tensor of its own and on top of zeros
+    assert torch.equal(rtl.rtl_adapters(c.X, c.LA, c.LB, c.plan, c.alpha, Y0=c.Y0), Y.t)
+    zeros = torch.zeros_like(c.Y0)
+    assert torch.equal(rtl.rtl_adapters(c.X, c.LA, c.LB, c.plan, c.alpha), rtl.rtl_adapters(c.X, c.LA, c.LB, c.plan, c.alpha, Y0=zeros))
