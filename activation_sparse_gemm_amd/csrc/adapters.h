@@ -257,7 +257,8 @@ __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4 (&w)[kParts]
 // (lane (r16, q): row r16, r = 8q .. 8q + 7 of 32), and `cols`, grad's, [tile][part][half][RB][lane] (r =
 // r16 of a block, rows 8q .. 8q + 7 of the half).  Rows and r past the tile's are zeros.
 // A launch of its own: summed by each workgroup of up that needed it, T cost 8 to 19 us of up's time
-// (4608 rows of 5120, R = 64, 72 tiles of 8 pieces on 512 workgroups: 53 us for 35; this takes 6).
+// (4608 rows, 2560 -> 7680, R = 64, 72 tiles of up to 8 pieces on 512 workgroups: 53 us for 35; this takes 6), but
+// for the few rows of join_here.
 struct JoinArgs {
   Plan plan;
   const float *part, *kept;  // one of them
