@@ -398,9 +398,9 @@ __device__ __forceinline__ float value_at(bool bf16, const void* p, int64_t at) 
 
 // Column sums of a workgroup's 32 columns: lane c of 32 / CV holds CV of them, row lane l of LR every
 // LR-th of the terms; the row lanes' sums are added in one order.  For 32 threads, column `col` of each.
-template <int CV>
+template <int CV, int THREADS>
 struct NormColumns {
-  static constexpr int LC = 32 / CV, LR = 256 / LC;
+  static constexpr int LC = 32 / CV, LR = THREADS / LC, K = THREADS / 32;
   double s[2][CV];
   __device__ __forceinline__ static int lane() { return threadIdx.x % LC * CV; }
   __device__ __forceinline__ static int row() { return threadIdx.x / LC; }
@@ -417,19 +417,29 @@ struct NormColumns {
       red[1][row()][lane() + i] = s[1][i];
     }
     __syncthreads();
-    s0 = s1 = 0.0;
-    if (threadIdx.x < 32)
-      for (int r = 0; r < LR; r++) {
-        s0 += red[0][r][threadIdx.x];
-        s1 += red[1][r][threadIdx.x];
+    const int c = threadIdx.x % 32, k = threadIdx.x / 32;
+    auto add = [&](int from, int step, int n) {
+      s0 = s1 = 0.0;
+#pragma unroll
+      for (int r = 0; r < n; r++) {
+        s0 += red[0][from + r * step][c];
+        s1 += red[1][from + r * step][c];
       }
+    };
+    if constexpr (LR > K) {  // every K-th, then the K sums
+      add(k, K, LR / K);
+      red[0][k][c] = s0;
+      red[1][k][c] = s1;
+      __syncthreads();
+    }
+    if (k == 0) add(0, 1, K);
   }
 };
 
 // The sums of group blockIdx.x over its chunks, 32 columns a workgroup, in double.
-template <bool BF16, int CV>
-__global__ __launch_bounds__(256) void norm_sum_kernel(const SumArgs a) {
-  typedef NormColumns<CV> Columns;
+template <bool BF16, int CV, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_sum_kernel(const SumArgs a) {
+  typedef NormColumns<CV, THREADS> Columns;
   Columns t;
   const int64_t g = blockIdx.x;
   const int col0 = blockIdx.y * 32, at = col0 + t.lane();
@@ -477,7 +487,7 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(const SumArgs a) {
 // dw and db over the groups: sum_g (1 + scale_g) S_g.
 template <bool BF16>
 __global__ __launch_bounds__(256) void norm_weight_kernel(const SumArgs a) {
-  typedef NormColumns<1> Columns;
+  typedef NormColumns<1, 256> Columns;
   Columns t;
   const int col0 = blockIdx.x * 32, at = col0 + t.lane();
   if (at < a.D) {
@@ -574,6 +584,10 @@ void norm_forward(const NormCall& c, hipStream_t stream) {
 // Waves a row of the gradient: up to four pieces a lane.
 int norm_back_waves(int64_t pieces) { return pieces <= 64 * 2 ? 1 : pieces <= 256 * 4 ? 4 : pieces <= 512 * 4 ? 8 : 16; }
 
+// Workgroups of 32 columns' sums below which each takes 1024 threads, not 256: fewer leave the chip's places free (the gradient of 7284 x
+// 200 20.8 us and 17.8 so, of 32760 x 1024 55.7 and 49.5, of 64 x 5120 12.9 and 13.2; with 640 workgroups no gain).
+constexpr int64_t kNormSumBlocks = 256;
+
 int norm_chunk(int64_t M) {
   // enough chunks to fill the chip, few enough that their sums stay small against the rows
   return (int)std::max<int64_t>(2, std::min<int64_t>(kNormChunk, M / 512));
@@ -663,8 +677,13 @@ hipError_t launch_norm_back(const NormCall& c, float* dw, float* db, float* dsca
   auto go = [&](auto bf16) {
     constexpr bool B = decltype(bf16)::value;
     const dim3 grid((unsigned)s.G, cols);
-    if (c.D % 4 == 0) hipLaunchKernelGGL((norm_sum_kernel<B, 4>), grid, dim3(256), 0, stream, s);
-    else hipLaunchKernelGGL((norm_sum_kernel<B, 1>), grid, dim3(256), 0, stream, s);
+    auto sum = [&](auto threads) {
+      constexpr int T = decltype(threads)::value;
+      if (c.D % 4 == 0) hipLaunchKernelGGL((norm_sum_kernel<B, 4, T>), grid, dim3(T), 0, stream, s);
+      else hipLaunchKernelGGL((norm_sum_kernel<B, 1, T>), grid, dim3(T), 0, stream, s);
+    };
+    if ((int64_t)cols * s.G < kNormSumBlocks) sum(Int<1024>());
+    else sum(Int<256>());
     if (several) hipLaunchKernelGGL(norm_weight_kernel<B>, dim3(cols), dim3(256), 0, stream, s);
   };
   if (c.dt == kDtBF16) go(std::true_type());
