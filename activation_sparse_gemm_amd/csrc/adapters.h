@@ -11,10 +11,11 @@
 // order of the requests.  What the plan holds is bounded where it is read: no access leaves the arrays.
 //
 // Bound: memory (X, Y0 and Y pass once, 2 R flops a byte of them).  T and dT are held in fp32 and enter
-// the next product in two bf16 parts (two_parts), 16 digits: its rounding to one, 2^-9, would be
-// the largest error of an adapter's share, and the products are too small to hold the kernels.
+// the next products in three bf16 parts (three_parts), all 24 digits.  One would leave 2^-9 of an adapter's
+// share, two 2^-16; the products are too small to hold the kernels (up in parts of three and two, whole calls: 24 rows of
+// 5120 -> 13824, R = 32 16.1 and 15.9 us; 4608 of 2560 -> 7680, R = 64 62.6 and 59.2; 32760 of 5120 -> 5120 253 and 251).
 // 32760 rows of 5120 -> 5120, R = 64: down 101 us, join 10, up 141; a copy of X's size 60, of Y0's to Y 120.
-// The gradients leave in fp32, and their sums take three parts, all 24 digits: with two they were 5e-6 off.
+// (The gradients' sums, which leave in fp32, were 5e-6 off with two.)
 //
 //   down:   T in pieces over K, the waves taking 64 of K in turn
 //   join:   T's pieces summed, T in the layouts of the products that it enters
@@ -34,7 +35,7 @@ namespace lora {
 constexpr int kTile = 64;     // rows of a tile
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kParts = 3;     // of T and dT in the gradients' sums
+constexpr int kParts = 3;     // of T and dT in the next products
 
 struct Plan {
   const int32_t *start, *tbase;  // [A + 2]: first position, first tile of each adapter; A: the rows without one
@@ -231,15 +232,6 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ void parts_of(const float (&v)[8], u32x4& hi, u32x4& lo) {
-  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const Bf16Parts x = two_parts(v[2 * i]), y = two_parts(v[2 * i + 1]);
-    hi[i] = __builtin_bit_cast(uint32_t, bf16x2_t{x.hi, y.hi});
-    lo[i] = __builtin_bit_cast(uint32_t, bf16x2_t{x.lo, y.lo});
-  }
-}
 __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4 (&w)[kParts]) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
@@ -307,10 +299,10 @@ __device__ __forceinline__ void form_rows(int RK, const float* lds, u32x4* to) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] = p[i];
-    u32x4 hi, lo;
-    parts_of(v, hi, lo);
-    to[id] = hi;
-    to[id + 4 * RK * 64] = lo;
+    u32x4 w[kParts];
+    parts_of(v, w);
+#pragma unroll
+    for (int h = 0; h < kParts; h++) to[id + h * 4 * RK * 64] = w[h];
   }
 }
 template <int THREADS>
@@ -321,7 +313,7 @@ __device__ __forceinline__ void join_half(const JoinArgs& a, int64_t index, int 
   sum_rows<THREADS, 32>(a, t, index, 32 * half, a.kept != nullptr ? 1 : a.down.len(used_tiles(a.plan)), a.t != nullptr, lds);
   if (bare) return;
   __syncthreads();
-  if (a.rows != nullptr) form_rows<THREADS, 2>(a.RK, lds, a.rows + (index * 8 + 2 * half) * a.RK * 64);
+  if (a.rows != nullptr) form_rows<THREADS, 2>(a.RK, lds, a.rows + (index * 4 * kParts + 2 * half) * a.RK * 64);
   if (a.cols != nullptr) {
     const int n = 2 * a.RB * 64;
     const int pitch = join_pitch(a.RK);
@@ -565,7 +557,7 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
   };
   auto form = [&](int64_t n, int b, bool in) {
     uint8_t* block = mine + (b & 1) * 2048;
-    u32x4 v[2], tb[2][RK];
+    u32x4 v[2], tb[kParts][RK];
     if (ADD) {
 #pragma unroll
       for (int i = 0; i < 2; i++) *reinterpret_cast<u32x4*>(block + line_at(8 * i + l8, chunk)) = y[b][i];
@@ -577,7 +569,7 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
 #pragma unroll
     for (int k = 0; k < RK; k++)
 #pragma unroll
-      for (int h = 0; h < 2; h++) tb[h][k] = tv[((h * 4 + b) * RK + k) * 64];
+      for (int h = 0; h < kParts; h++) tb[h][k] = tv[((h * 4 + b) * RK + k) * 64];
 #pragma unroll
     for (int s = 0; s < 2; s++) {
       u32x4 out;
@@ -585,10 +577,9 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
       for (int c = 0; c < 2; c++) {
         f32x4 z = {bf16lo(v[s][2 * c]), bf16hi(v[s][2 * c]), bf16lo(v[s][2 * c + 1]), bf16hi(v[s][2 * c + 1])};
 #pragma unroll
-        for (int k = 0; k < RK; k++) {
-          z = mfma16(f[2 * s + c][k], tb[0][k], z);
-          z = mfma16(f[2 * s + c][k], tb[1][k], z);
-        }
+        for (int k = 0; k < RK; k++)
+#pragma unroll
+          for (int h = 0; h < kParts; h++) z = mfma16(f[2 * s + c][k], tb[h][k], z);
         out[2 * c] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)z[0], (__bf16)z[1]});
         out[2 * c + 1] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)z[2], (__bf16)z[3]});
       }
@@ -613,13 +604,14 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
     form_rows<kThreads, MB>(RK, tile, operands);
     __syncthreads();
   } else {  // T, behind the first loads
-    const u32x4* t_from = a.t + index * (8 * RK * 64);
-    u32x4 v[2 * RK];
+    const u32x4* t_from = a.t + index * (4 * kParts * RK * 64);
+    u32x4 v[kParts * RK];
+    static_assert(kThreads == 4 * 64, "a part's blocks of RK in RK accesses");
 #pragma unroll
-    for (int j = 0; j < 2 * RK; j++) v[j] = t_from[threadIdx.x + j * kThreads];
+    for (int j = 0; j < kParts * RK; j++) v[j] = t_from[threadIdx.x + j * kThreads];
     __syncthreads();  // the tile before is read
 #pragma unroll
-    for (int j = 0; j < 2 * RK; j++) operands[threadIdx.x + j * kThreads] = v[j];
+    for (int j = 0; j < kParts * RK; j++) operands[threadIdx.x + j * kThreads] = v[j];
     __syncthreads();
   }
   // The next strip's factors go out first, each block of rows when this strip's is done with: every load has a
@@ -676,8 +668,8 @@ __device__ __forceinline__ void copy_piece(const UpArgs& a, const Tile& t, int64
 template <int RK, bool ADD, bool JOIN>
 __global__ __launch_bounds__(kThreads, up_per_cu(RK)) void up_kernel(const UpArgs a) {
   extern __shared__ __align__(16) uint8_t dynamic[];
-  u32x4* operands = reinterpret_cast<u32x4*>(dynamic);  // [2][4][RK][64]
-  uint8_t* lines = dynamic + 8 * RK * 1024;             // the waves' lines
+  u32x4* operands = reinterpret_cast<u32x4*>(dynamic);  // [kParts][4][RK][64]
+  uint8_t* lines = dynamic + 4 * kParts * RK * 1024;    // the waves' lines
   const bool zeros = JOIN && a.join.t != nullptr;  // T of rows without an adapter
   const int64_t used = used_tiles(a.plan), tiles = a.y0 == a.y && !zeros ? used : all_tiles(a.plan), len = a.stream.len(tiles);
   const int64_t down_len = JOIN ? a.join.down.len(used) : 0;
@@ -955,7 +947,7 @@ size_t part_bytes(int64_t M, int64_t A, int64_t R, int64_t C) {
   return align((size_t)(most + down_stream(most, C, R).groups) * kTile * R * 4);
 }
 
-size_t rows_bytes(int64_t M, int64_t A, int64_t R) { return (size_t)max_tiles(M, A) * 8 * rank_steps(R) * 1024; }
+size_t rows_bytes(int64_t M, int64_t A, int64_t R) { return (size_t)max_tiles(M, A) * 4 * kParts * rank_steps(R) * 1024; }
 
 JoinArgs join_of(const Plan& plan, int64_t R, const float* alpha) {
   JoinArgs a{};
@@ -993,7 +985,7 @@ void up(const Plan& plan, const void* w, const void* y0, int64_t y0_row, void* y
   const dim3 grid((unsigned)a.stream.groups);
   auto go = [&](auto k) {
     constexpr int RK = decltype(k)::value;
-    constexpr size_t lds = 8 * RK * 1024 + kWaves * up_lines(RK);
+    constexpr size_t lds = 4 * kParts * RK * 1024 + kWaves * up_lines(RK);
     static_assert(kWaves * up_lines(RK) >= kJoinHere * join_pitch(RK) * 4, "a tile's T in the lines' place");
     auto run = [&](auto add, auto here) {
       hipLaunchKernelGGL((up_kernel<RK, decltype(add)::value, decltype(here)::value>), grid, dim3(kThreads), lds, stream, a);

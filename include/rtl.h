@@ -426,8 +426,8 @@ rtl_status rtl_layer_norm_backward(rtl_dtype dt, int64_t M, int64_t D, const voi
  * serves all calls with that M and A, forward and back, until it is written again.  What it holds is
  * not checked, but no call goes past its tensors for it.
  *
- * Both products accumulate in fp32; T enters the second in two bf16 parts (2^-16 of it); one rounding at
- * the end.  Limits: K, N and R multiples of 8, R <= 128, K and N <= 2^22, A <= 4096, M <= 2^24, and
+ * Both products accumulate in fp32; T enters the second in three bf16 parts, which hold all its digits; one
+ * rounding at the end.  Limits: K, N and R multiples of 8, R <= 128, K and N <= 2^22, A <= 4096, M <= 2^24, and
  * A * max(K, N) <= 2^27.  Outputs overlap no input but Y0 as said.  Calls that share a workspace must be
  * serialised.
  */
