@@ -62,11 +62,19 @@ def lowrank_gradient(X: torch.Tensor, E: torch.Tensor, LA: torch.Tensor, LB: tor
     return dLA[0], dLB[0]
 
 
+def _batch(X: torch.Tensor, step: int, rows: int):
+    """Batch `step` of `rows` rows of X [M,K], M >= rows, where the last row is followed by the first."""
+    at = step * rows % X.shape[0]
+    past = at + rows - X.shape[0]
+    return X[at:at + rows] if past <= 0 else torch.cat([X[at:], X[:past]])
+
+
 def train_lowrank(X: torch.Tensor, E: torch.Tensor, R: int, steps: int = 2000, rows: int = 4096, lr: float = 1e-3,
                   LA=None, LB=None, seed: int = 0):
     """Rank-R factors (L_A [N,R], L_B [R,K], float32) after `steps` AdamW steps (no decay) on the mean of
-    (E - X (L_A L_B)^T)^2 over batches of `rows` rows of X [M,K] and E [M,N] (bf16 on the GPU), one
-    batch after another.  They start from L_A = 0 and a random L_B, or from those given."""
+    (E - X (L_A L_B)^T)^2 over batches of `rows` rows of X [M,K] and E [M,N] (bf16 on the GPU), one batch
+    after another: the one that ends past the last row goes on from the first, so that all rows count alike.  They start
+    from L_A = 0 and a random L_B, or from those given."""
     if X.dim() != 2 or E.dim() != 2 or X.shape[0] != E.shape[0] or X.dtype != torch.bfloat16 or E.dtype != torch.bfloat16:
         raise ValueError("X and E are [M,K] and [M,N] in bf16")
     M, K, N = X.shape[0], X.shape[1], E.shape[1]
@@ -85,8 +93,7 @@ def train_lowrank(X: torch.Tensor, E: torch.Tensor, R: int, steps: int = 2000, r
     plan = rtl_adapters_plan(torch.zeros((rows,), dtype=torch.int32, device=X.device), 1)
     scale = torch.full((1,), 2.0 / (rows * N), dtype=torch.float32, device=X.device)
     for step in range(steps):
-        at = step * rows % (M - rows + 1)
-        lowrank_gradient(X[at:at + rows], E[at:at + rows], *params, plan, *grads)
+        lowrank_gradient(_batch(X, step, rows), _batch(E, step, rows), *params, plan, *grads)
         rtl_adamw(tensors, step + 1, lr, weight_decay=0.0, grad_scale=scale)
     return masters[0], masters[1]
 

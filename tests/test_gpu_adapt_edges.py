@@ -2,9 +2,13 @@
 import pytest
 import torch
 
+import _adapt as A
+
 pytestmark = pytest.mark.gpu
 
 rtl = pytest.importorskip("activation_sparse_gemm_amd")
+
+from activation_sparse_gemm_amd import calib  # noqa: E402
 
 BF = torch.bfloat16
 
@@ -41,3 +45,23 @@ def test_every_digit_of_the_inner_product(M, R):
     LA[0, :3, 0], LA[0, :2, R - 1], LB[0, 0], LB[0, R - 1] = 1.0, -1.0, 1.0, 1.0
     dX = rtl.rtl_adapters_backward(X, LA, LB, plan, None, dY, need_dw=False)[0]
     assert torch.equal(dX, v[:, 2:].expand(M, K))
+
+
+@pytest.mark.parametrize("M", (128, 255, 256, 300))
+def test_trained_fit_walks_the_whole_set(M):
+    """The steps of the fit on the batches that its documentation names: the same factors to the bit."""
+    K, N, R, rows, lr = 64, 48, 8, 128, 1e-2
+    X, E = A.rnd(M, M, K), A.rnd(M + 1, M, N)
+    start = [A.rnd(3, N, R, std=0.3, dtype=torch.float32), A.rnd(4, R, K, std=0.3, dtype=torch.float32)]
+    got = calib.train_lowrank(X, E, R, steps=5, rows=rows, lr=lr, LA=start[0], LB=start[1])
+    masters = [t.clone() for t in start]
+    params = [t.to(BF) for t in masters]
+    grads, m, v = ([torch.zeros_like(t) for t in masters] for _ in range(3))
+    tensors = rtl.rtl_adamw_tensors(params, grads, m, v, masters=masters)
+    scale = torch.full((1,), 2.0 / (rows * N), device="cuda")
+    for step in range(5):
+        at = torch.arange(step * rows, (step + 1) * rows, device="cuda") % M
+        for to, t in zip(grads, calib.lowrank_gradient(X[at], E[at], *params)):
+            to.copy_(t)
+        rtl.rtl_adamw(tensors, step + 1, lr, weight_decay=0.0, grad_scale=scale)
+    assert all(torch.equal(a, b) for a, b in zip(got, masters))
