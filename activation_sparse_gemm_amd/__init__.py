@@ -39,7 +39,8 @@ __all__ = [
     "RTL_ROPE_ADJACENT", "RTL_ROPE_HALVES", "rtl_rope_axes", "rtl_qk_norm_rope", "rtl_qk_norm_rope_backward",
     "rtl_qk_norm_rope_backward_workspace_bytes",
     "RTL_ACT_SILU", "RTL_ACT_GELU", "rtl_glu_fused", "rtl_glu_backward", "rtl_glu_backward_workspace_bytes",
-    "rtl_layer_norm", "rtl_layer_norm_backward", "rtl_layer_norm_backward_workspace_bytes",
+    "RTL_REST_KEPT", "RTL_REST_ZEROS", "rtl_layer_norm", "rtl_layer_norm_backward",
+    "rtl_layer_norm_backward_workspace_bytes",
     "rtl_adapters_plan", "rtl_adapters_plan_bytes", "rtl_adapters", "rtl_adapters_workspace_bytes",
     "rtl_adapters_backward", "rtl_adapters_backward_workspace_bytes",
     "RTL_STATES_8", "RTL_STATES_32", "AdamWTensors", "rtl_adamw_tensors", "rtl_adamw",
@@ -58,6 +59,7 @@ RTL_MLP_AUTO, RTL_MLP_PRODUCER, RTL_MLP_CONSUMER = 0, 1, 2
 RTL_ROPE_ADJACENT, RTL_ROPE_HALVES = 0, 1
 RTL_ACT_SILU, RTL_ACT_GELU = 0, 1
 RTL_STATES_8, RTL_STATES_32 = 8, 32
+RTL_REST_KEPT, RTL_REST_ZEROS = 0, 1
 STATUS = {0: "RTL_OK", 1: "RTL_ERR_NULL", 2: "RTL_ERR_SHAPE", 3: "RTL_ERR_ALIGN", 4: "RTL_ERR_UNSUPPORTED",
           5: "RTL_ERR_ARG", 6: "RTL_ERR_WORKSPACE", 7: "RTL_ERR_HIP"}
 
@@ -67,8 +69,9 @@ EXPORTS = ["rtl_sparsify", "rtl_linear_fused_workspace_bytes", "rtl_linear_fused
            "rtl_mlp_fused_workspace_bytes", "rtl_mlp_fused", "rtl_quantize_weight_fp8",
            "rtl_linear_fused_fp8_workspace_bytes", "rtl_linear_fused_fp8", "rtl_rope_axes", "rtl_qk_norm_rope",
            "rtl_qk_norm_rope_backward_workspace_bytes", "rtl_qk_norm_rope_backward", "rtl_glu_fused",
-           "rtl_glu_backward_workspace_bytes", "rtl_glu_backward", "rtl_layer_norm",
-           "rtl_layer_norm_backward_workspace_bytes", "rtl_layer_norm_backward", "rtl_adapters_plan_bytes",
+           "rtl_glu_backward_workspace_bytes", "rtl_glu_backward", "rtl_layer_norm", "rtl_layer_norm_ex",
+           "rtl_layer_norm_backward_workspace_bytes", "rtl_layer_norm_backward", "rtl_layer_norm_backward_ex",
+           "rtl_adapters_plan_bytes",
            "rtl_adapters_plan", "rtl_adapters_workspace_bytes", "rtl_adapters",
            "rtl_adapters_backward_workspace_bytes", "rtl_adapters_backward", "rtl_adamw", "rtl_status_string",
            "rtl_last_error", "rtl_version"]
@@ -137,11 +140,13 @@ def _load() -> ctypes.CDLL:
     L.rtl_glu_backward.restype = i32
     rows = [p, i64]  # pointer, row stride
     L.rtl_layer_norm.argtypes = [i32, i64, i64, *rows, p, p, i64, p, *rows, *rows, f32, *rows, p, p]
-    L.rtl_layer_norm.restype = i32
+    L.rtl_layer_norm_ex.argtypes = [i32, *L.rtl_layer_norm.argtypes]
+    L.rtl_layer_norm.restype = L.rtl_layer_norm_ex.restype = i32
     L.rtl_layer_norm_backward_workspace_bytes.argtypes = [i64, i64, i64]
     L.rtl_layer_norm_backward_workspace_bytes.restype = sz
     L.rtl_layer_norm_backward.argtypes = [i32, i64, i64, *rows, p, *rows, p, p, i64, p, *rows, *rows, p, p, p, p, p, sz, p]
-    L.rtl_layer_norm_backward.restype = i32
+    L.rtl_layer_norm_backward_ex.argtypes = [i32, *L.rtl_layer_norm_backward.argtypes]
+    L.rtl_layer_norm_backward.restype = L.rtl_layer_norm_backward_ex.restype = i32
     L.rtl_adapters_plan_bytes.argtypes = [i64, i64]
     L.rtl_adapters_plan_bytes.restype = sz
     L.rtl_adapters_plan.argtypes = [i64, i64, p, p, sz, p]
@@ -671,7 +676,7 @@ def rtl_layer_norm(X: torch.Tensor, weight=None, bias=None, scale=None, shift=No
 
     ``weight`` and ``bias`` [D] (None: ones, zeros).  ``scale`` and ``shift`` [G,D] (any row stride; both or
     neither) belong to groups of rows: ``groups`` int32 [G+1] on the GPU holds ascending offsets, rows outside
-    them are left as they were; None: all rows are one group.  ``stats`` [M,2] float32, when given, receives
+    them are left as they were in a ``Y`` that is given, zeros in a new one; None: all rows are one group.  ``stats`` [M,2] float32, when given, receives
     each row's mean and 1 / deviation (rtl_layer_norm_backward takes them).  ``Y`` may be X."""
     M, D = X.shape
     shape, dt, ws = (M, D), X.dtype, (D,)
@@ -679,14 +684,14 @@ def rtl_layer_norm(X: torch.Tensor, weight=None, bias=None, scale=None, shift=No
     if there is not None:
         with there:
             return rtl_layer_norm(X, weight, bias, scale, shift, groups, eps, Y, stats, stream)
-    given = Y, stats
+    given, rest = (Y, stats), RTL_REST_KEPT
     if Y is None:
-        Y = _new(stream, X, shape, dt)
+        Y, rest = _new(stream, X, shape, dt), RTL_REST_ZEROS
     G, at = _groups(groups, scale)
-    _check(lib.rtl_layer_norm(_dt(X), M, D, *_rows("X", X, shape, dt), _flat("weight", weight, ws, dt),
-                              _flat("bias", bias, ws, dt), G, at, *_rows("scale", scale, (G, D), dt),
-                              *_rows("shift", shift, (G, D), dt), eps, *_rows("Y", Y, shape, dt),
-                              _flat("stats", stats, (M, 2), torch.float32), _queue(stream, X)))
+    _check(lib.rtl_layer_norm_ex(rest, _dt(X), M, D, *_rows("X", X, shape, dt), _flat("weight", weight, ws, dt),
+                                 _flat("bias", bias, ws, dt), G, at, *_rows("scale", scale, (G, D), dt),
+                                 *_rows("shift", shift, (G, D), dt), eps, *_rows("Y", Y, shape, dt),
+                                 _flat("stats", stats, (M, 2), torch.float32), _queue(stream, X)))
     _changed(given)
     return Y
 
@@ -701,8 +706,8 @@ def rtl_layer_norm_backward(X: torch.Tensor, stats: torch.Tensor, dY: torch.Tens
                             need_dw: bool = True, stream=None):
     """Gradient of rtl_layer_norm: (dX, dweight, dbias, dscale, dshift) from its inputs, the ``stats`` it
     left and dY.  The sums are float32, dweight and dbias [D] for a weight or bias that is given, dscale and
-    dshift [G,D] for a scale that is (else None; all None with ``need_dw`` False).  Rows outside the groups are
-    left as they were in dX and count in no sum.  Outputs given by the caller are written in place; dX may be dY or X."""
+    dshift [G,D] for a scale that is (else None; all None with ``need_dw`` False).  Rows outside the groups
+    count in no sum; in a dX that is given they are left as they were, in a new one they are zeros.  Outputs given by the caller are written in place; dX may be dY or X."""
     M, D = X.shape
     shape, dt, ws, f32 = (M, D), X.dtype, (D,), torch.float32
     there = _elsewhere(X, stats, dY, weight, bias, scale, groups, dX, dweight, dbias, dscale, dshift, workspace)
@@ -715,9 +720,9 @@ def rtl_layer_norm_backward(X: torch.Tensor, stats: torch.Tensor, dY: torch.Tens
         dweight = dbias = dscale = dshift = None
     if scale is None and (dscale is not None or dshift is not None):
         raise ValueError("dscale or dshift without scale")
-    given = dX, dweight, dbias, dscale, dshift
+    given, rest = (dX, dweight, dbias, dscale, dshift), RTL_REST_KEPT
     if dX is None:
-        dX = _new(stream, X, shape, dt)
+        dX, rest = _new(stream, X, shape, dt), RTL_REST_ZEROS
     if need_dw:
         if weight is not None and dweight is None:
             dweight = _new(stream, X, ws, f32)
@@ -728,8 +733,8 @@ def rtl_layer_norm_backward(X: torch.Tensor, stats: torch.Tensor, dY: torch.Tens
             dshift = _new(stream, X, (G, D), f32) if dshift is None else dshift
     if workspace is None:
         workspace = _new(stream, X, (max(rtl_layer_norm_backward_workspace_bytes(M, D, G), 1),), torch.uint8)
-    _check(lib.rtl_layer_norm_backward(
-        _dt(X), M, D, *_rows("X", X, shape, dt), _flat("stats", stats, (M, 2), f32), *_rows("dY", dY, shape, dt),
+    _check(lib.rtl_layer_norm_backward_ex(
+        rest, _dt(X), M, D, *_rows("X", X, shape, dt), _flat("stats", stats, (M, 2), f32), *_rows("dY", dY, shape, dt),
         _flat("weight", weight, ws, dt), _flat("bias", bias, ws, dt), G, at, *_rows("scale", scale, (G, D), dt),
         *_rows("dX", dX, shape, dt), _flat("dweight", dweight, ws, f32), _flat("dbias", dbias, ws, f32),
         _flat("dscale", dscale, (G, D), f32), _flat("dshift", dshift, (G, D), f32), *_space(workspace), _queue(stream, X)))

@@ -14,7 +14,7 @@
 // bf16: forward 122 us, 5.5 TB/s; the gradient's pass 210, 5.0 with its chunks' sums, and 26 to join them.
 // A row is held in the registers of W waves, so that it is read once for mean, squares and result.
 // Groups are ascending offsets in device memory: a row finds its group there, and rows outside
-// every group are left as they were.  Whatever the offsets hold, no access leaves the arrays.
+// every group are left as they were or become zeros.  Whatever the offsets hold, no access leaves the arrays.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -117,6 +117,7 @@ struct NormArgs {
   float* stats;           // [M, 2]
   float* part;            // gradient: [slots][2][D]
   int rows;               // gradient: rows of a chunk
+  bool clear;             // zeros to y's rows of no group
 };
 
 constexpr int kNormThreads = 256;
@@ -126,6 +127,17 @@ dim3 norm_grid(int64_t blocks) {
   return dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
 }
 __device__ __forceinline__ int64_t norm_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
+// Zeros to a row of y, a lane its pieces.
+template <bool BF16, int V, int W, int J>
+__device__ __forceinline__ void clear_row(const NormArgs& a, int64_t row, int at0) {
+  const float zeros[V] = {};
+#pragma unroll
+  for (int j = 0; j < J; j++) {
+    const int at = at0 + j * W * 64 * V;
+    if (at < a.D) Piece<BF16, V>::store(a.y, row * a.y_row + at, zeros);
+  }
+}
 
 // Forward: W waves a row, J pieces a lane.
 template <bool BF16, int V, int W, int J>
@@ -144,7 +156,10 @@ __global__ __launch_bounds__(W == 1 ? kNormThreads : W * 64) void norm_kernel(co
     if (at < a.D) raw[j] = P::load(a.x, row * a.x_row + at);
   }
   const int g = find_group(a.groups, a.G, row, lane);
-  if (g < 0 || g >= max(a.G, 1)) return;  // the same for all waves of the row
+  if (g < 0 || g >= max(a.G, 1)) {  // the same for all waves of the row
+    if (a.clear) clear_row<BF16, V, W, J>(a, row, at0);
+    return;
+  }
 
   auto across = [&](float v, int k) {
     v = lanes_sum(v);
@@ -302,7 +317,10 @@ __global__ __launch_bounds__(W == 1 ? kNormThreads : W * 64) void norm_back_kern
       g = find_group(a.groups, a.G, row, lane);
       end = g < a.G ? a.groups[g + 1] : a.M;
     }
-    if (g < 0 || g >= max(a.G, 1)) return;
+    if (g < 0 || g >= max(a.G, 1)) {
+      if (a.clear) clear_row<BF16, V, W, J>(a, row, at0);
+      return;
+    }
     if (g != open) {
       if (open >= 0 && a.part != nullptr) flush(open);
       open = g;
@@ -554,6 +572,7 @@ NormArgs norm_args(const NormCall& c) {
   a.inv_d = 1.f / (float)c.D;
   a.groups = c.groups;
   a.stats = const_cast<float*>(c.stats);
+  a.clear = c.clear;
   return a;
 }
 

@@ -773,6 +773,11 @@ rtl_status check_norm_sizes(rtl_dtype dt, int64_t M, int64_t D, int64_t G) {
   return RTL_OK;
 }
 
+rtl_status check_rest(rtl_rest rest) {
+  if (rest != RTL_REST_KEPT && rest != RTL_REST_ZEROS) return fail(RTL_ERR_ARG, "unsupported rest %d", (int)rest);
+  return RTL_OK;
+}
+
 rtl_status check_norm_width(const rtl::NormCall& c) {
   if (!rtl::norm_fits(c.dt, c.D, rtl::norm_is_wide(c)))
     return fail(RTL_ERR_UNSUPPORTED, "D above %lld needs 16-byte aligned rows (D=%lld)", (long long)rtl::kNormMaxDNarrow,
@@ -806,7 +811,16 @@ extern "C" {
 rtl_status rtl_layer_norm(rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const void* w, const void* b,
                           int64_t G, const int32_t* groups, const void* scale, int64_t scale_row, const void* shift,
                           int64_t shift_row, float eps, void* Y, int64_t y_row, float* stats, void* stream) {
+  return rtl_layer_norm_ex(RTL_REST_KEPT, dt, M, D, X, x_row, w, b, G, groups, scale, scale_row, shift, shift_row, eps, Y, y_row,
+                           stats, stream);
+}
+
+rtl_status rtl_layer_norm_ex(rtl_rest rest, rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const void* w,
+                             const void* b, int64_t G, const int32_t* groups, const void* scale, int64_t scale_row,
+                             const void* shift, int64_t shift_row, float eps, void* Y, int64_t y_row, float* stats,
+                             void* stream) {
   rtl_status st;
+  if ((st = check_rest(rest)) != RTL_OK) return st;
   if ((st = check_norm_sizes(dt, M, D, G)) != RTL_OK || (st = check_norm_eps(eps)) != RTL_OK) return st;
   const size_t es = elem_size(dt);
   const View x = rows_of(X, M, D, x_row, es), y = rows_of(Y, M, D, y_row, es);
@@ -822,6 +836,7 @@ rtl_status rtl_layer_norm(rtl_dtype dt, int64_t M, int64_t D, const void* X, int
   c.shift = rtl::RowsView{sh.p, sh.row};
   c.eps = eps;
   c.stats = stats;
+  c.clear = rest == RTL_REST_ZEROS;
   if ((st = check_norm_width(c)) != RTL_OK) return st;
   const Flat small[3] = {{w, (size_t)D * es}, {b, (size_t)D * es}, {groups, (size_t)(G + 1) * 4}};
   const Flat wide[2] = {scale ? range_of(sc) : Flat{nullptr, 0}, shift ? range_of(sh) : Flat{nullptr, 0}};
@@ -847,7 +862,17 @@ rtl_status rtl_layer_norm_backward(rtl_dtype dt, int64_t M, int64_t D, const voi
                                    const int32_t* groups, const void* scale, int64_t scale_row, void* dX, int64_t dx_row,
                                    float* dw, float* db, float* dscale, float* dshift, void* workspace, size_t ws_bytes,
                                    void* stream) {
+  return rtl_layer_norm_backward_ex(RTL_REST_KEPT, dt, M, D, X, x_row, stats, dY, dy_row, w, b, G, groups, scale, scale_row, dX,
+                                    dx_row, dw, db, dscale, dshift, workspace, ws_bytes, stream);
+}
+
+rtl_status rtl_layer_norm_backward_ex(rtl_rest rest, rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row,
+                                      const float* stats, const void* dY, int64_t dy_row, const void* w, const void* b,
+                                      int64_t G, const int32_t* groups, const void* scale, int64_t scale_row, void* dX,
+                                      int64_t dx_row, float* dw, float* db, float* dscale, float* dshift, void* workspace,
+                                      size_t ws_bytes, void* stream) {
   rtl_status st;
+  if ((st = check_rest(rest)) != RTL_OK) return st;
   if ((st = check_norm_sizes(dt, M, D, G)) != RTL_OK) return st;
   if (G * D >= (int64_t)1 << 29) return fail(RTL_ERR_SHAPE, "G x D is too large (G=%lld D=%lld)", (long long)G, (long long)D);
   const size_t es = elem_size(dt);
@@ -867,6 +892,7 @@ rtl_status rtl_layer_norm_backward(rtl_dtype dt, int64_t M, int64_t D, const voi
   c.y = rtl::RowsView{dx.p, dx.row};
   c.dy = rtl::RowsView{dy.p, dy.row};
   c.stats = stats;
+  c.clear = rest == RTL_REST_ZEROS;
   if ((st = check_norm_width(c)) != RTL_OK) return st;
   const size_t need = rtl::norm_back_workspace(M, D, G), wb = (size_t)D * 4, gb = (size_t)(G > 0 ? G : 1) * D * 4;
   const Flat outs[5] = {{dw, wb}, {db, wb}, {dscale, gb}, {dshift, gb}, {workspace, need}};

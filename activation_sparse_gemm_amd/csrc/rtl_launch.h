@@ -118,6 +118,7 @@ struct NormCall {
   const int32_t* groups;    // [G + 1] or null
   float eps;
   const float* stats;       // [M, 2]: forward writes them (null: not wanted), the gradient reads them
+  bool clear;               // y's rows of no group become zeros, else they stay
 };
 constexpr int64_t kNormMaxD = 32768;       // bf16 rows in 16-byte pieces (fp32: half)
 constexpr int64_t kNormMaxDNarrow = 8192;  // rows taken by the element

@@ -391,10 +391,18 @@ rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int
  * squares are summed in fp32 and must lie in its range.  Pointers are aligned to their elements.
  * Limits: where pointers, strides and D allow 16-byte accesses D <= 32768 (bf16) or 16384 (fp32), else
  * D <= 8192; M below 2^31, G below 2^31 - 1; eps in [2^-126, 1].
+ *
+ * rtl_layer_norm_ex and rtl_layer_norm_backward_ex say what becomes of the rows outside the groups in Y and dX:
+ * left as they were (as above), or zeros, for a Y or dX that holds nothing yet.
  */
+typedef enum { RTL_REST_RANGE_MIN_ = -0x7FFFFFFF - 1, RTL_REST_KEPT = 0, RTL_REST_ZEROS = 1, RTL_REST_RANGE_MAX_ = 0x7FFFFFFF } rtl_rest;
 rtl_status rtl_layer_norm(rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const void* w, const void* b,
                           int64_t G, const int32_t* groups, const void* scale, int64_t scale_row, const void* shift,
                           int64_t shift_row, float eps, void* Y, int64_t y_row, float* stats, void* stream);
+rtl_status rtl_layer_norm_ex(rtl_rest rest, rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row, const void* w,
+                             const void* b, int64_t G, const int32_t* groups, const void* scale, int64_t scale_row,
+                             const void* shift, int64_t shift_row, float eps, void* Y, int64_t y_row, float* stats,
+                             void* stream);
 
 /*
  * Gradient of rtl_layer_norm from its inputs, the stats it left and the gradient dY: dX [M, D] (which
@@ -410,6 +418,11 @@ rtl_status rtl_layer_norm_backward(rtl_dtype dt, int64_t M, int64_t D, const voi
                                    const int32_t* groups, const void* scale, int64_t scale_row, void* dX, int64_t dx_row,
                                    float* dw, float* db, float* dscale, float* dshift, void* workspace, size_t ws_bytes,
                                    void* stream);
+rtl_status rtl_layer_norm_backward_ex(rtl_rest rest, rtl_dtype dt, int64_t M, int64_t D, const void* X, int64_t x_row,
+                                      const float* stats, const void* dY, int64_t dy_row, const void* w, const void* b,
+                                      int64_t G, const int32_t* groups, const void* scale, int64_t scale_row, void* dX,
+                                      int64_t dx_row, float* dw, float* db, float* dscale, float* dshift, void* workspace,
+                                      size_t ws_bytes, void* stream);
 
 /*
  * Low-rank adapters of many requests beside a shared projection (bf16).  Row m of a batch has adapter

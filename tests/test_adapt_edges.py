@@ -2,7 +2,9 @@
 import pytest
 import torch
 
+import activation_sparse_gemm_amd as rtl
 from activation_sparse_gemm_amd import calib
+from test_block_abi import Buffers, refused
 
 
 @pytest.mark.parametrize("M,rows", [(1, 1), (128, 128), (129, 128), (255, 128), (256, 128), (300, 128), (383, 128), (384, 128),
@@ -18,3 +20,19 @@ def test_batches_take_all_rows_alike(M, rows):
         at += rows
         met += torch.bincount(batch, minlength=M)
         assert int(met.max()) - int(met.min()) <= 1
+
+
+@pytest.mark.parametrize("back", (False, True))
+@pytest.mark.parametrize("rest", (-1, 2, 2 ** 31 - 1))
+def test_rest_is_kept_or_zeros(back, rest):
+    b = Buffers()
+    M, D, G = 6, 64, 2
+    X, Y, dY, stats, groups = b(2 * M * D), b(2 * M * D), b(2 * M * D), b(8 * M), b(16)
+    if back:
+        need = rtl.rtl_layer_norm_backward_workspace_bytes(M, D, G)
+        st = rtl.lib.rtl_layer_norm_backward_ex(rest, rtl.RTL_BF16, M, D, X, D, stats, dY, D, None, None, G, groups, None, 0, Y, D,
+                                                None, None, None, None, b(need), need, None)
+    else:
+        st = rtl.lib.rtl_layer_norm_ex(rest, rtl.RTL_BF16, M, D, X, D, None, None, G, groups, None, 0, None, 0, 1e-6, Y, D, stats,
+                                       None)
+    refused(st, "RTL_ERR_ARG", b, rest)

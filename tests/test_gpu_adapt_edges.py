@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 
 rtl = pytest.importorskip("activation_sparse_gemm_amd")
 
-from activation_sparse_gemm_amd import calib  # noqa: E402
+from activation_sparse_gemm_amd import calib, policy  # noqa: E402
 
 BF = torch.bfloat16
 
@@ -65,3 +65,31 @@ def test_trained_fit_walks_the_whole_set(M):
             to.copy_(t)
         rtl.rtl_adamw(tensors, step + 1, lr, weight_decay=0.0, grad_scale=scale)
     assert all(torch.equal(a, b) for a, b in zip(got, masters))
+
+
+@pytest.mark.parametrize("dt", (BF, torch.float32), ids=("bf16", "f32"))
+@pytest.mark.parametrize("M,D", ((2, 64), (70, 136), (37, 1153), (1100, 64), (1500, 136), (5, 8191), (2049, 5120)))
+@pytest.mark.parametrize("groups", ("early", "void"))
+def test_rows_of_no_request_in_new_outputs(M, D, groups, dt, monkeypatch):
+    """Rows outside the groups are zeros in outputs that the call allocates, whatever their memory held, and as
+    they were in outputs that it is given."""
+    g = {"early": [M // 4, M // 2, M - M // 5], "void": [M // 2, M // 2, M // 2]}[groups]
+    at = torch.tensor(g, dtype=torch.int32, device="cuda")
+    X, dY, parts = A.rnd(1, M, D, dtype=dt), A.rnd(2, M, D, dtype=dt), A.rnd(3, 2, 2 * D, std=0.3, dtype=dt)
+    live = torch.from_numpy(A.norm_rows(M, g) >= 0).cuda()
+    X[~live] = dY[~live] = float("nan")
+    kept, stats = torch.full_like(X, 7.0), torch.zeros(M, 2, device="cuda")
+    scale, shift = parts[:, :D], parts[:, D:]
+    norm = policy.AdaptiveNorm()
+
+    fresh = rtl._new
+    monkeypatch.setattr(rtl, "_new", lambda *of: fresh(*of).view(torch.uint8).fill_(255).view(of[3]))  # NaN in each type
+    rtl.rtl_layer_norm(X, None, None, scale, shift, at, Y=kept, stats=stats)
+    assert bool((kept[~live] == 7).all())
+    Y = norm(X, scale, shift, at)
+    assert torch.equal(Y[live], kept[live]) and not bool(Y[~live].any())
+    want = rtl.rtl_layer_norm_backward(X, stats, dY, None, None, scale, at, dX=kept.fill_(7.0))
+    assert bool((kept[~live] == 7).all())
+    got = norm.backward(X, stats, dY, scale, at)
+    assert torch.equal(got[0][live], kept[live]) and not bool(got[0][~live].any())
+    assert all(torch.equal(a, b) for a, b in zip(got[3:], want[3:]))
