@@ -454,12 +454,15 @@ struct NormColumns {
   }
 };
 
-// The sums of group blockIdx.x over its chunks, 32 columns a workgroup, in double.
+// The sums of a group over its chunks, 32 columns a workgroup, in double.  Groups come in rows of kNormSumGroups (norm_grid's
+// reason).
+constexpr int64_t kNormSumGroups = 1 << 20;
 template <bool BF16, int CV, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_sum_kernel(const SumArgs a) {
   typedef NormColumns<CV, THREADS> Columns;
   Columns t;
-  const int64_t g = blockIdx.x;
+  const int64_t g = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+  if (g >= a.G) return;
   const int col0 = blockIdx.y * 32, at = col0 + t.lane();
   int64_t lo = 0, hi = a.M;
   if (a.groups != nullptr) {
@@ -695,7 +698,8 @@ hipError_t launch_norm_back(const NormCall& c, float* dw, float* db, float* dsca
   const unsigned cols = (unsigned)((c.D + 31) / 32);
   auto go = [&](auto bf16) {
     constexpr bool B = decltype(bf16)::value;
-    const dim3 grid((unsigned)s.G, cols);
+    const int64_t wide = std::min<int64_t>(s.G, kNormSumGroups);
+    const dim3 grid((unsigned)wide, cols, (unsigned)((s.G + wide - 1) / wide));
     auto sum = [&](auto threads) {
       constexpr int T = decltype(threads)::value;
       if (c.D % 4 == 0) hipLaunchKernelGGL((norm_sum_kernel<B, 4, T>), grid, dim3(T), 0, stream, s);

@@ -93,3 +93,24 @@ def test_rows_of_no_request_in_new_outputs(M, D, groups, dt, monkeypatch):
     got = norm.backward(X, stats, dY, scale, at)
     assert torch.equal(got[0][live], kept[live]) and not bool(got[0][~live].any())
     assert all(torch.equal(a, b) for a, b in zip(got[3:], want[3:]))
+
+
+@pytest.mark.parametrize("G,D", ((2 ** 24 + 3, 8), (2 ** 20 + 1, 40)))
+def test_sums_of_more_groups_than_a_grid_row_takes(G, D):
+    """A group of one row here and there among 2^24: each request's own gradients, zeros for the empty ones."""
+    M = 7
+    group = torch.tensor([0, 1, 2 ** 19, 2 ** 20 - 1, 2 ** 20, G - 2, G - 1]).sort().values  # each row's
+    offsets = torch.searchsorted(group, torch.arange(G + 1)).int().cuda()
+    X, dY, w = A.rnd(1, M, D), A.rnd(2, M, D, std=0.1), A.rnd(3, D, std=0.2, mean=1.0)
+    scale = torch.zeros(1, D, dtype=BF, device="cuda").expand(G, D)
+    stats = torch.zeros(M, 2, device="cuda")
+    rtl.rtl_layer_norm(X, w, None, scale, scale, offsets, stats=stats)
+    dX, dw, db, dscale, dshift = rtl.rtl_layer_norm_backward(X, stats, dY, w, None, scale, offsets)
+    some = group.unique(return_inverse=True)[1]
+    few = torch.searchsorted(some, torch.arange(int(some.max()) + 2)).int().cuda()
+    want = rtl.rtl_layer_norm_backward(X, stats, dY, w, None, scale[:len(few) - 1], few)
+    used = group.unique().cuda()
+    assert torch.equal(dX, want[0]) and torch.equal(dw, want[1]) and db is None
+    assert torch.equal(dscale[used], want[3]) and torch.equal(dshift[used], want[4])
+    for t in (dscale, dshift):
+        assert int(t.any(dim=1).sum()) == len(used)
