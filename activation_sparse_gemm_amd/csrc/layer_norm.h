@@ -410,6 +410,16 @@ struct SumArgs {
   double* group;                     // [G][2][D]: the groups' sums, for dw and db of several groups
 };
 
+// Rows [lo, hi) of group g, within M; none where hi <= lo.
+__device__ __forceinline__ void rows_of_group(const SumArgs& a, int64_t g, int64_t& lo, int64_t& hi) {
+  lo = 0;
+  hi = a.M;
+  if (a.groups != nullptr) {
+    lo = max((int64_t)a.groups[g], (int64_t)0);
+    hi = min((int64_t)a.groups[g + 1], a.M);
+  }
+}
+
 __device__ __forceinline__ float value_at(bool bf16, const void* p, int64_t at) {
   return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[at] << 16) : ((const float*)p)[at];
 }
@@ -464,11 +474,8 @@ __global__ __launch_bounds__(THREADS) void norm_sum_kernel(const SumArgs a) {
   const int64_t g = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
   if (g >= a.G) return;
   const int col0 = blockIdx.y * 32, at = col0 + t.lane();
-  int64_t lo = 0, hi = a.M;
-  if (a.groups != nullptr) {
-    lo = max((int64_t)a.groups[g], (int64_t)0);
-    hi = min((int64_t)a.groups[g + 1], a.M);
-  }
+  int64_t lo, hi;
+  rows_of_group(a, g, lo, hi);
   if (hi > lo && at < a.D) {
     const int64_t from = lo / a.rows + g, to = (hi - 1) / a.rows + g;
 #pragma unroll 4
@@ -493,7 +500,7 @@ __global__ __launch_bounds__(THREADS) void norm_sum_kernel(const SumArgs a) {
   if (threadIdx.x >= 32 || col >= a.D) return;
   if (a.dscale != nullptr) {
     const double w = a.w != nullptr ? (double)value_at(BF16, a.w, col) : 1.0, b = a.b != nullptr ? (double)value_at(BF16, a.b, col) : 0.0;
-    a.dscale[g * a.D + col] = (float)(w * s1 + b * s0);
+    a.dscale[g * a.D + col] = hi > lo ? (float)(w * s1 + b * s0) : 0.f;  // 0 too where w or b is infinite
   }
   if (a.dshift != nullptr) a.dshift[g * a.D + col] = (float)s0;
   if (a.group != nullptr) {
@@ -505,7 +512,8 @@ __global__ __launch_bounds__(THREADS) void norm_sum_kernel(const SumArgs a) {
   }
 }
 
-// dw and db over the groups: sum_g (1 + scale_g) S_g.
+// dw and db over the groups: sum_g (1 + scale_g) S_g.  An empty group's scale, which may hold anything, does
+// not enter.
 template <bool BF16>
 __global__ __launch_bounds__(256) void norm_weight_kernel(const SumArgs a) {
   typedef NormColumns<1, 256> Columns;
@@ -514,7 +522,9 @@ __global__ __launch_bounds__(256) void norm_weight_kernel(const SumArgs a) {
   if (at < a.D) {
 #pragma unroll 4
     for (int64_t g = t.row(); g < a.G; g += Columns::LR) {
-      const double k = a.scale != nullptr ? 1.0 + (double)value_at(BF16, a.scale, g * a.scale_row + at) : 1.0;
+      int64_t lo, hi;
+      rows_of_group(a, g, lo, hi);
+      const double k = a.scale != nullptr && hi > lo ? 1.0 + (double)value_at(BF16, a.scale, g * a.scale_row + at) : 1.0;
       t.s[0][0] += k * a.group[2 * g * a.D + at];
       t.s[1][0] += k * a.group[(2 * g + 1) * a.D + at];
     }

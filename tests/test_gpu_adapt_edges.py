@@ -114,3 +114,25 @@ def test_sums_of_more_groups_than_a_grid_row_takes(G, D):
     assert torch.equal(dscale[used], want[3]) and torch.equal(dshift[used], want[4])
     for t in (dscale, dshift):
         assert int(t.any(dim=1).sum()) == len(used)
+
+
+@pytest.mark.parametrize("dt", (BF, torch.float32), ids=("bf16", "f32"))
+@pytest.mark.parametrize("bad", (float("nan"), float("inf"), float("-inf")))
+def test_parameters_of_empty_requests_do_not_enter(dt, bad):
+    """Scale and shift of requests without rows, whatever they hold, and weights that are infinite, beside them."""
+    M, D = 50, 72
+    at = torch.tensor([0, 0, 20, 20, 20, 45, 45], dtype=torch.int32, device="cuda")
+    X, dY = A.rnd(1, M, D, dtype=dt), A.rnd(2, M, D, std=0.1, dtype=dt)
+    w, b, parts = A.rnd(3, D, dtype=dt), A.rnd(4, D, dtype=dt), A.rnd(5, 6, 2 * D, std=0.3, dtype=dt)
+    empty = torch.tensor([True, False, True, True, False, True], device="cuda")
+    stats, runs = torch.zeros(M, 2, device="cuda"), []
+    for value in (None, bad):
+        if value is not None:
+            parts[empty] = value
+        scale, shift = parts[:, :D], parts[:, D:]
+        runs.append((rtl.rtl_layer_norm(X, w, b, scale, shift, at, stats=stats),
+                     *rtl.rtl_layer_norm_backward(X, stats, dY, w, b, scale, at)))
+    assert all(torch.equal(a, c) for a, c in zip(*runs)) and not bool(runs[0][4][empty].any())
+    w[3], b[5] = bad, bad
+    dscale, dshift = rtl.rtl_layer_norm_backward(X, stats, dY, w, b, parts[:, :D], at)[3:]
+    assert not bool(dscale[empty].any()) and not bool(dshift[empty].any())
