@@ -20,8 +20,7 @@ from __future__ import annotations
 import torch
 
 from . import (EPS, RTL_ACT_SILU, RTL_ROPE_ADJACENT, rtl_adapters, rtl_adapters_backward, rtl_adapters_plan,
-               rtl_adapters_workspace_bytes, rtl_glu_fused, rtl_layer_norm, rtl_layer_norm_backward, rtl_linear_dense_ref,
-               rtl_linear_fused, rtl_linear_fused_workspace_bytes, rtl_qk_norm_rope, _dt)
+               rtl_glu_fused, rtl_layer_norm, rtl_layer_norm_backward, rtl_linear_dense_ref, rtl_linear_fused, rtl_linear_fused_workspace_bytes, rtl_qk_norm_rope, _dt, _empty, _stream)
 
 __all__ = ["LAYER_KINDS", "MODELS", "dense_layers", "is_sparse", "Linear", "build_block", "AdaptiveNorm", "AdaptedLinear",
            "AttentionInput", "GatedMLP"]
@@ -60,8 +59,8 @@ class Linear:
 
     Sparse: rtl_linear_fused (norm-compensated 2:4 + rank-R branch).  Dense:
     rtl_linear_dense_ref.  The workspace of the sparse layer is allocated on the first
-    call with a given number of rows and reused after that, so later calls allocate
-    nothing but Y (and not even Y when it is passed)."""
+    call with a given number of rows on a stream, for that stream, and reused after that, so
+    later calls allocate nothing but Y (and not even Y when it is passed)."""
 
     def __init__(self, W: torch.Tensor, LA=None, LB=None, sparse: bool = True, eps: float = EPS):
         if sparse and (LA is None) != (LB is None):
@@ -73,17 +72,20 @@ class Linear:
     def R(self) -> int:
         return 0 if self.LB is None else self.LB.shape[0]
 
-    def workspace(self, M: int):
-        if M not in self._ws:
+    def workspace(self, M: int, stream=None):
+        """What calls of M rows on `stream` (None: the current one) use: memory of that stream, so that neither other work
+        that torch gave it to nor another stream's calls meet there."""
+        key = M, _stream(stream).value if self.W.is_cuda else None
+        if key not in self._ws:
             need = rtl_linear_fused_workspace_bytes(_dt(self.W), M, self.W.shape[0], self.W.shape[1], self.R)
-            self._ws[M] = torch.empty((max(need, 1),), dtype=torch.uint8, device=self.W.device)
-        return self._ws[M]
+            self._ws[key] = _empty((max(need, 1),), torch.uint8, self.W.device, stream)
+        return self._ws[key]
 
     def __call__(self, X: torch.Tensor, Y=None, stream=None) -> torch.Tensor:
         if not self.sparse:
             return rtl_linear_dense_ref(X, self.W, Y=Y, stream=stream)
         return rtl_linear_fused(X, self.W, self.LA, self.LB, eps=self.eps, Y=Y,
-                                workspace=self.workspace(X.shape[0]), stream=stream)
+                                workspace=self.workspace(X.shape[0], stream), stream=stream)
 
 
 def build_block(model: str, stream: str, weights: dict) -> dict:
@@ -119,8 +121,8 @@ class AdaptiveNorm:
 class AdaptedLinear:
     """A projection that a batch's requests share, and beside it the low-rank adapters that they bring: Y = linear(X)
     + alpha_a (X LB_a^T) LA_a^T, a row's adapter a of LA [A,N,R] and LB [A,R,K] (bf16) as its batch's plan says.  The
-    adapters add to the projection's output in place: rows without one are the projection's own, to the bit.  Like
-    Linear it keeps one workspace for a number of rows, so two streams need two objects."""
+    adapters add to the projection's output in place: rows without one are the projection's own, to the bit.  The
+    adapters' workspace is the caller's, or allocated by each call on its stream."""
 
     def __init__(self, linear: Linear, LA: torch.Tensor, LB: torch.Tensor, alpha=None):
         N, K = linear.W.shape
@@ -129,29 +131,21 @@ class AdaptedLinear:
         if alpha is not None and tuple(alpha.shape) != (LA.shape[0],):
             raise ValueError(f"alpha is [{LA.shape[0]}], got {tuple(alpha.shape)}")
         self.linear, self.LA, self.LB, self.alpha = linear, LA, LB, alpha
-        self._ws = {}
 
     def plan(self, ids: torch.Tensor, plan=None, stream=None) -> torch.Tensor:
         """The plan of a batch whose row m has adapter ids[m] (int32; outside 0..A-1: none)."""
         return rtl_adapters_plan(ids, self.LA.shape[0], plan, stream=stream)
 
-    def workspace(self, M: int):
-        A, N, R = self.LA.shape
-        need = rtl_adapters_workspace_bytes(M, N, self.LB.shape[2], R, A)
-        if M not in self._ws or self._ws[M].numel() < need:
-            self._ws[M] = torch.empty((max(need, 1),), dtype=torch.uint8, device=self.LA.device)
-        return self._ws[M]
-
-    def __call__(self, X: torch.Tensor, plan: torch.Tensor, T=None, Y=None, stream=None) -> torch.Tensor:
-        """`T` [M,R] float32 receives what `backward` needs."""
+    def __call__(self, X: torch.Tensor, plan: torch.Tensor, T=None, Y=None, stream=None, workspace=None) -> torch.Tensor:
+        """`T` [M,R] float32 receives what `backward` needs; `workspace`: rtl_adapters_workspace_bytes bytes."""
         Y = self.linear(X, Y=Y, stream=stream)
-        return rtl_adapters(X, self.LA, self.LB, plan, self.alpha, Y0=Y, Y=Y, T=T, workspace=self.workspace(X.shape[0]),
-                            stream=stream)
+        return rtl_adapters(X, self.LA, self.LB, plan, self.alpha, Y0=Y, Y=Y, T=T, workspace=workspace, stream=stream)
 
     def backward(self, X: torch.Tensor, plan: torch.Tensor, T: torch.Tensor, dY: torch.Tensor, dX0=None, need_dx: bool = True,
-                 stream=None):
+                 stream=None, workspace=None):
         """(dX, dLA, dLB) of rtl_adapters_backward; `dX0`: what came through the projection."""
-        return rtl_adapters_backward(X, self.LA, self.LB, plan, T, dY, self.alpha, dX0=dX0, need_dx=need_dx, stream=stream)
+        return rtl_adapters_backward(X, self.LA, self.LB, plan, T, dY, self.alpha, dX0=dX0, workspace=workspace, need_dx=need_dx,
+                                     stream=stream)
 
 
 class AttentionInput:

@@ -136,3 +136,39 @@ def test_parameters_of_empty_requests_do_not_enter(dt, bad):
     w[3], b[5] = bad, bad
     dscale, dshift = rtl.rtl_layer_norm_backward(X, stats, dY, w, b, parts[:, :D], at)[3:]
     assert not bool(dscale[empty].any()) and not bool(dshift[empty].any())
+
+
+def test_layers_on_another_stream_leave_freed_memory_alone():
+    """A layer that is dropped while its call waits on another stream: tensors made then hold their values, and the
+    call gives what it gives alone.  A layer's calls on two streams do not meet either."""
+    M, K, N, R = 130, 256, 320, 24
+    X, plan = A.rnd(1, M, K), rtl.rtl_adapters_plan((torch.arange(M, device="cuda") % 3 - 1).int(), 2)
+
+    def layer():
+        shared = policy.Linear(W, LA, LB)
+        return policy.AdaptedLinear(shared, *factors)
+
+    W, LA, LB = A.rnd(2, N, K, std=K ** -0.5), A.rnd(3, N, 32, std=0.02), A.rnd(4, 32, K, std=0.02)
+    factors = A.rnd(5, 2, N, R, std=R ** -0.5), A.rnd(6, 2, R, K, std=K ** -0.5)
+    want = layer()(X, plan)
+    sizes = rtl.rtl_linear_fused_workspace_bytes(rtl.RTL_BF16, M, N, K, 32), rtl.rtl_adapters_workspace_bytes(M, N, K, R, 2)
+    side, Y = torch.cuda.Stream(), torch.empty_like(want)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        lin = layer()
+        lin(X, plan, Y=Y, stream=side)
+        del lin
+        held = [torch.full((n,), 85, dtype=torch.uint8, device="cuda") for n in sizes * 2]
+        torch.cuda.synchronize()
+        assert all(bool((t == 85).all()) for t in held) and torch.equal(Y, want)
+        del held
+    lin, other, outs = layer(), torch.cuda.Stream(), []
+    spaces = {lin.linear.workspace(M, s).data_ptr() for s in (None, side, other)}
+    assert len(spaces) == 3 and lin.linear.workspace(M, side).data_ptr() in spaces
+    for s in (side, other) * 8:
+        outs.append(lin(X, plan, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in outs)
