@@ -113,9 +113,12 @@ class AdaptiveNorm:
         receives what `backward` needs."""
         return rtl_layer_norm(X, self.weight, self.bias, scale, shift, groups, self.eps, Y=Y, stats=stats, stream=stream)
 
-    def backward(self, X: torch.Tensor, stats: torch.Tensor, dY: torch.Tensor, scale=None, groups=None, stream=None):
-        """(dX, dweight, dbias, dscale, dshift) of rtl_layer_norm_backward."""
-        return rtl_layer_norm_backward(X, stats, dY, self.weight, self.bias, scale, groups, stream=stream)
+    def backward(self, X: torch.Tensor, stats: torch.Tensor, dY: torch.Tensor, scale=None, groups=None, stream=None, dX=None,
+                 dweight=None, dbias=None, dscale=None, dshift=None):
+        """(dX, dweight, dbias, dscale, dshift) of rtl_layer_norm_backward, in the tensors that are given: an
+        optimizer's list (rtl_adamw_tensors) holds dweight and dbias from step to step."""
+        return rtl_layer_norm_backward(X, stats, dY, self.weight, self.bias, scale, groups, dX, dweight, dbias, dscale, dshift,
+                                       stream=stream)
 
 
 class AdaptedLinear:
@@ -142,10 +145,11 @@ class AdaptedLinear:
         return rtl_adapters(X, self.LA, self.LB, plan, self.alpha, Y0=Y, Y=Y, T=T, workspace=workspace, stream=stream)
 
     def backward(self, X: torch.Tensor, plan: torch.Tensor, T: torch.Tensor, dY: torch.Tensor, dX0=None, need_dx: bool = True,
-                 stream=None, workspace=None):
-        """(dX, dLA, dLB) of rtl_adapters_backward; `dX0`: what came through the projection."""
-        return rtl_adapters_backward(X, self.LA, self.LB, plan, T, dY, self.alpha, dX0=dX0, workspace=workspace, need_dx=need_dx,
-                                     stream=stream)
+                 stream=None, workspace=None, dX=None, dLA=None, dLB=None):
+        """(dX, dLA, dLB) of rtl_adapters_backward, in the tensors that are given: an optimizer's list
+        (rtl_adamw_tensors) holds dLA and dLB from step to step.  `dX0`: what came through the projection."""
+        return rtl_adapters_backward(X, self.LA, self.LB, plan, T, dY, self.alpha, dX0=dX0, dX=dX, dLA=dLA, dLB=dLB,
+                                     workspace=workspace, need_dx=need_dx, stream=stream)
 
 
 class AttentionInput:

@@ -172,3 +172,56 @@ def test_layers_on_another_stream_leave_freed_memory_alone():
         outs.append(lin(X, plan, stream=s))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in outs)
+
+
+def test_layers_write_the_gradients_that_an_optimizer_holds():
+    """Gradients in given tensors: the same values, and a step's list that is made once, captured with the
+    gradients and replayed on other batches."""
+    M, K, N, R = 90, 64, 72, 16
+    factors = [A.rnd(5, 2, N, R, std=R ** -0.5, dtype=torch.float32), A.rnd(6, 2, R, K, std=K ** -0.5, dtype=torch.float32)]
+    norm = policy.AdaptiveNorm(A.rnd(1, K, std=0.2, mean=1.0, dtype=BF), A.rnd(2, K, std=0.2))
+    lin = policy.AdaptedLinear(policy.Linear(A.rnd(3, N, K, std=K ** -0.5), sparse=False), *(t.to(BF) for t in factors))
+    at, ids = torch.tensor([0, 30, M], dtype=torch.int32, device="cuda"), (torch.arange(M, device="cuda") % 2).int()
+    X, dY, parts, plan = A.rnd(7, M, K), A.rnd(8, M, N), A.rnd(9, 2, 2 * K, std=0.3), lin.plan(ids)
+    scale, shift = parts[:, :K], parts[:, K:]
+    stats, T = torch.empty(M, 2, device="cuda"), torch.empty(M, R, device="cuda")
+    masters = [norm.weight.float(), norm.bias.float(), *factors]
+    params = [norm.weight, norm.bias, lin.LA, lin.LB]
+    grads = [torch.full_like(t, float("nan")) for t in masters]
+    m, v = ([torch.zeros_like(t) for t in masters] for _ in range(2))
+    tensors = rtl.rtl_adamw_tensors(params, grads, m, v, masters=masters)
+
+    def gradients(given):
+        h = norm(X, scale, shift, at, stats=stats)
+        lin(h, plan, T=T)
+        out = dict(zip(("dLA", "dLB"), grads[2:])) if given else {}
+        dh, dLA, dLB = lin.backward(h, plan, T, dY, **out)
+        out = dict(zip(("dweight", "dbias"), grads[:2])) if given else {}
+        return norm.backward(X, stats, dh, scale, at, **out)[1:3] + (dLA, dLB)
+
+    def step():
+        gradients(True)
+        rtl.rtl_adamw(tensors, 1, 1e-2)
+
+    want = gradients(False)
+    got = gradients(True)
+    assert all(a is b for a, b in zip(got, grads)) and all(torch.equal(a, b) for a, b in zip(grads, want))
+    dX, ds, dh = torch.empty_like(X), torch.empty(2, K, device="cuda"), torch.empty(2, K, device="cuda")
+    out = norm.backward(X, stats, X, scale, at, dX=dX, dscale=ds, dshift=dh)
+    assert out[0] is dX and out[3] is ds and out[4] is dh
+    out = lin.backward(X, plan, T, dY, dX=dX)
+    assert out[0] is dX
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    state = masters + m + v + params
+    for k in range(3):
+        X.copy_(A.rnd(20 + k, M, K))
+        before = [t.clone() for t in state]
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in state + grads]
+        for t, b in zip(state, before):
+            t.copy_(b)
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, state + grads))
