@@ -341,7 +341,9 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const JoinArgs a) {
 // of row r16; line_at is free of bank conflicts both ways).  Read as the instructions have it, neighbouring lanes on
 // different rows, every lane is an access of its own: 63 of them an instruction instead of 16, the address and data
 // units 85% busy, and down and up at 32760 x 5120, R = 64, took 105 and 170 us instead of 99 and 142.  The LDS
-// is the wave's own and its instructions run in order: no barrier.
+// is the wave's own and its instructions run in order: no barrier, only an order that the compiler keeps between
+// what one lane writes and another reads (in_order, which leaves no instruction).
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 __device__ __forceinline__ int line_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
 // down: piece[row][r] of a tile = sum over the piece's K of X[row][k] W[adapter][r][k].  The waves take 64 of
@@ -395,6 +397,7 @@ __device__ __forceinline__ void down_piece(const DownArgs& a, const Tile& t, int
       for (int i = 0; i < 2; i++) x[b][i] = *reinterpret_cast<const u32x4*>(xp[b][i] + k);
   };
   auto put = [&]() {
+    in_order();
 #pragma unroll
     for (int i = 0; i < 2; i++) {
 #pragma unroll
@@ -402,6 +405,7 @@ __device__ __forceinline__ void down_piece(const DownArgs& a, const Tile& t, int
 #pragma unroll
       for (int b = 0; b < MB; b++) *reinterpret_cast<u32x4*>(mine + b * 2048 + line_at(8 * i + row, chunk)) = x[b][i];
     }
+    in_order();
   };
   auto form = [&]() {
 #pragma unroll
@@ -547,8 +551,10 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
   };
   u32x4 f[4][RK];
   auto ready = [&]() {
+    in_order();
 #pragma unroll
     for (int j = 0; j < WL; j++) *reinterpret_cast<u32x4*>(mine_w + w_to[j]) = w[j];
+    in_order();
 #pragma unroll
     for (int c = 0; c < 4; c++)
 #pragma unroll
@@ -558,9 +564,11 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
   auto form = [&](int64_t n, int b, bool in) {
     uint8_t* block = mine + (b & 1) * 2048;
     u32x4 v[2], tb[kParts][RK];
+    in_order();
     if (ADD) {
 #pragma unroll
       for (int i = 0; i < 2; i++) *reinterpret_cast<u32x4*>(block + line_at(8 * i + l8, chunk)) = y[b][i];
+      in_order();
 #pragma unroll
       for (int s = 0; s < 2; s++) v[s] = *reinterpret_cast<const u32x4*>(block + line_at(r16, 4 * s + q));
     } else {
@@ -570,6 +578,7 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
     for (int k = 0; k < RK; k++)
 #pragma unroll
       for (int h = 0; h < kParts; h++) tb[h][k] = tv[((h * 4 + b) * RK + k) * 64];
+    in_order();
 #pragma unroll
     for (int s = 0; s < 2; s++) {
       u32x4 out;
@@ -585,6 +594,7 @@ __device__ __forceinline__ void up_piece(const UpArgs& a, const Tile& t, int64_t
       }
       *reinterpret_cast<u32x4*>(block + line_at(r16, 4 * s + q)) = out;
     }
+    in_order();
 #pragma unroll
     for (int k = 0; k < 2; k++) {
       const u32x4 out = *reinterpret_cast<const u32x4*>(block + line_at(8 * k + l8, chunk));
@@ -827,10 +837,12 @@ __device__ __forceinline__ void grad_run(const GradArgs& a, uint8_t* lds, int64_
       for (int l = 0; l < LOADS; l++)
         if (r0 + l * (64 / PER) + sub >= rows) zv[l] = u32x4{};
     }
+    in_order();
 #pragma unroll
     for (int l = 0; l < LOADS; l++) {
       *reinterpret_cast<u32x4*>(mine + ((put_at ^ (l >> 1 & 1) << 7) + l * (64 / PER) * C * 2)) = zv[l];
     }
+    in_order();
     // the next rows' loads go out ahead of this step's products, those of S behind them, into the
     // registers that the products have read
     const bool more = r0 + STEP < rows;
