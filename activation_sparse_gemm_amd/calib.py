@@ -82,6 +82,8 @@ def train_lowrank(X: torch.Tensor, E: torch.Tensor, R: int, steps: int = 2000, r
         raise ValueError(f"rank {R} outside 1..{min(K, N)}, or no rows, or fewer than no steps")
     if (LA is None) != (LB is None):
         raise ValueError("L_A and L_B go together")
+    if LA is not None and (tuple(LA.shape) != (N, R) or tuple(LB.shape) != (R, K)):
+        raise ValueError(f"L_A and L_B of rank {R} are [{N},{R}] and [{R},{K}], got {tuple(LA.shape)} and {tuple(LB.shape)}")
     rows = min(rows, M)
     if LA is None:
         LA = torch.zeros((N, R), device=X.device)

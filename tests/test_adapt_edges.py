@@ -36,3 +36,10 @@ def test_rest_is_kept_or_zeros(back, rest):
         st = rtl.lib.rtl_layer_norm_ex(rest, rtl.RTL_BF16, M, D, X, D, None, None, G, groups, None, 0, None, 0, 1e-6, Y, D, stats,
                                        None)
     refused(st, "RTL_ERR_ARG", b, rest)
+
+
+@pytest.mark.parametrize("LA,LB", [((48, 16), (16, 64)), ((48, 8), (8, 72)), ((40, 8), (8, 64)), ((48, 8), (64, 8)), ((8, 48), (8, 64))])
+def test_trained_fit_starts_from_factors_of_its_rank(LA, LB):
+    X, E = torch.zeros(16, 64, dtype=torch.bfloat16), torch.zeros(16, 48, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="rank 8"):
+        calib.train_lowrank(X, E, 8, LA=torch.zeros(LA), LB=torch.zeros(LB))
