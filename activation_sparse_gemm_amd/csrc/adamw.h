@@ -10,10 +10,11 @@
 // (no contraction), so that a value next to the border of two codes is coded the same wherever it
 // is computed so.
 //
-// Bound: memory (28 bytes an element with 32-bit states, 16 with 8-bit ones, 2 less where parameters or
-// gradients are bf16 beside fp32 masters).  A launch takes up to kAdamTensors tensors, their addresses in
+// Bound: memory (28 bytes an element with 32-bit states, 16 with 8-bit ones; 2 more where bf16 parameters are
+// written beside their masters, 2 less where gradients are bf16).  A launch takes up to kAdamTensors tensors, their addresses in
 // its arguments, so that nothing is copied to the device first and a captured call holds them.  Measured, bf16 beside
-// masters: 320 factors, 176 M elements, 32-bit states, 967 us, 5.1 TB/s; 212 M elements, 8-bit states, 630, 5.4 TB/s.
+// masters: 320 factors, 176 M elements, 32-bit states, 970 us, 5.1 TB/s (fp32 gradients 1008, 5.2); 212 M elements, 8-bit
+// states, 634, 5.4 TB/s.
 #pragma once
 #include <algorithm>
 

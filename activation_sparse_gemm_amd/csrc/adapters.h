@@ -12,9 +12,9 @@
 //
 // Bound: memory (X, Y0 and Y pass once, 2 R flops a byte of them).  T and dT are held in fp32 and enter
 // the next products in three bf16 parts (three_parts), all 24 digits.  One would leave 2^-9 of an adapter's
-// share, two 2^-16; the products are too small to hold the kernels (up in parts of three and two, whole calls: 24 rows of
-// 5120 -> 13824, R = 32 16.1 and 15.9 us; 4608 of 2560 -> 7680, R = 64 62.6 and 59.2; 32760 of 5120 -> 5120 253 and 251).
-// 32760 rows of 5120 -> 5120, R = 64: down 101 us, join 10, up 141; a copy of X's size 60, of Y0's to Y 120.
+// share, two 2^-16; the products are too small to hold the kernels (up with three parts and with two: 24 rows of 5120 -> 13824,
+// R = 32 8.0 and 7.6 us; 4608 of 2560 -> 7680, R = 64 39 and 37; 32760 of 5120 -> 5120, R = 64 145 and 141, join 11 and 10).
+// 32760 rows of 5120 -> 5120, R = 64: down 102 us, join 11, up 145; a read of X takes 60, a copy of Y0 to Y 120.
 // (The gradients' sums, which leave in fp32, were 5e-6 off with two.)
 //
 //   down:   T in pieces over K, the waves taking 64 of K in turn
@@ -247,7 +247,8 @@ __device__ __forceinline__ void parts_of(const float (&v)[8], u32x4 (&w)[kParts]
 // join: T of half a tile, 32 rows, the sum of down's pieces or (kept) its rows as they are; unscaled to `t`, and scaled
 // by alpha in bf16 parts as the products take it: `rows`, up's operand, [tile][part][block of 16 rows][RK][lane]
 // (lane (r16, q): row r16, r = 8q .. 8q + 7 of 32), and `cols`, grad's, [tile][part][half][RB][lane] (r =
-// r16 of a block, rows 8q .. 8q + 7 of the half).  Rows and r past the tile's are zeros.
+// r16 of a block, rows 8q .. 8q + 7 of the half).  Rows past the tile's are zeros, and r past R up to 32 RK; `cols` past
+// that (R of 72 to 96 in blocks for 128) hold what lies there, in sums that grad does not store.
 // A launch of its own: summed by each workgroup of up that needed it, T cost 8 to 19 us of up's time
 // (4608 rows, 2560 -> 7680, R = 64, 72 tiles of up to 8 pieces on 512 workgroups: 53 us for 35; this takes 6), but
 // for the few rows of join_here.
@@ -340,7 +341,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const JoinArgs a) {
 // passes through the wave's own LDS to and from the matrix instructions' layout (lane (r16, q): chunks q and 4 + q
 // of row r16; line_at is free of bank conflicts both ways).  Read as the instructions have it, neighbouring lanes on
 // different rows, every lane is an access of its own: 63 of them an instruction instead of 16, the address and data
-// units 85% busy, and down and up at 32760 x 5120, R = 64, took 105 and 170 us instead of 99 and 142.  The LDS
+// units 85% busy, and down and up at 32760 x 5120, R = 64, took 105 and 170 us instead of 99 and 142 (T in
+// two parts).  The LDS
 // is the wave's own and its instructions run in order: no barrier, only an order that the compiler keeps between
 // what one lane writes and another reads (in_order, which leaves no instruction).
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
@@ -971,7 +973,7 @@ JoinArgs join_of(const Plan& plan, int64_t R, const float* alpha) {
   return a;
 }
 // One block of rows at the most: up sums T itself, each workgroup what it needs, a launch less (5120 -> 5120, R = 128: one
-// row 15.5 us and 14.0 so, 8 rows of 8 adapters 17.0 and 15.1, 64 rows of one 24 and 58).
+// row 15.5 us and 14.4 so, 8 rows of 8 adapters 17.0 and 15.4, 64 rows of one 26 and, with T in two parts, 58).
 bool join_here(int64_t M) { return M <= kJoinHere; }
 void join(const JoinArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(join_kernel, dim3((unsigned)(2 * a.plan.most)), dim3(kJoinThreads), 0, stream, a);

@@ -382,13 +382,15 @@ rtl_status rtl_glu_backward(rtl_act act, rtl_dtype dt, int64_t M, int64_t K, int
  * X and Y are [M, D] with D contiguous and a row stride in elements (that of one row is ignored); Y may
  * be X (same pointer and stride), else it overlaps no input.  w and b [D] may be NULL (ones, zeros).
  * groups [G + 1] (device, int32): ascending offsets, rows groups[g] .. groups[g + 1] - 1 are group g,
- * which may be empty; rows before groups[0] and from groups[G] on are not read and left as they were.
+ * which may be empty; rows before groups[0] and from groups[G] on count for nothing (they may be read) and are
+ * left as they were in Y and stats.
  * groups NULL: all rows are one group (G 0 or 1).  scale and shift [G, D] with a row stride, both or
  * neither (NULL).  What groups holds is not checked, but no call goes past its tensors for it.
  * stats [M, 2] fp32 (NULL to skip) receives each row's mean and r, which the gradient takes.
  *
  * dt is bf16 or fp32, of all tensors but groups and stats; all arithmetic is fp32, rounded once.  The
- * squares are summed in fp32 and must lie in its range.  Pointers are aligned to their elements.
+ * squares are summed in fp32 and must lie in its range.  Pointers are aligned to their elements, stats to 8 bytes, the
+ * gradient's sums and workspace to 16.
  * Limits: where pointers, strides and D allow 16-byte accesses D <= 32768 (bf16) or 16384 (fp32), else
  * D <= 8192; M below 2^31, G below 2^31 - 1; eps in [2^-126, 1].
  *
