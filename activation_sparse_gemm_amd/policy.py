@@ -20,7 +20,7 @@ from __future__ import annotations
 import torch
 
 from . import (EPS, RTL_ACT_SILU, RTL_ROPE_ADJACENT, rtl_adapters, rtl_adapters_backward, rtl_adapters_plan,
-               rtl_glu_fused, rtl_layer_norm, rtl_layer_norm_backward, rtl_linear_dense_ref, rtl_linear_fused, rtl_linear_fused_workspace_bytes, rtl_qk_norm_rope, _dt, _empty, _stream)
+               rtl_glu_fused, rtl_layer_norm, rtl_layer_norm_backward, rtl_linear_dense_ref, rtl_linear_fused, rtl_linear_fused_workspace_bytes, rtl_qk_norm_rope, _dt, _elsewhere, _empty, _stream)
 
 __all__ = ["LAYER_KINDS", "MODELS", "dense_layers", "is_sparse", "Linear", "build_block", "AdaptiveNorm", "AdaptedLinear",
            "AttentionInput", "GatedMLP"]
@@ -82,6 +82,10 @@ class Linear:
         return self._ws[key]
 
     def __call__(self, X: torch.Tensor, Y=None, stream=None) -> torch.Tensor:
+        there = _elsewhere(X, self.W, Y)
+        if there is not None:
+            with there:
+                return self(X, Y, stream)
         if not self.sparse:
             return rtl_linear_dense_ref(X, self.W, Y=Y, stream=stream)
         return rtl_linear_fused(X, self.W, self.LA, self.LB, eps=self.eps, Y=Y,

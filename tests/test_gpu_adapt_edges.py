@@ -225,3 +225,40 @@ def test_layers_write_the_gradients_that_an_optimizer_holds():
             t.copy_(b)
         step()
         assert all(torch.equal(a, b) for a, b in zip(replayed, state + grads))
+
+
+def test_layers_while_another_gpu_is_current(monkeypatch):
+    """A projection, and one with adapters, makes its tensors' GPU the current one first (here the current device's
+    number and the context that changes it stand in for a second GPU)."""
+    M, K, N, R = 9, 64, 40, 8
+    X, W, ids = A.rnd(1, M, K), A.rnd(2, N, K), (torch.arange(M, device="cuda") % 2).int()
+    layers = [policy.Linear(W, sparse=False), policy.Linear(W, A.rnd(3, N, 32, std=0.1), A.rnd(4, 32, K, std=0.1))]
+    layers += [policy.AdaptedLinear(layer, A.rnd(5, 2, N, R), A.rnd(6, 2, R, K)) for layer in layers]
+
+    def calls():
+        plan = layers[2].plan(ids)
+        return [layer(X) for layer in layers[:2]] + [layer(X, plan) for layer in layers[2:]]
+
+    want, here, entered = calls(), X.get_device(), []
+    current = [here + 1]
+
+    class There:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+            current[0] = self.device
+
+        def __exit__(self, *exc):
+            current[0] = here + 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", There)
+    got = calls()
+    monkeypatch.undo()
+    assert len(entered) == 7 and set(entered) == {here}  # the plan, four projections, two calls of adapters
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for layer in layers[:2]:
+        with pytest.raises(ValueError):
+            layer(X.cpu())
